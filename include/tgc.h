@@ -1,6 +1,7 @@
 /*
- * tgc.h -- C ABI of libtgc.so: TGATHER row-concat gather and chunked
- * AllGather fused with a bf16 MatMul, for one sm_103a GPU.
+ * tgc.h -- C ABI of libtgc.so: TGATHER row-concat gather, chunked AllGather
+ * fused with a bf16 MatMul, and the transformer-block operators around that
+ * product (linear, experts, block norm), for one sm_103a GPU.
  *
  * Sources (web pages):
  *   [TG]  "CANN PTO-ISA TGATHER 指令深度解析：跨 Rank 行拼接 Gather 的实现原理与开发指南"
@@ -529,6 +530,217 @@ int64_t tgc_ag_matmul_schedule(int64_t M, int64_t N, int64_t comm_block_rows, in
  * pair of CTAs (128 each), BN is the width of one MMA column block (a tile is
  * one or two blocks wide, see tile_n), BK is the K depth of one pipeline stage. */
 void tgc_gemm_tile_shape(int *bm, int *bn, int *bk);
+
+/* ------------------------------------------------------------------------ */
+/* Transformer-block operators: linear, experts, block norm                  */
+/* ------------------------------------------------------------------------ */
+
+/* Activations of the linear operator (z -> act(z), in fp32):
+ *   RELU       max(z, 0)  (NaN stays NaN; derivative 1 where z > 0, else 0)
+ *   GELU       z * Phi(z), Phi the normal distribution function
+ *   GELU_TANH  0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))
+ *   SILU       z / (1 + exp(-z)) */
+typedef enum tgc_act {
+    TGC_ACT_NONE = 0, TGC_ACT_RELU = 1, TGC_ACT_GELU = 2, TGC_ACT_GELU_TANH = 3, TGC_ACT_SILU = 4
+} tgc_act;
+
+#define TGC_MAX_GROUPS 1024
+
+/*
+ * tgc_linear -- matrix product with bias, activation and residual in its epilogue:
+ *     z[m, n] = sum_k x[m, k] * w[n, k] + bias[n]
+ *     y[m, n] = act(z[m, n]) + residual[m, n]
+ * and, with `offsets`, the same product grouped by expert: rows
+ * [offsets[e], offsets[e+1]) of x are multiplied with expert e's weight and bias.
+ * Products are accumulated in fp32; bias, activation and residual are applied in
+ * fp32 and y (and z) rounded once to `dtype`.  The same inputs give the same bits
+ * on every call.  Zero-initialise the struct; 0 / NULL means the default.
+ *
+ * x         device (M, K), `dtype`.
+ * w         device (N, K), or (ngroups, N, K) with offsets.
+ * bias      device (N) or (ngroups, N), or NULL.
+ * residual  device (M, N) or NULL; may be y itself (same address and ldy).
+ * y         device (M, N), written; must overlap no input except as above.
+ * z         device (M, N) or NULL: receives the pre-activation z (what the
+ *           backward pass needs).
+ * ldx, ldw, ldres, ldy, ldz   elements from one row to the next; 0 = dense.
+ * w_stride  elements from one expert's weight to the next; 0 = N * ldw.
+ * dtype     TGC_BF16 or TGC_F16, of every tensor.
+ * offsets   device int32 array of ngroups + 1 non-decreasing row numbers, read by
+ *           the kernel (no host synchronisation), or NULL: one product over all
+ *           rows.  Experts without rows cost nothing.  Rows outside
+ *           [offsets[0], offsets[ngroups]) are neither used nor written.  Values
+ *           outside [0, M] are taken as the nearer bound, and a group that ends
+ *           before it begins as empty, so no value makes the kernel leave the
+ *           tensors.
+ * ngroups   1..TGC_MAX_GROUPS with offsets; 0 without.
+ *
+ * Requirements: K > 0; K % 8 == 0 and N % 8 == 0, row strides % 8 == 0 and every
+ * pointer 16-byte aligned (offsets 4-byte): TGC_ERR_ALIGN.  Row strides at least
+ * the row length, M, N, K < 2^31 and ngroups * N < 2^31: TGC_ERR_INVALID_ARG.  M == 0 or N == 0
+ * returns TGC_OK.  Asynchronous on `stream`, no allocation, no workspace; can be
+ * captured in a CUDA graph after one uncaptured call on the device.
+ */
+typedef struct tgc_linear_args {
+    const void *x;
+    const void *w;
+    const void *bias;
+    const void *residual;
+    void *y;
+    void *z;
+    int64_t M, K, N;
+    int64_t ldx, ldw, ldres, ldy, ldz;
+    int64_t w_stride;
+    tgc_dtype dtype;
+    tgc_act act;
+    const int32_t *offsets;
+    int ngroups;
+    cudaStream_t stream;
+} tgc_linear_args;
+
+int tgc_linear(const tgc_linear_args *args);
+
+/*
+ * tgc_linear_bwd -- gradients of tgc_linear (dense and grouped):
+ *     dz    = dy * act'(z)              (dy itself with TGC_ACT_NONE)
+ *     dx    = dz * w                    (M, K)
+ *     dw    = dz^T * x                  (N, K), or (ngroups, N, K)
+ *     dbias = sum over rows of dz       (N), or (ngroups, N)
+ * The residual's gradient is dy itself.  dx, dw, dbias may each be NULL (not
+ * computed).  z is what tgc_linear stored (needed unless act is NONE), x is needed
+ * for dw, w for dx.  dw and dbias of an expert without rows are written as zeros.
+ * Sums are fp32 in an order that does not change between calls; dz is rounded to `dtype`
+ * before the products (the tensor cores' operand type), dbias is summed from the
+ * unrounded values.
+ * Strides, alignment, limits and offsets as in tgc_linear; lddx 0 = K, dw dense
+ * (its row stride is K, its expert stride N * K).  N > 0.  M == 0 writes zeros to dw
+ * and dbias.
+ * workspace  device memory of tgc_linear_bwd_workspace_bytes() bytes, 128-byte
+ *            aligned; contents need no initialisation and mean nothing after the
+ *            call.  TGC_ERR_WORKSPACE if missing or too small.
+ */
+typedef struct tgc_linear_bwd_args {
+    const void *dy;
+    const void *x;
+    const void *w;
+    const void *z;
+    void *dx;
+    void *dw;
+    void *dbias;
+    int64_t M, K, N;
+    int64_t lddy, ldx, ldw, ldz, lddx;
+    int64_t w_stride;
+    tgc_dtype dtype;
+    tgc_act act;
+    const int32_t *offsets;
+    int ngroups;
+    void *workspace;
+    size_t workspace_bytes;
+    cudaStream_t stream;
+} tgc_linear_bwd_args;
+
+int tgc_linear_bwd(const tgc_linear_bwd_args *args);
+/* Bytes of workspace tgc_linear_bwd needs for these arguments (pointers are only tested
+ * for NULL; workspace itself is ignored); 0 for none or for arguments it would refuse. */
+size_t tgc_linear_bwd_workspace_bytes(const tgc_linear_bwd_args *args);
+
+/* Norms of tgc_block_norm, over the last axis, statistics in fp32:
+ *   RMS    v / sqrt(mean(v^2) + eps) * weight + bias
+ *   LAYER  (v - mean(v)) / sqrt(var(v) + eps) * weight + bias  (biased variance) */
+typedef enum tgc_norm { TGC_NORM_NONE = 0, TGC_NORM_RMS = 1, TGC_NORM_LAYER = 2 } tgc_norm;
+
+#define TGC_NORM_MAX_D 16384
+
+/*
+ * tgc_block_norm -- the boundary between two transformer blocks in one pass: the
+ * norm after a block, its gate and residual scale, and the norm before the next:
+ *     u = post(y)
+ *     r = res_scale * x + branch_scale * gate[m / (M/gates)] * u
+ *     h = pre(r)
+ * y (M, D) is the block's output, x (M, D) the residual stream it was fed from
+ * (NULL: no residual term), r (M, D) the new residual stream, h (M, D) the next
+ * block's input.  gate is (gates, D): every M/gates consecutive rows share one
+ * vector (gates = 1: one for all; gates = M: one a row); NULL with gates = 0: no
+ * gate.  r may be NULL (not stored), and h is given exactly when pre is not NONE.
+ * h is computed from the unrounded r.  A plain norm of y is post = NONE, x = gate =
+ * r = NULL, branch_scale = 1.  Weights and biases are (D) or NULL (1 and 0); they
+ * must be NULL where their norm is NONE.  eps > 0 where a norm is used.  r may be x
+ * or y itself, and h may be y (same address and stride).
+ * ldy, ldx, ldr, ldh  elements between rows, 0 = D.
+ * dtype     TGC_BF16, TGC_F16 or TGC_F32, of every tensor.  Pointers need their
+ *           element's alignment (16-byte aligned rows run faster).
+ * Errors: TGC_ERR_INVALID_ARG (null y, neither r nor h, gates not a divisor of M,
+ * D not in [1, TGC_NORM_MAX_D], M >= 2^31, eps, ...), TGC_ERR_DTYPE, TGC_ERR_ALIGN.  M == 0
+ * returns TGC_OK.  Asynchronous on `stream`.
+ */
+typedef struct tgc_block_norm_args {
+    const void *y;
+    const void *x;
+    const void *gate;
+    const void *post_weight;
+    const void *post_bias;
+    const void *pre_weight;
+    const void *pre_bias;
+    void *r;
+    void *h;
+    int64_t M, D, gates;
+    int64_t ldy, ldx, ldr, ldh;
+    tgc_norm post, pre;
+    float res_scale, branch_scale, eps;
+    tgc_dtype dtype;
+    cudaStream_t stream;
+} tgc_block_norm_args;
+
+int tgc_block_norm(const tgc_block_norm_args *args);
+
+/*
+ * tgc_block_norm_bwd -- gradients of tgc_block_norm from dr (of r) and dh (of h):
+ *     t  = dr + d pre(r) / d r * dh         dx    = res_scale * t
+ *     du = branch_scale * gate * t          dy    = d post(y) / d y * du
+ *     dgate = sum over a gate's rows of branch_scale * t * u
+ *     dpost_weight = sum du * yhat, dpost_bias = sum du,
+ *     dpre_weight = sum dh * rhat,  dpre_bias = sum dh      (sums over all rows)
+ * y and r are the forward pass's (r as it was stored); the statistics are computed
+ * again from them.  dr may be NULL (zero); dh is needed, with r, exactly when pre is
+ * not NONE.  y is needed when post is not NONE or dgate is asked for.  dx, dy and every
+ * parameter gradient may be NULL (not computed); those without a counterpart in the forward call
+ * (dgate without gate, dpost_* without post, dpre_* without pre) must be NULL.  dx
+ * may be dr or dh itself, dy may be y itself or any of dr, dh.
+ * Sums are fp32 in an order that does not change between calls, rounded once.
+ * M == 0 writes zeros to the parameter gradients.
+ * workspace  device memory of tgc_block_norm_bwd_workspace_bytes() bytes,
+ *            128-byte aligned, no initialisation needed.
+ */
+typedef struct tgc_block_norm_bwd_args {
+    const void *y;
+    const void *r;
+    const void *dr;
+    const void *dh;
+    const void *gate;
+    const void *post_weight;
+    const void *post_bias;
+    const void *pre_weight;
+    void *dx;
+    void *dy;
+    void *dgate;
+    void *dpost_weight;
+    void *dpost_bias;
+    void *dpre_weight;
+    void *dpre_bias;
+    int64_t M, D, gates;
+    int64_t ldy, ldr, lddr, lddh, lddx, lddy;
+    tgc_norm post, pre;
+    float res_scale, branch_scale, eps;
+    tgc_dtype dtype;
+    void *workspace;
+    size_t workspace_bytes;
+    cudaStream_t stream;
+} tgc_block_norm_bwd_args;
+
+int tgc_block_norm_bwd(const tgc_block_norm_bwd_args *args);
+/* Bytes of workspace tgc_block_norm_bwd needs for these arguments (pointers are only
+ * tested for NULL); 0 for none or for arguments it would refuse. */
+size_t tgc_block_norm_bwd_workspace_bytes(const tgc_block_norm_bwd_args *args);
 
 /* ------------------------------------------------------------------------ */
 /* Misc                                                                      */

@@ -1,4 +1,5 @@
-"""GB300-native chunked AllGather x MatMul: TGATHER gather + flag-driven tcgen05 GEMM.
+"""GB300-native chunked AllGather x MatMul: TGATHER gather + flag-driven tcgen05 GEMM, and the
+transformer-block operators around that product (linear, experts, block norm).
 
 The compute lives in libtgc.so (hand-written sm_103a kernels behind a C ABI,
 include/tgc.h); this package only builds it (``_build``), binds it with ctypes
@@ -8,6 +9,6 @@ plumbing of ranks that are separate processes (``ranks``).
 from ._lib import (  # noqa: F401
     TGCError, lib, tgc_ag_matmul, tgc_ag_matmul_ex, tgc_ag_matmul_noalloc, tgc_ag_matmul_plan,
     tgc_ag_matmul_schedule,
-    tgc_ag_matmul_workspace_bytes, tgc_gemm_tile_shape, tgc_ipc_close, tgc_ipc_export, tgc_ipc_open,
-    tgc_last_cuda_error, tgc_status_string, tgc_tgather, tgc_tgather_ex, tgc_tgather_strided, tgc_version,
+    tgc_ag_matmul_workspace_bytes, tgc_block_norm, tgc_block_norm_bwd, tgc_gemm_tile_shape, tgc_ipc_close, tgc_ipc_export, tgc_ipc_open,
+    tgc_last_cuda_error, tgc_linear, tgc_linear_bwd, tgc_status_string, tgc_tgather, tgc_tgather_ex, tgc_tgather_strided, tgc_version,
 )

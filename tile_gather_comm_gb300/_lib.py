@@ -33,6 +33,10 @@ DTYPES = {
     torch.uint8: 0, torch.int8: 1, torch.float16: 2, torch.bfloat16: 3,
     torch.int32: 4, torch.float32: 5, torch.int64: 6, torch.float64: 7,
 }
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+NORMS = {"none": 0, "rms": 1, "layer": 2}
+MAX_GROUPS = 1024              # TGC_MAX_GROUPS
+NORM_MAX_D = 16384             # TGC_NORM_MAX_D
 MAX_RANKS = 64
 TRACE_WORDS = 16
 TRACE = dict(start=0, wait_ns=1, waited_tiles=2, copy_first=3, copy_last=4, pieces=5, end=6, tiles=7,
@@ -77,6 +81,50 @@ class IpcHandle(ctypes.Structure):
 class AgMatmulPlan(ctypes.Structure):
     _fields_ = [("pivot", ctypes.c_int), ("band_n", ctypes.c_int), ("group_m", ctypes.c_int),
                 ("tile_n", ctypes.c_int)]
+
+
+class LinearArgs(ctypes.Structure):
+    _fields_ = [
+        ("x", _vp), ("w", _vp), ("bias", _vp), ("residual", _vp), ("y", _vp), ("z", _vp),
+        ("M", _i64), ("K", _i64), ("N", _i64),
+        ("ldx", _i64), ("ldw", _i64), ("ldres", _i64), ("ldy", _i64), ("ldz", _i64), ("w_stride", _i64),
+        ("dtype", ctypes.c_int), ("act", ctypes.c_int), ("offsets", _vp), ("ngroups", ctypes.c_int),
+        ("stream", _vp),
+    ]
+
+
+class LinearBwdArgs(ctypes.Structure):
+    _fields_ = [
+        ("dy", _vp), ("x", _vp), ("w", _vp), ("z", _vp), ("dx", _vp), ("dw", _vp), ("dbias", _vp),
+        ("M", _i64), ("K", _i64), ("N", _i64),
+        ("lddy", _i64), ("ldx", _i64), ("ldw", _i64), ("ldz", _i64), ("lddx", _i64), ("w_stride", _i64),
+        ("dtype", ctypes.c_int), ("act", ctypes.c_int), ("offsets", _vp), ("ngroups", ctypes.c_int),
+        ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t), ("stream", _vp),
+    ]
+
+
+class BlockNormArgs(ctypes.Structure):
+    _fields_ = [
+        ("y", _vp), ("x", _vp), ("gate", _vp), ("post_weight", _vp), ("post_bias", _vp),
+        ("pre_weight", _vp), ("pre_bias", _vp), ("r", _vp), ("h", _vp),
+        ("M", _i64), ("D", _i64), ("gates", _i64), ("ldy", _i64), ("ldx", _i64), ("ldr", _i64), ("ldh", _i64),
+        ("post", ctypes.c_int), ("pre", ctypes.c_int),
+        ("res_scale", ctypes.c_float), ("branch_scale", ctypes.c_float), ("eps", ctypes.c_float),
+        ("dtype", ctypes.c_int), ("stream", _vp),
+    ]
+
+
+class BlockNormBwdArgs(ctypes.Structure):
+    _fields_ = [
+        ("y", _vp), ("r", _vp), ("dr", _vp), ("dh", _vp), ("gate", _vp), ("post_weight", _vp),
+        ("post_bias", _vp), ("pre_weight", _vp), ("dx", _vp), ("dy", _vp), ("dgate", _vp),
+        ("dpost_weight", _vp), ("dpost_bias", _vp), ("dpre_weight", _vp), ("dpre_bias", _vp),
+        ("M", _i64), ("D", _i64), ("gates", _i64),
+        ("ldy", _i64), ("ldr", _i64), ("lddr", _i64), ("lddh", _i64), ("lddx", _i64), ("lddy", _i64),
+        ("post", ctypes.c_int), ("pre", ctypes.c_int),
+        ("res_scale", ctypes.c_float), ("branch_scale", ctypes.c_float), ("eps", ctypes.c_float),
+        ("dtype", ctypes.c_int), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t), ("stream", _vp),
+    ]
 
 
 class TGCError(RuntimeError):
@@ -135,6 +183,14 @@ def load_library(path: str) -> ctypes.CDLL:
     L.tgc_ag_matmul_schedule.restype = _i64
     L.tgc_gemm_tile_shape.argtypes = [ctypes.POINTER(ctypes.c_int)] * 3
     L.tgc_gemm_tile_shape.restype = None
+    for name, args in (("tgc_linear", LinearArgs), ("tgc_linear_bwd", LinearBwdArgs),
+                       ("tgc_block_norm", BlockNormArgs), ("tgc_block_norm_bwd", BlockNormBwdArgs)):
+        getattr(L, name).argtypes = [ctypes.POINTER(args)]
+        getattr(L, name).restype = ctypes.c_int
+    for name, args in (("tgc_linear_bwd_workspace_bytes", LinearBwdArgs),
+                       ("tgc_block_norm_bwd_workspace_bytes", BlockNormBwdArgs)):
+        getattr(L, name).argtypes = [ctypes.POINTER(args)]
+        getattr(L, name).restype = ctypes.c_size_t
     L.tgc_status_string.argtypes = [ctypes.c_int]
     L.tgc_status_string.restype = ctypes.c_char_p
     L.tgc_last_cuda_error.argtypes = []
@@ -339,3 +395,193 @@ def tgc_ag_matmul_schedule(M: int, N: int, comm_block_rows: int, nranks: int, ra
     lib().tgc_ag_matmul_schedule(M, N, comm_block_rows, nranks, rank, PIVOTS[pivot], group_m, band_n, grid,
                                  cta, buf, n, tile_n)
     return [(buf[2 * i], buf[2 * i + 1]) for i in range(n)]
+
+
+# ----------------------------------------------------------------------------- transformer-block operators
+
+
+def _rows(t, shape, dtype, name: str):
+    """(address, row stride) of a 2-D operand whose rows are contiguous; (None, 0) for None.
+    A tensor of another shape, type or inner stride raises ValueError: the C entry point sees
+    only the address."""
+    if t is None:
+        return None, 0
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name}: expected {dtype} of shape {tuple(shape)}, got {t.dtype} of {tuple(t.shape)}")
+    st = t.stride()
+    if shape[1] > 1 and st[1] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t.data_ptr(), st[0] if shape[0] > 1 else 0
+
+
+def _dense(t, shape, dtype, name: str):
+    """Address of a contiguous operand of exactly this shape; None for None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {dtype} of shape {shape}, got {t.dtype} of {tuple(t.shape)}"
+                         f" with strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _weight(w, K: int, dtype, ngroups: int):
+    """(address, N, row stride, expert stride) of a (N, K) or, with groups, (ngroups, N, K) weight."""
+    dims = 3 if ngroups else 2
+    if w.dtype != dtype or w.dim() != dims or w.shape[-1] != K or (ngroups and w.shape[0] != ngroups):
+        raise ValueError(f"w: expected {dtype} of shape {(ngroups, 'N', K) if ngroups else ('N', K)}, got {w.dtype} "
+                         f"of {tuple(w.shape)}")
+    st = w.stride()
+    if K > 1 and st[-1] != 1:
+        raise ValueError("w: the last dimension must be contiguous")
+    N = w.shape[-2]
+    return w.data_ptr(), N, st[-2] if N > 1 else 0, st[0] if ngroups > 1 else 0
+
+
+def _offsets(offsets):
+    """(address, number of groups) of the experts' row offsets; (None, 0) for None."""
+    if offsets is None:
+        return None, 0
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 or not offsets.is_contiguous():
+        raise ValueError("offsets: expected contiguous int32 of ngroups + 1 row numbers")
+    return offsets.data_ptr(), offsets.numel() - 1
+
+
+def _same_device(*ts):
+    """The operands live on the current device (addresses are all the library gets)."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("operands must be CUDA tensors")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"operands on {dev} and {t.device}")
+    if dev is not None and dev.index != torch.cuda.current_device():
+        raise ValueError(f"operands on {dev}, but the current device is {torch.cuda.current_device()}")
+
+
+def _workspace(workspace, nbytes: int, like, stream):
+    """The caller's workspace, or one from torch's allocator that belongs to the call's stream."""
+    if workspace is not None:
+        _same_device(like, workspace)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        return workspace, workspace.numel() * workspace.element_size()
+    if nbytes == 0:
+        return None, 0
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device), nbytes
+    s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+    with torch.cuda.stream(s):
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device), nbytes
+
+
+def tgc_linear(x, w, y, *, bias=None, act: str = "none", residual=None, z=None, offsets=None, stream=None,
+               check: bool = True) -> int:
+    """y = act(x @ w^T + bias) + residual (bf16 or f16), z receiving the pre-activation; with
+    ``offsets`` (int32, ngroups + 1) the product grouped by expert: w is (ngroups, N, K), bias
+    (ngroups, N).  Asynchronous on ``stream``."""
+    _same_device(x, w, y, bias, residual, z, offsets)
+    if x.dim() != 2:
+        raise ValueError("x: expected (M, K)")
+    M, K = x.shape
+    off, ngroups = _offsets(offsets)
+    pw, N, ldw, w_stride = _weight(w, K, x.dtype, ngroups)
+    mn = (M, N)
+    px, ldx = _rows(x, x.shape, x.dtype, "x")
+    py, ldy = _rows(y, mn, x.dtype, "y")
+    pr, ldres = _rows(residual, mn, x.dtype, "residual")
+    pz, ldz = _rows(z, mn, x.dtype, "z")
+    a = LinearArgs(px, pw, _dense(bias, (ngroups, N) if ngroups else (N,), x.dtype, "bias"), pr, py, pz, M, K, N,
+                   ldx, ldw, ldres, ldy, ldz, w_stride, DTYPES[x.dtype], ACTS[act], off, ngroups, _stream(stream))
+    rc = lib().tgc_linear(ctypes.byref(a))
+    return _check(rc, "tgc_linear") if check else rc
+
+
+def tgc_linear_bwd(dy, x, w, *, z=None, act: str = "none", dx=None, dw=None, dbias=None, offsets=None,
+                   workspace=None, stream=None, check: bool = True) -> int:
+    """Gradients of tgc_linear into dx, dw and dbias (each optional): dz = dy * act'(z),
+    dx = dz @ w, dw = dz^T @ x, dbias = dz summed over rows.  The residual's gradient is dy.
+    ``workspace``: a contiguous CUDA tensor of tgc_linear_bwd_workspace_bytes' size, by default
+    taken from torch's allocator.  Asynchronous on ``stream``."""
+    _same_device(dy, x, w, z, dx, dw, dbias, offsets)
+    if x.dim() != 2:
+        raise ValueError("x: expected (M, K)")
+    M, K = x.shape
+    off, ngroups = _offsets(offsets)
+    pw, N, ldw, w_stride = _weight(w, K, x.dtype, ngroups)
+    lead = (ngroups,) if ngroups else ()
+    mn = (M, N)
+    pdy, lddy = _rows(dy, mn, x.dtype, "dy")
+    px, ldx = _rows(x, x.shape, x.dtype, "x")
+    pz, ldz = _rows(z, mn, x.dtype, "z")
+    pdx, lddx = _rows(dx, (M, K), x.dtype, "dx")
+    a = LinearBwdArgs(pdy, px, pw, pz, pdx, _dense(dw, (*lead, N, K), x.dtype, "dw"),
+                      _dense(dbias, (*lead, N), x.dtype, "dbias"), M, K, N, lddy, ldx, ldw, ldz, lddx, w_stride,
+                      DTYPES[x.dtype], ACTS[act], off, ngroups, None, 0, _stream(stream))
+    ws, a.workspace_bytes = _workspace(workspace, lib().tgc_linear_bwd_workspace_bytes(ctypes.byref(a)), x, stream)
+    a.workspace = _ptr(ws)
+    rc = lib().tgc_linear_bwd(ctypes.byref(a))
+    return _check(rc, "tgc_linear_bwd") if check else rc
+
+
+def tgc_block_norm(y, r=None, h=None, *, x=None, gate=None, post: str = "none", post_weight=None, post_bias=None,
+                   pre: str = "rms", pre_weight=None, pre_bias=None, res_scale: float = 1.0,
+                   branch_scale: float = 1.0, eps: float = 1e-5, stream=None, check: bool = True) -> int:
+    """u = post(y); r = res_scale * x + branch_scale * gate * u; h = pre(r), one pass over (M, D)
+    tensors.  gate is (gates, D), each vector shared by M / gates consecutive rows; norms are
+    "none", "rms" or "layer".  Asynchronous on ``stream``."""
+    _same_device(y, x, r, h, gate, post_weight, post_bias, pre_weight, pre_bias)
+    if y.dim() != 2:
+        raise ValueError("y: expected (M, D)")
+    M, D = y.shape
+    dt, md = y.dtype, y.shape
+    py, ldy = _rows(y, md, dt, "y")
+    px, ldx = _rows(x, md, dt, "x")
+    pr, ldr = _rows(r, md, dt, "r")
+    ph, ldh = _rows(h, md, dt, "h")
+    gates = gate.shape[0] if gate is not None else 0
+    v = (D,)
+    a = BlockNormArgs(py, px, _dense(gate, (gates, D), dt, "gate"), _dense(post_weight, v, dt, "post_weight"),
+                      _dense(post_bias, v, dt, "post_bias"), _dense(pre_weight, v, dt, "pre_weight"),
+                      _dense(pre_bias, v, dt, "pre_bias"), pr, ph, M, D, gates, ldy, ldx, ldr, ldh, NORMS[post],
+                      NORMS[pre], res_scale, branch_scale, eps, DTYPES[dt], _stream(stream))
+    rc = lib().tgc_block_norm(ctypes.byref(a))
+    return _check(rc, "tgc_block_norm") if check else rc
+
+
+def tgc_block_norm_bwd(y, r, dr, dh, *, gate=None, post: str = "none", post_weight=None, post_bias=None,
+                       pre: str = "rms", pre_weight=None, res_scale: float = 1.0, branch_scale: float = 1.0,
+                       eps: float = 1e-5, dx=None, dy=None, dgate=None, dpost_weight=None, dpost_bias=None,
+                       dpre_weight=None, dpre_bias=None, workspace=None, stream=None, check: bool = True) -> int:
+    """Gradients of tgc_block_norm from dr and dh, into whichever outputs are given.  y and r are the
+    forward pass's; any of y, r, dr, dh may be None where the header says it is not needed.
+    ``workspace``: as for tgc_linear_bwd.  Asynchronous on ``stream``."""
+    outs = (dx, dy, dgate, dpost_weight, dpost_bias, dpre_weight, dpre_bias)
+    _same_device(y, r, dr, dh, gate, post_weight, post_bias, pre_weight, *outs)
+    like = next((t for t in (dh, dr, y, r) if t is not None), None)
+    if like is None or like.dim() != 2:
+        raise ValueError("expected (M, D) operands")
+    M, D = like.shape
+    dt, md = like.dtype, like.shape
+    py, ldy = _rows(y, md, dt, "y")
+    pr, ldr = _rows(r, md, dt, "r")
+    pdr, lddr = _rows(dr, md, dt, "dr")
+    pdh, lddh = _rows(dh, md, dt, "dh")
+    pdx, lddx = _rows(dx, md, dt, "dx")
+    pdy, lddy = _rows(dy, md, dt, "dy")
+    gates = gate.shape[0] if gate is not None else 0
+    v, g = (D,), (gates, D)
+    a = BlockNormBwdArgs(py, pr, pdr, pdh, _dense(gate, g, dt, "gate"), _dense(post_weight, v, dt, "post_weight"),
+                         _dense(post_bias, v, dt, "post_bias"), _dense(pre_weight, v, dt, "pre_weight"), pdx, pdy,
+                         _dense(dgate, g, dt, "dgate"), _dense(dpost_weight, v, dt, "dpost_weight"),
+                         _dense(dpost_bias, v, dt, "dpost_bias"), _dense(dpre_weight, v, dt, "dpre_weight"),
+                         _dense(dpre_bias, v, dt, "dpre_bias"), M, D, gates, ldy, ldr, lddr, lddh, lddx, lddy,
+                         NORMS[post], NORMS[pre], res_scale, branch_scale, eps, DTYPES[dt], None, 0, _stream(stream))
+    ws, a.workspace_bytes = _workspace(workspace, lib().tgc_block_norm_bwd_workspace_bytes(ctypes.byref(a)), like,
+                                       stream)
+    a.workspace = _ptr(ws)
+    rc = lib().tgc_block_norm_bwd(ctypes.byref(a))
+    return _check(rc, "tgc_block_norm_bwd") if check else rc

@@ -1,0 +1,402 @@
+// linear.cu -- tgc_linear and tgc_linear_bwd: matrix products with bias, activation and
+// residual in the epilogue, dense or grouped by expert, and their gradients.
+//
+//   forward   z = x w^T + b, y = act(z) + residual
+//   backward  dz = dy act'(z), dx = dz w, dw = dz^T x, db = sum of dz over rows
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "act.cuh"
+#include "groups.cuh"
+#include "internal.h"
+
+namespace tgc {
+
+static bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// ---------------------------------------------------------------- product
+
+// out(i, j) = sum_r a(i, r) b(j, r) over one group: either the i axis or (RED_ROWS) the
+// reduction runs over the group's rows.
+struct Product {
+    const void *a, *b;
+    int64_t ai, ar, bj, br;      // element strides along i / j and along the reduction
+    int64_t b_group, out_group;  // elements from one group's b / out to the next
+    void *out;
+    int64_t ldo;
+    int I, J, R;  // extents; the one that is grouped is M
+    int M;
+    const int32_t *offsets;
+    // epilogue (forward)
+    const void *bias, *residual;
+    void *z;
+    int64_t ldres, ldz;
+    int act;
+};
+
+constexpr int kST = 64, kSR = 16;
+
+template <typename T, bool RED_ROWS>
+__global__ void __launch_bounds__(256) product_kernel(const Product p) {
+    __shared__ float sa[kSR][kST + 1], sb[kSR][kST + 1];
+    const int e = blockIdx.z;
+    const RowRange g = group_range(p.offsets, e, p.M);
+    const int i_begin = RED_ROWS ? 0 : g.begin, i_end = RED_ROWS ? p.I : g.end;
+    const int r_begin = RED_ROWS ? g.begin : 0, r_end = RED_ROWS ? g.end : p.R;
+    const T *a = static_cast<const T *>(p.a);
+    const T *b = static_cast<const T *>(p.b) + (int64_t)e * p.b_group;
+    const int j0 = blockIdx.x * kST;
+    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+    for (int i0 = i_begin + blockIdx.y * kST; i0 < i_end; i0 += gridDim.y * kST) {
+        float acc[4][4] = {};
+        for (int r0 = r_begin; r0 < r_end; r0 += kSR) {
+            for (int q = threadIdx.x; q < kST * kSR; q += 256) {
+                // consecutive threads walk the axis that is contiguous in memory
+                const int ia = p.ar == 1 ? q / kSR : q % kST, ra = p.ar == 1 ? q % kSR : q / kST;
+                sa[ra][ia] = i0 + ia < i_end && r0 + ra < r_end
+                                 ? to_f32(a[(int64_t)(i0 + ia) * p.ai + (int64_t)(r0 + ra) * p.ar]) : 0.0f;
+                const int jb = p.br == 1 ? q / kSR : q % kST, rb = p.br == 1 ? q % kSR : q / kST;
+                sb[rb][jb] = j0 + jb < p.J && r0 + rb < r_end
+                                 ? to_f32(b[(int64_t)(j0 + jb) * p.bj + (int64_t)(r0 + rb) * p.br]) : 0.0f;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < kSR; ++r)
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) acc[u][v] += sa[r][ty + 16 * u] * sb[r][tx + 16 * v];
+            __syncthreads();
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int i = i0 + ty + 16 * u, j = j0 + tx + 16 * v;
+                if (i >= i_end || j >= p.J) continue;
+                float s = acc[u][v];
+                if (p.bias != nullptr) s += to_f32(static_cast<const T *>(p.bias)[(int64_t)e * p.J + j]);
+                if (p.z != nullptr) static_cast<T *>(p.z)[(int64_t)i * p.ldz + j] = from_f32<T>(s);
+                s = act_f32(s, p.act);
+                if (p.residual != nullptr)
+                    s += to_f32(static_cast<const T *>(p.residual)[(int64_t)i * p.ldres + j]);
+                static_cast<T *>(p.out)[(int64_t)e * p.out_group + (int64_t)i * p.ldo + j] = from_f32<T>(s);
+            }
+    }
+}
+
+static int launch_product(const Product &p, bool red_rows, int ngroups, tgc_dtype dt, cudaStream_t stream) {
+    const int rows = (p.I + kST - 1) / kST;
+    const dim3 grid((unsigned)((p.J + kST - 1) / kST), (unsigned)(rows < 65535 ? rows : 65535), (unsigned)ngroups);
+    if (dt == TGC_BF16) {
+        if (red_rows) product_kernel<__nv_bfloat16, true><<<grid, 256, 0, stream>>>(p);
+        else product_kernel<__nv_bfloat16, false><<<grid, 256, 0, stream>>>(p);
+    } else {
+        if (red_rows) product_kernel<__half, true><<<grid, 256, 0, stream>>>(p);
+        else product_kernel<__half, false><<<grid, 256, 0, stream>>>(p);
+    }
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? TGC_OK : cuda_fail(e);
+}
+
+// ---------------------------------------------------------------- dz and the bias gradient
+
+// dz = dy act'(z) and, in the same pass, the column sums of each chunk of kChunk rows (chunks
+// never cross a group): block (strip, chunk) holds 32 vectors of 8 columns x 8 row lanes.
+// Bound by memory: dy and z read once, dz written once, partial sums M/kChunk x N fp32.
+constexpr int kChunk = 64;
+
+struct DzParams {
+    const void *dy, *z;
+    void *dz;        // null: not stored (dy is the products' operand)
+    float *partial;  // null: no bias gradient
+    int M, N, ngroups;
+    int64_t lddy, ldz;
+    int act;
+    const int32_t *offsets;
+};
+
+template <typename T>
+struct alignas(16) Vec8 {
+    T v[8];
+};
+
+template <typename T>
+__global__ void __launch_bounds__(256) dz_kernel(const DzParams p) {
+    __shared__ float sums[8][32 * 8 + 8];
+    __shared__ int s_rows[2];
+    const int strips = (p.N + 255) / 256;
+    const int strip = (int)(blockIdx.x % (unsigned)strips), chunk = (int)(blockIdx.x / (unsigned)strips);
+    const int cv = threadIdx.x % 32, rl = threadIdx.x / 32;
+    const int n = (strip * 32 + cv) * 8;
+    if (threadIdx.x < 32) {
+        int idx = 0;
+        const int e = p.offsets == nullptr
+                          ? (idx = chunk, 0)
+                          : find_group_tile(p.offsets, p.ngroups, p.M, kChunk, chunk, threadIdx.x, &idx);
+        if (threadIdx.x == 0) {
+            const RowRange g = e >= 0 ? group_range(p.offsets, e, p.M) : RowRange{0, 0};
+            const int r0 = g.begin + idx * kChunk;
+            s_rows[0] = r0;
+            s_rows[1] = r0 + kChunk < g.end ? r0 + kChunk : g.end;
+        }
+    }
+    __syncthreads();
+    const int r0 = s_rows[0], r1 = s_rows[1];
+    if (r0 >= r1) return;
+    float acc[8] = {};
+    if (n < p.N) {
+        for (int m = r0 + rl; m < r1; m += 8) {
+            const Vec8<T> dy = *reinterpret_cast<const Vec8<T> *>(static_cast<const T *>(p.dy) + (int64_t)m * p.lddy + n);
+            float d[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) d[c] = to_f32(dy.v[c]);
+            if (p.act != TGC_ACT_NONE) {
+                const Vec8<T> z = *reinterpret_cast<const Vec8<T> *>(static_cast<const T *>(p.z) + (int64_t)m * p.ldz + n);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) d[c] *= act_grad_f32(to_f32(z.v[c]), p.act);
+            }
+            if (p.dz != nullptr) {
+                Vec8<T> o;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) o.v[c] = from_f32<T>(d[c]);
+                *reinterpret_cast<Vec8<T> *>(static_cast<T *>(p.dz) + (int64_t)m * p.N + n) = o;
+            }
+#pragma unroll
+            for (int c = 0; c < 8; ++c) acc[c] += d[c];
+        }
+    }
+    if (p.partial == nullptr) return;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) sums[rl][cv * 8 + c] = acc[c];
+    __syncthreads();
+    const int col = threadIdx.x, nn = strip * 256 + col;
+    if (nn < p.N) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += sums[i][col];
+        p.partial[(int64_t)chunk * p.N + nn] = s;
+    }
+}
+
+// Sums each group's chunks in order: 32 columns x 8 chunk lanes a block, then the lanes in order.
+template <typename T>
+__global__ void __launch_bounds__(256) bias_sum_kernel(const float *partial, T *db, int M, int N, const int32_t *offsets) {
+    __shared__ float part[8][32];
+    const int e = blockIdx.y;
+    int first = 0;  // this group's first chunk
+    if (offsets != nullptr) {
+        int mine = 0;
+        for (int i = threadIdx.x; i < e; i += 256) {
+            const RowRange g = group_range(offsets, i, M);
+            mine += (g.end - g.begin + kChunk - 1) / kChunk;
+        }
+        __shared__ int s_first;
+        if (threadIdx.x == 0) s_first = 0;
+        __syncthreads();
+        atomicAdd(&s_first, mine);  // integers: the order does not matter
+        __syncthreads();
+        first = s_first;
+    }
+    const RowRange g = group_range(offsets, e, M);
+    const int chunks = (g.end - g.begin + kChunk - 1) / kChunk;
+    const int c = threadIdx.x % 32, l = threadIdx.x / 32, n = blockIdx.x * 32 + c;
+    float s = 0.0f;
+    if (n < N)
+        for (int k = l; k < chunks; k += 8) s += partial[(int64_t)(first + k) * N + n];
+    part[l][c] = s;
+    __syncthreads();
+    if (l == 0 && n < N) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s += part[i][c];
+        db[(int64_t)e * N + n] = from_f32<T>(s);
+    }
+}
+
+// ---------------------------------------------------------------- checks
+
+static int check_common(tgc_dtype dtype, tgc_act act, int64_t M, int64_t K, int64_t N, const int32_t *offsets,
+                        int ngroups) {
+    if (M < 0 || K < 0 || N < 0) return TGC_ERR_INVALID_ARG;
+    const int64_t lim = int64_t(1) << 31;
+    if (M >= lim || K >= lim || N >= lim) return TGC_ERR_INVALID_ARG;
+    if (dtype != TGC_BF16 && dtype != TGC_F16) return TGC_ERR_DTYPE;
+    if (act < TGC_ACT_NONE || act > TGC_ACT_SILU) return TGC_ERR_INVALID_ARG;
+    if (offsets == nullptr ? ngroups != 0 : (ngroups < 1 || ngroups > TGC_MAX_GROUPS)) return TGC_ERR_INVALID_ARG;
+    if (!aligned(offsets, 4)) return TGC_ERR_ALIGN;
+    if (K == 0) return TGC_ERR_INVALID_ARG;
+    if (K % 8 != 0 || N % 8 != 0) return TGC_ERR_ALIGN;
+    if ((int64_t)(ngroups > 0 ? ngroups : 1) * N >= lim) return TGC_ERR_INVALID_ARG;
+    return TGC_OK;
+}
+
+// One (rows, cols) operand: resolves its stride and checks it.  null is fine unless `need`.
+static int check_matrix(const void *p, bool need, int64_t rows, int64_t cols, int64_t *ld) {
+    if (*ld == 0) *ld = cols;
+    if (p == nullptr) return need ? TGC_ERR_INVALID_ARG : TGC_OK;
+    if (*ld < cols) return TGC_ERR_INVALID_ARG;
+    if (*ld % 8 != 0 || !aligned(p, 16)) return TGC_ERR_ALIGN;
+    int64_t bytes = 0;
+    if (__builtin_mul_overflow(*ld, rows * 2, &bytes) || bytes >= (int64_t(1) << 62)) return TGC_ERR_INVALID_ARG;
+    if (*ld >= (int64_t(1) << 39)) return TGC_ERR_INVALID_ARG;  // a tensor map's row stride ends at 2^40 bytes
+    return TGC_OK;
+}
+
+static int check_weight_stride(int64_t *w_stride, int64_t N, int64_t ldw, int ngroups) {
+    if (*w_stride == 0) *w_stride = N * ldw;
+    if (ngroups <= 1) return TGC_OK;
+    if (*w_stride < (N - 1) * ldw) return TGC_ERR_INVALID_ARG;
+    if (*w_stride % 8 != 0) return TGC_ERR_ALIGN;
+    if (*w_stride >= (int64_t(1) << 39)) return TGC_ERR_INVALID_ARG;
+    return TGC_OK;
+}
+
+#define TGC_TRY(expr)                     \
+    do {                                  \
+        const int rc_ = (expr);           \
+        if (rc_ != TGC_OK) return rc_;    \
+    } while (0)
+
+// Fills the defaults of `a` in place; TGC_OK when there may be work.
+static int linear_check(tgc_linear_args &a) {
+    TGC_TRY(check_common(a.dtype, a.act, a.M, a.K, a.N, a.offsets, a.ngroups));
+    if (a.M == 0 || a.N == 0) return TGC_OK;
+    TGC_TRY(check_matrix(a.x, true, a.M, a.K, &a.ldx));
+    TGC_TRY(check_matrix(a.w, true, a.N, a.K, &a.ldw));
+    TGC_TRY(check_matrix(a.y, true, a.M, a.N, &a.ldy));
+    TGC_TRY(check_matrix(a.z, false, a.M, a.N, &a.ldz));
+    TGC_TRY(check_matrix(a.residual, false, a.M, a.N, &a.ldres));
+    if (!aligned(a.bias, 16)) return TGC_ERR_ALIGN;
+    TGC_TRY(check_weight_stride(&a.w_stride, a.N, a.ldw, a.ngroups));
+    if (a.residual == a.y && a.ldres != a.ldy) return TGC_ERR_INVALID_ARG;
+    return TGC_OK;
+}
+
+static int linear_impl(tgc_linear_args a) {
+    TGC_TRY(linear_check(a));
+    if (a.M == 0 || a.N == 0) return TGC_OK;
+    const int groups = a.offsets != nullptr ? a.ngroups : 1;
+    Product p{};
+    p.a = a.x; p.ai = a.ldx; p.ar = 1;
+    p.b = a.w; p.bj = a.ldw; p.br = 1; p.b_group = a.w_stride;
+    p.out = a.y; p.ldo = a.ldy;
+    p.I = (int)a.M; p.J = (int)a.N; p.R = (int)a.K; p.M = (int)a.M;
+    p.offsets = a.offsets;
+    p.bias = a.bias; p.residual = a.residual; p.z = a.z; p.ldres = a.ldres; p.ldz = a.ldz;
+    p.act = a.act;
+    return launch_product(p, false, groups, a.dtype, a.stream);
+}
+
+// Workspace of the backward pass: dz (M, N) in `dtype` unless dy serves, then the bias gradient's chunk sums.
+struct BwdLayout {
+    size_t dz, partial, total;
+    int64_t chunks;
+};
+static BwdLayout bwd_layout(const tgc_linear_bwd_args &a) {
+    auto up = [](size_t v) { return (v + 127) / 128 * 128; };
+    BwdLayout l{};
+    l.chunks = (a.M + kChunk - 1) / kChunk + (a.offsets != nullptr ? a.ngroups : 0);
+    const bool dz = a.act != TGC_ACT_NONE && (a.dx != nullptr || a.dw != nullptr);
+    l.partial = dz ? up((size_t)a.M * (size_t)a.N * 2) : 0;
+    l.total = l.partial + (a.dbias != nullptr ? up((size_t)l.chunks * (size_t)a.N * 4) : 0);
+    return l;
+}
+
+static int linear_bwd_check(tgc_linear_bwd_args &a) {
+    TGC_TRY(check_common(a.dtype, a.act, a.M, a.K, a.N, a.offsets, a.ngroups));
+    if (a.N == 0) return TGC_ERR_INVALID_ARG;
+    const bool some = a.M > 0;
+    TGC_TRY(check_matrix(a.dy, some, a.M, a.N, &a.lddy));
+    TGC_TRY(check_matrix(a.z, some && a.act != TGC_ACT_NONE, a.M, a.N, &a.ldz));
+    TGC_TRY(check_matrix(a.x, some && a.dw != nullptr, a.M, a.K, &a.ldx));
+    TGC_TRY(check_matrix(a.w, some && a.dx != nullptr, a.N, a.K, &a.ldw));
+    TGC_TRY(check_matrix(a.dx, false, a.M, a.K, &a.lddx));
+    if (!aligned(a.dw, 16) || !aligned(a.dbias, 16)) return TGC_ERR_ALIGN;
+    TGC_TRY(check_weight_stride(&a.w_stride, a.N, a.ldw, a.ngroups));
+    if (a.M * ((a.N + 255) / 256) / kChunk >= (int64_t(1) << 30)) return TGC_ERR_INVALID_ARG;  // the dz pass's blocks
+    int64_t bytes = 0;
+    const int groups = a.offsets != nullptr ? a.ngroups : 1;
+    if (__builtin_mul_overflow(a.N * groups, a.K * 2, &bytes) || bytes >= (int64_t(1) << 62)) return TGC_ERR_INVALID_ARG;
+    return TGC_OK;
+}
+
+static int linear_bwd_impl(tgc_linear_bwd_args a) {
+    TGC_TRY(linear_bwd_check(a));
+    const int groups = a.offsets != nullptr ? a.ngroups : 1;
+    if (a.M == 0) {
+        cudaError_t e = cudaSuccess;
+        if (a.dw != nullptr) e = cudaMemsetAsync(a.dw, 0, (size_t)groups * a.N * a.K * 2, a.stream);
+        if (e == cudaSuccess && a.dbias != nullptr) e = cudaMemsetAsync(a.dbias, 0, (size_t)groups * a.N * 2, a.stream);
+        return e == cudaSuccess ? TGC_OK : cuda_fail(e);
+    }
+    const BwdLayout l = bwd_layout(a);
+    if (l.total > 0) {
+        if (a.workspace == nullptr || a.workspace_bytes < l.total) return TGC_ERR_WORKSPACE;
+        if (!aligned(a.workspace, 128)) return TGC_ERR_ALIGN;
+    }
+    uint8_t *ws = static_cast<uint8_t *>(a.workspace);
+    const void *dz = a.dy;
+    int64_t lddz = a.lddy;
+    if (l.total > 0) {
+        DzParams d{};
+        d.dy = a.dy; d.z = a.z; d.lddy = a.lddy; d.ldz = a.ldz;
+        d.M = (int)a.M; d.N = (int)a.N; d.ngroups = a.ngroups; d.act = a.act; d.offsets = a.offsets;
+        if (l.partial > 0) {
+            d.dz = ws;
+            dz = ws;
+            lddz = a.N;
+        }
+        if (a.dbias != nullptr) d.partial = reinterpret_cast<float *>(ws + l.partial);
+        const unsigned grid = (unsigned)((a.N + 255) / 256 * l.chunks);
+        if (a.dtype == TGC_BF16) dz_kernel<__nv_bfloat16><<<grid, 256, 0, a.stream>>>(d);
+        else dz_kernel<__half><<<grid, 256, 0, a.stream>>>(d);
+        if (a.dbias != nullptr) {
+            const dim3 g2((unsigned)((a.N + 31) / 32), (unsigned)groups);
+            if (a.dtype == TGC_BF16)
+                bias_sum_kernel<<<g2, 256, 0, a.stream>>>(d.partial, static_cast<__nv_bfloat16 *>(a.dbias), (int)a.M,
+                                                          (int)a.N, a.offsets);
+            else
+                bias_sum_kernel<<<g2, 256, 0, a.stream>>>(d.partial, static_cast<__half *>(a.dbias), (int)a.M, (int)a.N,
+                                                          a.offsets);
+        }
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    if (a.dx != nullptr) {
+        Product p{};
+        p.a = dz; p.ai = lddz; p.ar = 1;
+        p.b = a.w; p.bj = 1; p.br = a.ldw; p.b_group = a.w_stride;
+        p.out = a.dx; p.ldo = a.lddx;
+        p.I = (int)a.M; p.J = (int)a.K; p.R = (int)a.N; p.M = (int)a.M; p.offsets = a.offsets;
+        TGC_TRY(launch_product(p, false, groups, a.dtype, a.stream));
+    }
+    if (a.dw != nullptr) {
+        Product p{};
+        p.a = dz; p.ai = 1; p.ar = lddz;
+        p.b = a.x; p.bj = 1; p.br = a.ldx;
+        p.out = a.dw; p.ldo = a.K; p.out_group = a.N * a.K;
+        p.I = (int)a.N; p.J = (int)a.K; p.R = (int)a.M; p.M = (int)a.M; p.offsets = a.offsets;
+        TGC_TRY(launch_product(p, true, groups, a.dtype, a.stream));
+    }
+    return TGC_OK;
+}
+
+}  // namespace tgc
+
+extern "C" int tgc_linear(const tgc_linear_args *args) {
+    if (args == nullptr) return TGC_ERR_INVALID_ARG;
+    return tgc::linear_impl(*args);
+}
+
+extern "C" int tgc_linear_bwd(const tgc_linear_bwd_args *args) {
+    if (args == nullptr) return TGC_ERR_INVALID_ARG;
+    return tgc::linear_bwd_impl(*args);
+}
+
+extern "C" size_t tgc_linear_bwd_workspace_bytes(const tgc_linear_bwd_args *args) {
+    if (args == nullptr) return 0;
+    tgc_linear_bwd_args a = *args;
+    if (tgc::linear_bwd_check(a) != TGC_OK || a.M == 0) return 0;
+    return tgc::bwd_layout(a).total;
+}
