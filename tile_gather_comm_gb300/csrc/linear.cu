@@ -10,95 +10,11 @@
 #include "act.cuh"
 #include "groups.cuh"
 #include "internal.h"
+#include "linear_gemm.cuh"
 
 namespace tgc {
 
 static bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// ---------------------------------------------------------------- product
-
-// out(i, j) = sum_r a(i, r) b(j, r) over one group: either the i axis or (RED_ROWS) the
-// reduction runs over the group's rows.
-struct Product {
-    const void *a, *b;
-    int64_t ai, ar, bj, br;      // element strides along i / j and along the reduction
-    int64_t b_group, out_group;  // elements from one group's b / out to the next
-    void *out;
-    int64_t ldo;
-    int I, J, R;  // extents; the one that is grouped is M
-    int M;
-    const int32_t *offsets;
-    // epilogue (forward)
-    const void *bias, *residual;
-    void *z;
-    int64_t ldres, ldz;
-    int act;
-};
-
-constexpr int kST = 64, kSR = 16;
-
-template <typename T, bool RED_ROWS>
-__global__ void __launch_bounds__(256) product_kernel(const Product p) {
-    __shared__ float sa[kSR][kST + 1], sb[kSR][kST + 1];
-    const int e = blockIdx.z;
-    const RowRange g = group_range(p.offsets, e, p.M);
-    const int i_begin = RED_ROWS ? 0 : g.begin, i_end = RED_ROWS ? p.I : g.end;
-    const int r_begin = RED_ROWS ? g.begin : 0, r_end = RED_ROWS ? g.end : p.R;
-    const T *a = static_cast<const T *>(p.a);
-    const T *b = static_cast<const T *>(p.b) + (int64_t)e * p.b_group;
-    const int j0 = blockIdx.x * kST;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    for (int i0 = i_begin + blockIdx.y * kST; i0 < i_end; i0 += gridDim.y * kST) {
-        float acc[4][4] = {};
-        for (int r0 = r_begin; r0 < r_end; r0 += kSR) {
-            for (int q = threadIdx.x; q < kST * kSR; q += 256) {
-                // consecutive threads walk the axis that is contiguous in memory
-                const int ia = p.ar == 1 ? q / kSR : q % kST, ra = p.ar == 1 ? q % kSR : q / kST;
-                sa[ra][ia] = i0 + ia < i_end && r0 + ra < r_end
-                                 ? to_f32(a[(int64_t)(i0 + ia) * p.ai + (int64_t)(r0 + ra) * p.ar]) : 0.0f;
-                const int jb = p.br == 1 ? q / kSR : q % kST, rb = p.br == 1 ? q % kSR : q / kST;
-                sb[rb][jb] = j0 + jb < p.J && r0 + rb < r_end
-                                 ? to_f32(b[(int64_t)(j0 + jb) * p.bj + (int64_t)(r0 + rb) * p.br]) : 0.0f;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int r = 0; r < kSR; ++r)
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) acc[u][v] += sa[r][ty + 16 * u] * sb[r][tx + 16 * v];
-            __syncthreads();
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int i = i0 + ty + 16 * u, j = j0 + tx + 16 * v;
-                if (i >= i_end || j >= p.J) continue;
-                float s = acc[u][v];
-                if (p.bias != nullptr) s += to_f32(static_cast<const T *>(p.bias)[(int64_t)e * p.J + j]);
-                if (p.z != nullptr) static_cast<T *>(p.z)[(int64_t)i * p.ldz + j] = from_f32<T>(s);
-                s = act_f32(s, p.act);
-                if (p.residual != nullptr)
-                    s += to_f32(static_cast<const T *>(p.residual)[(int64_t)i * p.ldres + j]);
-                static_cast<T *>(p.out)[(int64_t)e * p.out_group + (int64_t)i * p.ldo + j] = from_f32<T>(s);
-            }
-    }
-}
-
-static int launch_product(const Product &p, bool red_rows, int ngroups, tgc_dtype dt, cudaStream_t stream) {
-    const int rows = (p.I + kST - 1) / kST;
-    const dim3 grid((unsigned)((p.J + kST - 1) / kST), (unsigned)(rows < 65535 ? rows : 65535), (unsigned)ngroups);
-    if (dt == TGC_BF16) {
-        if (red_rows) product_kernel<__nv_bfloat16, true><<<grid, 256, 0, stream>>>(p);
-        else product_kernel<__nv_bfloat16, false><<<grid, 256, 0, stream>>>(p);
-    } else {
-        if (red_rows) product_kernel<__half, true><<<grid, 256, 0, stream>>>(p);
-        else product_kernel<__half, false><<<grid, 256, 0, stream>>>(p);
-    }
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? TGC_OK : cuda_fail(e);
-}
 
 // ---------------------------------------------------------------- dz and the bias gradient
 
@@ -277,15 +193,15 @@ static int linear_impl(tgc_linear_args a) {
     TGC_TRY(linear_check(a));
     if (a.M == 0 || a.N == 0) return TGC_OK;
     const int groups = a.offsets != nullptr ? a.ngroups : 1;
-    Product p{};
-    p.a = a.x; p.ai = a.ldx; p.ar = 1;
-    p.b = a.w; p.bj = a.ldw; p.br = 1; p.b_group = a.w_stride;
-    p.out = a.y; p.ldo = a.ldy;
-    p.I = (int)a.M; p.J = (int)a.N; p.R = (int)a.K; p.M = (int)a.M;
-    p.offsets = a.offsets;
-    p.bias = a.bias; p.residual = a.residual; p.z = a.z; p.ldres = a.ldres; p.ldz = a.ldz;
-    p.act = a.act;
-    return launch_product(p, false, groups, a.dtype, a.stream);
+    LinearProduct p{};
+    p.a = a.x; p.lda = a.ldx;
+    p.b = a.w; p.ldb = a.ldw; p.b_stride = a.w_stride;
+    p.M = a.M; p.J = a.N; p.R = a.K;
+    p.offsets = a.offsets; p.ngroups = groups;
+    p.bias = a.bias; p.residual = a.residual; p.y = a.y; p.z = a.z;
+    p.ldres = a.ldres; p.ldy = a.ldy; p.ldz = a.ldz;
+    p.act = a.act; p.f16 = a.dtype == TGC_F16;
+    return launch_linear(p, kFwd, a.stream);
 }
 
 // Workspace of the backward pass: dz (M, N) in `dtype` unless dy serves, then the bias gradient's chunk sums.
@@ -363,21 +279,22 @@ static int linear_bwd_impl(tgc_linear_bwd_args a) {
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return cuda_fail(e);
     }
+    LinearProduct p{};
+    p.a = dz; p.lda = lddz;
+    p.M = a.M; p.J = a.K;
+    p.offsets = a.offsets; p.ngroups = groups;
+    p.f16 = a.dtype == TGC_F16;
     if (a.dx != nullptr) {
-        Product p{};
-        p.a = dz; p.ai = lddz; p.ar = 1;
-        p.b = a.w; p.bj = 1; p.br = a.ldw; p.b_group = a.w_stride;
-        p.out = a.dx; p.ldo = a.lddx;
-        p.I = (int)a.M; p.J = (int)a.K; p.R = (int)a.N; p.M = (int)a.M; p.offsets = a.offsets;
-        TGC_TRY(launch_product(p, false, groups, a.dtype, a.stream));
+        p.b = a.w; p.ldb = a.ldw; p.b_stride = a.w_stride;
+        p.R = a.N;
+        p.y = a.dx; p.ldy = a.lddx;
+        TGC_TRY(launch_linear(p, kDgrad, a.stream));
     }
     if (a.dw != nullptr) {
-        Product p{};
-        p.a = dz; p.ai = 1; p.ar = lddz;
-        p.b = a.x; p.bj = 1; p.br = a.ldx;
-        p.out = a.dw; p.ldo = a.K; p.out_group = a.N * a.K;
-        p.I = (int)a.N; p.J = (int)a.K; p.R = (int)a.M; p.M = (int)a.M; p.offsets = a.offsets;
-        TGC_TRY(launch_product(p, true, groups, a.dtype, a.stream));
+        p.b = a.x; p.ldb = a.ldx; p.b_stride = 0;
+        p.I = a.N; p.R = 0;
+        p.y = a.dw; p.ldy = a.K;
+        TGC_TRY(launch_linear(p, kWgrad, a.stream));
     }
     return TGC_OK;
 }

@@ -1,0 +1,164 @@
+// linear_gemm.cuh -- what the linear operator's matrix product kernels share: the three products,
+// their parameters, the operand tiles in shared memory and the walk over groups.
+//
+// One product kernel serves the three products, out(i, j) = sum_r A(i, r) B(j, r):
+//   kFwd    y  = x  w^T    A = x  (rows, r contiguous)   B = w (r contiguous)
+//   kDgrad  dx = dz w      A = dz (rows, r contiguous)   B = w (j contiguous)
+//   kWgrad  dw = dz^T x    A = dz (i contiguous)         B = x (j contiguous)
+// kFwd and kDgrad tile the rows of each group; kWgrad reduces over them.  An operand whose r axis
+// is contiguous is K-major, the other kind MN-major; tcgen05 takes either from shared memory, so no
+// operand is ever transposed by a kernel of its own.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "act.cuh"
+#include "groups.cuh"
+#include "internal.h"
+#include "prims.cuh"
+#include "schedule.h"
+
+namespace tgc {
+
+enum : int { kFwd = 0, kDgrad = 1, kWgrad = 2 };
+
+constexpr int kRowBox = 32;  // rows of the small boxes that load a partial tile of rows
+
+struct LinearParams {
+    int M;           // rows of the grouped axis
+    int I, J, R;     // output rows (kWgrad only), output columns, reduction length (not kWgrad)
+    int num_m;       // tile rows of one group (kWgrad, or dense)
+    int num_n;       // tile columns
+    int ngroups;
+    int group_m;     // tile rows of a group of the raster
+    const int32_t *offsets;
+    // epilogue
+    const void *bias, *residual;
+    void *y, *z;
+    int64_t ldres, ldy, ldz;
+    int act;
+    int f16;
+    int *fault;           // set when a wait expired
+    uint64_t timeout_ns;
+};
+
+// One product as the entry points ask for it (arguments checked).
+struct LinearProduct {
+    const void *a, *b;
+    int64_t lda, ldb, b_stride;
+    int64_t M, I, J, R;  // grouped axis; output rows of kWgrad; output columns; reduction (not kWgrad)
+    const int32_t *offsets;
+    int ngroups;         // 1 without offsets
+    const void *bias, *residual;
+    void *y, *z;
+    int64_t ldres, ldy, ldz;
+    int act;
+    int f16;
+};
+int launch_linear(const LinearProduct &q, int mode, cudaStream_t stream);
+
+// Operand maps: A and B as 3-D (inner, rows, matrix) tensors; aSmall the same A with boxes of
+// kRowBox rows; y and z for the TMA stores.
+struct LinearMaps {
+    CUtensorMap a, a_small, b, y, z;
+};
+
+struct Tile {
+    int e;             // group
+    int m0;            // first output row (in y / dx: a row of the whole tensor; in dw: inside the group's matrix)
+    int n0;            // first output column
+    int rows;          // output rows of the tile that exist (may exceed the tile)
+    int red0, red;     // kWgrad: first row and number of rows of the reduction
+    int num_kb;        // 64-deep steps of the reduction, at least one
+};
+
+// Cumulative tile rows of the groups, built by one warp at kernel start: tile0[e] is the first
+// tile row of group e, tile0[ngroups] their number.
+__device__ __forceinline__ void build_tile_table(const LinearParams &p, int tile_m, int *tile0, int lane) {
+    int base = 0;
+    for (int e0 = 0; e0 < p.ngroups; e0 += 32) {
+        int n = 0;
+        if (e0 + lane < p.ngroups) {
+            const RowRange r = group_range(p.offsets, e0 + lane, p.M);
+            n = (r.end - r.begin + tile_m - 1) / tile_m;
+        }
+        int upto = n;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += v;
+        }
+        if (e0 + lane < p.ngroups) tile0[e0 + lane] = base + upto - n;
+        base += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (lane == 0) tile0[p.ngroups] = base;
+}
+
+template <int MODE>
+__device__ __forceinline__ int num_tiles(const LinearParams &p, const int *tile0) {
+    return MODE == kWgrad ? p.ngroups * p.num_m * p.num_n : tile0[p.ngroups] * p.num_n;
+}
+
+template <int MODE, int TM, int TN>
+__device__ __forceinline__ Tile get_tile(const LinearParams &p, const int *tile0, int t) {
+    Tile r;
+    TileSchedule s;
+    s.num_pid_n = p.num_n;
+    s.group_m = p.group_m;
+    s.pivot_off = 0;
+    s.band_n = 0;
+    int pm, pn;
+    if (MODE == kWgrad) {
+        const int per = p.num_m * p.num_n;
+        r.e = t / per;
+        s.num_pid_m = p.num_m;
+        s.tile(t - r.e * per, pm, pn);
+        const RowRange g = group_range(p.offsets, r.e, p.M);
+        r.red0 = g.begin;
+        r.red = g.end - g.begin;
+        r.m0 = pm * TM;
+        r.rows = p.I - r.m0;
+        r.num_kb = r.red > 0 ? (r.red + kBK - 1) / kBK : 1;
+    } else {
+        const int row = t / p.num_n;  // the last group whose first tile row is <= row
+        int lo = 0, hi = p.ngroups;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (tile0[mid] <= row) lo = mid; else hi = mid;
+        }
+        r.e = lo;
+        s.num_pid_m = tile0[lo + 1] - tile0[lo];
+        s.tile(t - tile0[lo] * p.num_n, pm, pn);
+        const RowRange g = group_range(p.offsets, lo, p.M);
+        r.m0 = g.begin + pm * TM;
+        r.rows = g.end - r.m0;
+        r.red0 = 0;
+        r.red = p.R;
+        r.num_kb = (p.R + kBK - 1) / kBK;
+    }
+    r.n0 = pn * TN;
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool f16) {
+    uint32_t r;
+    if (f16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ void unpack16(uint32_t w, bool f16, float *lo, float *hi) {
+    if (f16) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+        *lo = f.x;
+        *hi = f.y;
+    } else {
+        *lo = __uint_as_float(w << 16);
+        *hi = __uint_as_float(w & 0xffff0000u);
+    }
+}
+
+}  // namespace tgc
