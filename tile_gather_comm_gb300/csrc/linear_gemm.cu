@@ -443,8 +443,6 @@ static bool lin_map(CUtensorMap *m, const void *base, int64_t cols, int64_t rows
                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promote, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int kLinMaxDevices = 64;
-
 // Sets the kernel's shared-memory limit once per device and returns how many clusters fit at once.
 template <int CG, int MODE, int TN>
 static int lin_clusters(int dev, int sms, int *out) {
@@ -478,51 +476,56 @@ static int lin_clusters(int dev, int sms, int *out) {
     return TGC_OK;
 }
 
+bool lin_maps(LinearMaps *maps, const LinearProduct &q, int mode, int b_rows) {
+    std::memset(maps, 0, sizeof *maps);
+    const auto sw = CU_TENSOR_MAP_SWIZZLE_128B, sw_out = CU_TENSOR_MAP_SWIZZLE_64B;
+    const auto l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B, none = CU_TENSOR_MAP_L2_PROMOTION_NONE;
+    const int64_t E = q.ngroups;
+    bool ok;
+    if (mode == kWgrad) {
+        ok = lin_map(&maps->a, q.a, q.I, q.M, 1, q.lda, 0, 64, kBK, sw, l2) &&
+             lin_map(&maps->b, q.b, q.J, q.M, 1, q.ldb, 0, 64, kBK, sw, l2);
+    } else {
+        ok = lin_map(&maps->a, q.a, q.R, q.M, 1, q.lda, 0, kBK, 128, sw, l2) &&
+             lin_map(&maps->a_small, q.a, q.R, q.M, 1, q.lda, 0, kBK, kRowBox, sw, l2) &&
+             (mode == kFwd ? lin_map(&maps->b, q.b, q.R, q.J, E, q.ldb, q.b_stride, kBK, (uint32_t)b_rows, sw, l2)
+                           : lin_map(&maps->b, q.b, q.J, q.R, E, q.ldb, q.b_stride, 64, kBK, sw, l2));
+    }
+    const int64_t out_rows = mode == kWgrad ? q.I : q.M, out_count = mode == kWgrad ? E : 1;
+    ok = ok && lin_map(&maps->y, q.y, q.J, out_rows, out_count, q.ldy, q.I * q.ldy, 32, 32, sw_out, none);
+    if (q.z != nullptr) ok = ok && lin_map(&maps->z, q.z, q.J, q.M, 1, q.ldz, 0, 32, 32, sw_out, none);
+    return ok;
+}
+
+int lin_params(LinearParams *p, const LinearProduct &q, int tile_n) {
+    p->M = (int)q.M; p->I = (int)q.I; p->J = (int)q.J; p->R = (int)q.R;
+    p->num_n = (int)((q.J + tile_n - 1) / tile_n);
+    p->ngroups = q.ngroups;
+    p->group_m = TGC_DEFAULT_GROUP_M;
+    p->offsets = q.offsets;
+    p->bias = q.bias; p->residual = q.residual; p->y = q.y; p->z = q.z;
+    p->ldres = q.ldres; p->ldy = q.ldy; p->ldz = q.ldz;
+    p->act = q.act;
+    p->f16 = q.f16;
+    p->timeout_ns = 4ull * 1000 * 1000 * 1000;
+    void *fault = nullptr;
+    const cudaError_t e = cudaGetSymbolAddress(&fault, g_linear_fault);
+    if (e != cudaSuccess) return cuda_fail(e);
+    p->fault = static_cast<int *>(fault);
+    return TGC_OK;
+}
+
 template <int CG, int MODE, int TN>
 static int lin_launch(const LinearProduct &q, int dev, int sms, cudaStream_t stream) {
     using C = LCfg<CG, MODE, TN>;
     LinearMaps maps;
-    std::memset(&maps, 0, sizeof maps);
-    const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
-    const auto l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
-    const int64_t E = q.ngroups;
-    bool ok;
-    if (MODE == kFwd)
-        ok = lin_map(&maps.a, q.a, q.R, q.M, 1, q.lda, 0, kBK, 128, sw, l2) &&
-             lin_map(&maps.a_small, q.a, q.R, q.M, 1, q.lda, 0, kBK, kRowBox, sw, l2) &&
-             lin_map(&maps.b, q.b, q.R, q.J, E, q.ldb, q.b_stride, kBK, C::kBRows, sw, l2);
-    else if (MODE == kDgrad)
-        ok = lin_map(&maps.a, q.a, q.R, q.M, 1, q.lda, 0, kBK, 128, sw, l2) &&
-             lin_map(&maps.a_small, q.a, q.R, q.M, 1, q.lda, 0, kBK, kRowBox, sw, l2) &&
-             lin_map(&maps.b, q.b, q.J, q.R, E, q.ldb, q.b_stride, 64, kBK, sw, l2);
-    else
-        ok = lin_map(&maps.a, q.a, q.I, q.M, 1, q.lda, 0, 64, kBK, sw, l2) &&
-             lin_map(&maps.b, q.b, q.J, q.M, 1, q.ldb, 0, 64, kBK, sw, l2);
-    const auto sw_out = CU_TENSOR_MAP_SWIZZLE_64B;
-    const auto none = CU_TENSOR_MAP_L2_PROMOTION_NONE;
-    const int64_t out_rows = MODE == kWgrad ? q.I : q.M, out_count = MODE == kWgrad ? E : 1;
-    ok = ok && lin_map(&maps.y, q.y, q.J, out_rows, out_count, q.ldy, q.I * q.ldy, 32, 32, sw_out, none);
-    if (q.z != nullptr) ok = ok && lin_map(&maps.z, q.z, q.J, q.M, 1, q.ldz, 0, 32, 32, sw_out, none);
-    if (!ok) return TGC_ERR_CUDA;
-
+    if (!lin_maps(&maps, q, MODE, C::kBRows)) return TGC_ERR_CUDA;
     int clusters = 0;
-    const int rc = lin_clusters<CG, MODE, TN>(dev, sms, &clusters);
+    int rc = lin_clusters<CG, MODE, TN>(dev, sms, &clusters);
     if (rc != TGC_OK) return rc;
     LinearParams p{};
-    p.M = (int)q.M; p.I = (int)q.I; p.J = (int)q.J; p.R = (int)q.R;
-    p.num_n = (int)((q.J + TN - 1) / TN);
-    p.ngroups = q.ngroups;
-    p.group_m = TGC_DEFAULT_GROUP_M;
-    p.offsets = q.offsets;
-    p.bias = q.bias; p.residual = q.residual; p.y = q.y; p.z = q.z;
-    p.ldres = q.ldres; p.ldy = q.ldy; p.ldz = q.ldz;
-    p.act = q.act;
-    p.f16 = q.f16;
-    p.timeout_ns = 4ull * 1000 * 1000 * 1000;
-    void *fault = nullptr;
-    cudaError_t e = cudaGetSymbolAddress(&fault, g_linear_fault);
-    if (e != cudaSuccess) return cuda_fail(e);
-    p.fault = static_cast<int *>(fault);
+    rc = lin_params(&p, q, TN);
+    if (rc != TGC_OK) return rc;
     int64_t tiles;
     if (MODE == kWgrad) {
         p.num_m = (int)((q.I + C::kTM - 1) / C::kTM);
@@ -545,7 +548,7 @@ static int lin_launch(const LinearProduct &q, int dev, int sms, cudaStream_t str
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, linear_gemm_kernel<CG, MODE, TN>, maps, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_gemm_kernel<CG, MODE, TN>, maps, p);
     return e == cudaSuccess ? TGC_OK : cuda_fail(e);
 }
 
@@ -556,6 +559,19 @@ static int lin_dispatch(const LinearProduct &q, cudaStream_t stream) {
     if (e != cudaSuccess) return cuda_fail(e);
     const int sms = sm_count(dev);
     const int64_t rows = MODE == kWgrad ? q.I : q.M;
+    // Few tiles: split each one's reduction.  Two CTAs fit an SM.
+    if (MODE != kWgrad || q.offsets == nullptr) {
+        const int64_t steps = ((MODE == kWgrad ? q.M : q.R) + kBK - 1) / kBK, room = 2 * (int64_t)sms;
+        const int64_t tm = split_tiles(q, MODE);
+        const int64_t wide = tm * ((q.J + 127) / 128), narrow = tm * ((q.J + 63) / 64);
+        if (wide <= room) {
+            const int tn = narrow <= room && rows <= 128 ? 64 : 128;
+            const int64_t tiles = tn == 64 ? narrow : wide;
+            int parts = 1;
+            while (parts < kMaxSplit && tiles * parts * 2 <= room && steps >= parts * 4) parts *= 2;
+            return launch_linear_split(q, MODE, tn, parts, stream);
+        }
+    }
     const bool pair = rows > 128 && q.offsets == nullptr;
     if (pair) return lin_launch<2, MODE, 256>(q, dev, sms, stream);
     return q.J > 128 ? lin_launch<1, MODE, 256>(q, dev, sms, stream) : lin_launch<1, MODE, 128>(q, dev, sms, stream);

@@ -66,6 +66,21 @@ struct LinearMaps {
     CUtensorMap a, a_small, b, y, z;
 };
 
+// Fills the maps for B boxes of b_rows rows (K-major) or 64 columns (MN-major); what q.z == null
+// leaves out is not set.  lin_params sets everything but num_m.
+constexpr int kLinMaxDevices = 64;
+bool lin_maps(LinearMaps *maps, const LinearProduct &q, int mode, int b_rows);
+int lin_params(LinearParams *p, const LinearProduct &q, int tile_n);
+constexpr int kMaxSplit = 8;  // parts: a portable cluster
+// (linear_split.cu) The product with the reduction of each 128 x tn tile split over `parts` CTAs.
+int launch_linear_split(const LinearProduct &q, int mode, int tn, int parts, cudaStream_t stream);
+// Tile rows of 128 that the split kernel launches: with groups, no more than one partial one each.
+inline int64_t split_tiles(const LinearProduct &q, int mode) {
+    const int64_t rows = mode == kWgrad ? q.I : q.M;
+    if (mode == kWgrad || q.offsets == nullptr) return (rows + 127) / 128;
+    return rows / 128 + (q.ngroups < rows ? q.ngroups : rows);
+}
+
 struct Tile {
     int e;             // group
     int m0;            // first output row (in y / dx: a row of the whole tensor; in dw: inside the group's matrix)

@@ -1,0 +1,297 @@
+// linear_split.cu -- the linear operator's products when there are few tiles: the reduction of a
+// 128 x 64 or 128 x 128 tile is split over the CTAs of a cluster, which add their partial sums
+// through distributed shared memory.
+//
+// With few rows the product streams the weight once and is bound by HBM (one row: 1 flop a byte);
+// what matters is that every SM loads, with enough bytes in flight.  So: small tiles, two CTAs on
+// an SM (about 110 KiB each, all of it stages), the reduction cut into as many parts as fill the
+// SMs, and A's stage no larger than the rows there are (the MMA reads 128 rows of shared memory
+// whatever they hold; what it computes from rows that do not exist is never stored).  No partial
+// sum goes to memory and nothing is added atomically: every output is summed over the parts in
+// order by one thread, so the result is the same in every run.
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+
+#include "linear_gemm.cuh"
+
+namespace tgc {
+
+constexpr int kSplitThreads = 256;
+constexpr int kSplitSmem = 112 * 1024;             // two CTAs an SM
+constexpr int kSplitRing = kSplitSmem - 1024 - 512;  // less alignment slack and barriers
+constexpr int kSplitMaxStages = 12;
+
+struct SplitShape {
+    int a_bytes, stages;  // A's stage and their number
+    int parts;            // CTAs of a cluster
+};
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+template <int MODE, int TN>
+__global__ void __launch_bounds__(kSplitThreads, 2)
+    linear_split_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p, const SplitShape q) {
+    constexpr bool kAMn = MODE == kWgrad, kBMn = MODE != kFwd;
+    constexpr int kBBytes = TN * kBK * 2;
+    constexpr uint32_t kBoxMn = 64 * kBK * 2;
+    constexpr int kPitch = TN + 4;  // floats from one row of the partial tile to the next: no bank conflicts
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    uint8_t *sA = ring, *sB = ring + q.stages * q.a_bytes;
+    float *part = reinterpret_cast<float *>(ring);  // after the last product the ring holds the partial tile
+    uint64_t *full = reinterpret_cast<uint64_t *>(ring + kSplitRing);
+    uint64_t *empty = full + kSplitMaxStages;
+    uint64_t *done = empty + kSplitMaxStages;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(done + 1);
+    __shared__ Tile s_tile;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int part_id = (int)(blockIdx.x % (unsigned)q.parts), t = (int)(blockIdx.x / (unsigned)q.parts);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < q.stages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(done, 1);
+        fence_mbarrier_init();
+        fence_proxy_async_shared();
+        prefetch_tensormap(MODE == kWgrad ? &maps.a : &maps.a_small);
+        prefetch_tensormap(&maps.b);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_holder, TN);
+        tmem_relinquish();
+    }
+    if (warp == 2) {  // which tile
+        Tile tl;
+        int pm, pn = t % p.num_n;
+        if (MODE == kWgrad || p.offsets == nullptr) {  // (kWgrad with groups does not come here)
+            pm = t / p.num_n;
+            tl.e = 0;
+            tl.m0 = pm * 128;
+            tl.rows = (MODE == kWgrad ? p.I : p.M) - tl.m0;
+        } else {
+            tl.e = find_group_tile(p.offsets, p.ngroups, p.M, 128, t / p.num_n, lane, &pm);
+            const RowRange g = tl.e >= 0 ? group_range(p.offsets, tl.e, p.M) : RowRange{0, 0};
+            tl.m0 = g.begin + pm * 128;
+            tl.rows = tl.e >= 0 ? g.end - tl.m0 : 0;
+        }
+        tl.n0 = pn * TN;
+        tl.red0 = 0;
+        tl.red = MODE == kWgrad ? p.M : p.R;
+        tl.num_kb = (tl.red + kBK - 1) / kBK;
+        if (lane == 0) s_tile = tl;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    const Tile tl = s_tile;
+    const int rows = tl.rows < 128 ? tl.rows : 128;
+    // this CTA's share of the steps; every part has one (parts <= num_kb)
+    const int kb0 = (int)((int64_t)tl.num_kb * part_id / q.parts), kb1 = (int)((int64_t)tl.num_kb * (part_id + 1) / q.parts);
+    bool ok = true;
+    if (rows > 0) {  // the same for the whole cluster
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            const uint32_t a = smem_addr(bar);
+            if (mbar_try_wait(a, parity)) return true;
+            const uint64_t t0 = globaltimer_ns();
+            for (uint64_t it = 1; it < (1ull << 40); ++it) {
+                if (mbar_try_wait(a, parity)) return true;
+                if ((it & 63) == 0 && globaltimer_ns() - t0 > p.timeout_ns) break;
+            }
+            raise_status(p.fault, kStatusTimeout);
+            return false;
+        };
+        if (warp == 0 && lane == 0) {
+            const int boxes = kAMn ? 2 : (rows + kRowBox - 1) / kRowBox;
+            const uint32_t tx = (uint32_t)(boxes * (kAMn ? kBoxMn : kRowBox * kBK * 2) + kBBytes);
+            int s = 0;
+            uint32_t ph = 1;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!wait(&empty[s], ph)) break;
+                mbar_arrive_expect_tx(&full[s], tx);
+                uint8_t *a = sA + s * q.a_bytes, *b = sB + s * kBBytes;
+                const int r0 = kb * kBK;
+                if (kBMn) {
+#pragma unroll
+                    for (int c = 0; c < TN / 64; ++c)
+                        tma_load_3d(b + c * kBoxMn, &maps.b, &full[s], tl.n0 + c * 64, r0, MODE == kWgrad ? 0 : tl.e);
+                } else {
+                    tma_load_3d(b, &maps.b, &full[s], r0, tl.n0, tl.e);
+                }
+                if (kAMn) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        tma_load_3d(a + c * kBoxMn, &maps.a, &full[s], tl.m0 + c * 64, r0, 0);
+                } else {
+                    for (int c = 0; c < boxes; ++c)
+                        tma_load_3d(a + c * (kRowBox * kBK * 2), &maps.a_small, &full[s], r0, tl.m0 + c * kRowBox, 0);
+                }
+                if (++s == q.stages) { s = 0; ph ^= 1u; }
+            }
+        } else if (warp == 1 && lane == 0) {
+            const uint32_t idesc = make_idesc_16_f32(p.f16 != 0, kAMn, kBMn, 128, TN);
+            const uint32_t a0 = smem_addr(sA), b0 = smem_addr(sB);
+            int s = 0;
+            uint32_t ph = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!wait(&full[s], ph)) break;
+                tc_fence_after();
+                const uint64_t ad = kAMn ? make_sw128_mnmajor_desc(a0 + s * q.a_bytes, kBoxMn)
+                                         : make_sw128_kmajor_desc(a0 + s * q.a_bytes);
+                const uint64_t bd = kBMn ? make_sw128_mnmajor_desc(b0 + s * kBBytes, kBoxMn)
+                                         : make_sw128_kmajor_desc(b0 + s * kBBytes);
+#pragma unroll
+                for (int k = 0; k < kBK / 16; ++k)
+                    mma_bf16_ss(tmem, ad + (uint64_t)(k * (kAMn ? 2048 >> 4 : 32 >> 4)),
+                                bd + (uint64_t)(k * (kBMn ? 2048 >> 4 : 32 >> 4)), idesc, kb > kb0 || k > 0 ? 1u : 0u);
+                mma_commit(&empty[s]);
+                if (++s == q.stages) { s = 0; ph ^= 1u; }
+            }
+            mma_commit(done);
+        }
+        __syncwarp();
+        // Every load this CTA issued has landed once the MMAs that read it have completed, so the
+        // ring is free.  TMEM lane = row of the tile.
+        if (lane == 0) ok = wait(done, 0);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        tc_fence_after();
+        const int qrow = (warp & 3) * 32, row = qrow + lane, col0 = (warp >> 2) * (TN / 2);
+        if (ok && qrow < rows) {  // warps 0..3 the first half of the columns, 4..7 the second
+#pragma unroll 1
+            for (int j = 0; j < TN / 64; ++j) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(tmem + ((uint32_t)qrow << 16) + (uint32_t)(col0 + j * 32), v);
+                tmem_wait_ld();
+                if (row < rows) {
+                    float4 *to = reinterpret_cast<float4 *>(part + row * kPitch + col0 + j * 32);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        to[c] = make_float4(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1]),
+                                            __uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3]));
+                }
+            }
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TN);
+    }
+    if (q.parts > 1) cluster_sync();
+    if (rows > 0) {
+        // 8 columns a thread: the parts' sums in order, then the epilogue
+        const bool f16 = p.f16 != 0;
+        const int vecs = TN / 8, total = rows * vecs;
+        const uint32_t part0 = smem_addr(part);
+        for (int i = part_id * kSplitThreads + (int)threadIdx.x; i < total; i += q.parts * kSplitThreads) {
+            const int r = i / vecs, c = (i % vecs) * 8, n = tl.n0 + c;
+            if (n >= p.J) continue;
+            float v[8] = {};
+            const uint32_t at = part0 + (uint32_t)(r * kPitch + c) * 4u;
+            for (int k = 0; k < q.parts; ++k) {
+                const uint32_t from = q.parts > 1 ? mapa_shared(at, (uint32_t)k) : at;
+                const float4 a = ld_cluster_f4(from), b = ld_cluster_f4(from + 16u);
+                v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+                v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+            }
+            const int64_t m = tl.m0 + r;
+            auto add = [&](const uint4 w) {
+                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float lo, hi;
+                    unpack16(ws[k], f16, &lo, &hi);
+                    v[2 * k] += lo;
+                    v[2 * k + 1] += hi;
+                }
+            };
+            auto pack = [&] {
+                return make_uint4(pack16(v[0], v[1], f16), pack16(v[2], v[3], f16), pack16(v[4], v[5], f16),
+                                  pack16(v[6], v[7], f16));
+            };
+            if (MODE == kFwd) {
+                if (p.bias != nullptr)
+                    add(*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias) + (int64_t)tl.e * p.J + n));
+                if (p.z != nullptr) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.z) + m * p.ldz + n) = pack();
+                if (p.act != TGC_ACT_NONE)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] = act_f32(v[k], p.act);
+                if (p.residual != nullptr)
+                    add(*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.residual) + m * p.ldres + n));
+            }
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.y) + m * p.ldy + n) = pack();
+        }
+    }
+    __syncwarp();
+    if (q.parts > 1) cluster_sync();  // no CTA leaves while another reads its partial tile
+}
+
+// ---------------------------------------------------------------- host side
+
+template <int MODE, int TN>
+static int split_launch(const LinearProduct &q, int parts, cudaStream_t stream) {
+    static std::mutex mu;
+    static bool done[kLinMaxDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (dev < 0 || dev >= kLinMaxDevices) return TGC_ERR_INVALID_ARG;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!done[dev]) {
+            e = cudaFuncSetAttribute(linear_split_kernel<MODE, TN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kSplitSmem);
+            if (e != cudaSuccess) return cuda_fail(e);
+            done[dev] = true;
+        }
+    }
+    LinearMaps maps;
+    if (!lin_maps(&maps, q, MODE, TN)) return TGC_ERR_CUDA;
+    LinearParams p{};
+    int rc = lin_params(&p, q, TN);
+    if (rc != TGC_OK) return rc;
+    const int64_t rows = MODE == kWgrad ? q.I : q.M;
+    SplitShape s{};
+    s.parts = parts;
+    // A's stage: the boxes of 32 rows that a tile can need (a group may fill one; kWgrad always does)
+    s.a_bytes = MODE == kWgrad || rows > 96 ? 16384 : (int)((rows + kRowBox - 1) / kRowBox) * kRowBox * kBK * 2;
+    s.stages = kSplitRing / (s.a_bytes + TN * kBK * 2);
+    if (s.stages > kSplitMaxStages) s.stages = kSplitMaxStages;
+    const int64_t tiles = split_tiles(q, MODE) * p.num_n;
+    if (tiles * parts >= (int64_t(1) << 31)) return TGC_ERR_INVALID_ARG;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)parts;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(tiles * parts));
+    cfg.blockDim = dim3(kSplitThreads);
+    cfg.dynamicSmemBytes = kSplitSmem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, linear_split_kernel<MODE, TN>, maps, p, s);
+    return e == cudaSuccess ? TGC_OK : cuda_fail(e);
+}
+
+int launch_linear_split(const LinearProduct &q, int mode, int tn, int parts, cudaStream_t stream) {
+    if (tn == 64)
+        return mode == kFwd ? split_launch<kFwd, 64>(q, parts, stream)
+             : mode == kDgrad ? split_launch<kDgrad, 64>(q, parts, stream) : split_launch<kWgrad, 64>(q, parts, stream);
+    return mode == kFwd ? split_launch<kFwd, 128>(q, parts, stream)
+         : mode == kDgrad ? split_launch<kDgrad, 128>(q, parts, stream) : split_launch<kWgrad, 128>(q, parts, stream);
+}
+
+}  // namespace tgc
