@@ -742,6 +742,14 @@ int tgc_block_norm_bwd(const tgc_block_norm_bwd_args *args);
  * tested for NULL); 0 for none or for arguments it would refuse. */
 size_t tgc_block_norm_bwd_workspace_bytes(const tgc_block_norm_bwd_args *args);
 
+/*
+ * Every wait inside the kernels of tgc_linear, tgc_block_norm and their gradients is
+ * bounded.  Should one expire (the GPU stopped delivering a copy), its kernel ends
+ * with wrong results and marks a word of the device.  tgc_async_status synchronises
+ * `stream`, clears that word and returns what it held: TGC_OK or TGC_ERR_TIMEOUT.
+ */
+int tgc_async_status(cudaStream_t stream);
+
 /* ------------------------------------------------------------------------ */
 /* Misc                                                                      */
 /* ------------------------------------------------------------------------ */

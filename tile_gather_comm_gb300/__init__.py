@@ -8,7 +8,8 @@ plumbing of ranks that are separate processes (``ranks``).
 """
 from ._lib import (  # noqa: F401
     TGCError, lib, tgc_ag_matmul, tgc_ag_matmul_ex, tgc_ag_matmul_noalloc, tgc_ag_matmul_plan,
-    tgc_ag_matmul_schedule,
-    tgc_ag_matmul_workspace_bytes, tgc_block_norm, tgc_block_norm_bwd, tgc_gemm_tile_shape, tgc_ipc_close, tgc_ipc_export, tgc_ipc_open,
-    tgc_last_cuda_error, tgc_linear, tgc_linear_bwd, tgc_status_string, tgc_tgather, tgc_tgather_ex, tgc_tgather_strided, tgc_version,
+    tgc_ag_matmul_schedule, tgc_ag_matmul_workspace_bytes, tgc_async_status, tgc_block_norm,
+    tgc_block_norm_bwd, tgc_gemm_tile_shape, tgc_ipc_close, tgc_ipc_export, tgc_ipc_open,
+    tgc_last_cuda_error, tgc_linear, tgc_linear_bwd, tgc_status_string, tgc_tgather, tgc_tgather_ex,
+    tgc_tgather_strided, tgc_version,
 )

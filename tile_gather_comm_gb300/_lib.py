@@ -191,6 +191,8 @@ def load_library(path: str) -> ctypes.CDLL:
                        ("tgc_block_norm_bwd_workspace_bytes", BlockNormBwdArgs)):
         getattr(L, name).argtypes = [ctypes.POINTER(args)]
         getattr(L, name).restype = ctypes.c_size_t
+    L.tgc_async_status.argtypes = [_vp]
+    L.tgc_async_status.restype = ctypes.c_int
     L.tgc_status_string.argtypes = [ctypes.c_int]
     L.tgc_status_string.restype = ctypes.c_char_p
     L.tgc_last_cuda_error.argtypes = []
@@ -406,19 +408,19 @@ def _rows(t, shape, dtype, name: str):
     only the address."""
     if t is None:
         return None, 0
-    if t.dtype != dtype or t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name}: expected {dtype} of shape {tuple(shape)}, got {t.dtype} of {tuple(t.shape)}")
-    st = t.stride()
-    if shape[1] > 1 and st[1] != 1:
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return t.data_ptr(), st[0] if shape[0] > 1 else 0
+    return t.data_ptr(), ld if shape[0] > 1 else 0
 
 
 def _dense(t, shape, dtype, name: str):
     """Address of a contiguous operand of exactly this shape; None for None."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous {dtype} of shape {shape}, got {t.dtype} of {tuple(t.shape)}"
                          f" with strides {t.stride()}")
     return t.data_ptr()
@@ -446,26 +448,28 @@ def _offsets(offsets):
     return offsets.data_ptr(), offsets.numel() - 1
 
 
-def _same_device(*ts):
-    """The operands live on the current device (addresses are all the library gets)."""
-    dev = None
+def _device(*ts) -> int:
+    """Index of the device every operand lives on, which must be the current one (addresses are
+    all the library gets)."""
+    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
     for t in ts:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("operands must be CUDA tensors")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"operands on {dev} and {t.device}")
-    if dev is not None and dev.index != torch.cuda.current_device():
-        raise ValueError(f"operands on {dev}, but the current device is {torch.cuda.current_device()}")
+        if t is not None and (dev < 0 or t.get_device() != dev):
+            raise ValueError(f"operands must be CUDA tensors on the current device, got one on {t.device}")
+    return dev
+
+
+def _stream_of(stream, dev: int) -> int:
+    """Address of `stream`, by default torch's current one (read without the Stream object, whose
+    making costs more than the launch)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _workspace(workspace, nbytes: int, like, stream):
     """The caller's workspace, or one from torch's allocator that belongs to the call's stream."""
     if workspace is not None:
-        _same_device(like, workspace)
+        _device(like, workspace)
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
         return workspace, workspace.numel() * workspace.element_size()
@@ -483,7 +487,7 @@ def tgc_linear(x, w, y, *, bias=None, act: str = "none", residual=None, z=None, 
     """y = act(x @ w^T + bias) + residual (bf16 or f16), z receiving the pre-activation; with
     ``offsets`` (int32, ngroups + 1) the product grouped by expert: w is (ngroups, N, K), bias
     (ngroups, N).  Asynchronous on ``stream``."""
-    _same_device(x, w, y, bias, residual, z, offsets)
+    dev = _device(x, w, y, bias, residual, z, offsets)
     if x.dim() != 2:
         raise ValueError("x: expected (M, K)")
     M, K = x.shape
@@ -495,7 +499,7 @@ def tgc_linear(x, w, y, *, bias=None, act: str = "none", residual=None, z=None, 
     pr, ldres = _rows(residual, mn, x.dtype, "residual")
     pz, ldz = _rows(z, mn, x.dtype, "z")
     a = LinearArgs(px, pw, _dense(bias, (ngroups, N) if ngroups else (N,), x.dtype, "bias"), pr, py, pz, M, K, N,
-                   ldx, ldw, ldres, ldy, ldz, w_stride, DTYPES[x.dtype], ACTS[act], off, ngroups, _stream(stream))
+                   ldx, ldw, ldres, ldy, ldz, w_stride, DTYPES[x.dtype], ACTS[act], off, ngroups, _stream_of(stream, dev))
     rc = lib().tgc_linear(ctypes.byref(a))
     return _check(rc, "tgc_linear") if check else rc
 
@@ -506,7 +510,7 @@ def tgc_linear_bwd(dy, x, w, *, z=None, act: str = "none", dx=None, dw=None, dbi
     dx = dz @ w, dw = dz^T @ x, dbias = dz summed over rows.  The residual's gradient is dy.
     ``workspace``: a contiguous CUDA tensor of tgc_linear_bwd_workspace_bytes' size, by default
     taken from torch's allocator.  Asynchronous on ``stream``."""
-    _same_device(dy, x, w, z, dx, dw, dbias, offsets)
+    dev = _device(dy, x, w, z, dx, dw, dbias, offsets)
     if x.dim() != 2:
         raise ValueError("x: expected (M, K)")
     M, K = x.shape
@@ -520,7 +524,7 @@ def tgc_linear_bwd(dy, x, w, *, z=None, act: str = "none", dx=None, dw=None, dbi
     pdx, lddx = _rows(dx, (M, K), x.dtype, "dx")
     a = LinearBwdArgs(pdy, px, pw, pz, pdx, _dense(dw, (*lead, N, K), x.dtype, "dw"),
                       _dense(dbias, (*lead, N), x.dtype, "dbias"), M, K, N, lddy, ldx, ldw, ldz, lddx, w_stride,
-                      DTYPES[x.dtype], ACTS[act], off, ngroups, None, 0, _stream(stream))
+                      DTYPES[x.dtype], ACTS[act], off, ngroups, None, 0, _stream_of(stream, dev))
     ws, a.workspace_bytes = _workspace(workspace, lib().tgc_linear_bwd_workspace_bytes(ctypes.byref(a)), x, stream)
     a.workspace = _ptr(ws)
     rc = lib().tgc_linear_bwd(ctypes.byref(a))
@@ -533,7 +537,7 @@ def tgc_block_norm(y, r=None, h=None, *, x=None, gate=None, post: str = "none", 
     """u = post(y); r = res_scale * x + branch_scale * gate * u; h = pre(r), one pass over (M, D)
     tensors.  gate is (gates, D), each vector shared by M / gates consecutive rows; norms are
     "none", "rms" or "layer".  Asynchronous on ``stream``."""
-    _same_device(y, x, r, h, gate, post_weight, post_bias, pre_weight, pre_bias)
+    dev = _device(y, x, r, h, gate, post_weight, post_bias, pre_weight, pre_bias)
     if y.dim() != 2:
         raise ValueError("y: expected (M, D)")
     M, D = y.shape
@@ -547,7 +551,7 @@ def tgc_block_norm(y, r=None, h=None, *, x=None, gate=None, post: str = "none", 
     a = BlockNormArgs(py, px, _dense(gate, (gates, D), dt, "gate"), _dense(post_weight, v, dt, "post_weight"),
                       _dense(post_bias, v, dt, "post_bias"), _dense(pre_weight, v, dt, "pre_weight"),
                       _dense(pre_bias, v, dt, "pre_bias"), pr, ph, M, D, gates, ldy, ldx, ldr, ldh, NORMS[post],
-                      NORMS[pre], res_scale, branch_scale, eps, DTYPES[dt], _stream(stream))
+                      NORMS[pre], res_scale, branch_scale, eps, DTYPES[dt], _stream_of(stream, dev))
     rc = lib().tgc_block_norm(ctypes.byref(a))
     return _check(rc, "tgc_block_norm") if check else rc
 
@@ -560,7 +564,7 @@ def tgc_block_norm_bwd(y, r, dr, dh, *, gate=None, post: str = "none", post_weig
     forward pass's; any of y, r, dr, dh may be None where the header says it is not needed.
     ``workspace``: as for tgc_linear_bwd.  Asynchronous on ``stream``."""
     outs = (dx, dy, dgate, dpost_weight, dpost_bias, dpre_weight, dpre_bias)
-    _same_device(y, r, dr, dh, gate, post_weight, post_bias, pre_weight, *outs)
+    dev = _device(y, r, dr, dh, gate, post_weight, post_bias, pre_weight, *outs)
     like = next((t for t in (dh, dr, y, r) if t is not None), None)
     if like is None or like.dim() != 2:
         raise ValueError("expected (M, D) operands")
@@ -579,9 +583,15 @@ def tgc_block_norm_bwd(y, r, dr, dh, *, gate=None, post: str = "none", post_weig
                          _dense(dgate, g, dt, "dgate"), _dense(dpost_weight, v, dt, "dpost_weight"),
                          _dense(dpost_bias, v, dt, "dpost_bias"), _dense(dpre_weight, v, dt, "dpre_weight"),
                          _dense(dpre_bias, v, dt, "dpre_bias"), M, D, gates, ldy, ldr, lddr, lddh, lddx, lddy,
-                         NORMS[post], NORMS[pre], res_scale, branch_scale, eps, DTYPES[dt], None, 0, _stream(stream))
+                         NORMS[post], NORMS[pre], res_scale, branch_scale, eps, DTYPES[dt], None, 0, _stream_of(stream, dev))
     ws, a.workspace_bytes = _workspace(workspace, lib().tgc_block_norm_bwd_workspace_bytes(ctypes.byref(a)), like,
                                        stream)
     a.workspace = _ptr(ws)
     rc = lib().tgc_block_norm_bwd(ctypes.byref(a))
     return _check(rc, "tgc_block_norm_bwd") if check else rc
+
+
+def tgc_async_status(stream=None) -> None:
+    """Synchronizes the stream; raises TGCError if a bounded wait inside one of the asynchronous
+    operators' kernels expired on this device since the last call."""
+    _check(lib().tgc_async_status(_stream(stream)), "tgc_async_status")

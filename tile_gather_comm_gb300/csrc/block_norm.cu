@@ -14,19 +14,69 @@
 // is a warp (rows of up to 32 vectors; no barrier at all) or a whole block.
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include <cuda_runtime.h>
 
 #include "act.cuh"
 #include "internal.h"
+#include "pairs.cuh"
+#include "prims.cuh"
 
 namespace tgc {
 
-constexpr int kMaxTeam = 1024;
+// Threads of a block at most, and a kernel's register budget: 64 a thread where a thread holds one
+// vector (two teams of 512 on an SM) or a team may have 1024, 128 elsewhere.
+template <typename T, int VEC, int NV>
+constexpr int kTeamMax = (VEC == 1 && NV == 16) || (sizeof(T) == 4 && NV == 4 && VEC > 1) ? 1024 : 512;
+template <typename T, int VEC, int NV>
+constexpr int kTeamBlocks = kTeamMax<T, VEC, NV> == 512 && NV == 1 ? 2 : 1;
 
+// VEC consecutive elements as the words they are loaded in.  Arithmetic goes by L: two elements at
+// a time, or one where VEC is 1; get(i) is the i-th such lane in fp32, set(i, f) rounds it back.
 template <typename T, int VEC>
 struct alignas(sizeof(T) * VEC) Pack {
-    T v[VEC];
+    using L = F2;
+    uint32_t w[sizeof(T) * VEC / 4];
+    __device__ __forceinline__ F2 get(int i) const {
+        if constexpr (sizeof(T) == 4) {
+            return f2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+            return f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+        } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+            return f2(f.x, f.y);
+        }
+    }
+    __device__ __forceinline__ void set(int i, F2 v) {
+        const float2 f = split(v);
+        if constexpr (sizeof(T) == 4) {
+            w[2 * i] = __float_as_uint(f.x);
+            w[2 * i + 1] = __float_as_uint(f.y);
+        } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f.y), "f"(f.x));
+        } else {
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f.y), "f"(f.x));
+        }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (uint32_t &x : w) x = 0u;
+    }
+    // Elements used before are converted again after this, not kept in fp32 meanwhile.
+    __device__ __forceinline__ void forget() {
+#pragma unroll
+        for (uint32_t &x : w) asm volatile("" : "+r"(x));
+    }
+};
+template <typename T>
+struct Pack<T, 1> {
+    using L = float;
+    T v;
+    __device__ __forceinline__ float get(int) const { return to_f32(v); }
+    __device__ __forceinline__ void set(int, float f) { v = from_f32<T>(f); }
+    __device__ __forceinline__ void clear() { v = from_f32<T>(0.0f); }
+    __device__ __forceinline__ void forget() {}
 };
 
 template <typename T, int VEC>
@@ -34,11 +84,31 @@ __device__ __forceinline__ Pack<T, VEC> load_pack(const void *base, int64_t at) 
     return *reinterpret_cast<const Pack<T, VEC> *>(static_cast<const T *>(base) + at);
 }
 template <typename T, int VEC>
-__device__ __forceinline__ void store_pack(void *base, int64_t at, const float *f) {
+__device__ __forceinline__ void store_pack(void *base, int64_t at, const typename Pack<T, VEC>::L *f) {
     Pack<T, VEC> p;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) p.v[i] = from_f32<T>(f[i]);
+    for (int i = 0; i < (VEC > 1 ? VEC / 2 : 1); ++i) p.set(i, f[i]);
     *reinterpret_cast<Pack<T, VEC> *>(static_cast<T *>(base) + at) = p;
+}
+// fp32 in memory <-> lanes
+__device__ __forceinline__ void read_lanes(const float *from, float (&to)[1]) { to[0] = from[0]; }
+__device__ __forceinline__ void write_lanes(float *to, const float (&from)[1]) { to[0] = from[0]; }
+template <int NP>
+__device__ __forceinline__ void read_lanes(const float *from, F2 (&to)[NP]) {
+#pragma unroll
+    for (int i = 0; i < NP; i += 2) {
+        const float4 f = *reinterpret_cast<const float4 *>(from + 2 * i);
+        to[i] = f2(f.x, f.y);
+        to[i + 1] = f2(f.z, f.w);
+    }
+}
+template <int NP>
+__device__ __forceinline__ void write_lanes(float *to, const F2 (&from)[NP]) {
+#pragma unroll
+    for (int i = 0; i < NP; i += 2) {
+        const float2 a = split(from[i]), b = split(from[i + 1]);
+        *reinterpret_cast<float4 *>(to + 2 * i) = make_float4(a.x, a.y, b.x, b.y);
+    }
 }
 
 // Sums of N values over the team, the same in every thread and every run: shuffles inside a
@@ -66,111 +136,204 @@ __device__ __forceinline__ void team_sum(float (&v)[N], float (*smem)[N][32], in
     *buf ^= 1;
 }
 
+// The same for N = 8 or 16 values at once, with a fraction of the shuffles: in the first steps a
+// lane hands half of its values to its partner and keeps the other half, so after log2(N) steps
+// each lane holds one value's sum over a few lanes.  smem[value][warp]; unused warps' entries are
+// zero from the start (clear_sums).
+template <int N>
+__device__ __forceinline__ void team_sum_many(float (&v)[N], float (*smem)[N][32], int *buf) {
+    static_assert(N == 8 || N == 16, "values");
+    const int lane = threadIdx.x % 32;
+    int d = 16;
+#pragma unroll
+    for (int n = N; n > 1; n /= 2, d /= 2) {
+        const bool up = (lane & d) != 0;  // keeps the upper half of the n values
+#pragma unroll
+        for (int i = 0; i < n / 2; ++i) {
+            const float give = up ? v[i] : v[i + n / 2], keep = up ? v[i + n / 2] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, d);
+        }
+    }
+    float s = v[0];
+#pragma unroll
+    for (int e = 32 / N / 2; e > 0; e /= 2) s += __shfl_xor_sync(0xffffffffu, s, e);
+    // lanes l * (32 / N) .. hold value l: bit 16 of the lane chose its highest index bit, and so on
+    if (blockDim.y == 1 && blockDim.x > 32) {
+        constexpr int kPer = 32 / N;  // lanes of a value, each adding 32 / kPer warps
+        if (lane % kPer == 0) smem[*buf][lane / kPer][threadIdx.x / 32] = s;
+        __syncthreads();
+        const float4 *from = reinterpret_cast<const float4 *>(smem[*buf][lane / kPer] + (lane % kPer) * N);
+        s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const float4 f = from[i];
+            s += (f.x + f.y) + (f.z + f.w);
+        }
+#pragma unroll
+        for (int e = kPer / 2; e > 0; e /= 2) s += __shfl_xor_sync(0xffffffffu, s, e);
+        *buf ^= 1;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, s, i * (32 / N));
+}
+
+// Rows arrive through shared memory where a thread's vectors are aligned and a few rows of every
+// input fit beside each other: one thread asks for whole rows with bulk copies, two rows ahead.
+template <int VEC, int NV>
+constexpr bool kStaged = VEC > 1 && NV <= 2;
+template <int NV, bool FULL>
+constexpr int kBwdRows = NV == 1 && !FULL ? 2 : 1;  // rows the backward kernel works on at a time
+
+// Waits for the phase with this parity; gives up after about two seconds and marks the fault.
+__device__ __forceinline__ void row_wait(uint64_t *bar, uint32_t parity, int *fault) {
+    const uint32_t a = smem_addr(bar);
+    if (mbar_try_wait(a, parity)) return;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint64_t it = 1; it < (1ull << 40); ++it) {
+        if (mbar_try_wait(a, parity)) return;
+        if ((it & 63) == 0 && globaltimer_ns() - t0 > 2000000000ull) break;
+    }
+    raise_status(fault, kStatusTimeout);
+}
+
 // ---------------------------------------------------------------- forward
 
 struct NormParams {
     const void *y, *x, *gate, *post_w, *post_b, *pre_w, *pre_b;
     void *r, *h;
-    int M, D, rows_per_gate;
+    int M, D, rows_per_gate, workers;
     int64_t ldy, ldx, ldr, ldh;
     int post, pre;
     float res_scale, branch_scale, eps, inv_d;
 };
 
-template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(kMaxTeam) norm_kernel(const NormParams p) {
+// A worker (a team) takes a run of consecutive rows.  The weights stay in its registers, and a
+// row's y and x are asked for while the row before is still being reduced, so loads are in flight
+// all the time.  BIAS: some norm has a bias.
+template <typename T, int VEC, int NV, bool BIAS>
+__global__ void __launch_bounds__(kTeamMax<T, VEC, NV>, kTeamBlocks<T, VEC, NV>) norm_kernel(const NormParams p) {
+    using P = Pack<T, VEC>;
+    using L = typename P::L;
+    constexpr int NP = VEC > 1 ? VEC / 2 : 1;
     __shared__ float smem[2][1][32];
     int buf = 0;
-    const int m = blockIdx.x * blockDim.y + threadIdx.y;
-    if (m >= p.M) return;  // whole teams only: a block of one team, or warps that need no barrier
-    const int64_t row = m;
-    float v[NV][VEC];
-    // v := deviations of v from `mean`, and the reciprocal deviation
-    auto stats = [&](int kind) -> float {
-        if (kind == TGC_NORM_LAYER) {
-            float s[1] = {0.0f};
+    const int worker = blockIdx.x * blockDim.y + threadIdx.y;
+    if (worker >= p.workers) return;  // whole teams only: a block of one team, or warps that need no barrier
+    const int m0 = (int)((int64_t)p.M * worker / p.workers), m1 = (int)((int64_t)p.M * (worker + 1) / p.workers);
+    const int c0 = threadIdx.x * VEC, step = blockDim.x * VEC;
+    P w1[NV], w2[NV], g[NV], b1[BIAS ? NV : 1], b2[BIAS ? NV : 1], py[NV], px[NV];
+    auto fetch = [&](P (&to)[NV], const void *base, int64_t at) {
+        if (base == nullptr) return;
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) s[0] += v[k][i];
-            team_sum(s, smem, &buf);
-            const float mean = s[0] * p.inv_d;
-#pragma unroll
-            for (int k = 0; k < NV; ++k)
-                if ((k * (int)blockDim.x + (int)threadIdx.x) * VEC < p.D)
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) v[k][i] -= mean;
+        for (int k = 0; k < NV; ++k)
+            if (c0 + k * step < p.D) to[k] = load_pack<T, VEC>(base, at + c0 + k * step);
+    };
+    fetch(w1, p.post_w, 0);
+    fetch(w2, p.pre_w, 0);
+    if constexpr (BIAS) {
+        fetch(b1, p.post_b, 0);
+        fetch(b2, p.pre_b, 0);
+    }
+    fetch(py, p.y, m0 * p.ldy);
+    fetch(px, p.x, m0 * p.ldx);
+    int seg = -1;
+    for (int m = m0; m < m1; ++m) {
+        if (p.gate != nullptr && m / p.rows_per_gate != seg) {
+            seg = m / p.rows_per_gate;
+            fetch(g, p.gate, (int64_t)seg * p.D);
         }
-        float q[1] = {0.0f};
+        L v[NV][NP];  // columns past the row's end stay zeros
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) q[0] += v[k][i] * v[k][i];
-        team_sum(q, smem, &buf);
-        return rsqrtf(q[0] * p.inv_d + p.eps);
-    };
-    auto affine = [&](int kind, const void *w, const void *b) {
-        const float rstd = stats(kind);
+            for (int i = 0; i < NP; ++i) v[k][i] = c0 + k * step < p.D ? py[k].get(i) : every<L>(0.0f);
+        if (m + 1 < m1) fetch(py, p.y, (m + 1) * p.ldy);
+        // v := its deviations from the mean (layer); the reciprocal deviation
+        auto stats = [&](int kind) -> float {
+            if (kind == TGC_NORM_LAYER) {
+                L t = every<L>(0.0f);
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) t = add(t, v[k][i]);
+                float s[1] = {total(t)};
+                team_sum(s, smem, &buf);
+                const L mean = every<L>(-s[0] * p.inv_d);
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+                    if (c0 + k * step < p.D)
+#pragma unroll
+                        for (int i = 0; i < NP; ++i) v[k][i] = add(v[k][i], mean);
+            }
+            L t = every<L>(0.0f);
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int i = 0; i < NP; ++i) t = fma(v[k][i], v[k][i], t);
+            float q[1] = {total(t)};
+            team_sum(q, smem, &buf);
+            return rsqrtf(q[0] * p.inv_d + p.eps);
+        };
+        auto affine = [&](float scale, const void *w, const P (&pw)[NV], const void *b, const auto &pb) {
+            const L sc = every<L>(scale);
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+#pragma unroll
+                for (int i = 0; i < NP; ++i) v[k][i] = mul(v[k][i], sc);
+                if (w != nullptr)
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) v[k][i] = mul(v[k][i], pw[k].get(i));
+                if constexpr (BIAS) {
+                    if (b != nullptr)
+#pragma unroll
+                        for (int i = 0; i < NP; ++i) v[k][i] = add(v[k][i], pb[k].get(i));
+                }
+            }
+        };
+        if (p.post != TGC_NORM_NONE) affine(stats(p.post), p.post_w, w1, p.post_b, b1);
+        const L cs = every<L>(p.branch_scale), rs = every<L>(p.res_scale);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = (k * blockDim.x + threadIdx.x) * VEC;
-            if (c >= p.D) continue;
-            Pack<T, VEC> pw, pb;
-            if (w != nullptr) pw = load_pack<T, VEC>(w, c);
-            if (b != nullptr) pb = load_pack<T, VEC>(b, c);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                v[k][i] *= rstd;
-                if (w != nullptr) v[k][i] *= to_f32(pw.v[i]);
-                if (b != nullptr) v[k][i] += to_f32(pb.v[i]);
-            }
+            for (int i = 0; i < NP; ++i) v[k][i] = mul(v[k][i], cs);
+            if (p.gate != nullptr)
+#pragma unroll
+                for (int i = 0; i < NP; ++i) v[k][i] = mul(v[k][i], g[k].get(i));
+            if (p.x != nullptr)
+#pragma unroll
+                for (int i = 0; i < NP; ++i) v[k][i] = fma(px[k].get(i), rs, v[k][i]);
+            if (c0 + k * step >= p.D)
+#pragma unroll
+                for (int i = 0; i < NP; ++i) v[k][i] = every<L>(0.0f);
+            else if (p.r != nullptr) store_pack<T, VEC>(p.r, m * p.ldr + c0 + k * step, v[k]);
         }
-    };
-    Pack<T, VEC> px[NV];
+        if (m + 1 < m1) fetch(px, p.x, (m + 1) * p.ldx);
+        if (p.pre == TGC_NORM_NONE) continue;
+        affine(stats(p.pre), p.pre_w, w2, p.pre_b, b2);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int c = (k * blockDim.x + threadIdx.x) * VEC;
-        if (c < p.D) {
-            const Pack<T, VEC> py = load_pack<T, VEC>(p.y, row * p.ldy + c);
-            if (p.x != nullptr) px[k] = load_pack<T, VEC>(p.x, row * p.ldx + c);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) v[k][i] = to_f32(py.v[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) v[k][i] = 0.0f;
-        }
-    }
-    if (p.post != TGC_NORM_NONE) affine(p.post, p.post_w, p.post_b);
-    const int64_t gate_row = p.gate != nullptr ? (int64_t)(m / p.rows_per_gate) * p.D : 0;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int c = (k * blockDim.x + threadIdx.x) * VEC;
-        if (c >= p.D) continue;
-        Pack<T, VEC> pg;
-        if (p.gate != nullptr) pg = load_pack<T, VEC>(p.gate, gate_row + c);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            v[k][i] *= p.branch_scale;
-            if (p.gate != nullptr) v[k][i] *= to_f32(pg.v[i]);
-            if (p.x != nullptr) v[k][i] += p.res_scale * to_f32(px[k].v[i]);
-        }
-        if (p.r != nullptr) store_pack<T, VEC>(p.r, row * p.ldr + c, v[k]);
-    }
-    if (p.pre == TGC_NORM_NONE) return;
-    affine(p.pre, p.pre_w, p.pre_b);
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int c = (k * blockDim.x + threadIdx.x) * VEC;
-        if (c < p.D) store_pack<T, VEC>(p.h, row * p.ldh + c, v[k]);
+        for (int k = 0; k < NV; ++k)
+            if (c0 + k * step < p.D) store_pack<T, VEC>(p.h, m * p.ldh + c0 + k * step, v[k]);
     }
 }
 
 // ---------------------------------------------------------------- backward
 
 // Rows are dealt in units: a unit is up to unit_rows consecutive rows that share a gate
-// vector.  A worker (a team) takes units worker, worker + workers, ...; it keeps the sums for
-// weights and biases over all its units, and those for the gate over one unit, in registers.
-// The sums leave as fp32 partials that norm_sum_kernel adds in a fixed order.
+// vector.  A worker (a team) takes units worker, worker + workers, ... and keeps the sums over a unit's
+// rows in registers.  They leave as fp32
+// partials that norm_sum_kernel adds in a fixed order.
+//
+// One reduction a row (two with a layer norm, which takes the means first).  Written out, with
+// r and y already without their means, q = dh w_pre, b = c g w_post and t = dr + R (q - s1 - r R s0),
+// R and Y the reciprocal deviations, every mean the gradients need is one of
+//   r r, y y, q r,  b y dr, b y q, b y r   and for layer norms  q, b y, b dr, b q, b r, b
+// summed over the row, so all are taken in one pass and the rest is arithmetic on them:
+//   s0 = R mean(q r), s1 = mean(q) (layer)
+//   e0 = mean(b t yhat) = Y (mean(b y dr) + R (mean(b y q) - s1 mean(b y) - s0 R mean(b y r)))
+//   e1 = mean(b t)      = mean(b dr) + R (mean(b q) - s1 mean(b) - s0 R mean(b r))   (layer)
+//   dy = Y (b t - e1 - y Y e0)
+// The sums over rows need only S = sum c t yhat and T = sum c t of a unit: dgate = w_post S + b_post T,
+// and the unit adds g S and g T to dpost_weight and dpost_bias.
 struct NormBwdParams {
     const void *y, *r, *dr, *dh, *gate, *post_w, *post_b, *pre_w;
     void *dx, *dy, *dgate;
@@ -182,193 +345,319 @@ struct NormBwdParams {
     bool want[4];
     bool need_y;
     float res_scale, branch_scale, eps, inv_d;
+    int *fault;
 };
 
-// FULL: sums for biases too.
+// FULL: layer norms or sums for biases.  A thread that holds one vector of a row (NV = 1) keeps
+// the columns' factors in registers and, unless FULL, works on two rows at a time: one reduction
+// serves both and their arithmetic overlaps.  Wider rows read the factors from shared memory.
 template <typename T, int VEC, int NV, bool FULL>
-__global__ void __launch_bounds__(kMaxTeam) norm_bwd_kernel(const NormBwdParams p) {
-    __shared__ float smem[2][2][32];
-    int buf = 0;
+__global__ void __launch_bounds__(kTeamMax<T, VEC, NV>) norm_bwd_kernel(const NormBwdParams p) {
+    using P = Pack<T, VEC>;
+    using L = typename P::L;
+    constexpr int NP = VEC > 1 ? VEC / 2 : 1;
+    constexpr bool REGS = NV == 1;
+    constexpr int ROWS = kBwdRows<NV, FULL>;
+    constexpr int NQ = FULL ? 12 : 6;        // sums a row
+    constexpr int NS = FULL || ROWS == 2 ? 16 : 8;
+    constexpr bool STAGED = kStaged<VEC, NV>;
+    __shared__ alignas(16) float smem[2][NS][32];
+    __shared__ float means[2][2][32];
+    __shared__ uint64_t bars[4][2];
+    // A team's own: the columns' factors in fp32 (w_pre, and b of the unit being worked on), unless
+    // in registers; then, where rows are staged, two stages of ROWS rows of r, dh, y and dr.
+    extern __shared__ __align__(16) float dynamic[];
+    int buf = 0, mbuf = 0;
     const int worker = blockIdx.x * blockDim.y + threadIdx.y;
+    if (blockDim.y == 1) {
+        for (int i = threadIdx.x; i < 2 * NS * 32; i += blockDim.x) (&smem[0][0][0])[i] = 0.0f;
+        __syncthreads();
+    }
     if (worker >= p.workers) return;
-    float a_gate[NV][VEC], a_post[NV][VEC], a_pre[NV][VEC], a_postb[FULL ? NV : 1][VEC], a_preb[FULL ? NV : 1][VEC];
+    const int c0 = threadIdx.x * VEC, step = blockDim.x * VEC;
+    const int row_bytes = step * NV * (int)sizeof(T);  // of a stage: the row's, rounded up to the team's columns
+    float *const fw = dynamic + threadIdx.y * ((REGS ? 0 : 2 * step * NV) + (STAGED ? 2 * ROWS * row_bytes : 0));
+    float *const fb = fw + (REGS ? 0 : step * NV);
+    uint8_t *const stages = reinterpret_cast<uint8_t *>(fb + (REGS ? 0 : step * NV));
+    uint64_t *const bar = bars[threadIdx.y];
+    L a_s[NV][NP], a_pre[NV][NP], a_t[FULL ? NV : 1][NP], a_preb[FULL ? NV : 1][NP];
+    L rw[NP], rb[NP];  // the factors, where they are in registers
     auto clear = [](auto &a) {
 #pragma unroll
         for (auto &k : a)
 #pragma unroll
-            for (float &f : k) f = 0.0f;
+            for (L &f : k) f = every<L>(0.0f);
     };
-    clear(a_post); clear(a_pre); clear(a_postb); clear(a_preb);
-    // Deviations of v (in place) and the reciprocal deviation.
-    auto stats = [&](float (&v)[NV][VEC], int kind) -> float {
-        if (kind == TGC_NORM_LAYER) {
-            float s[2] = {0.0f, 0.0f};
+    clear(a_pre);
+    clear(a_preb);
+    const bool pre = p.pre != TGC_NORM_NONE, post = p.post != TGC_NORM_NONE;
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
+    for (int i = 0; i < NP; ++i) rw[i] = rb[i] = every<L>(0.0f);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) s[0] += v[k][i];
-            team_sum(s, smem, &buf);
-            const float mean = s[0] * p.inv_d;
+    for (int k = 0; k < NV; ++k) {
+        const int c = c0 + k * step;
+        if (c >= p.D) continue;
+        P pw;
+        L w[NP];
+        if (p.pre_w != nullptr) pw = load_pack<T, VEC>(p.pre_w, c);
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
-                if ((k * (int)blockDim.x + (int)threadIdx.x) * VEC < p.D)
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) v[k][i] -= mean;
+        for (int i = 0; i < NP; ++i) {
+            w[i] = p.pre_w != nullptr ? pw.get(i) : every<L>(1.0f);
+            if constexpr (REGS) rw[i] = w[i];
         }
-        float q[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) q[0] += v[k][i] * v[k][i];
-        team_sum(q, smem, &buf);
-        return rsqrtf(q[0] * p.inv_d + p.eps);
-    };
-    for (int unit = worker; unit < p.units; unit += p.workers) {
+        if constexpr (!REGS) write_lanes(fw + c, w);
+    }
+    auto unit_rows = [&](int unit, int *m0, int *m1) {
         const int seg = unit / p.units_per_gate, part = unit % p.units_per_gate;
-        const int m0 = seg * p.rows_per_gate + part * p.unit_rows;
+        *m0 = seg * p.rows_per_gate + part * p.unit_rows;
         const int seg_end = (seg + 1) * p.rows_per_gate;
-        const int m1 = m0 + p.unit_rows < seg_end ? m0 + p.unit_rows : seg_end;
-        clear(a_gate);
-        for (int m = m0; m < m1; ++m) {
-            const int64_t row = m;
-            float t[NV][VEC];  // dr, then t
+        *m1 = *m0 + p.unit_rows < seg_end ? *m0 + p.unit_rows : seg_end;
+    };
+    const void *const in[4] = {pre ? p.r : nullptr, pre ? p.dh : nullptr, p.need_y ? p.y : nullptr, p.dr};
+    const int64_t ld[4] = {p.ldr, p.lddh, p.ldy, p.lddr};
+    // The rows to ask for, in the order they are worked on (the asking thread's own walk): up to
+    // ROWS of one unit at a time.
+    int ask_unit = worker, ask_m = 0, ask_end = 0;
+    auto ask = [&](int stage) {
+        if (ask_unit >= p.units) return;
+        const int rows = ask_end - ask_m < ROWS ? ask_end - ask_m : ROWS;
+        const uint32_t bytes = (uint32_t)(p.D * (int)sizeof(T));
+        uint32_t total = 0;
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int c = (k * blockDim.x + threadIdx.x) * VEC;
+        for (int j = 0; j < 4; ++j) total += in[j] != nullptr ? bytes * rows : 0u;
+        mbar_arrive_expect_tx(&bar[stage], total);
+        for (int r = 0; r < rows; ++r) {
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) t[k][i] = 0.0f;
-                if (p.dr != nullptr && c < p.D) {
-                    const Pack<T, VEC> pk = load_pack<T, VEC>(p.dr, row * p.lddr + c);
+            for (int j = 0; j < 4; ++j)
+                if (in[j] != nullptr)
+                    bulk_g2s(stages + ((stage * ROWS + r) * 4 + j) * row_bytes,
+                             static_cast<const T *>(in[j]) + (ask_m + r) * ld[j], bytes, &bar[stage]);
+        }
+        ask_m += rows;
+        if (ask_m == ask_end) {
+            ask_unit += p.workers;
+            if (ask_unit < p.units) unit_rows(ask_unit, &ask_m, &ask_end);
+        }
+    };
+    if constexpr (STAGED) {
+        // an input that is not there reads as zeros
+        for (int i = threadIdx.x * 16; i < 8 * ROWS * row_bytes; i += blockDim.x * 16)
+            *reinterpret_cast<uint4 *>(stages + i) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_shared();
+        if (threadIdx.x == 0) {
+            mbar_init(&bar[0], 1);
+            mbar_init(&bar[1], 1);
+            fence_mbarrier_init();
+        }
+        if (blockDim.y == 1) __syncthreads(); else __syncwarp();
+        if (threadIdx.x == 0) {
+            unit_rows(ask_unit, &ask_m, &ask_end);
+            ask(0);
+            ask(1);
+        }
+    }
+    uint32_t turn = 0;  // the stage in use and its phase
+    for (int unit = worker; unit < p.units; unit += p.workers) {
+        const int seg = unit / p.units_per_gate;
+        int m0, m1;
+        unit_rows(unit, &m0, &m1);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) t[k][i] = to_f32(pk.v[i]);
-                }
+        for (int k = 0; k < NV; ++k) {
+            const int c = c0 + k * step;
+            if (c >= p.D) continue;
+            P pw, pg;
+            if (p.post_w != nullptr) pw = load_pack<T, VEC>(p.post_w, c);
+            if (p.gate != nullptr) pg = load_pack<T, VEC>(p.gate, (int64_t)seg * p.D + c);
+            L f[NP];
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                f[i] = every<L>(p.branch_scale);
+                if (p.post_w != nullptr) f[i] = mul(f[i], pw.get(i));
+                if (p.gate != nullptr) f[i] = mul(f[i], pg.get(i));
+                if constexpr (REGS) rb[i] = f[i];
             }
-            if (p.pre != TGC_NORM_NONE) {
-                float v[NV][VEC], q[NV][VEC];
+            if constexpr (!REGS) write_lanes(fb + c, f);
+        }
+        clear(a_s);
+        clear(a_t);
+        auto factors = [&](int k, L (&w)[NP], L (&b)[NP]) {
+            if constexpr (REGS) {
+#pragma unroll
+                for (int i = 0; i < NP; ++i) { w[i] = rw[i]; b[i] = rb[i]; }
+            } else {
+                read_lanes(fw + c0 + k * step, w);
+                read_lanes(fb + c0 + k * step, b);
+            }
+        };
+        for (int m = m0; m < m1; m += ROWS) {
+            const uint32_t stage = turn & 1u;
+            P pr[ROWS][NV], pd[ROWS][NV], py[ROWS][NV], pt[ROWS][NV];
+            if constexpr (STAGED) row_wait(&bar[stage], (turn >> 1) & 1u, p.fault);
+            auto fetch = [&](P (&to)[NV], int rr, int j) {
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
-                    const int c = (k * blockDim.x + threadIdx.x) * VEC;
-                    if (c < p.D) {
-                        const Pack<T, VEC> pr = load_pack<T, VEC>(p.r, row * p.ldr + c);
-                        const Pack<T, VEC> pd = load_pack<T, VEC>(p.dh, row * p.lddh + c);
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i) { v[k][i] = to_f32(pr.v[i]); q[k][i] = to_f32(pd.v[i]); }
+                    const int c = c0 + k * step;
+                    if constexpr (STAGED) {
+                        to[k] = *reinterpret_cast<const P *>(stages + ((stage * ROWS + rr) * 4 + j) * row_bytes +
+                                                             c * (int)sizeof(T));
                     } else {
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i) v[k][i] = q[k][i] = 0.0f;
+                        if (in[j] != nullptr && c < p.D && m + rr < m1) to[k] = load_pack<T, VEC>(in[j], (m + rr) * ld[j] + c);
+                        else to[k].clear();
                     }
                 }
-                const float rstd = stats(v, p.pre);
-                float s[2] = {0.0f, 0.0f};
+            };
 #pragma unroll
-                for (int k = 0; k < NV; ++k) {
-                    const int c = (k * blockDim.x + threadIdx.x) * VEC;
-                    if (c >= p.D) continue;
-                    Pack<T, VEC> pw;
-                    if (p.pre_w != nullptr) pw = load_pack<T, VEC>(p.pre_w, c);
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        v[k][i] *= rstd;
-                        a_pre[k][i] += q[k][i] * v[k][i];
-                        if (FULL) a_preb[k][i] += q[k][i];
-                        if (p.pre_w != nullptr) q[k][i] *= to_f32(pw.v[i]);
-                        s[0] += q[k][i] * v[k][i];
-                        s[1] += q[k][i];
-                    }
-                }
-                team_sum(s, smem, &buf);
-                const float s0 = s[0] * p.inv_d, s1 = p.pre == TGC_NORM_LAYER ? s[1] * p.inv_d : 0.0f;
-#pragma unroll
-                for (int k = 0; k < NV; ++k)
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) t[k][i] += rstd * (q[k][i] - s1 - v[k][i] * s0);
+            for (int rr = 0; rr < ROWS; ++rr) {
+                fetch(pr[rr], rr, 0);
+                fetch(pd[rr], rr, 1);
+                fetch(py[rr], rr, 2);
+                fetch(pt[rr], rr, 3);
             }
-            if (p.need_y) {
-                float v[NV][VEC], q[NV][VEC];
+            L mean_r = every<L>(0.0f), mean_y = every<L>(0.0f);  // negated
+            if constexpr (FULL) {
+                if (p.pre == TGC_NORM_LAYER || p.post == TGC_NORM_LAYER) {
+                    L t0 = every<L>(0.0f), t1 = every<L>(0.0f);
 #pragma unroll
-                for (int k = 0; k < NV; ++k) {
-                    const int c = (k * blockDim.x + threadIdx.x) * VEC;
+                    for (int k = 0; k < NV; ++k)
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) v[k][i] = 0.0f;
-                    if (c < p.D) {
-                        const Pack<T, VEC> py = load_pack<T, VEC>(p.y, row * p.ldy + c);
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i) v[k][i] = to_f32(py.v[i]);
-                    }
-                }
-                const float rstd = p.post != TGC_NORM_NONE ? stats(v, p.post) : 1.0f;
-                float s[2] = {0.0f, 0.0f};
-#pragma unroll
-                for (int k = 0; k < NV; ++k) {
-                    const int c = (k * blockDim.x + threadIdx.x) * VEC;
-                    if (c >= p.D) continue;
-                    Pack<T, VEC> pw, pb, pg;
-                    if (p.post_w != nullptr) pw = load_pack<T, VEC>(p.post_w, c);
-                    if (p.post_b != nullptr) pb = load_pack<T, VEC>(p.post_b, c);
-                    if (p.gate != nullptr) pg = load_pack<T, VEC>(p.gate, (int64_t)seg * p.D + c);
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        v[k][i] *= rstd;
-                        float u = v[k][i], du = p.branch_scale * t[k][i];
-                        if (p.post_w != nullptr) u *= to_f32(pw.v[i]);
-                        if (p.post_b != nullptr) u += to_f32(pb.v[i]);
-                        a_gate[k][i] += du * u;
-                        if (p.gate != nullptr) du *= to_f32(pg.v[i]);
-                        a_post[k][i] += du * v[k][i];
-                        if (FULL) a_postb[k][i] += du;
-                        q[k][i] = p.post_w != nullptr ? du * to_f32(pw.v[i]) : du;
-                        s[0] += q[k][i] * v[k][i];
-                        s[1] += q[k][i];
-                    }
-                }
-                if (p.post != TGC_NORM_NONE && p.dy != nullptr) team_sum(s, smem, &buf);
-                const float s0 = p.post != TGC_NORM_NONE ? s[0] * p.inv_d : 0.0f;
-                const float s1 = p.post == TGC_NORM_LAYER ? s[1] * p.inv_d : 0.0f;
-#pragma unroll
-                for (int k = 0; k < NV; ++k) {
-                    const int c = (k * blockDim.x + threadIdx.x) * VEC;
-                    if (c >= p.D || p.dy == nullptr) continue;
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) q[k][i] = rstd * (q[k][i] - s1 - v[k][i] * s0);
-                    store_pack<T, VEC>(p.dy, row * p.lddy + c, q[k]);
-                }
-            } else if (p.dy != nullptr) {  // no post norm: dy = du
-#pragma unroll
-                for (int k = 0; k < NV; ++k) {
-                    const int c = (k * blockDim.x + threadIdx.x) * VEC;
-                    if (c >= p.D) continue;
-                    Pack<T, VEC> pg;
-                    if (p.gate != nullptr) pg = load_pack<T, VEC>(p.gate, (int64_t)seg * p.D + c);
-                    float q[VEC];
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        q[i] = p.branch_scale * t[k][i];
-                        if (p.gate != nullptr) q[i] *= to_f32(pg.v[i]);
-                    }
-                    store_pack<T, VEC>(p.dy, row * p.lddy + c, q);
+                        for (int i = 0; i < NP; ++i) {
+                            t0 = add(t0, pr[0][k].get(i));
+                            t1 = add(t1, py[0][k].get(i));
+                        }
+                    float s[2] = {total(t0), total(t1)};
+                    team_sum(s, means, &mbuf);
+                    if (p.pre == TGC_NORM_LAYER) mean_r = every<L>(-s[0] * p.inv_d);
+                    if (p.post == TGC_NORM_LAYER) mean_y = every<L>(-s[1] * p.inv_d);
                 }
             }
-            if (p.dx != nullptr) {
+            float s[NS] = {};
+#pragma unroll
+            for (int rr = 0; rr < ROWS; ++rr) {
+                L sl[NQ];
+#pragma unroll
+                for (L &x : sl) x = every<L>(0.0f);
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
-                    const int c = (k * blockDim.x + threadIdx.x) * VEC;
-                    if (c >= p.D) continue;
-                    float q[VEC];
+                    if (c0 + k * step >= p.D) continue;
+                    L w[NP], b[NP];
+                    factors(k, w, b);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) q[i] = p.res_scale * t[k][i];
-                    store_pack<T, VEC>(p.dx, row * p.lddx + c, q);
+                    for (int i = 0; i < NP; ++i) {
+                        L r = pr[rr][k].get(i), y = py[rr][k].get(i);
+                        if (FULL) { r = add(r, mean_r); y = add(y, mean_y); }
+                        const L q = mul(pd[rr][k].get(i), w[i]), d = pt[rr][k].get(i), by = mul(b[i], y);
+                        sl[0] = fma(r, r, sl[0]);
+                        sl[1] = fma(y, y, sl[1]);
+                        sl[2] = fma(q, r, sl[2]);
+                        sl[3] = fma(by, d, sl[3]);
+                        sl[4] = fma(by, q, sl[4]);
+                        sl[5] = fma(by, r, sl[5]);
+                        if constexpr (FULL) {
+                            sl[6] = add(sl[6], q);
+                            sl[7] = add(sl[7], by);
+                            sl[8] = fma(b[i], d, sl[8]);
+                            sl[9] = fma(b[i], q, sl[9]);
+                            sl[10] = fma(b[i], r, sl[10]);
+                            sl[11] = add(sl[11], b[i]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < NQ; ++i) s[rr * (NS / ROWS) + i] = total(sl[i]);
+            }
+            team_sum_many(s, smem, &buf);
+            if constexpr (STAGED) {
+                // Past the sum every thread has its part of these rows in registers: the stage is free.
+                __syncwarp();
+                if (threadIdx.x == 0) ask((int)stage);
+                ++turn;
+            }
+#pragma unroll
+            for (int rr = 0; rr < ROWS; ++rr) {
+                if (ROWS > 1 && m + rr >= m1) break;
+                const float *const t0 = s + rr * (NS / ROWS);
+                const float R = pre ? rsqrtf(t0[0] * p.inv_d + p.eps) : 0.0f;
+                const float Y = post ? rsqrtf(t0[1] * p.inv_d + p.eps) : 1.0f;
+                const float s0 = R * t0[2] * p.inv_d;  // mean(q rhat)
+                float s1 = 0.0f, e0 = 0.0f, e1 = 0.0f;
+                if constexpr (FULL) {
+                    if (p.pre == TGC_NORM_LAYER) s1 = t0[6] * p.inv_d;
+                    if (post) e0 = Y * p.inv_d * (t0[3] + R * (t0[4] - s1 * t0[7] - s0 * R * t0[5]));
+                    if (p.post == TGC_NORM_LAYER) e1 = p.inv_d * (t0[8] + R * (t0[9] - s1 * t0[11] - s0 * R * t0[10]));
+                } else {
+                    if (post) e0 = Y * p.inv_d * (t0[3] + R * (t0[4] - s0 * R * t0[5]));
+                }
+                // t = dr + R q - (R s1) - (R s0) rhat;  dy = Y b t - (Y e1) - (Y e0) yhat
+                const L lR = every<L>(R), lY = every<L>(Y), k_r = every<L>(-R * s0), k_y = every<L>(-Y * e0);
+                const L l1 = every<L>(-R * s1), le = every<L>(-Y * e1), rs = every<L>(p.res_scale);
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
+                    pr[rr][k].forget(); pd[rr][k].forget(); py[rr][k].forget(); pt[rr][k].forget();
+                    const int c = c0 + k * step;
+                    if (c >= p.D) continue;
+                    L w[NP], b[NP], ox[NP], oy[NP];
+                    factors(k, w, b);
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) {
+                        L r = pr[rr][k].get(i), y = py[rr][k].get(i);
+                        if (FULL) { r = add(r, mean_r); y = add(y, mean_y); }
+                        const L rh = mul(lR, r), yh = mul(lY, y), dh = pd[rr][k].get(i);
+                        L t = fma(lR, mul(dh, w[i]), fma(k_r, rh, pt[rr][k].get(i)));
+                        if (FULL) t = add(t, l1);
+                        ox[i] = mul(rs, t);
+                        a_s[k][i] = fma(t, yh, a_s[k][i]);
+                        a_pre[k][i] = fma(dh, rh, a_pre[k][i]);
+                        oy[i] = fma(mul(lY, b[i]), t, mul(k_y, yh));
+                        if constexpr (FULL) {
+                            oy[i] = add(oy[i], le);
+                            a_t[k][i] = add(a_t[k][i], t);
+                            a_preb[k][i] = add(a_preb[k][i], dh);
+                        }
+                    }
+                    if (p.dx != nullptr) store_pack<T, VEC>(p.dx, (m + rr) * p.lddx + c, ox);
+                    if (p.dy != nullptr) store_pack<T, VEC>(p.dy, (m + rr) * p.lddy + c, oy);
                 }
             }
         }
-        if (p.dgate != nullptr) {
+        // The unit's share of the gate's and the post norm's gradients; the latter gather in the
+        // worker's own rows of the partials.
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int c = (k * blockDim.x + threadIdx.x) * VEC;
-                if (c >= p.D) continue;
-                if (p.gate_partial == nullptr) store_pack<T, VEC>(p.dgate, (int64_t)seg * p.D + c, a_gate[k]);
-                else
+        for (int k = 0; k < NV; ++k) {
+            const int c = c0 + k * step;
+            if (c >= p.D) continue;
+            P pw, pb, pg;
+            if (p.post_w != nullptr) pw = load_pack<T, VEC>(p.post_w, c);
+            if (p.post_b != nullptr) pb = load_pack<T, VEC>(p.post_b, c);
+            if (p.gate != nullptr) pg = load_pack<T, VEC>(p.gate, (int64_t)seg * p.D + c);
+            L dg[NP], gs[NP], gt[NP];
+            const L cs = every<L>(p.branch_scale);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) p.gate_partial[(int64_t)unit * p.D + c + i] = a_gate[k][i];
+            for (int i = 0; i < NP; ++i) {
+                const L S = mul(cs, a_s[k][i]);
+                dg[i] = p.post_w != nullptr ? mul(S, pw.get(i)) : S;
+                gs[i] = p.gate != nullptr ? mul(S, pg.get(i)) : S;
+                if constexpr (FULL) {
+                    const L t = mul(cs, a_t[k][i]);
+                    if (p.post_b != nullptr) dg[i] = fma(t, pb.get(i), dg[i]);
+                    gt[i] = p.gate != nullptr ? mul(t, pg.get(i)) : t;
+                }
+            }
+            auto gather = [&](int which, L (&x)[NP]) {
+                if (!p.want[which]) return;
+                float *to = p.partial + ((int64_t)which * p.workers + worker) * p.D + c;
+                if (unit != worker) {
+                    L old[NP];
+                    read_lanes(to, old);
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) x[i] = add(x[i], old[i]);
+                }
+                write_lanes(to, x);
+            };
+            gather(0, gs);
+            if constexpr (FULL) gather(1, gt);
+            if (p.dgate != nullptr) {
+                if (p.gate_partial == nullptr) store_pack<T, VEC>(p.dgate, (int64_t)seg * p.D + c, dg);
+                else write_lanes(p.gate_partial + (int64_t)unit * p.D + c, dg);
             }
         }
     }
@@ -376,19 +665,11 @@ __global__ void __launch_bounds__(kMaxTeam) norm_bwd_kernel(const NormBwdParams 
         if (!p.want[which]) return;
         float *to = p.partial + ((int64_t)which * p.workers + worker) * p.D;
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = (k * blockDim.x + threadIdx.x) * VEC;
-            if (c >= p.D) continue;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) to[c + i] = a[k][i];
-        }
+        for (int k = 0; k < NV; ++k)
+            if (c0 + k * step < p.D) write_lanes(to + c0 + k * step, a[k]);
     };
-    put(0, a_post);
     put(2, a_pre);
-    if constexpr (FULL) {
-        put(1, a_postb);
-        put(3, a_preb);
-    }
+    if constexpr (FULL) put(3, a_preb);
 }
 
 // Adds the partials of one output vector: blockIdx.y 0..3 the parameter vectors, then one a gate.
@@ -399,9 +680,10 @@ struct NormSumParams {
     int D, workers, units_per_gate;
 };
 
+// 32 columns a block: 8 threads of 4 columns x 32 lanes over the partials, then the lanes in order.
 template <typename T>
 __global__ void __launch_bounds__(256) norm_sum_kernel(const NormSumParams p) {
-    __shared__ float part[8][32];
+    __shared__ alignas(16) float part[32][32];
     const int which = blockIdx.y;
     const float *from;
     T *to;
@@ -417,16 +699,34 @@ __global__ void __launch_bounds__(256) norm_sum_kernel(const NormSumParams p) {
         to = static_cast<T *>(p.dgate) + g * p.D;
         n = p.units_per_gate;
     }
-    const int c = blockIdx.x * 32 + threadIdx.x % 32, l = threadIdx.x / 32;
-    float s = 0.0f;
-    if (c < p.D)
-        for (int i = l; i < n; i += 8) s += from[(int64_t)i * p.D + c];
-    part[l][threadIdx.x % 32] = s;
+    const int q = threadIdx.x % 8, l = threadIdx.x / 8, c = blockIdx.x * 32 + q * 4;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (p.D % 4 == 0) {
+        if (c < p.D) {
+#pragma unroll 8
+            for (int i = l; i < n; i += 32) {
+                const float4 f = *reinterpret_cast<const float4 *>(from + (int64_t)i * p.D + c);
+                s.x += f.x; s.y += f.y; s.z += f.z; s.w += f.w;
+            }
+        }
+    } else {
+#pragma unroll 4
+        for (int i = l; i < n; i += 32) {
+            const float *f = from + (int64_t)i * p.D + c;
+            if (c < p.D) s.x += f[0];
+            if (c + 1 < p.D) s.y += f[1];
+            if (c + 2 < p.D) s.z += f[2];
+            if (c + 3 < p.D) s.w += f[3];
+        }
+    }
+    *reinterpret_cast<float4 *>(&part[l][q * 4]) = s;
     __syncthreads();
-    if (l == 0 && c < p.D) {
+    const int col = blockIdx.x * 32 + threadIdx.x;
+    if (threadIdx.x < 32 && col < p.D) {
+        float t = 0.0f;
 #pragma unroll
-        for (int i = 1; i < 8; ++i) s += part[i][threadIdx.x];
-        to[c] = from_f32<T>(s);
+        for (int i = 0; i < 32; ++i) t += part[i][threadIdx.x];
+        to[col] = from_f32<T>(t);
     }
 }
 
@@ -450,38 +750,48 @@ static int norm_matrix(const void *p, int64_t rows, int64_t D, int es, int64_t *
 
 static bool norm_kind(tgc_norm k) { return k == TGC_NORM_NONE || k == TGC_NORM_RMS || k == TGC_NORM_LAYER; }
 
-// Threads a team and vectors a thread for rows of D: NV 1, 2 or 4 vectors, or 1, 4 or 16 single
-// elements, a thread (16384 columns for a team of 1024 at the widest).
+// Threads a team and vectors a thread for rows of D: 1, 2 or 4 vectors, or 1, 4 or 16 single
+// elements, a thread, the fewest that a team of 512 (1024 at the widest) covers the row with.
 struct TeamShape {
     int vec, nv, team, teams;  // teams a block
+    int per_sm;                // teams an SM holds, from the kernels' register budget
 };
-static TeamShape team_shape(int64_t D, int es, bool vec, int prefer) {
+static TeamShape team_shape(int64_t D, int es, bool vec) {
     TeamShape s{};
     s.vec = vec && D * es % 16 == 0 ? 16 / es : 1;
     const int64_t n = (D + s.vec - 1) / s.vec;
     const int steps[2][3] = {{1, 4, 16}, {1, 2, 4}};
     for (int i = 0; i < 3; ++i) {
         s.nv = steps[s.vec > 1][i];
-        if (n <= (int64_t)s.nv * prefer) break;
+        if (n <= (int64_t)s.nv * 512) break;
     }
     s.team = (int)((n + s.nv - 1) / s.nv + 31) / 32 * 32;
     s.teams = s.team == 32 ? 4 : 1;
+    const bool regs64 = s.nv == 1 || (s.vec == 1 && s.nv == 16) || (es == 4 && s.nv == 4 && s.vec > 1);
+    s.per_sm = (regs64 ? 1024 : 512) / s.team;
+    if (s.per_sm < 1) s.per_sm = 1;
     return s;
+}
+
+template <typename T, int V, int NV>
+static void launch_norm_nv(const NormParams &p, bool bias, dim3 grid, dim3 block, cudaStream_t stream) {
+    if (bias) norm_kernel<T, V, NV, true><<<grid, block, 0, stream>>>(p);
+    else norm_kernel<T, V, NV, false><<<grid, block, 0, stream>>>(p);
 }
 
 template <typename T>
 static void launch_norm(const NormParams &p, const TeamShape &s, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T);
-    const dim3 block(s.team, s.teams);
-    const unsigned grid = (unsigned)((p.M + s.teams - 1) / s.teams);
+    const dim3 block(s.team, s.teams), grid((unsigned)((p.workers + s.teams - 1) / s.teams));
+    const bool bias = p.post_b != nullptr || p.pre_b != nullptr;
     if (s.vec > 1) {
-        if (s.nv == 1) norm_kernel<T, V, 1><<<grid, block, 0, stream>>>(p);
-        else if (s.nv == 2) norm_kernel<T, V, 2><<<grid, block, 0, stream>>>(p);
-        else norm_kernel<T, V, 4><<<grid, block, 0, stream>>>(p);
+        if (s.nv == 1) launch_norm_nv<T, V, 1>(p, bias, grid, block, stream);
+        else if (s.nv == 2) launch_norm_nv<T, V, 2>(p, bias, grid, block, stream);
+        else launch_norm_nv<T, V, 4>(p, bias, grid, block, stream);
     } else {
-        if (s.nv == 1) norm_kernel<T, 1, 1><<<grid, block, 0, stream>>>(p);
-        else if (s.nv == 4) norm_kernel<T, 1, 4><<<grid, block, 0, stream>>>(p);
-        else norm_kernel<T, 1, 16><<<grid, block, 0, stream>>>(p);
+        if (s.nv == 1) launch_norm_nv<T, 1, 1>(p, bias, grid, block, stream);
+        else if (s.nv == 4) launch_norm_nv<T, 1, 4>(p, bias, grid, block, stream);
+        else launch_norm_nv<T, 1, 16>(p, bias, grid, block, stream);
     }
 }
 
@@ -513,7 +823,7 @@ static int norm_impl(tgc_block_norm_args a) {
         int64_t ld = a.D;
         TGC_TRY(norm_matrix(v, v == a.gate ? a.gates : 1, a.D, es, &ld, &vec));
     }
-    const TeamShape s = team_shape(a.D, es, vec, 512);
+    const TeamShape s = team_shape(a.D, es, vec);
     NormParams p{};
     p.y = a.y; p.x = a.x; p.gate = a.gate;
     p.post_w = a.post_weight; p.post_b = a.post_bias; p.pre_w = a.pre_weight; p.pre_b = a.pre_bias;
@@ -522,15 +832,21 @@ static int norm_impl(tgc_block_norm_args a) {
     p.ldy = a.ldy; p.ldx = a.ldx; p.ldr = a.ldr; p.ldh = a.ldh;
     p.post = a.post; p.pre = a.pre;
     p.res_scale = a.res_scale; p.branch_scale = a.branch_scale; p.eps = a.eps; p.inv_d = 1.0f / (float)a.D;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    const int64_t room = (int64_t)sm_count(dev) * s.per_sm;
+    p.workers = (int)(a.M < room ? a.M : room);
     if (a.dtype == TGC_BF16) launch_norm<__nv_bfloat16>(p, s, a.stream);
     else if (a.dtype == TGC_F16) launch_norm<__half>(p, s, a.stream);
     else launch_norm<float>(p, s, a.stream);
-    const cudaError_t e = cudaGetLastError();
+    e = cudaGetLastError();
     return e == cudaSuccess ? TGC_OK : cuda_fail(e);
 }
 
-// How the backward pass deals its rows.  About two workers an SM (more for narrow rows, whose
-// teams are small), units of at least 4 rows, and whole gate segments where there are enough.
+// How the backward pass deals its rows: a worker for every team that the card's 152 SMs hold at
+// once (one of 512 threads with 128 registers each, more for narrow rows), units of at least 4 rows, and whole gate segments where there are enough.  It
+// goes by D and the type alone, so the workspace's size does not depend on the pointers.
 struct NormPlan {
     int segments, rows_per_gate, units_per_gate, unit_rows, units, workers;
     size_t gate_off, total;
@@ -538,7 +854,8 @@ struct NormPlan {
 
 static NormPlan norm_plan(const tgc_block_norm_bwd_args &a) {
     NormPlan q{};
-    const int64_t target = a.D <= 512 ? 1216 : 304;
+    const int64_t row = a.D * norm_elem(a.dtype);
+    const int64_t target = 152 * (row >= 8192 ? 1 : row <= 1024 ? 8 : 8192 / row);
     q.segments = a.gate != nullptr ? (int)a.gates : 1;
     q.rows_per_gate = (int)(a.M / q.segments);
     int64_t upg = (target + q.segments - 1) / q.segments;
@@ -593,26 +910,38 @@ static int norm_bwd_check(tgc_block_norm_bwd_args &a, bool *vec) {
 }
 
 template <typename T, int V, int NV>
-static void launch_norm_bwd_nv(const NormBwdParams &p, bool full, dim3 grid, dim3 block, cudaStream_t stream) {
-    if (full) norm_bwd_kernel<T, V, NV, true><<<grid, block, 0, stream>>>(p);
-    else norm_bwd_kernel<T, V, NV, false><<<grid, block, 0, stream>>>(p);
+static int launch_norm_bwd_nv(const NormBwdParams &p, bool full, dim3 grid, dim3 block, cudaStream_t stream) {
+    // Two fp32 factors a column (128 KiB at the widest row) unless they are in registers, and two
+    // stages of four inputs.
+    const int columns = (int)(block.y * block.x) * V * NV, rows = full ? kBwdRows<NV, true> : kBwdRows<NV, false>;
+    const int smem = columns * ((NV == 1 ? 0 : 8) + (kStaged<V, NV> ? 8 * rows * (int)sizeof(T) : 0));
+    auto kernel = full ? norm_bwd_kernel<T, V, NV, true> : norm_bwd_kernel<T, V, NV, false>;
+    if (smem > 40 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    kernel<<<grid, block, smem, stream>>>(p);
+    return TGC_OK;
 }
 
 template <typename T>
-static void launch_norm_bwd(const NormBwdParams &p, const NormSumParams &q, int nsums, const TeamShape &s, bool full,
+static int launch_norm_bwd(const NormBwdParams &p, const NormSumParams &q, int nsums, const TeamShape &s, bool full,
                             cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T);
     const dim3 block(s.team, s.teams), grid((unsigned)((p.workers + s.teams - 1) / s.teams));
-    if (s.vec > 1) {
-        if (s.nv == 1) launch_norm_bwd_nv<T, V, 1>(p, full, grid, block, stream);
-        else if (s.nv == 2) launch_norm_bwd_nv<T, V, 2>(p, full, grid, block, stream);
-        else launch_norm_bwd_nv<T, V, 4>(p, full, grid, block, stream);
-    } else {
-        if (s.nv == 1) launch_norm_bwd_nv<T, 1, 1>(p, full, grid, block, stream);
-        else if (s.nv == 4) launch_norm_bwd_nv<T, 1, 4>(p, full, grid, block, stream);
-        else launch_norm_bwd_nv<T, 1, 16>(p, full, grid, block, stream);
-    }
+    int rc;
+    if (s.vec > 1)
+        rc = s.nv == 1 ? launch_norm_bwd_nv<T, V, 1>(p, full, grid, block, stream)
+           : s.nv == 2 ? launch_norm_bwd_nv<T, V, 2>(p, full, grid, block, stream)
+                       : launch_norm_bwd_nv<T, V, 4>(p, full, grid, block, stream);
+    else
+        rc = s.nv == 1 ? launch_norm_bwd_nv<T, 1, 1>(p, full, grid, block, stream)
+           : s.nv == 4 ? launch_norm_bwd_nv<T, 1, 4>(p, full, grid, block, stream)
+                       : launch_norm_bwd_nv<T, 1, 16>(p, full, grid, block, stream);
+    if (rc != TGC_OK) return rc;
     if (nsums > 0) norm_sum_kernel<T><<<dim3((unsigned)((p.D + 31) / 32), (unsigned)nsums), 256, 0, stream>>>(q);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? TGC_OK : cuda_fail(e);
 }
 
 static int norm_bwd_impl(tgc_block_norm_bwd_args a) {
@@ -633,7 +962,7 @@ static int norm_bwd_impl(tgc_block_norm_bwd_args a) {
         if (a.workspace == nullptr || a.workspace_bytes < q.total) return TGC_ERR_WORKSPACE;
         if (reinterpret_cast<uintptr_t>(a.workspace) % 128 != 0) return TGC_ERR_ALIGN;
     }
-    const TeamShape s = team_shape(a.D, norm_elem(a.dtype), vec, 512);
+    const TeamShape s = team_shape(a.D, norm_elem(a.dtype), vec);
     NormBwdParams p{};
     p.y = a.y; p.r = a.r; p.dr = a.dr; p.dh = a.dh; p.gate = a.gate;
     p.post_w = a.post_weight; p.post_b = a.post_bias; p.pre_w = a.pre_weight;
@@ -648,18 +977,21 @@ static int norm_bwd_impl(tgc_block_norm_bwd_args a) {
     for (int i = 0; i < 4; ++i) p.want[i] = outs[i] != nullptr;
     p.need_y = a.post != TGC_NORM_NONE || a.dgate != nullptr;
     p.res_scale = a.res_scale; p.branch_scale = a.branch_scale; p.eps = a.eps; p.inv_d = 1.0f / (float)a.D;
+    if (a.M > 0) {
+        const int rc = device_fault_word(&p.fault);
+        if (rc != TGC_OK) return rc;
+    }
     NormSumParams n{};
     n.partial = p.partial; n.gate_partial = p.gate_partial; n.dgate = a.dgate;
     for (int i = 0; i < 4; ++i) n.out[i] = outs[i];
     n.D = p.D; n.workers = p.workers; n.units_per_gate = p.units_per_gate;
     const bool sums = outs[0] != nullptr || outs[1] != nullptr || outs[2] != nullptr || outs[3] != nullptr;
     const int nsums = p.gate_partial != nullptr ? 4 + q.segments : sums ? 4 : 0;
-    const bool full = outs[1] != nullptr || outs[3] != nullptr;
-    if (a.dtype == TGC_BF16) launch_norm_bwd<__nv_bfloat16>(p, n, nsums, s, full, a.stream);
-    else if (a.dtype == TGC_F16) launch_norm_bwd<__half>(p, n, nsums, s, full, a.stream);
-    else launch_norm_bwd<float>(p, n, nsums, s, full, a.stream);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? TGC_OK : cuda_fail(e);
+    const bool full = outs[1] != nullptr || outs[3] != nullptr || a.post_bias != nullptr || a.post == TGC_NORM_LAYER ||
+                      a.pre == TGC_NORM_LAYER;
+    return a.dtype == TGC_BF16  ? launch_norm_bwd<__nv_bfloat16>(p, n, nsums, s, full, a.stream)
+           : a.dtype == TGC_F16 ? launch_norm_bwd<__half>(p, n, nsums, s, full, a.stream)
+                                : launch_norm_bwd<float>(p, n, nsums, s, full, a.stream);
 }
 
 }  // namespace tgc

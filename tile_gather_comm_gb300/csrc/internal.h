@@ -28,6 +28,9 @@ static_assert(kMinPieceBytes >= 4096 && kMinPieceBytes <= kMaxPieceBytes && kMin
 // Records a CUDA error for tgc_last_cuda_error() and maps it to a status.
 int cuda_fail(cudaError_t e);
 int sm_count(int device);
+// Address, on the current device, of the word that the asynchronous operators' kernels set when a
+// bounded wait of theirs expires (read and cleared by tgc_async_status).
+int device_fault_word(int **word);
 
 // Launch the TGATHER kernel; arguments already validated.
 struct TGatherLaunch {

@@ -14,6 +14,16 @@
 
 namespace tgc {
 
+__device__ int g_async_fault;
+
+int device_fault_word(int **word) {
+    void *p = nullptr;
+    const cudaError_t e = cudaGetSymbolAddress(&p, g_async_fault);
+    if (e != cudaSuccess) return cuda_fail(e);
+    *word = static_cast<int *>(p);
+    return TGC_OK;
+}
+
 static bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // ---------------------------------------------------------------- dz and the bias gradient
@@ -300,6 +310,16 @@ static int linear_bwd_impl(tgc_linear_bwd_args a) {
 }
 
 }  // namespace tgc
+
+extern "C" int tgc_async_status(cudaStream_t stream) {
+    int *word = nullptr, status = 0;
+    const int rc = tgc::device_fault_word(&word);
+    if (rc != TGC_OK) return rc;
+    cudaError_t e = cudaMemcpyAsync(&status, word, sizeof status, cudaMemcpyDeviceToHost, stream);
+    if (e == cudaSuccess) e = cudaMemsetAsync(word, 0, sizeof status, stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+    return e == cudaSuccess ? status : tgc::cuda_fail(e);
+}
 
 extern "C" int tgc_linear(const tgc_linear_args *args) {
     if (args == nullptr) return TGC_ERR_INVALID_ARG;

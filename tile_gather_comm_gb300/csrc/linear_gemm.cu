@@ -413,8 +413,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 
 // ---------------------------------------------------------------- host side
 
-__device__ int g_linear_fault;
-
 static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;
@@ -508,11 +506,7 @@ int lin_params(LinearParams *p, const LinearProduct &q, int tile_n) {
     p->act = q.act;
     p->f16 = q.f16;
     p->timeout_ns = 4ull * 1000 * 1000 * 1000;
-    void *fault = nullptr;
-    const cudaError_t e = cudaGetSymbolAddress(&fault, g_linear_fault);
-    if (e != cudaSuccess) return cuda_fail(e);
-    p->fault = static_cast<int *>(fault);
-    return TGC_OK;
+    return device_fault_word(&p->fault);
 }
 
 template <int CG, int MODE, int TN>
