@@ -29,7 +29,8 @@ static bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintp
 // ---------------------------------------------------------------- dz and the bias gradient
 
 // dz = dy act'(z) and, in the same pass, the column sums of each chunk of kChunk rows (chunks
-// never cross a group): block (strip, chunk) holds 32 vectors of 8 columns x 8 row lanes.
+// never cross a group): a block takes a strip of 32 vectors of 8 columns, 8 row lanes, each lane
+// 8 rows a chunk with all its loads under way before the first is used.
 // Bound by memory: dy and z read once, dz written once, partial sums M/kChunk x N fp32.
 constexpr int kChunk = 64;
 
@@ -43,12 +44,7 @@ struct DzParams {
     const int32_t *offsets;
 };
 
-template <typename T>
-struct alignas(16) Vec8 {
-    T v[8];
-};
-
-template <typename T>
+template <bool F16>
 __global__ void __launch_bounds__(256) dz_kernel(const DzParams p) {
     __shared__ float sums[8][32 * 8 + 8];
     __shared__ int s_rows[2];
@@ -56,42 +52,62 @@ __global__ void __launch_bounds__(256) dz_kernel(const DzParams p) {
     const int strip = (int)(blockIdx.x % (unsigned)strips), chunk = (int)(blockIdx.x / (unsigned)strips);
     const int cv = threadIdx.x % 32, rl = threadIdx.x / 32;
     const int n = (strip * 32 + cv) * 8;
-    if (threadIdx.x < 32) {
-        int idx = 0;
-        const int e = p.offsets == nullptr
-                          ? (idx = chunk, 0)
-                          : find_group_tile(p.offsets, p.ngroups, p.M, kChunk, chunk, threadIdx.x, &idx);
-        if (threadIdx.x == 0) {
-            const RowRange g = e >= 0 ? group_range(p.offsets, e, p.M) : RowRange{0, 0};
-            const int r0 = g.begin + idx * kChunk;
-            s_rows[0] = r0;
-            s_rows[1] = r0 + kChunk < g.end ? r0 + kChunk : g.end;
+    int r0 = chunk * kChunk, r1 = r0 + kChunk < p.M ? r0 + kChunk : p.M;
+    if (p.offsets != nullptr) {
+        if (threadIdx.x < 32) {
+            int idx = 0;
+            const int e = find_group_tile(p.offsets, p.ngroups, p.M, kChunk, chunk, threadIdx.x, &idx);
+            if (threadIdx.x == 0) {
+                const RowRange g = e >= 0 ? group_range(p.offsets, e, p.M) : RowRange{0, 0};
+                const int a = g.begin + idx * kChunk;
+                s_rows[0] = a;
+                s_rows[1] = a + kChunk < g.end ? a + kChunk : g.end;
+            }
         }
+        __syncthreads();
+        r0 = s_rows[0];
+        r1 = s_rows[1];
+        if (r0 >= r1) return;
     }
-    __syncthreads();
-    const int r0 = s_rows[0], r1 = s_rows[1];
-    if (r0 >= r1) return;
     float acc[8] = {};
     if (n < p.N) {
-        for (int m = r0 + rl; m < r1; m += 8) {
-            const Vec8<T> dy = *reinterpret_cast<const Vec8<T> *>(static_cast<const T *>(p.dy) + (int64_t)m * p.lddy + n);
-            float d[8];
+        constexpr int U = 4;  // rows of a lane in flight
+        const uint16_t *dy = static_cast<const uint16_t *>(p.dy) + n, *z = static_cast<const uint16_t *>(p.z) + n;
+        uint16_t *dz = static_cast<uint16_t *>(p.dz) + n;
+        with_act(p.act, [&](auto act) {
+            for (int m = r0 + rl; m < r1; m += 8 * U) {
+                uint4 a[U], b[U];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) d[c] = to_f32(dy.v[c]);
-            if (p.act != TGC_ACT_NONE) {
-                const Vec8<T> z = *reinterpret_cast<const Vec8<T> *>(static_cast<const T *>(p.z) + (int64_t)m * p.ldz + n);
+                for (int u = 0; u < U; ++u) {
+                    const int64_t row = m + 8 * u;
+                    if (row < r1) {
+                        a[u] = *reinterpret_cast<const uint4 *>(dy + row * p.lddy);
+                        if (decltype(act)::value != TGC_ACT_NONE) b[u] = *reinterpret_cast<const uint4 *>(z + row * p.ldz);
+                    }
+                }
 #pragma unroll
-                for (int c = 0; c < 8; ++c) d[c] *= act_grad_f32(to_f32(z.v[c]), p.act);
+                for (int u = 0; u < U; ++u) {
+                    const int64_t row = m + 8 * u;
+                    if (row >= r1) continue;
+                    const uint32_t aw[4] = {a[u].x, a[u].y, a[u].z, a[u].w}, bw[4] = {b[u].x, b[u].y, b[u].z, b[u].w};
+                    uint32_t o[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float d0, d1, z0, z1;
+                        unpack16(aw[i], F16, &d0, &d1);
+                        if (decltype(act)::value != TGC_ACT_NONE) {
+                            unpack16(bw[i], F16, &z0, &z1);
+                            d0 *= act_grad_of<decltype(act)::value>(z0);
+                            d1 *= act_grad_of<decltype(act)::value>(z1);
+                        }
+                        acc[2 * i] += d0;
+                        acc[2 * i + 1] += d1;
+                        o[i] = pack16(d0, d1, F16);
+                    }
+                    if (p.dz != nullptr) *reinterpret_cast<uint4 *>(dz + row * p.N) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
             }
-            if (p.dz != nullptr) {
-                Vec8<T> o;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) o.v[c] = from_f32<T>(d[c]);
-                *reinterpret_cast<Vec8<T> *>(static_cast<T *>(p.dz) + (int64_t)m * p.N + n) = o;
-            }
-#pragma unroll
-            for (int c = 0; c < 8; ++c) acc[c] += d[c];
-        }
+        });
     }
     if (p.partial == nullptr) return;
 #pragma unroll
@@ -275,8 +291,8 @@ static int linear_bwd_impl(tgc_linear_bwd_args a) {
         }
         if (a.dbias != nullptr) d.partial = reinterpret_cast<float *>(ws + l.partial);
         const unsigned grid = (unsigned)((a.N + 255) / 256 * l.chunks);
-        if (a.dtype == TGC_BF16) dz_kernel<__nv_bfloat16><<<grid, 256, 0, a.stream>>>(d);
-        else dz_kernel<__half><<<grid, 256, 0, a.stream>>>(d);
+        if (a.dtype == TGC_BF16) dz_kernel<false><<<grid, 256, 0, a.stream>>>(d);
+        else dz_kernel<true><<<grid, 256, 0, a.stream>>>(d);
         if (a.dbias != nullptr) {
             const dim3 g2((unsigned)((a.N + 31) / 32), (unsigned)groups);
             if (a.dtype == TGC_BF16)

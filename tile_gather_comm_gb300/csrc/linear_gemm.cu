@@ -306,10 +306,11 @@ __device__ void lin_role_epilogue(const LinearMaps &maps, const LinearParams &p,
                         w[i] = pack16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), f16);
                     put(&maps.z, p.z, p.ldz, n, w);
                 }
-                if (p.act != TGC_ACT_NONE) {
+                if (p.act != TGC_ACT_NONE)
+                    with_act(p.act, [&](auto act) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(act_f32(__uint_as_float(v[i]), p.act));
-                }
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(act_of<decltype(act)::value>(__uint_as_float(v[i])));
+                    });
                 if (p.residual != nullptr && row_ok) {
                     const uint4 *r = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.residual) +
                                                                      (int64_t)m * p.ldres + n);

@@ -226,8 +226,10 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
                     add(*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias) + (int64_t)tl.e * p.J + n));
                 if (p.z != nullptr) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.z) + m * p.ldz + n) = pack();
                 if (p.act != TGC_ACT_NONE)
+                    with_act(p.act, [&](auto act) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] = act_f32(v[k], p.act);
+                        for (int k = 0; k < 8; ++k) v[k] = act_of<decltype(act)::value>(v[k]);
+                    });
                 if (p.residual != nullptr)
                     add(*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.residual) + m * p.ldres + n));
             }
