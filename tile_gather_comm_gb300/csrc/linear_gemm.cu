@@ -30,6 +30,7 @@ namespace tgc {
 constexpr int kLinThreads = 384;
 constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
 constexpr int kBoxBytes = 32 * 32 * 2;  // an epilogue warp's staging box: 32 rows x 32 columns
+constexpr int kBiasBytes = 128 * 4;     // its columns' bias in fp32
 constexpr uint32_t kLinTmemCols = 512;
 constexpr uint64_t kLinDrainNs = 200ull * 1000 * 1000;
 
@@ -43,15 +44,18 @@ struct LCfg {
     static constexpr int kStages = 196608 / kStage;       // 4 of 48, 6 of 32, 8 of 24 KiB
     static constexpr bool kAMn = MODE == kWgrad, kBMn = MODE != kFwd;
     static constexpr uint32_t kBoxMn = 64 * kBK * 2;      // an MN-major box: 64 columns x 64 rows, 8 KiB
-    static constexpr int kSmem = 1024 + kStages * kStage + kEpiWarps * kBoxBytes + (TGC_MAX_GROUPS + 8) * 4 + 512;
+    static constexpr int kSmem = 1024 + kStages * kStage + kEpiWarps * (kBoxBytes + kBiasBytes) +
+                                  (TGC_MAX_GROUPS + 8) * 4 + 512;
 };
 
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool lin_wait(uint64_t *bar, uint32_t parity, const LinearParams &p) {
     const uint32_t a = smem_addr(bar);
-    if (mbar_try_wait(a, parity)) return true;
+    auto ready = [&] { return CLUSTER ? mbar_try_wait_cluster(a, parity) : mbar_try_wait(a, parity); };
+    if (ready()) return true;
     const uint64_t t0 = globaltimer_ns();
     for (uint64_t it = 1; it < (1ull << 40); ++it) {
-        if (mbar_try_wait(a, parity)) return true;
+        if (ready()) return true;
         if ((it & 63) == 0 && globaltimer_ns() - t0 > p.timeout_ns) break;
     }
     raise_status(p.fault, kStatusTimeout);
@@ -73,9 +77,10 @@ __device__ void lin_role_tma(const LinearMaps &maps, const LinearParams &p, cons
     bool ok = true;
     const uint32_t full0 = CG == 2 ? mapa_shared(smem_addr(full), 0) : smem_addr(full);
     const int tiles = num_tiles<MODE>(p, tile0);
-    uint64_t *count = full;  // the barriers that count the loads' bytes
+    bool cut = false;  // this step's bytes count on this CTA's own raw barrier
     auto load = [&](void *dst, const CUtensorMap *map, uint32_t s, int c0, int c1, int c2) {
-        if (CG == 1) tma_load_3d(dst, map, &count[s], c0, c1, c2);
+        if (MODE == kWgrad && cut) tma_load_3d(dst, map, &raw[s], c0, c1, c2);
+        else if (CG == 1) tma_load_3d(dst, map, &full[s], c0, c1, c2);
         else tma_load_3d_pair(dst, map, full0 + s * 8u, c0, c1, c2);
     };
     // boxes of A that a CTA with `rows` existing rows loads: all 128 rows at once, or 32 at a time
@@ -94,12 +99,13 @@ __device__ void lin_role_tma(const LinearMaps &maps, const LinearParams &p, cons
         for (int kb = 0; kb < tl.num_kb; ++kb, ++it) {
             const uint32_t s = it % C::kStages, ph = (it / C::kStages) & 1u;
             if (!lin_wait(&empty[s], ph ^ 1u, p)) { ok = false; break; }
-            if (MODE == kWgrad && CG == 1) {
-                const bool cut = needs_repair(p, tl, kb);
-                count = cut ? raw : full;
-                if (cut) mbar_arrive(&full[s]);
+            if (MODE == kWgrad) cut = needs_repair(p, tl, kb);
+            if (cut) {
+                mbar_arrive_expect_tx(&raw[s], C::kABytes + C::kBBytes);
+                if (CG == 1 || crank == 0) mbar_arrive(&full[s]);
+            } else if (CG == 1 || crank == 0) {
+                mbar_arrive_expect_tx(&full[s], tx);
             }
-            if (CG == 1 || crank == 0) mbar_arrive_expect_tx(&count[s], tx);
             uint8_t *a = sA + s * C::kABytes, *b = sB + s * C::kBBytes;
             const int r0 = (MODE == kWgrad ? tl.red0 : 0) + kb * kBK;
             if (C::kAMn) {
@@ -154,8 +160,8 @@ __device__ void lin_role_mma(const LinearParams &p, const int *tile0, uint8_t *s
         const uint32_t d = tmem_base + acc * (uint32_t)TN;
         for (int kb = 0; kb < tl.num_kb; ++kb, ++it) {
             const uint32_t s = it % C::kStages, ph = (it / C::kStages) & 1u;
-            if (MODE == kWgrad && CG == 1 && needs_repair(p, tl, kb)) {
-                if (!lin_wait(&fixed[s], (fixes >> s) & 1u, p)) { ok = false; break; }
+            if (MODE == kWgrad && needs_repair(p, tl, kb)) {
+                if (!lin_wait<CG == 2>(&fixed[s], (fixes >> s) & 1u, p)) { ok = false; break; }
                 fixes ^= 1u << s;
             }
             if (!lin_wait(&full[s], ph, p)) { ok = false; break; }
@@ -191,7 +197,8 @@ __device__ void lin_role_fix(const LinearParams &p, const int *tile0, uint8_t *s
     using C = LCfg<CG, MODE, TN>;
     uint32_t it = 0, phases = 0;  // phases: per stage, the parity of its next cut step
     const int tiles = num_tiles<MODE>(p, tile0);
-    for (int t = (int)blockIdx.x; t < tiles; t += (int)gridDim.x) {
+    const uint32_t fixed0 = CG == 2 ? mapa_shared(smem_addr(fixed), 0) : smem_addr(fixed);
+    for (int t = (int)blockIdx.x / CG; t < tiles; t += (int)gridDim.x / CG) {
         const Tile tl = get_tile<MODE, C::kTM, TN>(p, tile0, t);
         it += (uint32_t)tl.num_kb;
         if (!needs_repair(p, tl, tl.num_kb - 1)) continue;
@@ -211,7 +218,10 @@ __device__ void lin_role_fix(const LinearParams &p, const int *tile0, uint8_t *s
         for (int c = 0; c < C::kBRows / 64; ++c) wipe(sB + s * C::kBBytes + c * C::kBoxMn);
         fence_proxy_async_shared();  // the MMA reads through the async proxy
         __syncwarp();
-        if (lane == 0) mbar_arrive(&fixed[s]);
+        if (lane == 0) {
+            if (CG == 1) mbar_arrive(&fixed[s]);
+            else mbar_arrive_cluster(fixed0 + s * 8u);
+        }
     }
 }
 
@@ -219,12 +229,13 @@ __device__ void lin_role_fix(const LinearParams &p, const int *tile0, uint8_t *s
 
 template <int CG, int MODE, int TN>
 __device__ void lin_role_epilogue(const LinearMaps &maps, const LinearParams &p, const int *tile0, uint8_t *sC,
-                                  uint64_t *tfull, uint64_t *tempty, uint32_t tmem_base, uint32_t crank, int warp,
+                                  float *sBias, uint64_t *tfull, uint64_t *tempty, uint32_t tmem_base, uint32_t crank, int warp,
                                   int lane) {
     using C = LCfg<CG, MODE, TN>;
     const int ew = warp - kEpiWarp0, q = warp & 3;  // q: the TMEM lane quarter a warp may read
     const int col0 = (ew >> 2) * (TN / 2);
     uint8_t *box = sC + ew * kBoxBytes;
+    float *bias = sBias + ew * (kBiasBytes / 4);
     const uint32_t tempty0 = CG == 2 ? mapa_shared(smem_addr(tempty), 0) : smem_addr(tempty);
     const bool f16 = p.f16 != 0;
     const int tiles = num_tiles<MODE>(p, tile0);
@@ -238,6 +249,36 @@ __device__ void lin_role_epilogue(const LinearMaps &maps, const LinearParams &p,
         // dense outputs and dw are clipped by their tensor map; inside grouped rows a cut box is not
         const bool by_tma = rows > 0 && (rows >= 32 || MODE == kWgrad || p.offsets == nullptr);
         const bool row_ok = lane < rows;
+        // What the epilogue reads is asked for before the products are done: the bias of this
+        // warp's columns (to shared memory, in fp32) and a chunk of the residual at a time.
+        uint4 res[4];
+        auto fetch_residual = [&](int n) {
+            const uint4 *r = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.residual) +
+                                                             (int64_t)m * p.ldres + n);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (row_ok && n + c * 8 < p.J) res[c] = r[c];
+        };
+        if (MODE == kFwd) {
+            const int n = tl.n0 + col0;
+            if (p.bias != nullptr) {
+                __syncwarp();  // the last tile's readers are done
+                if (lane * 8 < TN / 2 && n + lane * 8 < p.J) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias) +
+                                                                     (int64_t)tl.e * p.J + n + lane * 8);
+                    float f[8];
+                    unpack16(w.x, f16, &f[0], &f[1]);
+                    unpack16(w.y, f16, &f[2], &f[3]);
+                    unpack16(w.z, f16, &f[4], &f[5]);
+                    unpack16(w.w, f16, &f[6], &f[7]);
+                    float4 *to = reinterpret_cast<float4 *>(bias + lane * 8);
+                    to[0] = make_float4(f[0], f[1], f[2], f[3]);
+                    to[1] = make_float4(f[4], f[5], f[6], f[7]);
+                }
+            }
+            if (p.residual != nullptr) fetch_residual(n);
+            __syncwarp();
+        }
         bool ok = true;
         if (lane == 0) ok = lin_wait(&tfull[acc], aph, p);
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;  // warp-uniform: tcgen05.ld is .sync.aligned
@@ -283,20 +324,13 @@ __device__ void lin_role_epilogue(const LinearMaps &maps, const LinearParams &p,
             if (n >= p.J || rows <= 0) continue;  // warp-uniform
             if (MODE == kFwd) {
                 if (p.bias != nullptr) {
-                    const uint4 *b = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias) +
-                                                                     (int64_t)tl.e * p.J + n);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        if (n + c * 8 >= p.J) continue;
-                        const uint4 w = b[c];
-                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float lo, hi;
-                            unpack16(ws[i], f16, &lo, &hi);
-                            v[c * 8 + 2 * i] = __float_as_uint(__uint_as_float(v[c * 8 + 2 * i]) + lo);
-                            v[c * 8 + 2 * i + 1] = __float_as_uint(__uint_as_float(v[c * 8 + 2 * i + 1]) + hi);
-                        }
+                    for (int c = 0; c < 8; ++c) {  // the same address in every lane
+                        const float4 f = reinterpret_cast<const float4 *>(bias + j * 32)[c];
+                        v[4 * c] = __float_as_uint(__uint_as_float(v[4 * c]) + f.x);
+                        v[4 * c + 1] = __float_as_uint(__uint_as_float(v[4 * c + 1]) + f.y);
+                        v[4 * c + 2] = __float_as_uint(__uint_as_float(v[4 * c + 2]) + f.z);
+                        v[4 * c + 3] = __float_as_uint(__uint_as_float(v[4 * c + 3]) + f.w);
                     }
                 }
                 if (p.z != nullptr) {
@@ -311,22 +345,22 @@ __device__ void lin_role_epilogue(const LinearMaps &maps, const LinearParams &p,
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(act_of<decltype(act)::value>(__uint_as_float(v[i])));
                     });
-                if (p.residual != nullptr && row_ok) {
-                    const uint4 *r = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.residual) +
-                                                                     (int64_t)m * p.ldres + n);
+                if (p.residual != nullptr) {
+                    if (row_ok) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        if (n + c * 8 >= p.J) continue;
-                        const uint4 w = r[c];
-                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                        for (int c = 0; c < 4; ++c) {
+                            if (n + c * 8 >= p.J) continue;
+                            const uint32_t ws[4] = {res[c].x, res[c].y, res[c].z, res[c].w};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float lo, hi;
-                            unpack16(ws[i], f16, &lo, &hi);
-                            v[c * 8 + 2 * i] = __float_as_uint(__uint_as_float(v[c * 8 + 2 * i]) + lo);
-                            v[c * 8 + 2 * i + 1] = __float_as_uint(__uint_as_float(v[c * 8 + 2 * i + 1]) + hi);
+                            for (int i = 0; i < 4; ++i) {
+                                float lo, hi;
+                                unpack16(ws[i], f16, &lo, &hi);
+                                v[c * 8 + 2 * i] = __float_as_uint(__uint_as_float(v[c * 8 + 2 * i]) + lo);
+                                v[c * 8 + 2 * i + 1] = __float_as_uint(__uint_as_float(v[c * 8 + 2 * i + 1]) + hi);
+                            }
                         }
                     }
+                    if (j + 1 < TN / 64) fetch_residual(n + 32);
                 }
             }
             uint32_t w[16];
@@ -350,7 +384,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     uint8_t *sA = smem;
     uint8_t *sB = sA + C::kStages * C::kABytes;
     uint8_t *sC = sB + C::kStages * C::kBBytes;
-    int *tile0 = reinterpret_cast<int *>(sC + kEpiWarps * kBoxBytes);
+    float *sBias = reinterpret_cast<float *>(sC + kEpiWarps * kBoxBytes);
+    int *tile0 = reinterpret_cast<int *>(sBias + kEpiWarps * (kBiasBytes / 4));
     uint64_t *full = reinterpret_cast<uint64_t *>(tile0 + TGC_MAX_GROUPS + 8);
     uint64_t *empty = full + C::kStages;
     uint64_t *fixed = empty + C::kStages;
@@ -367,7 +402,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
-            mbar_init(&fixed[s], 1);
+            mbar_init(&fixed[s], CG);
             mbar_init(&raw[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
@@ -396,10 +431,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (lane == 0 && crank == 0)
             lin_role_mma<CG, MODE, TN>(p, tile0, sA, sB, full, fixed, empty, tfull, tempty, drain, tmem_base);
     } else if (warp == 2) {
-        if (MODE == kWgrad && CG == 1 && p.offsets != nullptr)
+        if (MODE == kWgrad && p.offsets != nullptr)
             lin_role_fix<CG, MODE, TN>(p, tile0, sA, sB, raw, fixed, lane);
     } else if (warp >= kEpiWarp0) {
-        lin_role_epilogue<CG, MODE, TN>(maps, p, tile0, sC, tfull, tempty, tmem_base, crank, warp, lane);
+        lin_role_epilogue<CG, MODE, TN>(maps, p, tile0, sC, sBias, tfull, tempty, tmem_base, crank,
+                                          warp, lane);
     }
     // in a pair the even CTA's MMAs read the odd one's shared memory: neither leaves before both are done
     __syncwarp();
@@ -475,7 +511,7 @@ static int lin_clusters(int dev, int sms, int *out) {
     return TGC_OK;
 }
 
-bool lin_maps(LinearMaps *maps, const LinearProduct &q, int mode, int b_rows) {
+bool lin_maps(LinearMaps *maps, const LinearProduct &q, int mode, int b_rows, int row_box) {
     std::memset(maps, 0, sizeof *maps);
     const auto sw = CU_TENSOR_MAP_SWIZZLE_128B, sw_out = CU_TENSOR_MAP_SWIZZLE_64B;
     const auto l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B, none = CU_TENSOR_MAP_L2_PROMOTION_NONE;
@@ -486,7 +522,7 @@ bool lin_maps(LinearMaps *maps, const LinearProduct &q, int mode, int b_rows) {
              lin_map(&maps->b, q.b, q.J, q.M, 1, q.ldb, 0, 64, kBK, sw, l2);
     } else {
         ok = lin_map(&maps->a, q.a, q.R, q.M, 1, q.lda, 0, kBK, 128, sw, l2) &&
-             lin_map(&maps->a_small, q.a, q.R, q.M, 1, q.lda, 0, kBK, kRowBox, sw, l2) &&
+             lin_map(&maps->a_small, q.a, q.R, q.M, 1, q.lda, 0, kBK, (uint32_t)row_box, sw, l2) &&
              (mode == kFwd ? lin_map(&maps->b, q.b, q.R, q.J, E, q.ldb, q.b_stride, kBK, (uint32_t)b_rows, sw, l2)
                            : lin_map(&maps->b, q.b, q.J, q.R, E, q.ldb, q.b_stride, 64, kBK, sw, l2));
     }
@@ -514,7 +550,7 @@ template <int CG, int MODE, int TN>
 static int lin_launch(const LinearProduct &q, int dev, int sms, cudaStream_t stream) {
     using C = LCfg<CG, MODE, TN>;
     LinearMaps maps;
-    if (!lin_maps(&maps, q, MODE, C::kBRows)) return TGC_ERR_CUDA;
+    if (!lin_maps(&maps, q, MODE, C::kBRows, kRowBox)) return TGC_ERR_CUDA;
     int clusters = 0;
     int rc = lin_clusters<CG, MODE, TN>(dev, sms, &clusters);
     if (rc != TGC_OK) return rc;
@@ -547,29 +583,82 @@ static int lin_launch(const LinearProduct &q, int dev, int sms, cudaStream_t str
     return e == cudaSuccess ? TGC_OK : cuda_fail(e);
 }
 
+// ---------------------------------------------------------------- which kernel, which tile
+
+// Every form is bound by what one SM takes in: a row of 128 bytes of an operand costs it about
+// 2.1 cycles (60 bytes a cycle; measured on 777 x 4096 x 5000: 128 x 256 tiles 806 cycles a 64-deep
+// step, 128 x 128 538, the pair's 256 x 256 560 for each CTA's 128 x 256).  So a form's time is its
+// number of rounds times its steps times the rows a step loads, plus what the last tile's epilogue
+// adds; the least wins.
+struct LinearForm {
+    int cg, tn;  // the persistent kernel's; cg 0: the split kernel's tn and parts
+    int parts;
+    int64_t cycles;
+};
+
+template <int MODE>
+static LinearForm lin_choose(const LinearProduct &q, int sms, const int (&room)[kMaxSplit + 1]) {
+    const int64_t groups = q.offsets != nullptr ? q.ngroups : 1;
+    const int64_t rows = MODE == kWgrad ? q.I : q.M;
+    const int64_t steps = ((MODE == kWgrad ? (q.M + groups - 1) / groups : q.R) + kBK - 1) / kBK;
+    // Tile rows of height h: exact without groups; with them (kFwd, kDgrad) half a tile more a
+    // group that can have rows.
+    auto tile_rows = [&](int64_t h) -> int64_t {
+        if (MODE == kWgrad) return groups * ((rows + h - 1) / h);
+        if (q.offsets == nullptr) return (rows + h - 1) / h;
+        const int64_t used = groups < rows ? groups : rows;
+        return rows / h + (used + 1) / 2;
+    };
+    auto cycles = [](int64_t box_rows) { return box_rows * 21 / 10; };
+    LinearForm best{};
+    best.cycles = INT64_MAX;
+    auto consider = [&](int cg, int tn, int parts, int64_t c) {
+        if (c < best.cycles) best = {cg, tn, parts, c};
+    };
+    static constexpr int kForms[4][2] = {{2, 256}, {2, 128}, {1, 256}, {1, 128}};
+    for (const auto &f : kForms) {
+        const int cg = f[0], tn = f[1];
+        const int64_t tiles = tile_rows(128 * cg) * ((q.J + tn - 1) / tn);
+        const int64_t rounds = (tiles + sms / cg - 1) / (sms / cg);
+        int64_t step = cycles(128 + tn / cg);
+        if (step < 2 * tn) step = 2 * tn;  // the products themselves
+        const int64_t epilogue = tn * 16;
+        const int64_t tile = steps * step > epilogue ? steps * step : epilogue;
+        consider(cg, tn, 0, rounds * tile + epilogue + 1500);
+    }
+    if (MODE == kWgrad && q.offsets != nullptr) return best;
+    const int64_t tm = split_tiles(q, MODE);
+    const int64_t a_rows = MODE == kWgrad || rows > 96 ? 128 : (rows + split_row_box(q.M) - 1) / split_row_box(q.M) * split_row_box(q.M);
+    for (int tn = 128; tn >= 48; tn -= 16) {
+        if (MODE != kFwd && tn % 64 != 0) continue;
+        const int64_t tiles = tm * ((q.J + tn - 1) / tn);
+        for (int parts = 1; parts <= kMaxSplit && parts <= steps; ++parts) {
+            if (room[parts] <= 0) continue;
+            // one CTA on an SM while there are no more than SMs, two beyond; then further rounds
+            const int64_t rounds = (tiles + room[parts] - 1) / room[parts];
+            const int64_t shared = tiles * parts <= sms ? 1 : 2 * rounds;
+            const int64_t mine = (steps + parts - 1) / parts;
+            const int64_t reduce = parts > 1 ? 1000 + 300 * parts : 0;
+            consider(0, tn, parts, shared * (mine * cycles(a_rows + tn)) + rounds * (reduce + tn * 16) + 1500);
+        }
+    }
+    return best;
+}
+
 template <int MODE>
 static int lin_dispatch(const LinearProduct &q, cudaStream_t stream) {
     int dev = 0;
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e);
     const int sms = sm_count(dev);
-    const int64_t rows = MODE == kWgrad ? q.I : q.M;
-    // Few tiles: split each one's reduction.  Two CTAs fit an SM.
-    if (MODE != kWgrad || q.offsets == nullptr) {
-        const int64_t steps = ((MODE == kWgrad ? q.M : q.R) + kBK - 1) / kBK, room = 2 * (int64_t)sms;
-        const int64_t tm = split_tiles(q, MODE);
-        const int64_t wide = tm * ((q.J + 127) / 128), narrow = tm * ((q.J + 63) / 64);
-        if (wide <= room) {
-            const int tn = narrow <= room && rows <= 128 ? 64 : 128;
-            const int64_t tiles = tn == 64 ? narrow : wide;
-            int parts = 1;
-            while (parts < kMaxSplit && tiles * parts * 2 <= room && steps >= parts * 4) parts *= 2;
-            return launch_linear_split(q, MODE, tn, parts, stream);
-        }
-    }
-    const bool pair = rows > 128 && q.offsets == nullptr;
-    if (pair) return lin_launch<2, MODE, 256>(q, dev, sms, stream);
-    return q.J > 128 ? lin_launch<1, MODE, 256>(q, dev, sms, stream) : lin_launch<1, MODE, 128>(q, dev, sms, stream);
+    int room[kMaxSplit + 1];
+    const int rc = split_room(MODE, dev, room);
+    if (rc != TGC_OK) return rc;
+    const LinearForm f = lin_choose<MODE>(q, sms, room);
+    if (f.cg == 0) return launch_linear_split(q, MODE, f.tn, f.parts, stream);
+    if (f.cg == 2)
+        return f.tn == 256 ? lin_launch<2, MODE, 256>(q, dev, sms, stream) : lin_launch<2, MODE, 128>(q, dev, sms, stream);
+    return f.tn == 256 ? lin_launch<1, MODE, 256>(q, dev, sms, stream) : lin_launch<1, MODE, 128>(q, dev, sms, stream);
 }
 
 int launch_linear(const LinearProduct &q, int mode, cudaStream_t stream) {

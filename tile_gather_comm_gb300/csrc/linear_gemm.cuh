@@ -60,8 +60,8 @@ struct LinearProduct {
 };
 int launch_linear(const LinearProduct &q, int mode, cudaStream_t stream);
 
-// Operand maps: A and B as 3-D (inner, rows, matrix) tensors; aSmall the same A with boxes of
-// kRowBox rows; y and z for the TMA stores.
+// Operand maps: A and B as 3-D (inner, rows, matrix) tensors; a_small the same A with boxes of
+// few rows; y and z for the TMA stores.
 struct LinearMaps {
     CUtensorMap a, a_small, b, y, z;
 };
@@ -69,11 +69,16 @@ struct LinearMaps {
 // Fills the maps for B boxes of b_rows rows (K-major) or 64 columns (MN-major); what q.z == null
 // leaves out is not set.  lin_params sets everything but num_m.
 constexpr int kLinMaxDevices = 64;
-bool lin_maps(LinearMaps *maps, const LinearProduct &q, int mode, int b_rows);
+bool lin_maps(LinearMaps *maps, const LinearProduct &q, int mode, int b_rows, int row_box);
 int lin_params(LinearParams *p, const LinearProduct &q, int tile_n);
 constexpr int kMaxSplit = 8;  // parts: a portable cluster
 // (linear_split.cu) The product with the reduction of each 128 x tn tile split over `parts` CTAs.
 int launch_linear_split(const LinearProduct &q, int mode, int tn, int parts, cudaStream_t stream);
+// room[c]: clusters of c CTAs of the split kernel that the device holds at once.
+int split_room(int mode, int device, int (&room)[kMaxSplit + 1]);
+// Rows of the boxes that the split kernel loads A in: TMA spends its time by box rows, whether
+// they exist or not, so a few tokens load 8 at a time.
+inline int split_row_box(int64_t M) { return M <= 8 ? 8 : M <= 16 ? 16 : kRowBox; }
 // Tile rows of 128 that the split kernel launches: with groups, no more than one partial one each.
 inline int64_t split_tiles(const LinearProduct &q, int mode) {
     const int64_t rows = mode == kWgrad ? q.I : q.M;

@@ -1,6 +1,6 @@
 // linear_split.cu -- the linear operator's products when there are few tiles: the reduction of a
-// 128 x 64 or 128 x 128 tile is split over the CTAs of a cluster, which add their partial sums
-// through distributed shared memory.
+// tile of 128 rows and up to 128 columns is split over the CTAs of a cluster, which add their
+// partial sums through distributed shared memory.
 //
 // With few rows the product streams the weight once and is bound by HBM (one row: 1 flop a byte);
 // what matters is that every SM loads, with enough bytes in flight.  So: small tiles, two CTAs on
@@ -25,7 +25,11 @@ constexpr int kSplitMaxStages = 12;
 struct SplitShape {
     int a_bytes, stages;  // A's stage and their number
     int parts;            // CTAs of a cluster
+    int tn;               // columns of a tile: a multiple of 16, of 64 where B is MN-major
+    int row_box;          // rows of the boxes A is loaded in
 };
+
+constexpr uint32_t kSplitTmemCols = 128;
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     float4 v;
@@ -36,13 +40,13 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     return v;
 }
 
-template <int MODE, int TN>
+template <int MODE>
 __global__ void __launch_bounds__(kSplitThreads, 2)
     linear_split_kernel(const __grid_constant__ LinearMaps maps, const LinearParams p, const SplitShape q) {
     constexpr bool kAMn = MODE == kWgrad, kBMn = MODE != kFwd;
-    constexpr int kBBytes = TN * kBK * 2;
     constexpr uint32_t kBoxMn = 64 * kBK * 2;
-    constexpr int kPitch = TN + 4;  // floats from one row of the partial tile to the next: no bank conflicts
+    const int TN = q.tn, kBBytes = TN * kBK * 2;
+    const int kPitch = TN + 4;  // floats from one row of the partial tile to the next: no bank conflicts
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t *sA = ring, *sB = ring + q.stages * q.a_bytes;
@@ -67,7 +71,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         prefetch_tensormap(&maps.b);
     }
     if (warp == 1) {
-        tmem_alloc(tmem_holder, TN);
+        tmem_alloc(tmem_holder, kSplitTmemCols);
         tmem_relinquish();
     }
     if (warp == 2) {  // which tile
@@ -112,8 +116,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
             return false;
         };
         if (warp == 0 && lane == 0) {
-            const int boxes = kAMn ? 2 : (rows + kRowBox - 1) / kRowBox;
-            const uint32_t tx = (uint32_t)(boxes * (kAMn ? kBoxMn : kRowBox * kBK * 2) + kBBytes);
+            const int box_bytes = kAMn ? (int)kBoxMn : q.row_box * kBK * 2;
+            const int boxes = kAMn ? 2 : (rows + q.row_box - 1) / q.row_box;
+            const uint32_t tx = (uint32_t)(boxes * box_bytes + kBBytes);
             int s = 0;
             uint32_t ph = 1;
             for (int kb = kb0; kb < kb1; ++kb) {
@@ -122,7 +127,6 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
                 uint8_t *a = sA + s * q.a_bytes, *b = sB + s * kBBytes;
                 const int r0 = kb * kBK;
                 if (kBMn) {
-#pragma unroll
                     for (int c = 0; c < TN / 64; ++c)
                         tma_load_3d(b + c * kBoxMn, &maps.b, &full[s], tl.n0 + c * 64, r0, MODE == kWgrad ? 0 : tl.e);
                 } else {
@@ -134,7 +138,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
                         tma_load_3d(a + c * kBoxMn, &maps.a, &full[s], tl.m0 + c * 64, r0, 0);
                 } else {
                     for (int c = 0; c < boxes; ++c)
-                        tma_load_3d(a + c * (kRowBox * kBK * 2), &maps.a_small, &full[s], r0, tl.m0 + c * kRowBox, 0);
+                        tma_load_3d(a + c * box_bytes, &maps.a_small, &full[s], r0, tl.m0 + c * q.row_box, 0);
                 }
                 if (++s == q.stages) { s = 0; ph ^= 1u; }
             }
@@ -165,18 +169,19 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         if (lane == 0) ok = wait(done, 0);
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         tc_fence_after();
-        const int qrow = (warp & 3) * 32, row = qrow + lane, col0 = (warp >> 2) * (TN / 2);
-        if (ok && qrow < rows) {  // warps 0..3 the first half of the columns, 4..7 the second
+        const int qrow = (warp & 3) * 32, row = qrow + lane;
+        if (ok && qrow < rows) {  // warps 0..3 take the even 32-column chunks, 4..7 the odd ones
 #pragma unroll 1
-            for (int j = 0; j < TN / 64; ++j) {
+            for (int j = warp >> 2; j * 32 < TN; j += 2) {
                 uint32_t v[32];
-                tmem_ld_32x32b_x32(tmem + ((uint32_t)qrow << 16) + (uint32_t)(col0 + j * 32), v);
+                tmem_ld_32x32b_x32(tmem + ((uint32_t)qrow << 16) + (uint32_t)(j * 32), v);
                 tmem_wait_ld();
                 if (row < rows) {
-                    float4 *to = reinterpret_cast<float4 *>(part + row * kPitch + col0 + j * 32);
+                    float4 *to = reinterpret_cast<float4 *>(part + row * kPitch + j * 32);
+                    const int nc = TN - j * 32 >= 32 ? 8 : 4;  // TN is a multiple of 16
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
-                        to[c] = make_float4(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1]),
+                        if (c < nc) to[c] = make_float4(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1]),
                                             __uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3]));
                 }
             }
@@ -187,7 +192,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, TN);
+        tmem_dealloc(tmem, kSplitTmemCols);
     }
     if (q.parts > 1) cluster_sync();
     if (rows > 0) {
@@ -242,35 +247,68 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
 
 // ---------------------------------------------------------------- host side
 
-template <int MODE, int TN>
-static int split_launch(const LinearProduct &q, int parts, cudaStream_t stream) {
+struct SplitRoom {
+    bool done;
+    int room[kMaxSplit + 1];
+};
+
+// Sets the kernel's shared-memory limit and asks what fits, once per device.
+template <int MODE>
+static int split_setup(int dev, SplitRoom **out) {
     static std::mutex mu;
-    static bool done[kLinMaxDevices] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return cuda_fail(e);
+    static SplitRoom cached[kLinMaxDevices] = {};
     if (dev < 0 || dev >= kLinMaxDevices) return TGC_ERR_INVALID_ARG;
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        if (!done[dev]) {
-            e = cudaFuncSetAttribute(linear_split_kernel<MODE, TN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     kSplitSmem);
+    std::lock_guard<std::mutex> lock(mu);
+    SplitRoom &r = cached[dev];
+    if (!r.done) {
+        cudaError_t e = cudaFuncSetAttribute(linear_split_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kSplitSmem);
+        if (e != cudaSuccess) return cuda_fail(e);
+        for (int c = 1; c <= kMaxSplit; ++c) {
+            cudaLaunchConfig_t cfg{};
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = (unsigned)c;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.gridDim = dim3((unsigned)(c * 1024));
+            cfg.blockDim = dim3(kSplitThreads);
+            cfg.dynamicSmemBytes = kSplitSmem;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&r.room[c], linear_split_kernel<MODE>, &cfg);
             if (e != cudaSuccess) return cuda_fail(e);
-            done[dev] = true;
         }
+        r.done = true;
     }
-    LinearMaps maps;
-    if (!lin_maps(&maps, q, MODE, TN)) return TGC_ERR_CUDA;
-    LinearParams p{};
-    int rc = lin_params(&p, q, TN);
-    if (rc != TGC_OK) return rc;
+    *out = &r;
+    return TGC_OK;
+}
+
+int split_room(int mode, int device, int (&room)[kMaxSplit + 1]) {
+    SplitRoom *r = nullptr;
+    const int rc = mode == kFwd     ? split_setup<kFwd>(device, &r)
+                   : mode == kDgrad ? split_setup<kDgrad>(device, &r)
+                                    : split_setup<kWgrad>(device, &r);
+    if (rc == TGC_OK) std::memcpy(room, r->room, sizeof r->room);
+    return rc;
+}
+
+template <int MODE>
+static int split_launch(const LinearProduct &q, int tn, int parts, cudaStream_t stream) {
     const int64_t rows = MODE == kWgrad ? q.I : q.M;
     SplitShape s{};
     s.parts = parts;
-    // A's stage: the boxes of 32 rows that a tile can need (a group may fill one; kWgrad always does)
-    s.a_bytes = MODE == kWgrad || rows > 96 ? 16384 : (int)((rows + kRowBox - 1) / kRowBox) * kRowBox * kBK * 2;
-    s.stages = kSplitRing / (s.a_bytes + TN * kBK * 2);
+    s.tn = tn;
+    s.row_box = split_row_box(q.M);
+    // A's stage: the boxes that a tile can need (a group may fill it; kWgrad always does)
+    s.a_bytes = MODE == kWgrad || rows > 96 ? 16384 : (int)((rows + s.row_box - 1) / s.row_box) * s.row_box * kBK * 2;
+    s.stages = kSplitRing / (s.a_bytes + tn * kBK * 2);
     if (s.stages > kSplitMaxStages) s.stages = kSplitMaxStages;
+    LinearMaps maps;
+    if (!lin_maps(&maps, q, MODE, tn, s.row_box)) return TGC_ERR_CUDA;
+    LinearParams p{};
+    const int rc = lin_params(&p, q, tn);
+    if (rc != TGC_OK) return rc;
     const int64_t tiles = split_tiles(q, MODE) * p.num_n;
     if (tiles * parts >= (int64_t(1) << 31)) return TGC_ERR_INVALID_ARG;
     cudaLaunchConfig_t cfg{};
@@ -284,16 +322,14 @@ static int split_launch(const LinearProduct &q, int parts, cudaStream_t stream) 
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, linear_split_kernel<MODE, TN>, maps, p, s);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_split_kernel<MODE>, maps, p, s);
     return e == cudaSuccess ? TGC_OK : cuda_fail(e);
 }
 
 int launch_linear_split(const LinearProduct &q, int mode, int tn, int parts, cudaStream_t stream) {
-    if (tn == 64)
-        return mode == kFwd ? split_launch<kFwd, 64>(q, parts, stream)
-             : mode == kDgrad ? split_launch<kDgrad, 64>(q, parts, stream) : split_launch<kWgrad, 64>(q, parts, stream);
-    return mode == kFwd ? split_launch<kFwd, 128>(q, parts, stream)
-         : mode == kDgrad ? split_launch<kDgrad, 128>(q, parts, stream) : split_launch<kWgrad, 128>(q, parts, stream);
+    return mode == kFwd     ? split_launch<kFwd>(q, tn, parts, stream)
+           : mode == kDgrad ? split_launch<kDgrad>(q, tn, parts, stream)
+                            : split_launch<kWgrad>(q, tn, parts, stream);
 }
 
 }  // namespace tgc
