@@ -218,6 +218,8 @@ __global__ void __launch_bounds__(kTeamMax<T, VEC, NV>, kTeamBlocks<T, VEC, NV>)
     __shared__ float smem[2][1][32];
     int buf = 0;
     const int worker = blockIdx.x * blockDim.y + threadIdx.y;
+    stream_wait();
+    stream_release();
     if (worker >= p.workers) return;  // whole teams only: a block of one team, or warps that need no barrier
     const int m0 = (int)((int64_t)p.M * worker / p.workers), m1 = (int)((int64_t)p.M * (worker + 1) / p.workers);
     const int c0 = threadIdx.x * VEC, step = blockDim.x * VEC;
@@ -373,6 +375,8 @@ __global__ void __launch_bounds__(kTeamMax<T, VEC, NV>) norm_bwd_kernel(const No
         for (int i = threadIdx.x; i < 2 * NS * 32; i += blockDim.x) (&smem[0][0][0])[i] = 0.0f;
         __syncthreads();
     }
+    stream_wait();
+    stream_release();
     if (worker >= p.workers) return;
     const int c0 = threadIdx.x * VEC, step = blockDim.x * VEC;
     const int row_bytes = step * NV * (int)sizeof(T);  // of a stage: the row's, rounded up to the team's columns
@@ -684,6 +688,8 @@ struct NormSumParams {
 template <typename T>
 __global__ void __launch_bounds__(256) norm_sum_kernel(const NormSumParams p) {
     __shared__ alignas(16) float part[32][32];
+    stream_wait();
+    stream_release();
     const int which = blockIdx.y;
     const float *from;
     T *to;
@@ -773,26 +779,21 @@ static TeamShape team_shape(int64_t D, int es, bool vec) {
     return s;
 }
 
-template <typename T, int V, int NV>
-static void launch_norm_nv(const NormParams &p, bool bias, dim3 grid, dim3 block, cudaStream_t stream) {
-    if (bias) norm_kernel<T, V, NV, true><<<grid, block, 0, stream>>>(p);
-    else norm_kernel<T, V, NV, false><<<grid, block, 0, stream>>>(p);
-}
-
 template <typename T>
-static void launch_norm(const NormParams &p, const TeamShape &s, cudaStream_t stream) {
+static cudaError_t launch_norm(const NormParams &p, const TeamShape &s, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T);
     const dim3 block(s.team, s.teams), grid((unsigned)((p.workers + s.teams - 1) / s.teams));
     const bool bias = p.post_b != nullptr || p.pre_b != nullptr;
-    if (s.vec > 1) {
-        if (s.nv == 1) launch_norm_nv<T, V, 1>(p, bias, grid, block, stream);
-        else if (s.nv == 2) launch_norm_nv<T, V, 2>(p, bias, grid, block, stream);
-        else launch_norm_nv<T, V, 4>(p, bias, grid, block, stream);
-    } else {
-        if (s.nv == 1) launch_norm_nv<T, 1, 1>(p, bias, grid, block, stream);
-        else if (s.nv == 4) launch_norm_nv<T, 1, 4>(p, bias, grid, block, stream);
-        else launch_norm_nv<T, 1, 16>(p, bias, grid, block, stream);
-    }
+    void (*kernel)(NormParams);
+    if (s.vec > 1)
+        kernel = s.nv == 1   ? (bias ? norm_kernel<T, V, 1, true> : norm_kernel<T, V, 1, false>)
+                 : s.nv == 2 ? (bias ? norm_kernel<T, V, 2, true> : norm_kernel<T, V, 2, false>)
+                             : (bias ? norm_kernel<T, V, 4, true> : norm_kernel<T, V, 4, false>);
+    else
+        kernel = s.nv == 1   ? (bias ? norm_kernel<T, 1, 1, true> : norm_kernel<T, 1, 1, false>)
+                 : s.nv == 4 ? (bias ? norm_kernel<T, 1, 4, true> : norm_kernel<T, 1, 4, false>)
+                             : (bias ? norm_kernel<T, 1, 16, true> : norm_kernel<T, 1, 16, false>);
+    return launch_overlapped(kernel, grid, block, 0, 1, stream, p);
 }
 
 #define TGC_TRY(expr)                     \
@@ -837,10 +838,9 @@ static int norm_impl(tgc_block_norm_args a) {
     if (e != cudaSuccess) return cuda_fail(e);
     const int64_t room = (int64_t)sm_count(dev) * s.per_sm;
     p.workers = (int)(a.M < room ? a.M : room);
-    if (a.dtype == TGC_BF16) launch_norm<__nv_bfloat16>(p, s, a.stream);
-    else if (a.dtype == TGC_F16) launch_norm<__half>(p, s, a.stream);
-    else launch_norm<float>(p, s, a.stream);
-    e = cudaGetLastError();
+    e = a.dtype == TGC_BF16  ? launch_norm<__nv_bfloat16>(p, s, a.stream)
+        : a.dtype == TGC_F16 ? launch_norm<__half>(p, s, a.stream)
+                             : launch_norm<float>(p, s, a.stream);
     return e == cudaSuccess ? TGC_OK : cuda_fail(e);
 }
 
@@ -920,8 +920,8 @@ static int launch_norm_bwd_nv(const NormBwdParams &p, bool full, dim3 grid, dim3
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return cuda_fail(e);
     }
-    kernel<<<grid, block, smem, stream>>>(p);
-    return TGC_OK;
+    const cudaError_t e = launch_overlapped(kernel, grid, block, (size_t)smem, 1, stream, p);
+    return e == cudaSuccess ? TGC_OK : cuda_fail(e);
 }
 
 template <typename T>
@@ -939,8 +939,9 @@ static int launch_norm_bwd(const NormBwdParams &p, const NormSumParams &q, int n
            : s.nv == 4 ? launch_norm_bwd_nv<T, 1, 4>(p, full, grid, block, stream)
                        : launch_norm_bwd_nv<T, 1, 16>(p, full, grid, block, stream);
     if (rc != TGC_OK) return rc;
-    if (nsums > 0) norm_sum_kernel<T><<<dim3((unsigned)((p.D + 31) / 32), (unsigned)nsums), 256, 0, stream>>>(q);
-    const cudaError_t e = cudaGetLastError();
+    if (nsums == 0) return TGC_OK;
+    const cudaError_t e = launch_overlapped(norm_sum_kernel<T>, dim3((unsigned)((p.D + 31) / 32), (unsigned)nsums), dim3(256),
+                                            0, 1, stream, q);
     return e == cudaSuccess ? TGC_OK : cuda_fail(e);
 }
 

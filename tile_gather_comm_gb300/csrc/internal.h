@@ -32,6 +32,29 @@ int sm_count(int device);
 // bounded wait of theirs expires (read and cleared by tgc_async_status).
 int device_fault_word(int **word);
 
+// Launches a kernel whose start may overlap the end of the kernel before it in the stream: the
+// launch and the kernel's own set-up (barriers, TMEM, descriptors) then cost the stream nothing.
+// Every such kernel calls stream_wait() before it touches global memory, or, where its inputs
+// were complete before its predecessor started (`early`), before it ends.
+template <typename... P, typename... A>
+inline cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, int cluster,
+                                     cudaStream_t stream, A &&...args) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Launch the TGATHER kernel; arguments already validated.
 struct TGatherLaunch {
     const void *srcs[TGC_MAX_RANKS];

@@ -48,6 +48,8 @@ template <bool F16>
 __global__ void __launch_bounds__(256) dz_kernel(const DzParams p) {
     __shared__ float sums[8][32 * 8 + 8];
     __shared__ int s_rows[2];
+    stream_wait();
+    stream_release();
     const int strips = (p.N + 255) / 256;
     const int strip = (int)(blockIdx.x % (unsigned)strips), chunk = (int)(blockIdx.x / (unsigned)strips);
     const int cv = threadIdx.x % 32, rl = threadIdx.x / 32;
@@ -124,8 +126,10 @@ __global__ void __launch_bounds__(256) dz_kernel(const DzParams p) {
 
 // Sums each group's chunks in order: 32 columns x 8 chunk lanes a block, then the lanes in order.
 template <typename T>
-__global__ void __launch_bounds__(256) bias_sum_kernel(const float *partial, T *db, int M, int N, const int32_t *offsets) {
+__global__ void __launch_bounds__(256) bias_sum_kernel(const float *partial, T *db, int M, int N, const int32_t *offsets, int early) {
     __shared__ float part[8][32];
+    if (!early) stream_wait();
+    stream_release();
     const int e = blockIdx.y;
     int first = 0;  // this group's first chunk
     if (offsets != nullptr) {
@@ -154,6 +158,7 @@ __global__ void __launch_bounds__(256) bias_sum_kernel(const float *partial, T *
         for (int i = 1; i < 8; ++i) s += part[i][c];
         db[(int64_t)e * N + n] = from_f32<T>(s);
     }
+    if (early) stream_wait();
 }
 
 // ---------------------------------------------------------------- checks
@@ -291,20 +296,13 @@ static int linear_bwd_impl(tgc_linear_bwd_args a) {
         }
         if (a.dbias != nullptr) d.partial = reinterpret_cast<float *>(ws + l.partial);
         const unsigned grid = (unsigned)((a.N + 255) / 256 * l.chunks);
-        if (a.dtype == TGC_BF16) dz_kernel<false><<<grid, 256, 0, a.stream>>>(d);
-        else dz_kernel<true><<<grid, 256, 0, a.stream>>>(d);
-        if (a.dbias != nullptr) {
-            const dim3 g2((unsigned)((a.N + 31) / 32), (unsigned)groups);
-            if (a.dtype == TGC_BF16)
-                bias_sum_kernel<<<g2, 256, 0, a.stream>>>(d.partial, static_cast<__nv_bfloat16 *>(a.dbias), (int)a.M,
-                                                          (int)a.N, a.offsets);
-            else
-                bias_sum_kernel<<<g2, 256, 0, a.stream>>>(d.partial, static_cast<__half *>(a.dbias), (int)a.M, (int)a.N,
-                                                          a.offsets);
-        }
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_overlapped(a.dtype == TGC_BF16 ? dz_kernel<false> : dz_kernel<true>, dim3(grid),
+                                                dim3(256), 0, 1, a.stream, d);
         if (e != cudaSuccess) return cuda_fail(e);
     }
+    // The kernels from here on need only what is complete when the first of them starts, so the
+    // later ones need not wait for the earlier: they fill the SMs that those leave.
+    int early = 0;
     LinearProduct p{};
     p.a = dz; p.lda = lddz;
     p.M = a.M; p.J = a.K;
@@ -315,12 +313,26 @@ static int linear_bwd_impl(tgc_linear_bwd_args a) {
         p.R = a.N;
         p.y = a.dx; p.ldy = a.lddx;
         TGC_TRY(launch_linear(p, kDgrad, a.stream));
+        early = 1;
     }
     if (a.dw != nullptr) {
         p.b = a.x; p.ldb = a.ldx; p.b_stride = 0;
         p.I = a.N; p.R = 0;
         p.y = a.dw; p.ldy = a.K;
+        p.early = early;
         TGC_TRY(launch_linear(p, kWgrad, a.stream));
+        early = 1;
+    }
+    if (a.dbias != nullptr) {
+        const float *partial = reinterpret_cast<const float *>(ws + l.partial);
+        const dim3 grid((unsigned)((a.N + 31) / 32), (unsigned)groups);
+        const cudaError_t e =
+            a.dtype == TGC_BF16
+                ? launch_overlapped(bias_sum_kernel<__nv_bfloat16>, grid, dim3(256), 0, 1, a.stream, partial,
+                                    static_cast<__nv_bfloat16 *>(a.dbias), (int)a.M, (int)a.N, a.offsets, early)
+                : launch_overlapped(bias_sum_kernel<__half>, grid, dim3(256), 0, 1, a.stream, partial,
+                                    static_cast<__half *>(a.dbias), (int)a.M, (int)a.N, a.offsets, early);
+        if (e != cudaSuccess) return cuda_fail(e);
     }
     return TGC_OK;
 }

@@ -419,6 +419,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (CG == 1) { tmem_alloc(tmem_holder, kLinTmemCols); tmem_relinquish(); }
         else { tmem_alloc_pair(tmem_holder, kLinTmemCols); tmem_relinquish_pair(); }
     }
+    if (!p.early) stream_wait();
+    stream_release();
     if (warp == 2 && MODE != kWgrad) build_tile_table(p, C::kTM, tile0, lane);
     tc_fence_before();
     if (CG == 1) __syncthreads(); else cluster_sync();
@@ -446,6 +448,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (CG == 1) tmem_dealloc(tmem_base, kLinTmemCols);
         else tmem_dealloc_pair(tmem_base, kLinTmemCols);
     }
+    if (p.early) stream_wait();
 }
 
 // ---------------------------------------------------------------- host side
@@ -542,6 +545,7 @@ int lin_params(LinearParams *p, const LinearProduct &q, int tile_n) {
     p->ldres = q.ldres; p->ldy = q.ldy; p->ldz = q.ldz;
     p->act = q.act;
     p->f16 = q.f16;
+    p->early = q.early;
     p->timeout_ns = 4ull * 1000 * 1000 * 1000;
     return device_fault_word(&p->fault);
 }
@@ -568,18 +572,8 @@ static int lin_launch(const LinearProduct &q, int dev, int sms, cudaStream_t str
     }
     if (tiles >= (int64_t(1) << 31)) return TGC_ERR_INVALID_ARG;
     if (clusters > tiles) clusters = (int)tiles;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CG;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)(clusters * CG));
-    cfg.blockDim = dim3(kLinThreads);
-    cfg.dynamicSmemBytes = C::kSmem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_gemm_kernel<CG, MODE, TN>, maps, p);
+    const cudaError_t e = launch_overlapped(linear_gemm_kernel<CG, MODE, TN>, dim3((unsigned)(clusters * CG)),
+                                            dim3(kLinThreads), C::kSmem, CG, stream, maps, p);
     return e == cudaSuccess ? TGC_OK : cuda_fail(e);
 }
 

@@ -41,6 +41,7 @@ struct LinearParams {
     int64_t ldres, ldy, ldz;
     int act;
     int f16;
+    int early;            // inputs complete before the kernel before this one started
     int *fault;           // set when a wait expired
     uint64_t timeout_ns;
 };
@@ -57,6 +58,7 @@ struct LinearProduct {
     int64_t ldres, ldy, ldz;
     int act;
     int f16;
+    int early;           // see launch_overlapped
 };
 int launch_linear(const LinearProduct &q, int mode, cudaStream_t stream);
 

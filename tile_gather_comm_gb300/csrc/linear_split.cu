@@ -74,6 +74,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         tmem_alloc(tmem_holder, kSplitTmemCols);
         tmem_relinquish();
     }
+    if (!p.early) stream_wait();
+    stream_release();
     if (warp == 2) {  // which tile
         Tile tl;
         int pm, pn = t % p.num_n;
@@ -243,6 +245,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     }
     __syncwarp();
     if (q.parts > 1) cluster_sync();  // no CTA leaves while another reads its partial tile
+    if (p.early) stream_wait();
 }
 
 // ---------------------------------------------------------------- host side
@@ -311,18 +314,8 @@ static int split_launch(const LinearProduct &q, int tn, int parts, cudaStream_t 
     if (rc != TGC_OK) return rc;
     const int64_t tiles = split_tiles(q, MODE) * p.num_n;
     if (tiles * parts >= (int64_t(1) << 31)) return TGC_ERR_INVALID_ARG;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)parts;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)(tiles * parts));
-    cfg.blockDim = dim3(kSplitThreads);
-    cfg.dynamicSmemBytes = kSplitSmem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_split_kernel<MODE>, maps, p, s);
+    const cudaError_t e = launch_overlapped(linear_split_kernel<MODE>, dim3((unsigned)(tiles * parts)), dim3(kSplitThreads),
+                                            kSplitSmem, parts, stream, maps, p, s);
     return e == cudaSuccess ? TGC_OK : cuda_fail(e);
 }
 
