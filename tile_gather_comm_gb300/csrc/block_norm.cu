@@ -181,6 +181,8 @@ __device__ __forceinline__ void team_sum_many(float (&v)[N], float (*smem)[N][32
 // input fit beside each other: one thread asks for whole rows with bulk copies, two rows ahead.
 template <int VEC, int NV>
 constexpr bool kStaged = VEC > 1 && NV <= 2;
+template <int NV>
+constexpr int kFwdRows = NV == 1 ? 2 : 1;  // staged rows the forward kernel works on at a time
 template <int NV, bool FULL>
 constexpr int kBwdRows = NV == 1 && !FULL ? 2 : 1;  // rows the backward kernel works on at a time
 
@@ -205,116 +207,197 @@ struct NormParams {
     int64_t ldy, ldx, ldr, ldh;
     int post, pre;
     float res_scale, branch_scale, eps, inv_d;
+    int *fault;
 };
 
-// A worker (a team) takes a run of consecutive rows.  The weights stay in its registers, and a
-// row's y and x are asked for while the row before is still being reduced, so loads are in flight
-// all the time.  BIAS: some norm has a bias.
-template <typename T, int VEC, int NV, bool BIAS>
+// A worker (a team) takes a run of consecutive rows, kFwdRows at a time, so that one reduction
+// serves them all; the weights stay in its registers.  The next rows are on their way meanwhile:
+// to shared memory (staged), or to registers.  BIAS: some norm has a bias.
+// STAGED false: also the form for few rows, one a worker, where nothing is to be had ahead.
+template <typename T, int VEC, int NV, bool BIAS, bool STAGED>
 __global__ void __launch_bounds__(kTeamMax<T, VEC, NV>, kTeamBlocks<T, VEC, NV>) norm_kernel(const NormParams p) {
     using P = Pack<T, VEC>;
     using L = typename P::L;
     constexpr int NP = VEC > 1 ? VEC / 2 : 1;
-    __shared__ float smem[2][1][32];
+    constexpr int ROWS = STAGED ? kFwdRows<NV> : 1;
+    __shared__ float smem[2][ROWS][32];
+    __shared__ uint64_t bars[4][2];
+    extern __shared__ __align__(16) uint8_t staged[];  // a team's own: two stages of ROWS rows of y and x
     int buf = 0;
     const int worker = blockIdx.x * blockDim.y + threadIdx.y;
+    uint64_t *const bar = bars[threadIdx.y];
+    if (STAGED && threadIdx.x == 0) {
+        mbar_init(&bar[0], 1);
+        mbar_init(&bar[1], 1);
+        fence_mbarrier_init();
+    }
+    if (STAGED && blockDim.y == 1) __syncthreads(); else __syncwarp();
     stream_wait();
     stream_release();
     if (worker >= p.workers) return;  // whole teams only: a block of one team, or warps that need no barrier
     const int m0 = (int)((int64_t)p.M * worker / p.workers), m1 = (int)((int64_t)p.M * (worker + 1) / p.workers);
     const int c0 = threadIdx.x * VEC, step = blockDim.x * VEC;
-    P w1[NV], w2[NV], g[NV], b1[BIAS ? NV : 1], b2[BIAS ? NV : 1], py[NV], px[NV];
-    auto fetch = [&](P (&to)[NV], const void *base, int64_t at) {
+    const int row_bytes = step * NV * (int)sizeof(T);
+    uint8_t *const stages = staged + threadIdx.y * (STAGED ? 4 * ROWS * row_bytes : 0);
+    P w1[NV], w2[NV], g[NV], b1[BIAS ? NV : 1], b2[BIAS ? NV : 1];
+    P ny[STAGED ? 1 : NV], nx[STAGED ? 1 : NV];  // the next row, where it is not staged
+    auto fetch = [&](auto &to, const void *base, int64_t at) {
         if (base == nullptr) return;
 #pragma unroll
         for (int k = 0; k < NV; ++k)
             if (c0 + k * step < p.D) to[k] = load_pack<T, VEC>(base, at + c0 + k * step);
     };
+    auto ask = [&](int m, int stage) {
+        if (m >= m1) return;
+        const int rows = m1 - m < ROWS ? m1 - m : ROWS;
+        const uint32_t bytes = (uint32_t)(p.D * (int)sizeof(T));
+        mbar_arrive_expect_tx(&bar[stage], bytes * rows * (p.x != nullptr ? 2 : 1));
+        for (int r = 0; r < rows; ++r) {
+            uint8_t *to = stages + (stage * ROWS + r) * 2 * row_bytes;
+            bulk_g2s(to, static_cast<const T *>(p.y) + (m + r) * p.ldy, bytes, &bar[stage]);
+            if (p.x != nullptr) bulk_g2s(to + row_bytes, static_cast<const T *>(p.x) + (m + r) * p.ldx, bytes, &bar[stage]);
+        }
+    };
+    if constexpr (STAGED) {
+        if (threadIdx.x == 0) {
+            ask(m0, 0);
+            ask(m0 + ROWS, 1);
+        }
+    } else {
+        fetch(ny, p.y, m0 * p.ldy);
+        fetch(nx, p.x, m0 * p.ldx);
+    }
     fetch(w1, p.post_w, 0);
     fetch(w2, p.pre_w, 0);
     if constexpr (BIAS) {
         fetch(b1, p.post_b, 0);
         fetch(b2, p.pre_b, 0);
     }
-    fetch(py, p.y, m0 * p.ldy);
-    fetch(px, p.x, m0 * p.ldx);
     int seg = -1;
-    for (int m = m0; m < m1; ++m) {
-        if (p.gate != nullptr && m / p.rows_per_gate != seg) {
-            seg = m / p.rows_per_gate;
-            fetch(g, p.gate, (int64_t)seg * p.D);
-        }
-        L v[NV][NP];  // columns past the row's end stay zeros
+    uint32_t turn = 0;
+    for (int m = m0; m < m1; m += ROWS, ++turn) {
+        const uint32_t stage = turn & 1u;
+        const uint8_t *const here = stages + stage * ROWS * 2 * row_bytes;
+        if constexpr (STAGED) row_wait(&bar[stage], (turn >> 1) & 1u, p.fault);
+        L v[ROWS][NV][NP];  // columns past the row's end, and rows past the last, stay zeros
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
+        for (int rr = 0; rr < ROWS; ++rr)
 #pragma unroll
-            for (int i = 0; i < NP; ++i) v[k][i] = c0 + k * step < p.D ? py[k].get(i) : every<L>(0.0f);
-        if (m + 1 < m1) fetch(py, p.y, (m + 1) * p.ldy);
-        // v := its deviations from the mean (layer); the reciprocal deviation
-        auto stats = [&](int kind) -> float {
+            for (int k = 0; k < NV; ++k) {
+                P py;
+                const bool in = c0 + k * step < p.D && (ROWS == 1 || m + rr < m1);
+                if constexpr (STAGED)
+                    py = *reinterpret_cast<const P *>(here + rr * 2 * row_bytes + (c0 + k * step) * (int)sizeof(T));
+                else py = ny[k];
+#pragma unroll
+                for (int i = 0; i < NP; ++i) v[rr][k][i] = in ? py.get(i) : every<L>(0.0f);
+            }
+        if constexpr (!STAGED)
+            if (m + 1 < m1) fetch(ny, p.y, (m + 1) * p.ldy);
+        // v := its deviations from the mean (layer); the reciprocal deviations
+        auto stats = [&](int kind, float (&rstd)[ROWS]) {
+            float s[ROWS];
             if (kind == TGC_NORM_LAYER) {
+#pragma unroll
+                for (int rr = 0; rr < ROWS; ++rr) {
+                    L t = every<L>(0.0f);
+#pragma unroll
+                    for (int k = 0; k < NV; ++k)
+#pragma unroll
+                        for (int i = 0; i < NP; ++i) t = add(t, v[rr][k][i]);
+                    s[rr] = total(t);
+                }
+                team_sum(s, smem, &buf);
+#pragma unroll
+                for (int rr = 0; rr < ROWS; ++rr) {
+                    const L mean = every<L>(-s[rr] * p.inv_d);
+#pragma unroll
+                    for (int k = 0; k < NV; ++k)
+                        if (c0 + k * step < p.D)
+#pragma unroll
+                            for (int i = 0; i < NP; ++i) v[rr][k][i] = add(v[rr][k][i], mean);
+                }
+            }
+#pragma unroll
+            for (int rr = 0; rr < ROWS; ++rr) {
                 L t = every<L>(0.0f);
 #pragma unroll
                 for (int k = 0; k < NV; ++k)
 #pragma unroll
-                    for (int i = 0; i < NP; ++i) t = add(t, v[k][i]);
-                float s[1] = {total(t)};
-                team_sum(s, smem, &buf);
-                const L mean = every<L>(-s[0] * p.inv_d);
-#pragma unroll
-                for (int k = 0; k < NV; ++k)
-                    if (c0 + k * step < p.D)
-#pragma unroll
-                        for (int i = 0; i < NP; ++i) v[k][i] = add(v[k][i], mean);
+                    for (int i = 0; i < NP; ++i) t = fma(v[rr][k][i], v[rr][k][i], t);
+                s[rr] = total(t);
             }
-            L t = every<L>(0.0f);
+            team_sum(s, smem, &buf);
 #pragma unroll
-            for (int k = 0; k < NV; ++k)
-#pragma unroll
-                for (int i = 0; i < NP; ++i) t = fma(v[k][i], v[k][i], t);
-            float q[1] = {total(t)};
-            team_sum(q, smem, &buf);
-            return rsqrtf(q[0] * p.inv_d + p.eps);
+            for (int rr = 0; rr < ROWS; ++rr) rstd[rr] = rsqrtf(s[rr] * p.inv_d + p.eps);
         };
-        auto affine = [&](float scale, const void *w, const P (&pw)[NV], const void *b, const auto &pb) {
+        auto affine = [&](L (&x)[NV][NP], float scale, const void *w, const P (&pw)[NV], const void *b, const auto &pb) {
             const L sc = every<L>(scale);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
 #pragma unroll
-                for (int i = 0; i < NP; ++i) v[k][i] = mul(v[k][i], sc);
+                for (int i = 0; i < NP; ++i) x[k][i] = mul(x[k][i], sc);
                 if (w != nullptr)
 #pragma unroll
-                    for (int i = 0; i < NP; ++i) v[k][i] = mul(v[k][i], pw[k].get(i));
+                    for (int i = 0; i < NP; ++i) x[k][i] = mul(x[k][i], pw[k].get(i));
                 if constexpr (BIAS) {
                     if (b != nullptr)
 #pragma unroll
-                        for (int i = 0; i < NP; ++i) v[k][i] = add(v[k][i], pb[k].get(i));
+                        for (int i = 0; i < NP; ++i) x[k][i] = add(x[k][i], pb[k].get(i));
                 }
             }
         };
-        if (p.post != TGC_NORM_NONE) affine(stats(p.post), p.post_w, w1, p.post_b, b1);
+        float rstd[ROWS];
+        if (p.post != TGC_NORM_NONE) stats(p.post, rstd);
         const L cs = every<L>(p.branch_scale), rs = every<L>(p.res_scale);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
+        for (int rr = 0; rr < ROWS; ++rr) {
+            if (ROWS > 1 && m + rr >= m1) break;
+            if (p.gate != nullptr && (m + rr) / p.rows_per_gate != seg) {
+                seg = (m + rr) / p.rows_per_gate;
+                fetch(g, p.gate, (int64_t)seg * p.D);
+            }
+            if (p.post != TGC_NORM_NONE) affine(v[rr], rstd[rr], p.post_w, w1, p.post_b, b1);
 #pragma unroll
-            for (int i = 0; i < NP; ++i) v[k][i] = mul(v[k][i], cs);
-            if (p.gate != nullptr)
+            for (int k = 0; k < NV; ++k) {
+                const int c = c0 + k * step;
 #pragma unroll
-                for (int i = 0; i < NP; ++i) v[k][i] = mul(v[k][i], g[k].get(i));
-            if (p.x != nullptr)
+                for (int i = 0; i < NP; ++i) v[rr][k][i] = mul(v[rr][k][i], cs);
+                if (p.gate != nullptr)
 #pragma unroll
-                for (int i = 0; i < NP; ++i) v[k][i] = fma(px[k].get(i), rs, v[k][i]);
-            if (c0 + k * step >= p.D)
+                    for (int i = 0; i < NP; ++i) v[rr][k][i] = mul(v[rr][k][i], g[k].get(i));
+                if (p.x != nullptr) {
+                    P px;
+                    if constexpr (STAGED)
+                        px = *reinterpret_cast<const P *>(here + (rr * 2 + 1) * row_bytes + c * (int)sizeof(T));
+                    else px = nx[k];
 #pragma unroll
-                for (int i = 0; i < NP; ++i) v[k][i] = every<L>(0.0f);
-            else if (p.r != nullptr) store_pack<T, VEC>(p.r, m * p.ldr + c0 + k * step, v[k]);
+                    for (int i = 0; i < NP; ++i) v[rr][k][i] = fma(px.get(i), rs, v[rr][k][i]);
+                }
+                if (c >= p.D)
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) v[rr][k][i] = every<L>(0.0f);
+                else if (p.r != nullptr) store_pack<T, VEC>(p.r, (m + rr) * p.ldr + c, v[rr][k]);
+            }
         }
-        if (m + 1 < m1) fetch(px, p.x, (m + 1) * p.ldx);
+        if constexpr (!STAGED)
+            if (m + 1 < m1) fetch(nx, p.x, (m + 1) * p.ldx);
+        if (p.pre != TGC_NORM_NONE) stats(p.pre, rstd);
+        else if (STAGED && blockDim.y == 1) __syncthreads();
+        if constexpr (STAGED) {
+            // past the sum (or the barrier) every thread has read this stage
+            __syncwarp();
+            if (threadIdx.x == 0) ask(m + 2 * ROWS, (int)stage);
+        }
         if (p.pre == TGC_NORM_NONE) continue;
-        affine(stats(p.pre), p.pre_w, w2, p.pre_b, b2);
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-            if (c0 + k * step < p.D) store_pack<T, VEC>(p.h, m * p.ldh + c0 + k * step, v[k]);
+        for (int rr = 0; rr < ROWS; ++rr) {
+            if (ROWS > 1 && m + rr >= m1) break;
+            affine(v[rr], rstd[rr], p.pre_w, w2, p.pre_b, b2);
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                if (c0 + k * step < p.D) store_pack<T, VEC>(p.h, (m + rr) * p.ldh + c0 + k * step, v[rr][k]);
+        }
     }
 }
 
@@ -443,6 +526,25 @@ __global__ void __launch_bounds__(kTeamMax<T, VEC, NV>) norm_bwd_kernel(const No
             if (ask_unit < p.units) unit_rows(ask_unit, &ask_m, &ask_end);
         }
     };
+    // Rows that are not staged come from memory, the next ones while the last are worked on where
+    // there are registers for them.
+    constexpr bool AHEAD = !STAGED && NV <= 4;
+    auto from_memory = [&](int j, int m, int m1, int k) {
+        P v;
+        const int c = c0 + k * step;
+        if (in[j] != nullptr && c < p.D && m < m1) v = load_pack<T, VEC>(in[j], m * ld[j] + c);
+        else v.clear();
+        return v;
+    };
+    P next[4][AHEAD ? ROWS : 1][AHEAD ? NV : 1];
+    auto fetch_next = [&](int m, int m1) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int rr = 0; rr < (AHEAD ? ROWS : 1); ++rr)
+#pragma unroll
+                for (int k = 0; k < (AHEAD ? NV : 1); ++k) next[j][rr][k] = from_memory(j, m + rr, m1, k);
+    };
     if constexpr (STAGED) {
         // an input that is not there reads as zeros
         for (int i = threadIdx.x * 16; i < 8 * ROWS * row_bytes; i += blockDim.x * 16)
@@ -493,6 +595,7 @@ __global__ void __launch_bounds__(kTeamMax<T, VEC, NV>) norm_bwd_kernel(const No
                 read_lanes(fb + c0 + k * step, b);
             }
         };
+        if constexpr (AHEAD) fetch_next(m0, m1);
         for (int m = m0; m < m1; m += ROWS) {
             const uint32_t stage = turn & 1u;
             P pr[ROWS][NV], pd[ROWS][NV], py[ROWS][NV], pt[ROWS][NV];
@@ -501,13 +604,11 @@ __global__ void __launch_bounds__(kTeamMax<T, VEC, NV>) norm_bwd_kernel(const No
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
                     const int c = c0 + k * step;
-                    if constexpr (STAGED) {
+                    if constexpr (STAGED)
                         to[k] = *reinterpret_cast<const P *>(stages + ((stage * ROWS + rr) * 4 + j) * row_bytes +
                                                              c * (int)sizeof(T));
-                    } else {
-                        if (in[j] != nullptr && c < p.D && m + rr < m1) to[k] = load_pack<T, VEC>(in[j], (m + rr) * ld[j] + c);
-                        else to[k].clear();
-                    }
+                    else if constexpr (AHEAD) to[k] = next[j][rr][k];
+                    else to[k] = from_memory(j, m + rr, m1, k);
                 }
             };
 #pragma unroll
@@ -517,6 +618,7 @@ __global__ void __launch_bounds__(kTeamMax<T, VEC, NV>) norm_bwd_kernel(const No
                 fetch(py[rr], rr, 2);
                 fetch(pt[rr], rr, 3);
             }
+            if constexpr (AHEAD) fetch_next(m + ROWS, m1);
             L mean_r = every<L>(0.0f), mean_y = every<L>(0.0f);  // negated
             if constexpr (FULL) {
                 if (p.pre == TGC_NORM_LAYER || p.post == TGC_NORM_LAYER) {
@@ -684,10 +786,11 @@ struct NormSumParams {
     int D, workers, units_per_gate;
 };
 
-// 32 columns a block: 8 threads of 4 columns x 32 lanes over the partials, then the lanes in order.
+// 32 columns a block: 8 threads of 4 columns x 32 or 64 lanes over the partials, then the lanes in
+// a fixed order.
 template <typename T>
-__global__ void __launch_bounds__(256) norm_sum_kernel(const NormSumParams p) {
-    __shared__ alignas(16) float part[32][32];
+__global__ void __launch_bounds__(512) norm_sum_kernel(const NormSumParams p) {
+    __shared__ alignas(16) float part[64][36];
     stream_wait();
     stream_release();
     const int which = blockIdx.y;
@@ -705,19 +808,20 @@ __global__ void __launch_bounds__(256) norm_sum_kernel(const NormSumParams p) {
         to = static_cast<T *>(p.dgate) + g * p.D;
         n = p.units_per_gate;
     }
+    const int lanes = blockDim.x / 8, warps = blockDim.x / 32;
     const int q = threadIdx.x % 8, l = threadIdx.x / 8, c = blockIdx.x * 32 + q * 4;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (p.D % 4 == 0) {
         if (c < p.D) {
 #pragma unroll 8
-            for (int i = l; i < n; i += 32) {
+            for (int i = l; i < n; i += lanes) {
                 const float4 f = *reinterpret_cast<const float4 *>(from + (int64_t)i * p.D + c);
                 s.x += f.x; s.y += f.y; s.z += f.z; s.w += f.w;
             }
         }
     } else {
 #pragma unroll 4
-        for (int i = l; i < n; i += 32) {
+        for (int i = l; i < n; i += lanes) {
             const float *f = from + (int64_t)i * p.D + c;
             if (c < p.D) s.x += f[0];
             if (c + 1 < p.D) s.y += f[1];
@@ -727,12 +831,12 @@ __global__ void __launch_bounds__(256) norm_sum_kernel(const NormSumParams p) {
     }
     *reinterpret_cast<float4 *>(&part[l][q * 4]) = s;
     __syncthreads();
-    const int col = blockIdx.x * 32 + threadIdx.x;
-    if (threadIdx.x < 32 && col < p.D) {
-        float t = 0.0f;
+    for (int col = threadIdx.x / 32; col < 32; col += warps) {
+        const int lane = threadIdx.x % 32;
+        float t = part[lane][col] + (lanes > 32 ? part[lane + 32][col] : 0.0f);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) t += part[i][threadIdx.x];
-        to[col] = from_f32<T>(t);
+        for (int d = 16; d > 0; d /= 2) t += __shfl_xor_sync(0xffffffffu, t, d);
+        if (lane == 0 && blockIdx.x * 32 + col < p.D) to[blockIdx.x * 32 + col] = from_f32<T>(t);
     }
 }
 
@@ -779,21 +883,33 @@ static TeamShape team_shape(int64_t D, int es, bool vec) {
     return s;
 }
 
+template <typename T, int V, int NV, bool STAGED>
+static int launch_norm_nv(const NormParams &p, bool bias, dim3 grid, dim3 block, cudaStream_t stream) {
+    if constexpr (STAGED)
+        if (p.M <= p.workers) return launch_norm_nv<T, V, NV, false>(p, bias, grid, block, stream);
+    auto kernel = bias ? norm_kernel<T, V, NV, true, STAGED> : norm_kernel<T, V, NV, false, STAGED>;
+    // two stages of y and x
+    const int smem = STAGED ? (int)(block.x * block.y) * V * NV * 4 * kFwdRows<NV> * (int)sizeof(T) : 0;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    const cudaError_t e = launch_overlapped(kernel, grid, block, (size_t)smem, 1, stream, p);
+    return e == cudaSuccess ? TGC_OK : cuda_fail(e);
+}
+
 template <typename T>
-static cudaError_t launch_norm(const NormParams &p, const TeamShape &s, cudaStream_t stream) {
+static int launch_norm(const NormParams &p, const TeamShape &s, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T);
     const dim3 block(s.team, s.teams), grid((unsigned)((p.workers + s.teams - 1) / s.teams));
     const bool bias = p.post_b != nullptr || p.pre_b != nullptr;
-    void (*kernel)(NormParams);
     if (s.vec > 1)
-        kernel = s.nv == 1   ? (bias ? norm_kernel<T, V, 1, true> : norm_kernel<T, V, 1, false>)
-                 : s.nv == 2 ? (bias ? norm_kernel<T, V, 2, true> : norm_kernel<T, V, 2, false>)
-                             : (bias ? norm_kernel<T, V, 4, true> : norm_kernel<T, V, 4, false>);
-    else
-        kernel = s.nv == 1   ? (bias ? norm_kernel<T, 1, 1, true> : norm_kernel<T, 1, 1, false>)
-                 : s.nv == 4 ? (bias ? norm_kernel<T, 1, 4, true> : norm_kernel<T, 1, 4, false>)
-                             : (bias ? norm_kernel<T, 1, 16, true> : norm_kernel<T, 1, 16, false>);
-    return launch_overlapped(kernel, grid, block, 0, 1, stream, p);
+        return s.nv == 1   ? launch_norm_nv<T, V, 1, kStaged<V, 1>>(p, bias, grid, block, stream)
+               : s.nv == 2 ? launch_norm_nv<T, V, 2, kStaged<V, 2>>(p, bias, grid, block, stream)
+                           : launch_norm_nv<T, V, 4, kStaged<V, 4>>(p, bias, grid, block, stream);
+    return s.nv == 1   ? launch_norm_nv<T, 1, 1, kStaged<1, 1>>(p, bias, grid, block, stream)
+           : s.nv == 4 ? launch_norm_nv<T, 1, 4, kStaged<1, 4>>(p, bias, grid, block, stream)
+                       : launch_norm_nv<T, 1, 16, kStaged<1, 16>>(p, bias, grid, block, stream);
 }
 
 #define TGC_TRY(expr)                     \
@@ -838,14 +954,14 @@ static int norm_impl(tgc_block_norm_args a) {
     if (e != cudaSuccess) return cuda_fail(e);
     const int64_t room = (int64_t)sm_count(dev) * s.per_sm;
     p.workers = (int)(a.M < room ? a.M : room);
-    e = a.dtype == TGC_BF16  ? launch_norm<__nv_bfloat16>(p, s, a.stream)
-        : a.dtype == TGC_F16 ? launch_norm<__half>(p, s, a.stream)
-                             : launch_norm<float>(p, s, a.stream);
-    return e == cudaSuccess ? TGC_OK : cuda_fail(e);
+    TGC_TRY(device_fault_word(&p.fault));
+    return a.dtype == TGC_BF16  ? launch_norm<__nv_bfloat16>(p, s, a.stream)
+           : a.dtype == TGC_F16 ? launch_norm<__half>(p, s, a.stream)
+                                : launch_norm<float>(p, s, a.stream);
 }
 
 // How the backward pass deals its rows: a worker for every team that the card's 152 SMs hold at
-// once (one of 512 threads with 128 registers each, more for narrow rows), units of at least 4 rows, and whole gate segments where there are enough.  It
+// once (one of 512 threads with 128 registers each, more for narrow rows), units of at least 2 rows, and whole gate segments where there are enough.  It
 // goes by D and the type alone, so the workspace's size does not depend on the pointers.
 struct NormPlan {
     int segments, rows_per_gate, units_per_gate, unit_rows, units, workers;
@@ -859,7 +975,7 @@ static NormPlan norm_plan(const tgc_block_norm_bwd_args &a) {
     q.segments = a.gate != nullptr ? (int)a.gates : 1;
     q.rows_per_gate = (int)(a.M / q.segments);
     int64_t upg = (target + q.segments - 1) / q.segments;
-    const int64_t most = (q.rows_per_gate + 3) / 4;
+    const int64_t most = (q.rows_per_gate + 1) / 2;
     if (upg > most) upg = most;
     q.unit_rows = (int)((q.rows_per_gate + upg - 1) / upg);
     q.units_per_gate = (q.rows_per_gate + q.unit_rows - 1) / q.unit_rows;
@@ -940,7 +1056,8 @@ static int launch_norm_bwd(const NormBwdParams &p, const NormSumParams &q, int n
                        : launch_norm_bwd_nv<T, 1, 16>(p, full, grid, block, stream);
     if (rc != TGC_OK) return rc;
     if (nsums == 0) return TGC_OK;
-    const cudaError_t e = launch_overlapped(norm_sum_kernel<T>, dim3((unsigned)((p.D + 31) / 32), (unsigned)nsums), dim3(256),
+    const int threads = q.workers > 200 || q.units_per_gate > 200 ? 512 : 256;
+    const cudaError_t e = launch_overlapped(norm_sum_kernel<T>, dim3((unsigned)((p.D + 31) / 32), (unsigned)nsums), dim3(threads),
                                             0, 1, stream, q);
     return e == cudaSuccess ? TGC_OK : cuda_fail(e);
 }
