@@ -159,15 +159,3 @@ def test_the_binding_refuses_host_tensors():
         tgc.tgc_linear(x, w, y)
     with pytest.raises(ValueError):
         tgc.tgc_block_norm(x, y, y)
-
-
-@pytest.mark.parametrize("shape,dtype,stride", [((3, 8), torch.float32, None), ((2, 8), torch.bfloat16, None),
-                                                ((2, 8), torch.float32, (1, 2))])
-def test_the_binding_checks_operands(shape, dtype, stride):
-    t = torch.zeros(64, dtype=dtype)[:shape[0] * shape[1]].view(shape)
-    if stride:
-        t = torch.as_strided(torch.zeros(64, dtype=dtype), shape, stride)
-    with pytest.raises(ValueError):
-        _lib._rows(t, (2, 8), torch.float32, "t")
-    with pytest.raises(ValueError):
-        _lib._offsets(torch.zeros(4, dtype=torch.int64))

@@ -1,4 +1,5 @@
-"""Build libtgc.so in-tree with nvcc for sm_103a (no torch extension machinery).
+"""Build libtgc.so in-tree with nvcc for sm_103a (no torch extension machinery), and _ops.so, the
+native argument marshalling, with g++ against Python's and torch's headers.
 
 Each translation unit under csrc/ is compiled in parallel to an object file,
 then nvcc links them into ``tile_gather_comm_gb300/libtgc.so`` with the CUDA
@@ -18,6 +19,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libtgc.so")
+OPS = os.path.join(PKG, "_ops.so")
 SOURCES = ["api.cu", "tgather.cu", "gemm.cu", "noalloc.cu", "ipc.cu", "linear.cu", "linear_gemm.cu", "linear_split.cu", "block_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -37,16 +39,40 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(OPS):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(OPS))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     if not force and up_to_date():
         return LIB
-    return _compile(os.path.join(PKG, "_build"), LIB, [], verbose, ptxas_info)
+    with concurrent.futures.ThreadPoolExecutor(1) as ex:
+        ops = ex.submit(_compile_ops)
+        lib = _compile(os.path.join(PKG, "_build"), LIB, [], verbose, ptxas_info)
+        ops.result()
+    return lib
+
+
+def _compile_ops() -> None:
+    """_ops.so: host code only, against the headers of the Python and torch that run this."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = OPS + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), os.path.join(CSRC, "binding.cpp"), "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, OPS)
 
 
 def build_variant(out_dir: str, defines: dict) -> str:

@@ -13,6 +13,7 @@ import os
 import torch
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtgc.so")
+OPS_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_ops.so")
 
 TGC_OK = 0
 TGC_ERR_INVALID_ARG = -1
@@ -401,85 +402,32 @@ def tgc_ag_matmul_schedule(M: int, N: int, comm_block_rows: int, nranks: int, ra
 
 # ----------------------------------------------------------------------------- transformer-block operators
 
+# The marshalling of these is native (csrc/binding.cpp): operands are checked there -- device,
+# type, shape, inner stride; ValueError where they do not fit -- and passed on.
 
-def _rows(t, shape, dtype, name: str):
-    """(address, row stride) of a 2-D operand whose rows are contiguous; (None, 0) for None.
-    A tensor of another shape, type or inner stride raises ValueError: the C entry point sees
-    only the address."""
-    if t is None:
-        return None, 0
-    if t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{name}: expected {dtype} of shape {tuple(shape)}, got {t.dtype} of {tuple(t.shape)}")
-    ld, one = t.stride()
-    if one != 1 and shape[1] > 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return t.data_ptr(), ld if shape[0] > 1 else 0
+_ops = None
 
 
-def _dense(t, shape, dtype, name: str):
-    """Address of a contiguous operand of exactly this shape; None for None."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: expected contiguous {dtype} of shape {shape}, got {t.dtype} of {tuple(t.shape)}"
-                         f" with strides {t.stride()}")
-    return t.data_ptr()
+def _native():
+    """The _ops module, bound to the loaded library (raises if it is not built)."""
+    global _ops
+    if _ops is None:
+        L = lib()
+        try:
+            from . import _ops as m
+        except ImportError as e:
+            raise ImportError(f"{OPS_PATH} is not built for this Python and torch; run "
+                              "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+        m.bind(*[ctypes.cast(getattr(L, n), _vp).value for n in (
+            "tgc_linear", "tgc_linear_bwd", "tgc_linear_bwd_workspace_bytes", "tgc_block_norm", "tgc_block_norm_bwd",
+            "tgc_block_norm_bwd_workspace_bytes")])
+        _ops = m
+    return _ops
 
 
-def _weight(w, K: int, dtype, ngroups: int):
-    """(address, N, row stride, expert stride) of a (N, K) or, with groups, (ngroups, N, K) weight."""
-    dims = 3 if ngroups else 2
-    if w.dtype != dtype or w.dim() != dims or w.shape[-1] != K or (ngroups and w.shape[0] != ngroups):
-        raise ValueError(f"w: expected {dtype} of shape {(ngroups, 'N', K) if ngroups else ('N', K)}, got {w.dtype} "
-                         f"of {tuple(w.shape)}")
-    st = w.stride()
-    if K > 1 and st[-1] != 1:
-        raise ValueError("w: the last dimension must be contiguous")
-    N = w.shape[-2]
-    return w.data_ptr(), N, st[-2] if N > 1 else 0, st[0] if ngroups > 1 else 0
-
-
-def _offsets(offsets):
-    """(address, number of groups) of the experts' row offsets; (None, 0) for None."""
-    if offsets is None:
-        return None, 0
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 or not offsets.is_contiguous():
-        raise ValueError("offsets: expected contiguous int32 of ngroups + 1 row numbers")
-    return offsets.data_ptr(), offsets.numel() - 1
-
-
-def _device(*ts) -> int:
-    """Index of the device every operand lives on, which must be the current one (addresses are
-    all the library gets)."""
-    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
-    for t in ts:
-        if t is not None and (dev < 0 or t.get_device() != dev):
-            raise ValueError(f"operands must be CUDA tensors on the current device, got one on {t.device}")
-    return dev
-
-
-def _stream_of(stream, dev: int) -> int:
-    """Address of `stream`, by default torch's current one (read without the Stream object, whose
-    making costs more than the launch)."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return stream if isinstance(stream, int) else stream.cuda_stream
-
-
-def _workspace(workspace, nbytes: int, like, stream):
-    """The caller's workspace, or one from torch's allocator that belongs to the call's stream."""
-    if workspace is not None:
-        _device(like, workspace)
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-        return workspace, workspace.numel() * workspace.element_size()
-    if nbytes == 0:
-        return None, 0
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=like.device), nbytes
-    s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
-    with torch.cuda.stream(s):
-        return torch.empty(nbytes, dtype=torch.uint8, device=like.device), nbytes
+def _address(stream):
+    """A stream's address for _ops; None stays None (torch's current stream)."""
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
 def tgc_linear(x, w, y, *, bias=None, act: str = "none", residual=None, z=None, offsets=None, stream=None,
@@ -487,20 +435,7 @@ def tgc_linear(x, w, y, *, bias=None, act: str = "none", residual=None, z=None, 
     """y = act(x @ w^T + bias) + residual (bf16 or f16), z receiving the pre-activation; with
     ``offsets`` (int32, ngroups + 1) the product grouped by expert: w is (ngroups, N, K), bias
     (ngroups, N).  Asynchronous on ``stream``."""
-    dev = _device(x, w, y, bias, residual, z, offsets)
-    if x.dim() != 2:
-        raise ValueError("x: expected (M, K)")
-    M, K = x.shape
-    off, ngroups = _offsets(offsets)
-    pw, N, ldw, w_stride = _weight(w, K, x.dtype, ngroups)
-    mn = (M, N)
-    px, ldx = _rows(x, x.shape, x.dtype, "x")
-    py, ldy = _rows(y, mn, x.dtype, "y")
-    pr, ldres = _rows(residual, mn, x.dtype, "residual")
-    pz, ldz = _rows(z, mn, x.dtype, "z")
-    a = LinearArgs(px, pw, _dense(bias, (ngroups, N) if ngroups else (N,), x.dtype, "bias"), pr, py, pz, M, K, N,
-                   ldx, ldw, ldres, ldy, ldz, w_stride, DTYPES[x.dtype], ACTS[act], off, ngroups, _stream_of(stream, dev))
-    rc = lib().tgc_linear(ctypes.byref(a))
+    rc = (_ops or _native()).linear(x, w, y, bias, ACTS[act], residual, z, offsets, _address(stream))
     return _check(rc, "tgc_linear") if check else rc
 
 
@@ -510,24 +445,7 @@ def tgc_linear_bwd(dy, x, w, *, z=None, act: str = "none", dx=None, dw=None, dbi
     dx = dz @ w, dw = dz^T @ x, dbias = dz summed over rows.  The residual's gradient is dy.
     ``workspace``: a contiguous CUDA tensor of tgc_linear_bwd_workspace_bytes' size, by default
     taken from torch's allocator.  Asynchronous on ``stream``."""
-    dev = _device(dy, x, w, z, dx, dw, dbias, offsets)
-    if x.dim() != 2:
-        raise ValueError("x: expected (M, K)")
-    M, K = x.shape
-    off, ngroups = _offsets(offsets)
-    pw, N, ldw, w_stride = _weight(w, K, x.dtype, ngroups)
-    lead = (ngroups,) if ngroups else ()
-    mn = (M, N)
-    pdy, lddy = _rows(dy, mn, x.dtype, "dy")
-    px, ldx = _rows(x, x.shape, x.dtype, "x")
-    pz, ldz = _rows(z, mn, x.dtype, "z")
-    pdx, lddx = _rows(dx, (M, K), x.dtype, "dx")
-    a = LinearBwdArgs(pdy, px, pw, pz, pdx, _dense(dw, (*lead, N, K), x.dtype, "dw"),
-                      _dense(dbias, (*lead, N), x.dtype, "dbias"), M, K, N, lddy, ldx, ldw, ldz, lddx, w_stride,
-                      DTYPES[x.dtype], ACTS[act], off, ngroups, None, 0, _stream_of(stream, dev))
-    ws, a.workspace_bytes = _workspace(workspace, lib().tgc_linear_bwd_workspace_bytes(ctypes.byref(a)), x, stream)
-    a.workspace = _ptr(ws)
-    rc = lib().tgc_linear_bwd(ctypes.byref(a))
+    rc = (_ops or _native()).linear_bwd(dy, x, w, z, ACTS[act], dx, dw, dbias, offsets, workspace, _address(stream))
     return _check(rc, "tgc_linear_bwd") if check else rc
 
 
@@ -537,22 +455,8 @@ def tgc_block_norm(y, r=None, h=None, *, x=None, gate=None, post: str = "none", 
     """u = post(y); r = res_scale * x + branch_scale * gate * u; h = pre(r), one pass over (M, D)
     tensors.  gate is (gates, D), each vector shared by M / gates consecutive rows; norms are
     "none", "rms" or "layer".  Asynchronous on ``stream``."""
-    dev = _device(y, x, r, h, gate, post_weight, post_bias, pre_weight, pre_bias)
-    if y.dim() != 2:
-        raise ValueError("y: expected (M, D)")
-    M, D = y.shape
-    dt, md = y.dtype, y.shape
-    py, ldy = _rows(y, md, dt, "y")
-    px, ldx = _rows(x, md, dt, "x")
-    pr, ldr = _rows(r, md, dt, "r")
-    ph, ldh = _rows(h, md, dt, "h")
-    gates = gate.shape[0] if gate is not None else 0
-    v = (D,)
-    a = BlockNormArgs(py, px, _dense(gate, (gates, D), dt, "gate"), _dense(post_weight, v, dt, "post_weight"),
-                      _dense(post_bias, v, dt, "post_bias"), _dense(pre_weight, v, dt, "pre_weight"),
-                      _dense(pre_bias, v, dt, "pre_bias"), pr, ph, M, D, gates, ldy, ldx, ldr, ldh, NORMS[post],
-                      NORMS[pre], res_scale, branch_scale, eps, DTYPES[dt], _stream_of(stream, dev))
-    rc = lib().tgc_block_norm(ctypes.byref(a))
+    rc = (_ops or _native()).block_norm(y, r, h, x, gate, NORMS[post], post_weight, post_bias, NORMS[pre], pre_weight,
+                                        pre_bias, res_scale, branch_scale, eps, _address(stream))
     return _check(rc, "tgc_block_norm") if check else rc
 
 
@@ -563,31 +467,9 @@ def tgc_block_norm_bwd(y, r, dr, dh, *, gate=None, post: str = "none", post_weig
     """Gradients of tgc_block_norm from dr and dh, into whichever outputs are given.  y and r are the
     forward pass's; any of y, r, dr, dh may be None where the header says it is not needed.
     ``workspace``: as for tgc_linear_bwd.  Asynchronous on ``stream``."""
-    outs = (dx, dy, dgate, dpost_weight, dpost_bias, dpre_weight, dpre_bias)
-    dev = _device(y, r, dr, dh, gate, post_weight, post_bias, pre_weight, *outs)
-    like = next((t for t in (dh, dr, y, r) if t is not None), None)
-    if like is None or like.dim() != 2:
-        raise ValueError("expected (M, D) operands")
-    M, D = like.shape
-    dt, md = like.dtype, like.shape
-    py, ldy = _rows(y, md, dt, "y")
-    pr, ldr = _rows(r, md, dt, "r")
-    pdr, lddr = _rows(dr, md, dt, "dr")
-    pdh, lddh = _rows(dh, md, dt, "dh")
-    pdx, lddx = _rows(dx, md, dt, "dx")
-    pdy, lddy = _rows(dy, md, dt, "dy")
-    gates = gate.shape[0] if gate is not None else 0
-    v, g = (D,), (gates, D)
-    a = BlockNormBwdArgs(py, pr, pdr, pdh, _dense(gate, g, dt, "gate"), _dense(post_weight, v, dt, "post_weight"),
-                         _dense(post_bias, v, dt, "post_bias"), _dense(pre_weight, v, dt, "pre_weight"), pdx, pdy,
-                         _dense(dgate, g, dt, "dgate"), _dense(dpost_weight, v, dt, "dpost_weight"),
-                         _dense(dpost_bias, v, dt, "dpost_bias"), _dense(dpre_weight, v, dt, "dpre_weight"),
-                         _dense(dpre_bias, v, dt, "dpre_bias"), M, D, gates, ldy, ldr, lddr, lddh, lddx, lddy,
-                         NORMS[post], NORMS[pre], res_scale, branch_scale, eps, DTYPES[dt], None, 0, _stream_of(stream, dev))
-    ws, a.workspace_bytes = _workspace(workspace, lib().tgc_block_norm_bwd_workspace_bytes(ctypes.byref(a)), like,
-                                       stream)
-    a.workspace = _ptr(ws)
-    rc = lib().tgc_block_norm_bwd(ctypes.byref(a))
+    rc = (_ops or _native()).block_norm_bwd(y, r, dr, dh, gate, NORMS[post], post_weight, post_bias, NORMS[pre],
+                                            pre_weight, res_scale, branch_scale, eps, dx, dy, dgate, dpost_weight,
+                                            dpost_bias, dpre_weight, dpre_bias, workspace, _address(stream))
     return _check(rc, "tgc_block_norm_bwd") if check else rc
 
 
