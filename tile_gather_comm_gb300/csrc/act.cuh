@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/tgc.h"
+#include "pairs.cuh"
 
 namespace tgc {
 
@@ -24,62 +25,94 @@ __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2hal
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-constexpr float kGeluC = 0.7978845608028654f;   // sqrt(2 / pi)
-constexpr float kGeluA = 0.044715f;
-constexpr float kSqrtHalf = 0.7071067811865476f;
+// The activations work on pairs (packed fp32): beside the products the epilogue's arithmetic is not
+// free -- 13 single instructions an element more took 13 % off the tensor pipe of a 4096 x 4096 x
+// 14336 product, whose other limits they do not touch.
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInvSqrt2Pi = 0.3989422804014327f;
+constexpr float kTanhK1 = 1.5957691216057308f;    // 2 sqrt(2 / pi)
+constexpr float kTanhK2 = 0.07135481627260025f;   // 2 sqrt(2 / pi) 0.044715
 
-// 1 / (1 + exp(-v)).  __expf and __fdividef are good to about 2^-21 here, far below the
-// 2^-9 or 2^-11 of the 16-bit result.
-__device__ __forceinline__ float sigmoid_f32(float v) { return __fdividef(1.0f, 1.0f + __expf(-v)); }
+// 2^x and 1 / x by the hardware's approximations (about 2^-22): far below the 2^-9 or 2^-11 that
+// rounding the result to 16 bits costs.
+__device__ __forceinline__ F2 exp2_f2(F2 a) {
+    float2 f = split(a);
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(f.x));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(f.y));
+    return f2(f.x, f.y);
+}
+__device__ __forceinline__ F2 rcp_f2(F2 a) {
+    float2 f = split(a);
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(f.x));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(f.y));
+    return f2(f.x, f.y);
+}
 
-// The normal distribution function Phi(z) and g = exp(-z^2 / 2), which gelu and its derivative
+// 1 / (1 + exp(-v))
+__device__ __forceinline__ F2 sigmoid_f2(F2 v) {
+    return rcp_f2(add(exp2_f2(mul(v, every<F2>(-kLog2e))), every<F2>(1.0f)));
+}
+
+// The normal distribution function Phi(z) and e = exp(-z^2 / 2), which gelu and its derivative
 // both need.  Phi by Abramowitz and Stegun 7.1.26: erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2),
 // t = 1 / (1 + p x), x >= 0, off by at most 1.5e-7 (so Phi by 0.75e-7): a tenth of what rounding
 // the result to 16 bits does, for one exponential that the derivative shares.  erff instead took
 // the backward's elementwise pass from memory-bound to 168 us for 8192 x 14336 (floor 104 us).
-__device__ __forceinline__ float normal_cdf(float z, float *g) {
-    const float x = fabsf(z) * kSqrtHalf, e = __expf(-0.5f * z * z);
-    const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
-    float q = fmaf(1.061405429f, t, -1.453152027f);
-    q = fmaf(q, t, 1.421413741f);
-    q = fmaf(q, t, -0.284496736f);
-    q = fmaf(q, t, 0.254829592f);
-    const float tail = 0.5f * q * t * e;  // Phi(-|z|)
-    *g = e;
-    return z < 0.0f ? tail : 1.0f - tail;
+__device__ __forceinline__ F2 normal_cdf(F2 z, F2 *e) {
+    const F2 x = F2{z.v & 0x7fffffff7fffffffull};
+    *e = exp2_f2(mul(mul(z, z), every<F2>(-0.5f * kLog2e)));
+    const F2 t = rcp_f2(fma(x, every<F2>(0.3275911f * 0.7071067811865476f), every<F2>(1.0f)));
+    F2 q = fma(t, every<F2>(0.5f * 1.061405429f), every<F2>(0.5f * -1.453152027f));
+    q = fma(q, t, every<F2>(0.5f * 1.421413741f));
+    q = fma(q, t, every<F2>(0.5f * -0.284496736f));
+    q = fma(q, t, every<F2>(0.5f * 0.254829592f));
+    const F2 tail = mul(mul(q, t), *e);  // Phi(-|z|)
+    const float2 zs = split(z), lo = split(tail), hi = split(fma(tail, every<F2>(-1.0f), every<F2>(1.0f)));
+    return f2(zs.x < 0.0f ? lo.x : hi.x, zs.y < 0.0f ? lo.y : hi.y);
+}
+
+// 0.5 (1 + tanh(u)) = 1 / (1 + exp(-2u)), u = sqrt(2 / pi) (z + 0.044715 z^3)
+__device__ __forceinline__ F2 tanh_gate(F2 z, F2 zz) {
+    return sigmoid_f2(mul(z, fma(zz, every<F2>(kTanhK2), every<F2>(kTanhK1))));
 }
 
 template <int ACT>
-__device__ __forceinline__ float act_of(float z) {
-    if constexpr (ACT == TGC_ACT_RELU) return z < 0.0f ? 0.0f : z;  // NaN stays NaN
-    if constexpr (ACT == TGC_ACT_GELU) {
-        float g;
-        return z * normal_cdf(z, &g);
+__device__ __forceinline__ F2 act_of(F2 z) {
+    if constexpr (ACT == TGC_ACT_RELU) {
+        const float2 f = split(z);
+        return f2(f.x < 0.0f ? 0.0f : f.x, f.y < 0.0f ? 0.0f : f.y);  // NaN stays NaN
     }
-    // 0.5 (1 + tanh(u)) = 1 / (1 + exp(-2u))
-    if constexpr (ACT == TGC_ACT_GELU_TANH) return z * sigmoid_f32(2.0f * kGeluC * z * fmaf(kGeluA * z, z, 1.0f));
-    if constexpr (ACT == TGC_ACT_SILU) return z * sigmoid_f32(z);
+    if constexpr (ACT == TGC_ACT_GELU) {
+        F2 e;
+        return mul(z, normal_cdf(z, &e));
+    }
+    if constexpr (ACT == TGC_ACT_GELU_TANH) return mul(z, tanh_gate(z, mul(z, z)));
+    if constexpr (ACT == TGC_ACT_SILU) return mul(z, sigmoid_f2(z));
     return z;
 }
 
 template <int ACT>
-__device__ __forceinline__ float act_grad_of(float z) {
-    if constexpr (ACT == TGC_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+__device__ __forceinline__ F2 act_grad_of(F2 z) {
+    const F2 one = every<F2>(1.0f), minus = every<F2>(-1.0f);
+    if constexpr (ACT == TGC_ACT_RELU) {
+        const float2 f = split(z);
+        return f2(f.x > 0.0f ? 1.0f : 0.0f, f.y > 0.0f ? 1.0f : 0.0f);
+    }
     if constexpr (ACT == TGC_ACT_GELU) {
-        float g;
-        const float phi = normal_cdf(z, &g);
-        return fmaf(z * kInvSqrt2Pi, g, phi);
+        F2 e;
+        const F2 phi = normal_cdf(z, &e);
+        return fma(mul(z, every<F2>(kInvSqrt2Pi)), e, phi);
     }
     if constexpr (ACT == TGC_ACT_GELU_TANH) {
-        const float s = sigmoid_f32(2.0f * kGeluC * z * fmaf(kGeluA * z, z, 1.0f));
-        return s + z * s * (1.0f - s) * 2.0f * kGeluC * fmaf(3.0f * kGeluA * z, z, 1.0f);
+        const F2 zz = mul(z, z), s = tanh_gate(z, zz);
+        const F2 slope = fma(zz, every<F2>(3.0f * kTanhK2), every<F2>(kTanhK1));
+        return fma(mul(mul(z, s), fma(s, minus, one)), slope, s);
     }
     if constexpr (ACT == TGC_ACT_SILU) {
-        const float s = sigmoid_f32(z);
-        return s * fmaf(z, 1.0f - s, 1.0f);
+        const F2 s = sigmoid_f2(z);
+        return fma(mul(z, s), fma(s, minus, one), s);
     }
-    return 1.0f;
+    return one;
 }
 
 // f(integral constant of the activation): one branch for many elements.

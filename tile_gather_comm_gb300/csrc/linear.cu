@@ -71,7 +71,9 @@ __global__ void __launch_bounds__(256) dz_kernel(const DzParams p) {
         r1 = s_rows[1];
         if (r0 >= r1) return;
     }
-    float acc[8] = {};
+    F2 acc[4];
+#pragma unroll
+    for (F2 &v : acc) v = every<F2>(0.0f);
     if (n < p.N) {
         constexpr int U = 4;  // rows of a lane in flight
         const uint16_t *dy = static_cast<const uint16_t *>(p.dy) + n, *z = static_cast<const uint16_t *>(p.z) + n;
@@ -95,16 +97,11 @@ __global__ void __launch_bounds__(256) dz_kernel(const DzParams p) {
                     uint32_t o[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        float d0, d1, z0, z1;
-                        unpack16(aw[i], F16, &d0, &d1);
-                        if (decltype(act)::value != TGC_ACT_NONE) {
-                            unpack16(bw[i], F16, &z0, &z1);
-                            d0 *= act_grad_of<decltype(act)::value>(z0);
-                            d1 *= act_grad_of<decltype(act)::value>(z1);
-                        }
-                        acc[2 * i] += d0;
-                        acc[2 * i + 1] += d1;
-                        o[i] = pack16(d0, d1, F16);
+                        F2 d = unpack16(aw[i], F16);
+                        if (decltype(act)::value != TGC_ACT_NONE)
+                            d = mul(d, act_grad_of<decltype(act)::value>(unpack16(bw[i], F16)));
+                        acc[i] = add(acc[i], d);
+                        o[i] = pack16(d, F16);
                     }
                     if (p.dz != nullptr) *reinterpret_cast<uint4 *>(dz + row * p.N) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
@@ -113,7 +110,11 @@ __global__ void __launch_bounds__(256) dz_kernel(const DzParams p) {
     }
     if (p.partial == nullptr) return;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) sums[rl][cv * 8 + c] = acc[c];
+    for (int c = 0; c < 4; ++c) {
+        const float2 f = split(acc[c]);
+        sums[rl][cv * 8 + 2 * c] = f.x;
+        sums[rl][cv * 8 + 2 * c + 1] = f.y;
+    }
     __syncthreads();
     const int col = threadIdx.x, nn = strip * 256 + col;
     if (nn < p.N) {

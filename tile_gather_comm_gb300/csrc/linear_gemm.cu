@@ -266,14 +266,11 @@ __device__ void lin_role_epilogue(const LinearMaps &maps, const LinearParams &p,
                 if (lane * 8 < TN / 2 && n + lane * 8 < p.J) {
                     const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias) +
                                                                      (int64_t)tl.e * p.J + n + lane * 8);
-                    float f[8];
-                    unpack16(w.x, f16, &f[0], &f[1]);
-                    unpack16(w.y, f16, &f[2], &f[3]);
-                    unpack16(w.z, f16, &f[4], &f[5]);
-                    unpack16(w.w, f16, &f[6], &f[7]);
-                    float4 *to = reinterpret_cast<float4 *>(bias + lane * 8);
-                    to[0] = make_float4(f[0], f[1], f[2], f[3]);
-                    to[1] = make_float4(f[4], f[5], f[6], f[7]);
+                    F2 *to = reinterpret_cast<F2 *>(bias + lane * 8);
+                    to[0] = unpack16(w.x, f16);
+                    to[1] = unpack16(w.y, f16);
+                    to[2] = unpack16(w.z, f16);
+                    to[3] = unpack16(w.w, f16);
                 }
             }
             if (p.residual != nullptr) fetch_residual(n);
@@ -322,50 +319,42 @@ __device__ void lin_role_epilogue(const LinearMaps &maps, const LinearParams &p,
             }
             const int n = tl.n0 + col0 + j * 32;
             if (n >= p.J || rows <= 0) continue;  // warp-uniform
+            F2 f[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) f[i] = f2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+            auto packed = [&](uint32_t (&w)[16]) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = pack16(f[i], f16);
+            };
+            uint32_t w[16];
             if (MODE == kFwd) {
                 if (p.bias != nullptr) {
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {  // the same address in every lane
-                        const float4 f = reinterpret_cast<const float4 *>(bias + j * 32)[c];
-                        v[4 * c] = __float_as_uint(__uint_as_float(v[4 * c]) + f.x);
-                        v[4 * c + 1] = __float_as_uint(__uint_as_float(v[4 * c + 1]) + f.y);
-                        v[4 * c + 2] = __float_as_uint(__uint_as_float(v[4 * c + 2]) + f.z);
-                        v[4 * c + 3] = __float_as_uint(__uint_as_float(v[4 * c + 3]) + f.w);
+                        const ulonglong2 b = reinterpret_cast<const ulonglong2 *>(bias + j * 32)[c];
+                        f[2 * c] = add(f[2 * c], F2{b.x});
+                        f[2 * c + 1] = add(f[2 * c + 1], F2{b.y});
                     }
                 }
                 if (p.z != nullptr) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        w[i] = pack16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), f16);
+                    packed(w);
                     put(&maps.z, p.z, p.ldz, n, w);
                 }
                 if (p.act != TGC_ACT_NONE)
                     with_act(p.act, [&](auto act) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(act_of<decltype(act)::value>(__uint_as_float(v[i])));
+                        for (int i = 0; i < 16; ++i) f[i] = act_of<decltype(act)::value>(f[i]);
                     });
                 if (p.residual != nullptr) {
                     if (row_ok) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            if (n + c * 8 >= p.J) continue;
-                            const uint32_t ws[4] = {res[c].x, res[c].y, res[c].z, res[c].w};
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                float lo, hi;
-                                unpack16(ws[i], f16, &lo, &hi);
-                                v[c * 8 + 2 * i] = __float_as_uint(__uint_as_float(v[c * 8 + 2 * i]) + lo);
-                                v[c * 8 + 2 * i + 1] = __float_as_uint(__uint_as_float(v[c * 8 + 2 * i + 1]) + hi);
-                            }
-                        }
+                        for (int c = 0; c < 4; ++c)
+                            if (n + c * 8 < p.J) add16(reinterpret_cast<F2(&)[4]>(f[4 * c]), res[c], f16);
                     }
                     if (j + 1 < TN / 64) fetch_residual(n + 32);
                 }
             }
-            uint32_t w[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = pack16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), f16);
+            packed(w);
             put(&maps.y, p.y, p.ldy, n, w);
         }
     }

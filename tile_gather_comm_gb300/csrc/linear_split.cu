@@ -205,42 +205,37 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         for (int i = part_id * kSplitThreads + (int)threadIdx.x; i < total; i += q.parts * kSplitThreads) {
             const int r = i / vecs, c = (i % vecs) * 8, n = tl.n0 + c;
             if (n >= p.J) continue;
-            float v[8] = {};
+            F2 v[4];
+#pragma unroll
+            for (F2 &f : v) f = every<F2>(0.0f);
             const uint32_t at = part0 + (uint32_t)(r * kPitch + c) * 4u;
             for (int k = 0; k < q.parts; ++k) {
                 const uint32_t from = q.parts > 1 ? mapa_shared(at, (uint32_t)k) : at;
                 const float4 a = ld_cluster_f4(from), b = ld_cluster_f4(from + 16u);
-                v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-                v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+                v[0] = add(v[0], f2(a.x, a.y));
+                v[1] = add(v[1], f2(a.z, a.w));
+                v[2] = add(v[2], f2(b.x, b.y));
+                v[3] = add(v[3], f2(b.z, b.w));
             }
             const int64_t m = tl.m0 + r;
-            auto add = [&](const uint4 w) {
-                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float lo, hi;
-                    unpack16(ws[k], f16, &lo, &hi);
-                    v[2 * k] += lo;
-                    v[2 * k + 1] += hi;
-                }
-            };
-            auto pack = [&] {
-                return make_uint4(pack16(v[0], v[1], f16), pack16(v[2], v[3], f16), pack16(v[4], v[5], f16),
-                                  pack16(v[6], v[7], f16));
+            auto packed = [&] {
+                return make_uint4(pack16(v[0], f16), pack16(v[1], f16), pack16(v[2], f16), pack16(v[3], f16));
             };
             if (MODE == kFwd) {
                 if (p.bias != nullptr)
-                    add(*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias) + (int64_t)tl.e * p.J + n));
-                if (p.z != nullptr) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.z) + m * p.ldz + n) = pack();
+                    add16(v, *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.bias) + (int64_t)tl.e * p.J + n),
+                          f16);
+                if (p.z != nullptr) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.z) + m * p.ldz + n) = packed();
                 if (p.act != TGC_ACT_NONE)
                     with_act(p.act, [&](auto act) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) v[k] = act_of<decltype(act)::value>(v[k]);
+                        for (int k = 0; k < 4; ++k) v[k] = act_of<decltype(act)::value>(v[k]);
                     });
                 if (p.residual != nullptr)
-                    add(*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.residual) + m * p.ldres + n));
+                    add16(v, *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.residual) + m * p.ldres + n),
+                          f16);
             }
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.y) + m * p.ldy + n) = pack();
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.y) + m * p.ldy + n) = packed();
         }
     }
     __syncwarp();
