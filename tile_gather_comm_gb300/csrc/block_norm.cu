@@ -529,21 +529,33 @@ __global__ void __launch_bounds__(kTeamMax<T, VEC, NV>) norm_bwd_kernel(const No
     // Rows that are not staged come from memory, the next ones while the last are worked on where
     // there are registers for them.
     constexpr bool AHEAD = !STAGED && NV <= 4;
-    auto from_memory = [&](int j, int m, int m1, int k) {
-        P v;
-        const int c = c0 + k * step;
-        if (in[j] != nullptr && c < p.D && m < m1) v = load_pack<T, VEC>(in[j], m * ld[j] + c);
-        else v.clear();
-        return v;
-    };
     P next[4][AHEAD ? ROWS : 1][AHEAD ? NV : 1];
-    auto fetch_next = [&](int m, int m1) {
+    const T *src[4];  // each input's next row to ask for, at this thread's first column
+    bool has[AHEAD ? NV : 1];
+    if constexpr (AHEAD) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) has[k] = c0 + k * step < p.D;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int rr = 0; rr < (AHEAD ? ROWS : 1); ++rr)
+            for (int rr = 0; rr < ROWS; ++rr)
 #pragma unroll
-                for (int k = 0; k < (AHEAD ? NV : 1); ++k) next[j][rr][k] = from_memory(j, m + rr, m1, k);
+                for (int k = 0; k < NV; ++k) next[j][rr][k].clear();
+    }
+    auto fetch_next = [&](int left) {  // rows of the unit from src on
+        if (left <= 0) return;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (in[j] == nullptr) continue;
+#pragma unroll
+            for (int rr = 0; rr < (AHEAD ? ROWS : 1); ++rr) {
+                if (rr < left)
+#pragma unroll
+                    for (int k = 0; k < (AHEAD ? NV : 1); ++k)
+                        if (has[k]) next[j][rr][k] = *reinterpret_cast<const P *>(src[j] + k * step);
+                src[j] += ld[j];
+            }
+        }
     };
     if constexpr (STAGED) {
         // an input that is not there reads as zeros
@@ -595,7 +607,11 @@ __global__ void __launch_bounds__(kTeamMax<T, VEC, NV>) norm_bwd_kernel(const No
                 read_lanes(fb + c0 + k * step, b);
             }
         };
-        if constexpr (AHEAD) fetch_next(m0, m1);
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) src[j] = static_cast<const T *>(in[j]) + m0 * ld[j] + c0;
+            fetch_next(m1 - m0);
+        }
         for (int m = m0; m < m1; m += ROWS) {
             const uint32_t stage = turn & 1u;
             P pr[ROWS][NV], pd[ROWS][NV], py[ROWS][NV], pt[ROWS][NV];
@@ -608,7 +624,8 @@ __global__ void __launch_bounds__(kTeamMax<T, VEC, NV>) norm_bwd_kernel(const No
                         to[k] = *reinterpret_cast<const P *>(stages + ((stage * ROWS + rr) * 4 + j) * row_bytes +
                                                              c * (int)sizeof(T));
                     else if constexpr (AHEAD) to[k] = next[j][rr][k];
-                    else to[k] = from_memory(j, m + rr, m1, k);
+                    else if (in[j] != nullptr && c < p.D) to[k] = load_pack<T, VEC>(in[j], (m + rr) * ld[j] + c);
+                    else to[k].clear();
                 }
             };
 #pragma unroll
@@ -618,7 +635,7 @@ __global__ void __launch_bounds__(kTeamMax<T, VEC, NV>) norm_bwd_kernel(const No
                 fetch(py[rr], rr, 2);
                 fetch(pt[rr], rr, 3);
             }
-            if constexpr (AHEAD) fetch_next(m + ROWS, m1);
+            if constexpr (AHEAD) fetch_next(m1 - m - ROWS);
             L mean_r = every<L>(0.0f), mean_y = every<L>(0.0f);  // negated
             if constexpr (FULL) {
                 if (p.pre == TGC_NORM_LAYER || p.post == TGC_NORM_LAYER) {
