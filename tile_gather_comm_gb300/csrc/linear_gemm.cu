@@ -6,8 +6,11 @@
 // pair (CG = 2, 256 rows, tcgen05 cta_group::2, which halves the bytes of B a CTA stages) walks
 // tiles of 128 or 256 columns; two accumulators in TMEM alternate, so a tile's epilogue runs under
 // the next tile's products.
-//   warp 0      TMA loads into a ring of 64-deep stages (128-byte swizzle); a tile with fewer rows
-//               than it could hold loads boxes of 32 rows and no more
+//   warps 0, 3  TMA loads into a ring of 64-deep stages (128-byte swizzle); a tile with fewer rows
+//               than it could hold loads boxes of 32 rows and no more.  MN-major operands take a
+//               load for every 64 columns, so in kDgrad and kWgrad A's and B's are issued by a
+//               warp each (8192 x 4096 x 14336: weight gradient 531 -> 505 us); kFwd's two a
+//               stage by one (528 us against 535)
 //   warp 1      TMEM owner; one lane issues the MMAs
 //   warp 2      kWgrad with groups: a group's last stage also holds rows of the next group (or
 //               beyond the last); it zeroes them in both operands before the MMA reads them, so
@@ -69,7 +72,8 @@ __device__ __forceinline__ bool needs_repair(const LinearParams &p, const Tile &
 
 // ---------------------------------------------------------------- loads
 
-template <int CG, int MODE, int TN>
+// The loads of A (which also announce the stage's bytes), of B, or of both.
+template <int CG, int MODE, int TN, bool A, bool B>
 __device__ void lin_role_tma(const LinearMaps &maps, const LinearParams &p, const int *tile0, uint8_t *sA, uint8_t *sB,
                              uint64_t *full, uint64_t *empty, uint64_t *raw, uint32_t crank) {
     using C = LCfg<CG, MODE, TN>;
@@ -100,29 +104,35 @@ __device__ void lin_role_tma(const LinearMaps &maps, const LinearParams &p, cons
             const uint32_t s = it % C::kStages, ph = (it / C::kStages) & 1u;
             if (!lin_wait(&empty[s], ph ^ 1u, p)) { ok = false; break; }
             if (MODE == kWgrad) cut = needs_repair(p, tl, kb);
-            if (cut) {
-                mbar_arrive_expect_tx(&raw[s], C::kABytes + C::kBBytes);
-                if (CG == 1 || crank == 0) mbar_arrive(&full[s]);
-            } else if (CG == 1 || crank == 0) {
-                mbar_arrive_expect_tx(&full[s], tx);
+            if (A) {
+                if (cut) {
+                    mbar_arrive_expect_tx(&raw[s], C::kABytes + C::kBBytes);
+                    if (CG == 1 || crank == 0) mbar_arrive(&full[s]);
+                } else if (CG == 1 || crank == 0) {
+                    mbar_arrive_expect_tx(&full[s], tx);
+                }
             }
-            uint8_t *a = sA + s * C::kABytes, *b = sB + s * C::kBBytes;
             const int r0 = (MODE == kWgrad ? tl.red0 : 0) + kb * kBK;
-            if (C::kAMn) {
+            uint8_t *a = sA + s * C::kABytes, *b = sB + s * C::kBBytes;
+            if (A) {
+                if (C::kAMn) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c) load(a + c * C::kBoxMn, &maps.a, s, m0 + c * 64, r0, 0);
-            } else if (boxes == 4) {
-                load(a, &maps.a, s, r0, m0, 0);
-            } else {
-                for (int c = 0; c < boxes; ++c)
-                    load(a + c * (C::kABytes / 4), &maps.a_small, s, r0, m0 + c * kRowBox, 0);
+                    for (int c = 0; c < 2; ++c) load(a + c * C::kBoxMn, &maps.a, s, m0 + c * 64, r0, 0);
+                } else if (boxes == 4) {
+                    load(a, &maps.a, s, r0, m0, 0);
+                } else {
+                    for (int c = 0; c < boxes; ++c)
+                        load(a + c * (C::kABytes / 4), &maps.a_small, s, r0, m0 + c * kRowBox, 0);
+                }
             }
-            if (C::kBMn) {
+            if (B) {
+                if (C::kBMn) {
 #pragma unroll
-                for (int c = 0; c < C::kBRows / 64; ++c)
-                    load(b + c * C::kBoxMn, &maps.b, s, j0 + c * 64, r0, MODE == kWgrad ? 0 : tl.e);
-            } else {
-                load(b, &maps.b, s, r0, j0, tl.e);
+                    for (int c = 0; c < C::kBRows / 64; ++c)
+                        load(b + c * C::kBoxMn, &maps.b, s, j0 + c * 64, r0, MODE == kWgrad ? 0 : tl.e);
+                } else {
+                    load(b, &maps.b, s, r0, j0, tl.e);
+                }
             }
         }
     }
@@ -417,7 +427,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const uint32_t tmem_base = *tmem_holder;
 
     if (warp == 0) {
-        if (lane == 0) lin_role_tma<CG, MODE, TN>(maps, p, tile0, sA, sB, full, empty, raw, crank);
+        if (lane == 0) lin_role_tma<CG, MODE, TN, true, MODE == kFwd>(maps, p, tile0, sA, sB, full, empty, raw, crank);
+    } else if (warp == 3) {
+        if (MODE != kFwd && lane == 0)
+            lin_role_tma<CG, MODE, TN, false, true>(maps, p, tile0, sA, sB, full, empty, raw, crank);
     } else if (warp == 1) {
         if (lane == 0 && crank == 0)
             lin_role_mma<CG, MODE, TN>(p, tile0, sA, sB, full, fixed, empty, tfull, tempty, drain, tmem_base);
@@ -568,19 +581,30 @@ static int lin_launch(const LinearProduct &q, int dev, int sms, cudaStream_t str
 
 // ---------------------------------------------------------------- which kernel, which tile
 
-// Every form is bound by what one SM takes in: a row of 128 bytes of an operand costs it about
-// 2.1 cycles (60 bytes a cycle; measured on 777 x 4096 x 5000: 128 x 256 tiles 806 cycles a 64-deep
-// step, 128 x 128 538, the pair's 256 x 256 560 for each CTA's 128 x 256).  So a form's time is its
-// number of rounds times its steps times the rows a step loads, plus what the last tile's epilogue
-// adds; the least wins.
+// A form's time in SM cycles is the largest of three bounds and what nothing overlaps:
+//   l2     what L2 hands out: 2.83 / SMs cycles for every 128-byte row of an operand tile that any SM
+//          takes in; rows that do not start on a 128-byte line (they take two) 1.09 times that
+//   hbm    every operand once, 2120 bytes a cycle
+//   sm     the busiest SM's steps -- the products (2 cycles a column of the tile) or the rows it takes
+//          in -- and, for the persistent kernel, no less than an epilogue a tile
+//   extra  start, the last epilogue, and the split kernel's exchange
+// The constants were fitted to 13,900 timings (190 shapes of 1..8192 x 64..14336 x 64..14336, three
+// products, every form): the form taken is 2.5 % slower than the best on the geometric mean, where
+// one persistent form for all rows above 128 and the split kernel below was 18 % slower.
 struct LinearForm {
     int cg, tn;  // the persistent kernel's; cg 0: the split kernel's tn and parts
     int parts;
-    int64_t cycles;
+    int64_t l2, hbm, sm, extra;
+    int64_t bound() const { return l2 > hbm ? (l2 > sm ? l2 : sm) : (hbm > sm ? hbm : sm); }
+    int64_t cycles() const { return bound() + extra; }
 };
 
+enum : int { kPairs = 1, kNarrowPairs = 2, kSingles = 4, kSplits = 8, kAllForms = 15 };
+
+// The best of `forms` on `sms` of the device's `all` SMs; false if none fits.
 template <int MODE>
-static LinearForm lin_choose(const LinearProduct &q, int sms, const int (&room)[kMaxSplit + 1]) {
+static bool lin_choose(const LinearProduct &q, int all, int sms, const int (&room)[kMaxSplit + 1], int forms,
+                       LinearForm *best) {
     const int64_t groups = q.offsets != nullptr ? q.ngroups : 1;
     const int64_t rows = MODE == kWgrad ? q.I : q.M;
     const int64_t steps = ((MODE == kWgrad ? (q.M + groups - 1) / groups : q.R) + kBK - 1) / kBK;
@@ -592,26 +616,35 @@ static LinearForm lin_choose(const LinearProduct &q, int sms, const int (&room)[
         const int64_t used = groups < rows ? groups : rows;
         return rows / h + (used + 1) / 2;
     };
-    auto cycles = [](int64_t box_rows) { return box_rows * 21 / 10; };
-    LinearForm best{};
-    best.cycles = INT64_MAX;
-    auto consider = [&](int cg, int tn, int parts, int64_t c) {
-        if (c < best.cycles) best = {cg, tn, parts, c};
+    // L2 cycles of `count` steps that take in so many rows of A and of B; what HBM needs
+    const int64_t a_cost = q.lda % 64 != 0 ? 308 : 283, b_cost = q.ldb % 64 != 0 ? 308 : 283;
+    const int64_t inner = MODE == kWgrad ? q.M : q.R;
+    const int64_t hbm = 2 * (rows * inner + inner * q.J * (MODE == kWgrad ? 1 : groups) +
+                             rows * q.J * (MODE == kWgrad ? groups : 1)) / 2120;
+    auto l2_of = [&](int64_t count, int64_t a_rows, int64_t b_rows) {
+        return count * (a_rows * a_cost + b_rows * b_cost) / (100 * all);
+    };
+    auto step_of = [](int64_t tn, int64_t load) { return 2 * tn > load ? 2 * tn : load; };
+    bool any = false;
+    auto consider = [&](const LinearForm &f) {
+        if (!any || f.cycles() < best->cycles()) *best = f;
+        any = true;
     };
     static constexpr int kForms[4][2] = {{2, 256}, {2, 128}, {1, 256}, {1, 128}};
     for (const auto &f : kForms) {
         const int cg = f[0], tn = f[1];
+        if (!(forms & (cg == 1 ? kSingles : tn == 256 ? kPairs : kNarrowPairs)) || sms < cg) continue;
         const int64_t tiles = tile_rows(128 * cg) * ((q.J + tn - 1) / tn);
         const int64_t rounds = (tiles + sms / cg - 1) / (sms / cg);
-        int64_t step = cycles(128 + tn / cg);
-        if (step < 2 * tn) step = 2 * tn;  // the products themselves
-        const int64_t epilogue = tn * 16;
-        const int64_t tile = steps * step > epilogue ? steps * step : epilogue;
-        consider(cg, tn, 0, rounds * tile + epilogue + 1500);
+        const int64_t epilogue = cg == 2 ? 5340 + tn * 25 / 2 : 1690 + tn * 21;
+        const int64_t tile = steps * step_of(tn, (128 + tn / cg) * 231 / 100);
+        consider({cg, tn, 0, l2_of(tiles * cg * steps, 128, tn / cg), hbm, rounds * (tile > epilogue ? tile : epilogue),
+                  epilogue * 6 / 10 + (cg == 2 ? 14400 : 4700)});
     }
-    if (MODE == kWgrad && q.offsets != nullptr) return best;
+    if (!(forms & kSplits) || (MODE == kWgrad && q.offsets != nullptr)) return any;
     const int64_t tm = split_tiles(q, MODE);
-    const int64_t a_rows = MODE == kWgrad || rows > 96 ? 128 : (rows + split_row_box(q.M) - 1) / split_row_box(q.M) * split_row_box(q.M);
+    const int box = split_row_box(q.M);
+    const int64_t a_rows = MODE == kWgrad || rows > 96 ? 128 : (rows + box - 1) / box * box;
     for (int tn = 128; tn >= 48; tn -= 16) {
         if (MODE != kFwd && tn % 64 != 0) continue;
         const int64_t tiles = tm * ((q.J + tn - 1) / tn);
@@ -619,13 +652,25 @@ static LinearForm lin_choose(const LinearProduct &q, int sms, const int (&room)[
             if (room[parts] <= 0) continue;
             // one CTA on an SM while there are no more than SMs, two beyond; then further rounds
             const int64_t rounds = (tiles + room[parts] - 1) / room[parts];
-            const int64_t shared = tiles * parts <= sms ? 1 : 2 * rounds;
             const int64_t mine = (steps + parts - 1) / parts;
-            const int64_t reduce = parts > 1 ? 1000 + 300 * parts : 0;
-            consider(0, tn, parts, shared * (mine * cycles(a_rows + tn)) + rounds * (reduce + tn * 16) + 1500);
+            const int64_t load = (a_rows * 250 + tn * (MODE == kFwd ? 432 : 604)) / 100;
+            int64_t step = step_of(tn, load) * (tiles * parts <= sms ? 1 : 2);
+            const int64_t late = 2660 / split_stages(a_rows, tn);  // a load's way through the ring
+            if (step < late) step = late;
+            const int64_t exchange = parts > 1 ? 740 + 221 * parts : 0;
+            const int64_t epilogue = 4190 + (rows < 128 ? rows : 128) * tn * 264 / (1000 * parts);
+            consider({0, tn, parts, l2_of(tiles * steps, a_rows, tn), hbm, rounds * (mine * step + exchange + epilogue), 5330});
         }
     }
-    return best;
+    return any;
+}
+
+template <int MODE>
+static int lin_launch_form(const LinearProduct &q, const LinearForm &f, int dev, int sms, cudaStream_t stream) {
+    if (f.cg == 0) return launch_linear_split(q, MODE, f.tn, f.parts, stream);
+    if (f.cg == 2)
+        return f.tn == 256 ? lin_launch<2, MODE, 256>(q, dev, sms, stream) : lin_launch<2, MODE, 128>(q, dev, sms, stream);
+    return f.tn == 256 ? lin_launch<1, MODE, 256>(q, dev, sms, stream) : lin_launch<1, MODE, 128>(q, dev, sms, stream);
 }
 
 template <int MODE>
@@ -637,11 +682,40 @@ static int lin_dispatch(const LinearProduct &q, cudaStream_t stream) {
     int room[kMaxSplit + 1];
     const int rc = split_room(MODE, dev, room);
     if (rc != TGC_OK) return rc;
-    const LinearForm f = lin_choose<MODE>(q, sms, room);
-    if (f.cg == 0) return launch_linear_split(q, MODE, f.tn, f.parts, stream);
-    if (f.cg == 2)
-        return f.tn == 256 ? lin_launch<2, MODE, 256>(q, dev, sms, stream) : lin_launch<2, MODE, 128>(q, dev, sms, stream);
-    return f.tn == 256 ? lin_launch<1, MODE, 256>(q, dev, sms, stream) : lin_launch<1, MODE, 128>(q, dev, sms, stream);
+    LinearForm f;
+    if (!lin_choose<MODE>(q, sms, sms, room, kAllForms, &f)) return TGC_ERR_INVALID_ARG;
+    // A last tile row that is mostly empty can cost a whole round.  Where the full rows' tiles leave
+    // SMs idle, the rest of the rows go to the split kernel on those, at the same time: 777 x 4104 x
+    // 5000 44 -> 36 us (kFwd; kDgrad's MN-major weight made the rest the longer part).
+    const int64_t full = q.M / 256 * 256;
+    if (MODE == kFwd && q.offsets == nullptr && full > 0 && full < q.M) {
+        LinearProduct main = q, rest = q;
+        main.M = full;
+        rest.M = q.M - full;
+        rest.early = 1;  // needs what the main part needs
+        auto rows_on = [&](auto *p, int64_t ld) { return p == nullptr ? p : (decltype(p))((char *)p + full * ld * 2); };
+        rest.a = rows_on(q.a, q.lda);
+        rest.y = rows_on(q.y, q.ldy);
+        rest.z = rows_on(q.z, q.ldz);
+        rest.residual = rows_on(q.residual, q.ldres);
+        LinearForm fm, fr;
+        lin_choose<MODE>(main, sms, sms, room, kPairs, &fm);
+        const int64_t tiles = full / 256 * ((q.J + 255) / 256);
+        const int idle = sms - 2 * (int)(tiles < sms / 2 ? tiles : sms / 2);
+        int there[kMaxSplit + 1] = {};
+        for (int c = 1; c <= kMaxSplit; ++c) there[c] = room[c] < 2 * idle / c ? room[c] : 2 * idle / c;
+        if (idle > 0 && lin_choose<MODE>(rest, sms, idle, there, kSplits, &fr)) {
+            int64_t both = fm.bound();
+            if (both < fm.l2 + fr.l2) both = fm.l2 + fr.l2;
+            if (both < fr.sm / 2) both = fr.sm / 2;  // the weight comes from L2: the main part has read it
+            both += (fm.extra > fr.extra ? fm.extra : fr.extra) + 2000;
+            if (both * 11 / 10 < f.cycles()) {
+                const int r = lin_launch_form<MODE>(main, fm, dev, sms, stream);
+                return r != TGC_OK ? r : lin_launch_form<MODE>(rest, fr, dev, sms, stream);
+            }
+        }
+    }
+    return lin_launch_form<MODE>(q, f, dev, sms, stream);
 }
 
 int launch_linear(const LinearProduct &q, int mode, cudaStream_t stream) {

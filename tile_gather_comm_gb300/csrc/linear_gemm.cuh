@@ -78,6 +78,8 @@ constexpr int kMaxSplit = 8;  // parts: a portable cluster
 int launch_linear_split(const LinearProduct &q, int mode, int tn, int parts, cudaStream_t stream);
 // room[c]: clusters of c CTAs of the split kernel that the device holds at once.
 int split_room(int mode, int device, int (&room)[kMaxSplit + 1]);
+// Stages of its ring for tiles of so many rows of A and columns.
+int split_stages(int64_t a_rows, int64_t tn);
 // Rows of the boxes that the split kernel loads A in: TMA spends its time by box rows, whether
 // they exist or not, so a few tokens load 8 at a time.
 inline int split_row_box(int64_t M) { return M <= 8 ? 8 : M <= 16 ? 16 : kRowBox; }

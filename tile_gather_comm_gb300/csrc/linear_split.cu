@@ -18,7 +18,7 @@
 namespace tgc {
 
 constexpr int kSplitThreads = 256;
-constexpr int kSplitSmem = 112 * 1024;             // two CTAs an SM
+constexpr int kSplitSmem = 110 * 1024;             // two CTAs an SM, with what the system and static data take
 constexpr int kSplitRing = kSplitSmem - 1024 - 512;  // less alignment slack and barriers
 constexpr int kSplitMaxStages = 12;
 
@@ -245,6 +245,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
 
 // ---------------------------------------------------------------- host side
 
+int split_stages(int64_t a_rows, int64_t tn) {
+    const int64_t n = kSplitRing / ((a_rows + tn) * kBK * 2);
+    return n < kSplitMaxStages ? (int)n : kSplitMaxStages;
+}
+
 struct SplitRoom {
     bool done;
     int room[kMaxSplit + 1];
@@ -261,7 +266,13 @@ static int split_setup(int dev, SplitRoom **out) {
     if (!r.done) {
         cudaError_t e = cudaFuncSetAttribute(linear_split_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              kSplitSmem);
+        // the whole of it as shared memory, so that two CTAs fit (and the query counts them)
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(linear_split_kernel<MODE>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                     cudaSharedmemCarveoutMaxShared);
         if (e != cudaSuccess) return cuda_fail(e);
+        // The query counts one CTA an SM although two run there (a grid of 224 single CTAs starts
+        // within 0.8 us on 152 SMs): its answers are doubled.
         for (int c = 1; c <= kMaxSplit; ++c) {
             cudaLaunchConfig_t cfg{};
             cudaLaunchAttribute attr[1];
@@ -275,6 +286,7 @@ static int split_setup(int dev, SplitRoom **out) {
             cfg.numAttrs = 1;
             e = cudaOccupancyMaxActiveClusters(&r.room[c], linear_split_kernel<MODE>, &cfg);
             if (e != cudaSuccess) return cuda_fail(e);
+            r.room[c] *= 2;
         }
         r.done = true;
     }
@@ -300,8 +312,7 @@ static int split_launch(const LinearProduct &q, int tn, int parts, cudaStream_t 
     s.row_box = split_row_box(q.M);
     // A's stage: the boxes that a tile can need (a group may fill it; kWgrad always does)
     s.a_bytes = MODE == kWgrad || rows > 96 ? 16384 : (int)((rows + s.row_box - 1) / s.row_box) * s.row_box * kBK * 2;
-    s.stages = kSplitRing / (s.a_bytes + tn * kBK * 2);
-    if (s.stages > kSplitMaxStages) s.stages = kSplitMaxStages;
+    s.stages = split_stages(s.a_bytes / (kBK * 2), tn);
     LinearMaps maps;
     if (!lin_maps(&maps, q, MODE, tn, s.row_box)) return TGC_ERR_CUDA;
     LinearParams p{};
