@@ -148,6 +148,46 @@ def test_experts_are_exact_on_whole_numbers(sizes, dtype, K, N, before, after):
     assert torch.equal(db, rb.to(dtype))
 
 
+# Sizes at which each form of the products is taken: CTA pairs with wide and narrow tiles, single
+# CTAs, split reductions of several parts, full tiles with a ragged end's rows beside them.
+FORMS = [(777, 4104, 5000), (300, 4096, 4096), (2048, 2048, 2048), (4100, 1032, 2056), (9, 14336, 1024),
+         (520, 8192, 520), (1, 4096, 14336), (6000, 264, 3000)]
+
+
+@pytest.mark.parametrize("M,K,N", FORMS)
+def test_every_form_is_exact_on_whole_numbers(M, K, N):
+    g = gen(M + N)
+    x, w = ints(g, M, K, lo=-1, hi=2), ints(g, N, K, lo=-1, hi=2)
+    b, res, dy = ints(g, N), ints(g, M, N), ints(g, M, N, lo=-1, hi=2)
+    y, z = (torch.full((M, N), float("nan"), device="cuda", dtype=BF) for _ in range(2))
+    tgc.tgc_linear(x, w, y, bias=b, act="relu", residual=res, z=z)
+    z64, y64 = forward64(x, w, b, res, "relu")
+    assert torch.equal(z, z64.to(BF)) and torch.equal(y, y64.to(BF))
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty_like(b)
+    tgc.tgc_linear_bwd(dy, x, w, z=z, act="relu", dx=dx, dw=dw, dbias=db)
+    rx, rw, rb, _ = backward64(dy, x, w, z, "relu")
+    assert torch.equal(dx, rx.to(BF)) and torch.equal(dw, rw.to(BF)) and torch.equal(db, rb.to(BF))
+
+
+@pytest.mark.parametrize("sizes,K,N", [([700, 0, 1500, 33, 257, 1], 1032, 2056), ([3000, 40], 520, 4096)])
+def test_large_experts_are_exact_on_whole_numbers(sizes, K, N):
+    g = gen(K)
+    offsets = [0]
+    for n in sizes:
+        offsets.append(offsets[-1] + n)
+    M, En = offsets[-1], len(sizes)
+    x, w = ints(g, M, K, lo=-1, hi=2), ints(g, En, N, K, lo=-1, hi=2)
+    dy, off = ints(g, M, N, lo=-1, hi=2), torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    y = torch.full((M, N), float("nan"), device="cuda", dtype=BF)
+    tgc.tgc_linear(x, w, y, offsets=off)
+    assert torch.equal(y, forward64(x, w, None, None, "none", offsets)[1].to(BF))
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    db = torch.empty(En, N, device="cuda", dtype=BF)
+    tgc.tgc_linear_bwd(dy, x, w, dx=dx, dw=dw, dbias=db, offsets=off)
+    rx, rw, rb, _ = backward64(dy, x, w, None, "none", offsets)
+    assert torch.equal(dx, rx.to(BF)) and torch.equal(dw, rw.to(BF)) and torch.equal(db, rb.to(BF))
+
+
 def test_many_experts_and_offsets_out_of_range():
     g = gen(1)
     En, K, N = 1024, 64, 64
