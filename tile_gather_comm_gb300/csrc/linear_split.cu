@@ -74,8 +74,20 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         tmem_alloc(tmem_holder, kSplitTmemCols);
         tmem_relinquish();
     }
+    if (MODE != kWgrad && p.offsets == nullptr && threadIdx.x == 96) {
+        // The weight's first stages come into L2 while the kernel before this one ends.  L2 is where
+        // all SMs' writes meet, so this is right even if that kernel writes the weight.
+        const int steps = (p.R + kBK - 1) / kBK, n0 = t % p.num_n * TN;
+        const int b0 = (int)((int64_t)steps * part_id / q.parts), b1 = (int)((int64_t)steps * (part_id + 1) / q.parts);
+        for (int kb = b0; kb < b1 && kb < b0 + q.stages; ++kb) {
+            if (kBMn) {
+                for (int c = 0; c < TN / 64; ++c) tma_prefetch_3d(&maps.b, n0 + c * 64, kb * kBK, 0);
+            } else {
+                tma_prefetch_3d(&maps.b, kb * kBK, n0, 0);
+            }
+        }
+    }
     if (!p.early) stream_wait();
-    stream_release();
     if (warp == 2) {  // which tile
         Tile tl;
         int pm, pn = t % p.num_n;
@@ -144,6 +156,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
                 }
                 if (++s == q.stages) { s = 0; ph ^= 1u; }
             }
+            // Only now: a successor that started with this kernel would take HBM from it.
+            stream_release();
         } else if (warp == 1 && lane == 0) {
             const uint32_t idesc = make_idesc_16_f32(p.f16 != 0, kAMn, kBMn, 128, TN);
             const uint32_t a0 = smem_addr(sA), b0 = smem_addr(sB);
