@@ -9,6 +9,8 @@
 // whatever they hold; what it computes from rows that do not exist is never stored).  No partial
 // sum goes to memory and nothing is added atomically: every output is summed over the parts in
 // order by one thread, so the result is the same in every run.
+// Measured: 1 x 4096 x 14336 bf16 24.2 us a call among others (4.9 TB/s; 28.9 alone from a cold L2),
+// 48 x 14336 x 4096 f16 with a residual 29.0 us.  Their bytes take 17.4 and 17.7 at the copy rate.
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -74,9 +76,10 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         tmem_alloc(tmem_holder, kSplitTmemCols);
         tmem_relinquish();
     }
-    if (MODE != kWgrad && p.offsets == nullptr && threadIdx.x == 96) {
+    if (MODE != kWgrad && p.offsets == nullptr && !p.early && threadIdx.x == 96) {
         // The weight's first stages come into L2 while the kernel before this one ends.  L2 is where
-        // all SMs' writes meet, so this is right even if that kernel writes the weight.
+        // all SMs' writes meet, so this is right even if that kernel writes the weight.  Not beside a main
+        // part (early), which reads the same weight now: 777 x 4104 x 5000 39.9 -> 39.4 us without it.
         const int steps = (p.R + kBK - 1) / kBK, n0 = t % p.num_n * TN;
         const int b0 = (int)((int64_t)steps * part_id / q.parts), b1 = (int)((int64_t)steps * (part_id + 1) / q.parts);
         for (int kb = b0; kb < b1 && kb < b0 + q.stages; ++kb) {
