@@ -291,3 +291,20 @@ def test_side_stream_and_graph():
     torch.cuda.synchronize()
     for k in first:
         assert torch.equal(first[k], other[k]) and torch.equal(first[k], graphed[k])
+
+
+@pytest.mark.parametrize("M,D", [(1, 64), (300, 64), (300, 777)])
+def test_a_workspace_of_the_queried_size_serves_and_a_smaller_one_is_refused(M, D):
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    y, r, dh = (torch.randn(M, D, device="cuda", generator=gen) for _ in range(3))
+    w = torch.ones(D, device="cuda")
+    out = lambda: dict(dy=torch.empty_like(y), dpre_weight=torch.empty_like(w))
+    kw, one, own = dict(pre="rms", pre_weight=w), out(), out()
+    n = tgc.tgc_block_norm_bwd_workspace_bytes(y, r, None, dh, **kw, **one)
+    assert n > 0
+    tgc.tgc_block_norm_bwd(y, r, None, dh, **kw, **one)
+    tgc.tgc_block_norm_bwd(y, r, None, dh, **kw, **own, workspace=torch.empty(n, device="cuda", dtype=torch.uint8))
+    assert all(torch.equal(one[k], own[k]) for k in one)
+    with pytest.raises(tgc.TGCError):
+        tgc.tgc_block_norm_bwd(y, r, None, dh, **kw, **own,
+                               workspace=torch.empty(n - 1, device="cuda", dtype=torch.uint8))

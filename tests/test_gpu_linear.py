@@ -411,3 +411,22 @@ def test_the_binding_refuses_operands_that_do_not_fit():
         tgc.tgc_linear_bwd(y, x, w, dw=torch.zeros(64, 32, device="cuda", dtype=BF))
     with pytest.raises(tgc.TGCError):
         tgc.tgc_linear(torch.zeros(4, 63, device="cuda", dtype=BF), torch.zeros(32, 63, device="cuda", dtype=BF), y)
+
+
+@pytest.mark.parametrize("M,groups", [(1, 0), (300, 0), (300, 3)])
+def test_a_workspace_of_the_queried_size_serves_and_a_smaller_one_is_refused(M, groups):
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x, dy, z = ints(g, M, 64), ints(g, M, 48), ints(g, M, 48)
+    lead = (groups,) if groups else ()
+    w = ints(g, *lead, 48, 64)
+    offsets = torch.tensor([0, 7, 7, M], device="cuda", dtype=torch.int32) if groups else None
+    out = lambda: dict(dx=torch.empty_like(x), dw=torch.empty_like(w),
+                       dbias=torch.empty(*lead, 48, device="cuda", dtype=x.dtype))
+    kw, one, own = dict(z=z, act="relu", offsets=offsets), out(), out()
+    n = tgc.tgc_linear_bwd_workspace_bytes(dy, x, w, **kw, **one)
+    assert n > 0
+    tgc.tgc_linear_bwd(dy, x, w, **kw, **one)
+    tgc.tgc_linear_bwd(dy, x, w, **kw, **own, workspace=torch.empty(n, device="cuda", dtype=torch.uint8))
+    assert all(torch.equal(one[k], own[k]) for k in one)
+    with pytest.raises(tgc.TGCError):
+        tgc.tgc_linear_bwd(dy, x, w, **kw, **own, workspace=torch.empty(n - 1, device="cuda", dtype=torch.uint8))

@@ -1,9 +1,10 @@
-"""ctypes binding of libtgc.so: argument marshalling only.
+"""Binding of libtgc.so: argument marshalling only, by ctypes, and natively (_ops.so) for the
+transformer-block operators, whose small calls the ctypes form would have held up.
 
 Every function here has the name of the C entry point it calls (include/tgc.h)
 and does nothing but turn torch tensors / Python values into pointers and
 integers; every step of the computation runs in the library's CUDA kernels.
-Loading fails loudly if libtgc.so has not been built: there is no fallback.
+Loading fails loudly if either library has not been built: there is no fallback.
 """
 from __future__ import annotations
 
@@ -449,6 +450,12 @@ def tgc_linear_bwd(dy, x, w, *, z=None, act: str = "none", dx=None, dw=None, dbi
     return _check(rc, "tgc_linear_bwd") if check else rc
 
 
+def tgc_linear_bwd_workspace_bytes(dy, x, w, *, z=None, act: str = "none", dx=None, dw=None, dbias=None,
+                                   offsets=None) -> int:
+    """Bytes of ``workspace`` the same call of tgc_linear_bwd takes (0: none, or it would refuse)."""
+    return (_ops or _native()).linear_bwd_bytes(dy, x, w, z, ACTS[act], dx, dw, dbias, offsets, None, None)
+
+
 def tgc_block_norm(y, r=None, h=None, *, x=None, gate=None, post: str = "none", post_weight=None, post_bias=None,
                    pre: str = "rms", pre_weight=None, pre_bias=None, res_scale: float = 1.0,
                    branch_scale: float = 1.0, eps: float = 1e-5, stream=None, check: bool = True) -> int:
@@ -471,6 +478,16 @@ def tgc_block_norm_bwd(y, r, dr, dh, *, gate=None, post: str = "none", post_weig
                                             pre_weight, res_scale, branch_scale, eps, dx, dy, dgate, dpost_weight,
                                             dpost_bias, dpre_weight, dpre_bias, workspace, _address(stream))
     return _check(rc, "tgc_block_norm_bwd") if check else rc
+
+
+def tgc_block_norm_bwd_workspace_bytes(y, r, dr, dh, *, gate=None, post: str = "none", post_weight=None,
+                                       post_bias=None, pre: str = "rms", pre_weight=None, res_scale: float = 1.0,
+                                       branch_scale: float = 1.0, eps: float = 1e-5, dx=None, dy=None, dgate=None,
+                                       dpost_weight=None, dpost_bias=None, dpre_weight=None, dpre_bias=None) -> int:
+    """Bytes of ``workspace`` the same call of tgc_block_norm_bwd takes (0: none, or it would refuse)."""
+    return (_ops or _native()).block_norm_bwd_bytes(
+        y, r, dr, dh, gate, NORMS[post], post_weight, post_bias, NORMS[pre], pre_weight, res_scale, branch_scale, eps,
+        dx, dy, dgate, dpost_weight, dpost_bias, dpre_weight, dpre_bias, None, None)
 
 
 def tgc_async_status(stream=None) -> None:

@@ -168,7 +168,7 @@ PyObject *guarded(Py_ssize_t n, Py_ssize_t want, F &&f) {
         return nullptr;
     }
     try {
-        return PyLong_FromLong(f());
+        return PyLong_FromLongLong((long long)f());
     } catch (const Refused &) {
     } catch (const std::exception &e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
@@ -203,9 +203,10 @@ PyObject *linear(PyObject *, PyObject *const *o, Py_ssize_t n) {
     });
 }
 
-// dy, x, w, z, act, dx, dw, dbias, offsets, workspace, stream
+// dy, x, w, z, act, dx, dw, dbias, offsets, workspace, stream.  QUERY: the workspace's bytes, no call.
+template <bool QUERY>
 PyObject *linear_bwd(PyObject *, PyObject *const *o, Py_ssize_t n) {
-    return guarded(n, 11, [&] {
+    return guarded(n, 11, [&]() -> int64_t {
         int dev = -1;
         const at::Tensor *dy = needed(o[0], "dy", &dev);
         const at::Tensor &x = *needed(o[1], "x", &dev), &w = *needed(o[2], "w", &dev);
@@ -229,6 +230,7 @@ PyObject *linear_bwd(PyObject *, PyObject *const *o, Py_ssize_t n) {
         a.dtype = dtype_of(type);
         a.act = (tgc_act)int_of(o[4]);
         a.stream = stream_of(o[10], dev);
+        if (QUERY) return (int64_t)g_linear_bwd_bytes(&a);
         const Workspace ws(o[9], g_linear_bwd_bytes(&a), x, o[10], a.stream, &dev);
         a.workspace = ws.ptr;
         a.workspace_bytes = ws.bytes;
@@ -269,9 +271,10 @@ PyObject *block_norm(PyObject *, PyObject *const *o, Py_ssize_t n) {
 }
 
 // y, r, dr, dh, gate, post, post_weight, post_bias, pre, pre_weight, res_scale, branch_scale, eps,
-// dx, dy, dgate, dpost_weight, dpost_bias, dpre_weight, dpre_bias, workspace, stream
+// dx, dy, dgate, dpost_weight, dpost_bias, dpre_weight, dpre_bias, workspace, stream.  QUERY: as above.
+template <bool QUERY>
 PyObject *block_norm_bwd(PyObject *, PyObject *const *o, Py_ssize_t n) {
-    return guarded(n, 22, [&] {
+    return guarded(n, 22, [&]() -> int64_t {
         int dev = -1;
         static const char *const names[4] = {"y", "r", "dr", "dh"};
         const at::Tensor *in[4], *like = nullptr;
@@ -307,6 +310,7 @@ PyObject *block_norm_bwd(PyObject *, PyObject *const *o, Py_ssize_t n) {
         a.dpre_bias = dense_of(tensor(o[19], "dpre_bias", &dev), "dpre_bias", type, -1, D);
         a.dtype = dtype_of(type);
         a.stream = stream_of(o[21], dev);
+        if (QUERY) return (int64_t)g_norm_bwd_bytes(&a);
         const Workspace ws(o[20], g_norm_bwd_bytes(&a), *like, o[21], a.stream, &dev);
         a.workspace = ws.ptr;
         a.workspace_bytes = ws.bytes;
@@ -339,9 +343,11 @@ PyCFunction fast(F f) {
 
 PyMethodDef methods[] = {{"bind", fast(bind), METH_FASTCALL, nullptr},
                          {"linear", fast(linear), METH_FASTCALL, nullptr},
-                         {"linear_bwd", fast(linear_bwd), METH_FASTCALL, nullptr},
+                         {"linear_bwd", fast(linear_bwd<false>), METH_FASTCALL, nullptr},
+                         {"linear_bwd_bytes", fast(linear_bwd<true>), METH_FASTCALL, nullptr},
                          {"block_norm", fast(block_norm), METH_FASTCALL, nullptr},
-                         {"block_norm_bwd", fast(block_norm_bwd), METH_FASTCALL, nullptr},
+                         {"block_norm_bwd", fast(block_norm_bwd<false>), METH_FASTCALL, nullptr},
+                         {"block_norm_bwd_bytes", fast(block_norm_bwd<true>), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops", "argument marshalling of the transformer-block operators", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

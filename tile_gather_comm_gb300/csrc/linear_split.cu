@@ -9,8 +9,8 @@
 // whatever they hold; what it computes from rows that do not exist is never stored).  No partial
 // sum goes to memory and nothing is added atomically: every output is summed over the parts in
 // order by one thread, so the result is the same in every run.
-// Measured: 1 x 4096 x 14336 bf16 24.2 us a call among others (4.9 TB/s; 28.9 alone from a cold L2),
-// 48 x 14336 x 4096 f16 with a residual 29.0 us.  Their bytes take 17.4 and 17.7 at the copy rate.
+// Measured: 1 x 4096 x 14336 bf16 23.7 to 24.2 us a call among others (4.9 TB/s; 28.9 alone from a cold L2),
+// 48 x 14336 x 4096 f16 with a residual 29 us.  Their bytes take 17.4 and 17.7 at the copy rate.
 #include <cstdint>
 #include <cstring>
 #include <mutex>
