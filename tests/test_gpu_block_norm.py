@@ -151,6 +151,17 @@ def test_backward(D, dtype, post, pre, gates, M, biases):
         assert close(outs[k], v, bounds[k], dtype), (k, float((outs[k].double() - v).abs().max()))
 
 
+@pytest.mark.parametrize("D", [513, 2047, 2049, 2501, 4095, 4097, 8191, 8193])
+@pytest.mark.parametrize("dtype", [BF, F16, F32])
+@pytest.mark.parametrize("post,pre,gates,M,biases", [("rms", "rms", 2, 38, False), ("layer", "layer", 1, 29, True),
+                                                     ("none", "rms", 5, 5, False), ("layer", "none", 0, 3, True),
+                                                     ("rms", "layer", 4, 400, False)])
+def test_odd_widths_of_every_length(D, dtype, post, pre, gates, M, biases):
+    """Single elements, 4 to 32 a thread, on both sides of each step."""
+    test_forward(D, dtype, post, pre, gates, M)
+    test_backward(D, dtype, post, pre, gates, M, biases)
+
+
 @pytest.mark.parametrize("M,gates", [(1, 1), (1, 0), (4096, 4096), (4096, 2), (4099, 1), (4099, 4099), (3000, 600)])
 @pytest.mark.parametrize("dtype,D", [(BF, 256), (F32, 33), (BF, 1024)])
 def test_backward_over_many_rows(M, gates, dtype, D):

@@ -28,12 +28,15 @@
 
 namespace tgc {
 
-// Threads of a block at most, and a kernel's register budget: 64 a thread where a thread holds one
-// vector (two teams of 512 on an SM) or a team may have 1024, 128 elsewhere.
+// Threads of a block at most, and with them a kernel's register budget.  Forward: 64 a thread where a
+// thread holds one vector (two teams of 512 on an SM) or a team may have 1024, 128 elsewhere.
+// Backward: 128, and 96 where a thread holds four single elements: more teams then fit an SM
+// (2500 x 1191 f16 33 -> 30 us, with layer norms 4096 x 1191 bf16 81 -> 61; 1000 x 777 fp32
+// 18.7 -> 19.5).
 template <typename T, int VEC, int NV>
-constexpr int kTeamMax = (VEC == 1 && NV == 16) || (sizeof(T) == 4 && NV == 4 && VEC > 1) ? 1024 : 512;
-template <typename T, int VEC, int NV>
-constexpr int kTeamBlocks = kTeamMax<T, VEC, NV> == 512 && NV == 1 ? 2 : 1;
+constexpr int kFwdMax = (VEC == 1 && NV == 16) || (sizeof(T) == 4 && NV == 4 && VEC > 1) ? 1024 : 512;
+template <int VEC, int NV>
+constexpr int kBwdMax = VEC == 1 && NV == 4 ? 640 : 512;
 
 // VEC consecutive elements as the words they are loaded in.  Arithmetic goes by L: two elements at
 // a time, or one where VEC is 1; get(i) is the i-th such lane in fp32, set(i, f) rounds it back.
@@ -184,6 +187,11 @@ __device__ __forceinline__ void team_sum_many(float (&v)[N], float (*smem)[N][32
 // input fit beside each other: one thread asks for whole rows with bulk copies, two rows ahead.
 template <int VEC, int NV>
 constexpr bool kStaged = VEC > 1 && NV <= 2;
+// The backward pass of wider rows: registers hold a few vectors of its inputs at a time, read where
+// they are used and twice a row (the second time from L1 or L2).  Held whole, rows spilled: 4000 x
+// 2501 bf16 took 1161 us (139), 2000 x 16384 bf16 422 (142), 2000 x 8192 fp32 692 (107).
+template <int VEC, int NV>
+constexpr bool kLean = !kStaged<VEC, NV> && VEC * NV > 4;
 template <int NV>
 constexpr int kFwdRows = NV == 1 ? 2 : 1;  // staged rows the forward kernel works on at a time
 template <int NV, bool FULL>
@@ -218,7 +226,7 @@ struct NormParams {
 // to shared memory (staged), or to registers.  BIAS: some norm has a bias.
 // STAGED false: also the form for few rows, one a worker, where nothing is to be had ahead.
 template <typename T, int VEC, int NV, bool BIAS, bool STAGED>
-__global__ void __launch_bounds__(kTeamMax<T, VEC, NV>, kTeamBlocks<T, VEC, NV>) norm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kFwdMax<T, VEC, NV>, NV == 1 ? 2 : 1) norm_kernel(const NormParams p) {
     using P = Pack<T, VEC>;
     using L = typename P::L;
     constexpr int NP = VEC > 1 ? VEC / 2 : 1;
@@ -440,7 +448,7 @@ struct NormBwdParams {
 // the columns' factors in registers and, unless FULL, works on two rows at a time: one reduction
 // serves both and their arithmetic overlaps.  Wider rows read the factors from shared memory.
 template <typename T, int VEC, int NV, bool FULL>
-__global__ void __launch_bounds__(kTeamMax<T, VEC, NV>) norm_bwd_kernel(const NormBwdParams p) {
+__global__ void __launch_bounds__(kBwdMax<VEC, NV>) norm_bwd_kernel(const NormBwdParams p) {
     using P = Pack<T, VEC>;
     using L = typename P::L;
     constexpr int NP = VEC > 1 ? VEC / 2 : 1;
@@ -448,7 +456,9 @@ __global__ void __launch_bounds__(kTeamMax<T, VEC, NV>) norm_bwd_kernel(const No
     constexpr int ROWS = kBwdRows<NV, FULL>;
     constexpr int NQ = FULL ? 12 : 6;        // sums a row
     constexpr int NS = FULL || ROWS == 2 ? 16 : 8;
-    constexpr bool STAGED = kStaged<VEC, NV>;
+    constexpr bool STAGED = kStaged<VEC, NV>, LEAN = kLean<VEC, NV>;
+    // Vectors of each input in registers at a time.
+    constexpr int HELD = LEAN ? (VEC == 1 ? 8 : FULL ? 1 : 2) : NV;
     __shared__ alignas(16) float smem[2][NS][32];
     __shared__ float means[2][2][32];
     __shared__ uint64_t bars[4][2];
@@ -531,7 +541,7 @@ __global__ void __launch_bounds__(kTeamMax<T, VEC, NV>) norm_bwd_kernel(const No
     };
     // Rows that are not staged come from memory, the next ones while the last are worked on where
     // there are registers for them.
-    constexpr bool AHEAD = !STAGED && NV <= 4;
+    constexpr bool AHEAD = !STAGED && !LEAN;
     P next[4][AHEAD ? ROWS : 1][AHEAD ? NV : 1];
     const T *src[4];  // each input's next row to ask for, at this thread's first column
     bool has[AHEAD ? NV : 1];
@@ -617,12 +627,12 @@ __global__ void __launch_bounds__(kTeamMax<T, VEC, NV>) norm_bwd_kernel(const No
         }
         for (int m = m0; m < m1; m += ROWS) {
             const uint32_t stage = turn & 1u;
-            P pr[ROWS][NV], pd[ROWS][NV], py[ROWS][NV], pt[ROWS][NV];
+            P pr[ROWS][HELD], pd[ROWS][HELD], py[ROWS][HELD], pt[ROWS][HELD];
             if constexpr (STAGED) row_wait(&bar[stage], (turn >> 1) & 1u, p.fault);
-            auto fetch = [&](P (&to)[NV], int rr, int j) {
+            auto fetch = [&](P (&to)[HELD], int rr, int j, int k0) {
 #pragma unroll
-                for (int k = 0; k < NV; ++k) {
-                    const int c = c0 + k * step;
+                for (int k = 0; k < HELD; ++k) {
+                    const int c = c0 + (k0 + k) * step;
                     if constexpr (STAGED)
                         to[k] = *reinterpret_cast<const P *>(stages + ((stage * ROWS + rr) * 4 + j) * row_bytes +
                                                              c * (int)sizeof(T));
@@ -633,23 +643,35 @@ __global__ void __launch_bounds__(kTeamMax<T, VEC, NV>) norm_bwd_kernel(const No
             };
 #pragma unroll
             for (int rr = 0; rr < ROWS; ++rr) {
-                fetch(pr[rr], rr, 0);
-                fetch(pd[rr], rr, 1);
-                fetch(py[rr], rr, 2);
-                fetch(pt[rr], rr, 3);
+                if (LEAN) break;
+                fetch(pr[rr], rr, 0, 0);
+                fetch(pd[rr], rr, 1, 0);
+                fetch(py[rr], rr, 2, 0);
+                fetch(pt[rr], rr, 3, 0);
             }
+            // LEAN: the next HELD vectors of the row, or of r and y alone
+            auto refill = [&](int k, bool all) {
+                if (!LEAN || k % HELD != 0) return;
+                fetch(pr[0], 0, 0, k);
+                fetch(py[0], 0, 2, k);
+                if (!all) return;
+                fetch(pd[0], 0, 1, k);
+                fetch(pt[0], 0, 3, k);
+            };
             if constexpr (AHEAD) fetch_next(m1 - m - ROWS);
             L mean_r = every<L>(0.0f), mean_y = every<L>(0.0f);  // negated
             if constexpr (FULL) {
                 if (p.pre == TGC_NORM_LAYER || p.post == TGC_NORM_LAYER) {
                     L t0 = every<L>(0.0f), t1 = every<L>(0.0f);
 #pragma unroll
-                    for (int k = 0; k < NV; ++k)
+                    for (int k = 0; k < NV; ++k) {
+                        refill(k, false);
 #pragma unroll
                         for (int i = 0; i < NP; ++i) {
-                            t0 = add(t0, pr[0][k].get(i));
-                            t1 = add(t1, py[0][k].get(i));
+                            t0 = add(t0, pr[0][k % HELD].get(i));
+                            t1 = add(t1, py[0][k % HELD].get(i));
                         }
+                    }
                     float s[2] = {total(t0), total(t1)};
                     team_sum(s, means, &mbuf);
                     if (p.pre == TGC_NORM_LAYER) mean_r = every<L>(-s[0] * p.inv_d);
@@ -664,14 +686,15 @@ __global__ void __launch_bounds__(kTeamMax<T, VEC, NV>) norm_bwd_kernel(const No
                 for (L &x : sl) x = every<L>(0.0f);
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
+                    refill(k, true);
                     if (c0 + k * step >= p.D) continue;
                     L w[NP], b[NP];
                     factors(k, w, b);
 #pragma unroll
                     for (int i = 0; i < NP; ++i) {
-                        L r = pr[rr][k].get(i), y = py[rr][k].get(i);
+                        L r = pr[rr][k % HELD].get(i), y = py[rr][k % HELD].get(i);
                         if (FULL) { r = add(r, mean_r); y = add(y, mean_y); }
-                        const L q = mul(pd[rr][k].get(i), w[i]), d = pt[rr][k].get(i), by = mul(b[i], y);
+                        const L q = mul(pd[rr][k % HELD].get(i), w[i]), d = pt[rr][k % HELD].get(i), by = mul(b[i], y);
                         sl[0] = fma(r, r, sl[0]);
                         sl[1] = fma(y, y, sl[1]);
                         sl[2] = fma(q, r, sl[2]);
@@ -718,17 +741,20 @@ __global__ void __launch_bounds__(kTeamMax<T, VEC, NV>) norm_bwd_kernel(const No
                 const L l1 = every<L>(-R * s1), le = every<L>(-Y * e1), rs = every<L>(p.res_scale);
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
-                    pr[rr][k].forget(); pd[rr][k].forget(); py[rr][k].forget(); pt[rr][k].forget();
+                    if constexpr (!LEAN) {
+                        pr[rr][k].forget(); pd[rr][k].forget(); py[rr][k].forget(); pt[rr][k].forget();
+                    }
+                    refill(k, true);
                     const int c = c0 + k * step;
                     if (c >= p.D) continue;
                     L w[NP], b[NP], ox[NP], oy[NP];
                     factors(k, w, b);
 #pragma unroll
                     for (int i = 0; i < NP; ++i) {
-                        L r = pr[rr][k].get(i), y = py[rr][k].get(i);
+                        L r = pr[rr][k % HELD].get(i), y = py[rr][k % HELD].get(i);
                         if (FULL) { r = add(r, mean_r); y = add(y, mean_y); }
-                        const L rh = mul(lR, r), yh = mul(lY, y), dh = pd[rr][k].get(i);
-                        L t = fma(lR, mul(dh, w[i]), fma(k_r, rh, pt[rr][k].get(i)));
+                        const L rh = mul(lR, r), yh = mul(lY, y), dh = pd[rr][k % HELD].get(i);
+                        L t = fma(lR, mul(dh, w[i]), fma(k_r, rh, pt[rr][k % HELD].get(i)));
                         if (FULL) t = add(t, l1);
                         ox[i] = mul(rs, t);
                         a_s[k][i] = fma(t, yh, a_s[k][i]);
@@ -880,26 +906,30 @@ static int norm_matrix(const void *p, int64_t rows, int64_t D, int es, int64_t *
 
 static bool norm_kind(tgc_norm k) { return k == TGC_NORM_NONE || k == TGC_NORM_RMS || k == TGC_NORM_LAYER; }
 
-// Threads a team and vectors a thread for rows of D: 1, 2 or 4 vectors, or 1, 4 or 16 single
-// elements, a thread, the fewest that a team of 512 (1024 at the widest) covers the row with.
+// Threads a team and vectors a thread for rows of D, the fewest vectors that a team of 512 covers the
+// row with.  Forward: 1, 2 or 4 vectors or 1, 4, 8 or 16 single elements, the last of each with
+// teams of up to 1024 where 512 do not cover the row.  Backward, whose threads keep sums too: up to
+// 8 vectors or 32 elements, no team above 512.
 struct TeamShape {
     int vec, nv, team, teams;  // teams a block
-    int per_sm;                // teams an SM holds, from the kernels' register budget
+    int per_sm;                // teams an SM holds, from the kernel's register budget
 };
-static TeamShape team_shape(int64_t D, int es, bool vec) {
+static TeamShape team_shape(int64_t D, int es, bool vec, bool backward) {
     TeamShape s{};
     s.vec = vec && D * es % 16 == 0 ? 16 / es : 1;
     const int64_t n = (D + s.vec - 1) / s.vec;
-    const int steps[2][3] = {{1, 4, 16}, {1, 2, 4}};
-    for (int i = 0; i < 3; ++i) {
-        s.nv = steps[s.vec > 1][i];
-        if (n <= (int64_t)s.nv * 512) break;
+    const int steps[2][5] = {{1, 4, 8, 16, 32}, {1, 2, 4, 8, 8}};
+    const int last = s.vec > 1 ? (backward ? 8 : 4) : backward ? 32 : 16;
+    for (const int nv : steps[s.vec > 1]) {
+        s.nv = nv;
+        if (nv == last || n <= (int64_t)nv * 512) break;
     }
     s.team = (int)((n + s.nv - 1) / s.nv + 31) / 32 * 32;
     s.teams = s.team == 32 ? 4 : 1;
-    const bool regs64 = s.nv == 1 || (s.vec == 1 && s.nv == 16) || (es == 4 && s.nv == 4 && s.vec > 1);
-    s.per_sm = (regs64 ? 1024 : 512) / s.team;
-    if (s.per_sm < 1) s.per_sm = 1;
+    int threads;
+    if (backward) threads = s.vec == 1 && s.nv == 4 ? 640 : 512;
+    else threads = s.nv == 1 || (s.vec == 1 && s.nv == 16) || (es == 4 && s.nv == 4 && s.vec > 1) ? 1024 : 512;
+    s.per_sm = threads / s.team;
     return s;
 }
 
@@ -929,6 +959,7 @@ static int launch_norm(const NormParams &p, const TeamShape &s, cudaStream_t str
                            : launch_norm_nv<T, V, 4, kStaged<V, 4>>(p, bias, grid, block, stream);
     return s.nv == 1   ? launch_norm_nv<T, 1, 1, kStaged<1, 1>>(p, bias, grid, block, stream)
            : s.nv == 4 ? launch_norm_nv<T, 1, 4, kStaged<1, 4>>(p, bias, grid, block, stream)
+           : s.nv == 8 ? launch_norm_nv<T, 1, 8, kStaged<1, 8>>(p, bias, grid, block, stream)
                        : launch_norm_nv<T, 1, 16, kStaged<1, 16>>(p, bias, grid, block, stream);
 }
 
@@ -960,7 +991,7 @@ static int norm_impl(tgc_block_norm_args a) {
         int64_t ld = a.D;
         TGC_TRY(norm_matrix(v, v == a.gate ? a.gates : 1, a.D, es, &ld, &vec));
     }
-    const TeamShape s = team_shape(a.D, es, vec);
+    const TeamShape s = team_shape(a.D, es, vec, false);
     NormParams p{};
     p.y = a.y; p.x = a.x; p.gate = a.gate;
     p.post_w = a.post_weight; p.post_b = a.post_bias; p.pre_w = a.pre_weight; p.pre_b = a.pre_bias;
@@ -981,8 +1012,10 @@ static int norm_impl(tgc_block_norm_args a) {
 }
 
 // How the backward pass deals its rows: a worker for every team that the card's 152 SMs hold at
-// once (one of 512 threads with 128 registers each, more for narrow rows), units of at least 2 rows, and whole gate segments where there are enough.  It
-// goes by D and the type alone, so the workspace's size does not depend on the pointers.
+// once, units of at least 2 rows, and whole gate segments where there are enough.  It goes by D and
+// the type alone, so the workspace's size does not depend on the pointers.  Teams an SM: 16 warps
+// where rows come in 16-byte vectors; rows of odd widths, read element by element, take more warps
+// and fewer teams fit.
 struct NormPlan {
     int segments, rows_per_gate, units_per_gate, unit_rows, units, workers;
     size_t gate_off, total;
@@ -991,7 +1024,9 @@ struct NormPlan {
 static NormPlan norm_plan(const tgc_block_norm_bwd_args &a) {
     NormPlan q{};
     const int64_t row = a.D * norm_elem(a.dtype);
-    const int64_t target = 152 * (row >= 8192 ? 1 : row <= 1024 ? 8 : 8192 / row);
+    const TeamShape s = team_shape(a.D, norm_elem(a.dtype), true, true);
+    const int64_t per_sm = s.vec == 1 ? s.per_sm : row >= 8192 ? 1 : 8192 / row;
+    const int64_t target = 152 * (per_sm > 8 ? 8 : per_sm);
     q.segments = a.gate != nullptr ? (int)a.gates : 1;
     q.rows_per_gate = (int)(a.M / q.segments);
     int64_t upg = (target + q.segments - 1) / q.segments;
@@ -1069,11 +1104,14 @@ static int launch_norm_bwd(const NormBwdParams &p, const NormSumParams &q, int n
     if (s.vec > 1)
         rc = s.nv == 1 ? launch_norm_bwd_nv<T, V, 1>(p, full, grid, block, stream)
            : s.nv == 2 ? launch_norm_bwd_nv<T, V, 2>(p, full, grid, block, stream)
-                       : launch_norm_bwd_nv<T, V, 4>(p, full, grid, block, stream);
+           : V == 8 || s.nv == 4 ? launch_norm_bwd_nv<T, V, 4>(p, full, grid, block, stream)
+                                 : launch_norm_bwd_nv<T, V, V == 8 ? 4 : 8>(p, full, grid, block, stream);
     else
         rc = s.nv == 1 ? launch_norm_bwd_nv<T, 1, 1>(p, full, grid, block, stream)
-           : s.nv == 4 ? launch_norm_bwd_nv<T, 1, 4>(p, full, grid, block, stream)
-                       : launch_norm_bwd_nv<T, 1, 16>(p, full, grid, block, stream);
+           : s.nv == 4  ? launch_norm_bwd_nv<T, 1, 4>(p, full, grid, block, stream)
+           : s.nv == 8  ? launch_norm_bwd_nv<T, 1, 8>(p, full, grid, block, stream)
+           : s.nv == 16 ? launch_norm_bwd_nv<T, 1, 16>(p, full, grid, block, stream)
+                        : launch_norm_bwd_nv<T, 1, 32>(p, full, grid, block, stream);
     if (rc != TGC_OK) return rc;
     if (nsums == 0) return TGC_OK;
     const int threads = q.workers > 200 || q.units_per_gate > 200 ? 512 : 256;
@@ -1100,7 +1138,7 @@ static int norm_bwd_impl(tgc_block_norm_bwd_args a) {
         if (a.workspace == nullptr || a.workspace_bytes < q.total) return TGC_ERR_WORKSPACE;
         if (reinterpret_cast<uintptr_t>(a.workspace) % 128 != 0) return TGC_ERR_ALIGN;
     }
-    const TeamShape s = team_shape(a.D, norm_elem(a.dtype), vec);
+    const TeamShape s = team_shape(a.D, norm_elem(a.dtype), vec, true);
     NormBwdParams p{};
     p.y = a.y; p.r = a.r; p.dr = a.dr; p.dh = a.dh; p.gate = a.gate;
     p.post_w = a.post_weight; p.post_b = a.post_bias; p.pre_w = a.pre_weight;

@@ -21,9 +21,9 @@
 //               through shared memory and TMA stores; boxes that a group's end cuts are stored by
 //               the lanes whose rows exist
 // Measured, bf16, 8192 x 4096 x 14336: plain 492 us in a burst (1955 TFLOP/s) and 570 in a loop of a
-// second (1689); with bias, gelu and z 609 to 613 a pass.  At 2048 rows the tensor pipe is active 79 % of
+// second (1689); with bias, gelu and z 609 to 620 a pass.  At 2048 rows the tensor pipe is active 79 % of
 // the time forward, 76 % for the input gradient, 83 % for the weight gradient.  16 experts of 4096 x
-// 4096 over 16384 uneven rows: 389 to 398 us with tanh-gelu and z, 71 tile rows where even groups fill 64.
+// 4096 over 16384 uneven rows: 389 to 408 us with tanh-gelu and z, 71 tile rows where even groups fill 64.
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -690,7 +690,7 @@ static int lin_dispatch(const LinearProduct &q, cudaStream_t stream) {
     if (!lin_choose<MODE>(q, sms, sms, room, kAllForms, &f)) return TGC_ERR_INVALID_ARG;
     // A last tile row that is mostly empty can cost a whole round.  Where the full rows' tiles leave
     // SMs idle, the rest of the rows go to the split kernel on those, at the same time: 777 x 4104 x
-    // 5000 44 -> 36 us (45.6 -> 39.7 with a residual; kFwd only, kDgrad's MN-major weight made the rest
+    // 5000 44 -> 36 us (45.6 -> 39.2 with a residual; kFwd only, kDgrad's MN-major weight made the rest
     // the longer part).
     const int64_t full = q.M / 256 * 256;
     if (MODE == kFwd && q.offsets == nullptr && full > 0 && full < q.M) {
