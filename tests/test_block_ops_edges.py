@@ -1,0 +1,43 @@
+"""The transformer-block operators at the edges of what they accept, without a GPU: index arithmetic for
+offsets that decrease, compiled for the host from the kernels' own header."""
+import os
+import subprocess
+
+import pytest
+
+from tile_gather_comm_gb300 import _build
+
+CSRC = _build.CSRC
+
+
+def _run(tmp_path, body, headers):
+    """Compiles a main() around `body` with nvcc and returns the whole numbers it prints."""
+    src, exe = tmp_path / "edge.cu", tmp_path / "edge"
+    src.write_text("#include <cstdio>\n#include <vector>\n" + "".join(f'#include "{h}"\n' for h in headers) +
+                   "using namespace tgc;\nint main() {\n" + body + "\nreturn 0;\n}\n")
+    subprocess.run([_build.nvcc(), *_build.ARCH, "-std=c++17", "-I", CSRC, "-I", _build.INCLUDE, str(src), "-o", str(exe)],
+                   check=True)
+    return [int(v) for v in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()]
+
+
+@pytest.mark.parametrize("M,groups", [(8192, 16), (300, 1024), ((1 << 31) - (1 << 16), 512)])
+@pytest.mark.parametrize("offsets", ["e % 2 ? M : 0", "M - e", "e % 3 ? 0x7fffffff : -5", "(int)((long long)M * e / groups)"])
+def test_the_bias_sum_stays_inside_its_partials(M, groups, offsets, tmp_path):
+    """Groups of 64-row chunks, as many partials as M rows and the groups size: no group's chunks lie past them,
+    and offsets that do not decrease lose none."""
+    past, lost = _run(tmp_path, f"""
+    const int M = {M}, groups = {groups}, kChunk = 64;
+    std::vector<int32_t> off(groups + 1);
+    for (int e = 0; e <= groups; ++e) off[e] = {offsets};
+    const int64_t listed = ((int64_t)M + kChunk - 1) / kChunk + groups;
+    int64_t first = 0, past = 0, lost = 0;
+    for (int e = 0; e < groups; ++e) {{
+        const RowRange g = group_range(off.data(), e, M);
+        const int n = (g.end - g.begin + kChunk - 1) / kChunk, k = listed_tiles(first, n, listed);
+        past += k < 0 || k > n || (k > 0 && first + k > listed);
+        lost += n - k;
+        first += n;
+    }}
+    printf("%lld %lld\\n", (long long)past, (long long)lost);""", ["groups.cuh"])
+    assert past == 0
+    assert lost >= 0 and (lost == 0 or "groups" not in offsets)

@@ -1,0 +1,50 @@
+"""What the transformer-block operators do at the edges of what they accept, on the GPU: offsets that decrease."""
+import pytest
+import torch
+
+import tile_gather_comm_gb300 as tgc
+from tests.helpers import requires_gpu
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    requires_gpu()
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+# ---------------------------------------------------------------- offsets
+
+
+@pytest.mark.parametrize("M,groups", [(300, 16), (1000, 7), (300, 1000)])
+@pytest.mark.parametrize("act", ["none", "relu"])
+def test_offsets_that_decrease_stay_inside_the_workspace(M, groups, act):
+    """Offsets 0, M, 0, M, ...: every even group has all rows, more chunks in all than the workspace has partial
+    sums.  What lies behind the queried size is NaN, far past any place those chunks would have had."""
+    g, K, N = gen(M + groups), 64, 48
+    ints = lambda *s: torch.randint(-2, 3, s, generator=g, device="cuda").to(BF)  # noqa: E731
+    x, dy, z, w1 = ints(M, K), ints(M, N), ints(M, N), ints(N, K)
+    w = w1.expand(groups, N, K).contiguous()
+    offsets = torch.tensor([0, M] * ((groups + 2) // 2), device="cuda", dtype=torch.int32)[:groups + 1]
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    db = torch.empty(groups, N, device="cuda", dtype=BF)
+    kw = dict(z=z, act=act, dx=dx, dw=dw, dbias=db, offsets=offsets)
+    n = tgc.tgc_linear_bwd_workspace_bytes(dy, x, w, **kw)
+    chunks = (M + 63) // 64
+    ws = torch.full((n + 4 * N * chunks * groups,), 0xff, device="cuda", dtype=torch.uint8)
+    tgc.tgc_linear_bwd(dy, x, w, workspace=ws, **kw)
+    dz = dy.double() * (z > 0) if act == "relu" else dy.double()
+    assert torch.equal(dx, (dz @ w1.double()).to(BF))
+    full = (dz.t() @ x.double()).to(BF)
+    assert bool((dw[0::2] == full).all()) and not dw[1::2].any()
+    assert not db.isnan().any() and bool((ws[n:] == 0xff).all())
+    whole = [e for e in range(0, groups, 2) if (e // 2 + 1) * chunks <= chunks + groups]
+    assert 0 in whole and bool((db[whole] == dz.sum(0).to(BF)).all()) and not db[1::2].any()
+    y = torch.empty(M, N, device="cuda", dtype=BF)
+    tgc.tgc_linear(x, w, y, offsets=offsets)
+    assert torch.equal(y, (x.double() @ w1.double().t()).to(BF))

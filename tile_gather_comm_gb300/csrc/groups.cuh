@@ -13,12 +13,19 @@ struct RowRange {
 };
 
 // offsets == nullptr: one group of all M rows.
-__device__ __forceinline__ RowRange group_range(const int32_t *offsets, int e, int M) {
+__host__ __device__ inline RowRange group_range(const int32_t *offsets, int e, int M) {
     if (offsets == nullptr) return {0, M};
     int a = offsets[e], b = offsets[e + 1];
     a = a < 0 ? 0 : a > M ? M : a;
     b = b < a ? a : b > M ? M : b;
     return {a, b};
+}
+
+// Of the n tiles that a group has from place `first` of a list on, how many the list of `listed` tiles
+// holds.  Offsets that decrease give groups that overlap, with more tiles in all than the list that M
+// rows and the number of groups size; what lies past its end does not exist.
+__host__ __device__ inline int listed_tiles(int64_t first, int n, int64_t listed) {
+    return first >= listed ? 0 : listed - first < n ? (int)(listed - first) : n;
 }
 
 // Warp-collective: tile `t` of the list that cuts every group into tiles of `tile` rows, in

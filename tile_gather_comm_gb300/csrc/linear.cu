@@ -127,33 +127,35 @@ __global__ void __launch_bounds__(256) dz_kernel(const DzParams p) {
 }
 
 // Sums each group's chunks in order: 32 columns x 8 chunk lanes a block, then the lanes in order.
+// `listed`: chunks that dz_kernel was launched for.
 // 4.7 us for the 32 chunks of 2048 x 14336: a launch's length.
 template <typename T>
-__global__ void __launch_bounds__(256) bias_sum_kernel(const float *partial, T *db, int M, int N, const int32_t *offsets, int early) {
+__global__ void __launch_bounds__(256) bias_sum_kernel(const float *partial, T *db, int M, int N, const int32_t *offsets,
+                                                       int64_t listed, int early) {
     __shared__ float part[8][32];
     if (!early) stream_wait();
     stream_release();
     const int e = blockIdx.y;
-    int first = 0;  // this group's first chunk
+    int64_t first = 0;  // this group's first chunk
     if (offsets != nullptr) {
-        int mine = 0;
+        unsigned long long mine = 0;  // groups that overlap can have more chunks than 32 bits count
         for (int i = threadIdx.x; i < e; i += 256) {
             const RowRange g = group_range(offsets, i, M);
-            mine += (g.end - g.begin + kChunk - 1) / kChunk;
+            mine += (unsigned)((g.end - g.begin + kChunk - 1) / kChunk);
         }
-        __shared__ int s_first;
+        __shared__ unsigned long long s_first;
         if (threadIdx.x == 0) s_first = 0;
         __syncthreads();
         atomicAdd(&s_first, mine);  // integers: the order does not matter
         __syncthreads();
-        first = s_first;
+        first = (int64_t)s_first;
     }
     const RowRange g = group_range(offsets, e, M);
-    const int chunks = (g.end - g.begin + kChunk - 1) / kChunk;
+    const int chunks = listed_tiles(first, (g.end - g.begin + kChunk - 1) / kChunk, listed);
     const int c = threadIdx.x % 32, l = threadIdx.x / 32, n = blockIdx.x * 32 + c;
     float s = 0.0f;
     if (n < N)
-        for (int k = l; k < chunks; k += 8) s += partial[(int64_t)(first + k) * N + n];
+        for (int k = l; k < chunks; k += 8) s += partial[(first + k) * N + n];
     part[l][c] = s;
     __syncthreads();
     if (l == 0 && n < N) {
@@ -332,9 +334,9 @@ static int linear_bwd_impl(tgc_linear_bwd_args a) {
         const cudaError_t e =
             a.dtype == TGC_BF16
                 ? launch_overlapped(bias_sum_kernel<__nv_bfloat16>, grid, dim3(256), 0, 1, a.stream, partial,
-                                    static_cast<__nv_bfloat16 *>(a.dbias), (int)a.M, (int)a.N, a.offsets, early)
+                                    static_cast<__nv_bfloat16 *>(a.dbias), (int)a.M, (int)a.N, a.offsets, l.chunks, early)
                 : launch_overlapped(bias_sum_kernel<__half>, grid, dim3(256), 0, 1, a.stream, partial,
-                                    static_cast<__half *>(a.dbias), (int)a.M, (int)a.N, a.offsets, early);
+                                    static_cast<__half *>(a.dbias), (int)a.M, (int)a.N, a.offsets, l.chunks, early);
         if (e != cudaSuccess) return cuda_fail(e);
     }
     return TGC_OK;
