@@ -41,3 +41,35 @@ def test_the_bias_sum_stays_inside_its_partials(M, groups, offsets, tmp_path):
     printf("%lld %lld\\n", (long long)past, (long long)lost);""", ["groups.cuh"])
     assert past == 0
     assert lost >= 0 and (lost == 0 or "groups" not in offsets)
+
+
+@pytest.mark.parametrize("tile", [128, 256])
+@pytest.mark.parametrize("M,groups", [(8192, 16), (300, 1024), (65536, 1024), ((1 << 31) - (1 << 16), 1024)])
+@pytest.mark.parametrize("offsets", ["e % 2 ? M : 0", "M - e", "(int)((long long)M * e / groups)"])
+def test_the_tile_table_ends_where_its_list_does(tile, M, groups, offsets, tmp_path):
+    """The products' table of tile rows, 32 groups at a time: places never decrease and never pass the list, and
+    are the plain sums where offsets do not decrease."""
+    wrong, cut = _run(tmp_path, f"""
+    const int M = {M}, groups = {groups}, tile = {tile};
+    std::vector<int32_t> off(groups + 1);
+    for (int e = 0; e <= groups; ++e) off[e] = {offsets};
+    const int listed = M / tile + (groups < M ? groups : M) + 1;
+    int64_t sum = 0, wrong = 0, cut = 0;
+    int base = 0, last = 0;
+    for (int e0 = 0; e0 < groups; e0 += 32) {{
+        int upto = 0;
+        for (int e = e0; e < e0 + 32 && e < groups; ++e) {{
+            const RowRange g = group_range(off.data(), e, M);
+            const int at = listed_place(base, upto, listed), n = (g.end - g.begin + tile - 1) / tile;
+            wrong += at < last || at > listed || at > sum;
+            cut += at < sum;
+            last = at;
+            upto += n;
+            sum += n;
+        }}
+        base = listed_place(base, upto, listed);
+    }}
+    wrong += base < last || base > listed;
+    printf("%lld %lld\\n", (long long)wrong, (long long)(cut + (base < sum)));""", ["groups.cuh"])
+    assert wrong == 0
+    assert cut == 0 or "groups" not in offsets

@@ -28,6 +28,11 @@ __host__ __device__ inline int listed_tiles(int64_t first, int n, int64_t listed
     return first >= listed ? 0 : listed - first < n ? (int)(listed - first) : n;
 }
 
+// The place in that list behind n tiles from place `at` on: never past its end, so neither a place nor
+// its product with what the list's length was checked against leaves 32 bits (n: the tiles of up to 32
+// groups of at least 128 rows a tile).
+__host__ __device__ inline int listed_place(int at, int n, int listed) { return at + n < listed ? at + n : listed; }
+
 // Warp-collective: tile `t` of the list that cuts every group into tiles of `tile` rows, in
 // order.  Returns the group, or -1 past the last tile; *index is the tile's place inside it.
 __device__ __forceinline__ int find_group_tile(const int32_t *offsets, int ngroups, int M, int tile, int t, int lane,

@@ -573,8 +573,10 @@ static int lin_launch(const LinearProduct &q, int dev, int sms, cudaStream_t str
         tiles = (int64_t)q.ngroups * p.num_m * p.num_n;
     } else {
         // with groups: no more than one partial tile row each
-        tiles = (q.M / C::kTM + (q.offsets != nullptr ? (q.ngroups < q.M ? q.ngroups : q.M) : 0) +
-                 (q.M % C::kTM != 0 || q.offsets != nullptr ? 1 : 0)) * p.num_n;
+        const int64_t listed = q.M / C::kTM + (q.offsets != nullptr ? (q.ngroups < q.M ? q.ngroups : q.M) : 0) +
+                               (q.M % C::kTM != 0 || q.offsets != nullptr ? 1 : 0);
+        p.listed = (int)listed;
+        tiles = listed * p.num_n;
     }
     if (tiles >= (int64_t(1) << 31)) return TGC_ERR_INVALID_ARG;
     if (clusters > tiles) clusters = (int)tiles;

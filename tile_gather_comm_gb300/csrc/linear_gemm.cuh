@@ -30,7 +30,8 @@ constexpr int kRowBox = 32;  // rows of the small boxes that load a partial tile
 struct LinearParams {
     int M;           // rows of the grouped axis
     int I, J, R;     // output rows (kWgrad only), output columns, reduction length (not kWgrad)
-    int num_m;       // tile rows of one group (kWgrad, or dense)
+    int num_m;       // tile rows of one group (kWgrad)
+    int listed;      // tile rows of all groups at most (not kWgrad)
     int num_n;       // tile columns
     int ngroups;
     int group_m;     // tile rows of a group of the raster
@@ -69,7 +70,7 @@ struct LinearMaps {
 };
 
 // Fills the maps for B boxes of b_rows rows (K-major) or 64 columns (MN-major); what q.z == null
-// leaves out is not set.  lin_params sets everything but num_m.
+// leaves out is not set.  lin_params sets everything but num_m and listed.
 constexpr int kLinMaxDevices = 64;
 bool lin_maps(LinearMaps *maps, const LinearProduct &q, int mode, int b_rows, int row_box);
 int lin_params(LinearParams *p, const LinearProduct &q, int tile_n);
@@ -100,7 +101,7 @@ struct Tile {
 };
 
 // Cumulative tile rows of the groups, built by one warp at kernel start: tile0[e] is the first
-// tile row of group e, tile0[ngroups] their number.
+// tile row of group e, tile0[ngroups] their number (p.listed where groups overlap and have more).
 __device__ __forceinline__ void build_tile_table(const LinearParams &p, int tile_m, int *tile0, int lane) {
     int base = 0;
     for (int e0 = 0; e0 < p.ngroups; e0 += 32) {
@@ -115,8 +116,8 @@ __device__ __forceinline__ void build_tile_table(const LinearParams &p, int tile
             const int v = __shfl_up_sync(0xffffffffu, upto, d);
             if (lane >= d) upto += v;
         }
-        if (e0 + lane < p.ngroups) tile0[e0 + lane] = base + upto - n;
-        base += __shfl_sync(0xffffffffu, upto, 31);
+        if (e0 + lane < p.ngroups) tile0[e0 + lane] = listed_place(base, upto - n, p.listed);
+        base = listed_place(base, __shfl_sync(0xffffffffu, upto, 31), p.listed);
     }
     if (lane == 0) tile0[p.ngroups] = base;
 }
