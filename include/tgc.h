@@ -545,6 +545,9 @@ typedef enum tgc_act {
 } tgc_act;
 
 #define TGC_MAX_GROUPS 1024
+/* Rows, columns and depth of the transformer-block operators at most, 2^31 - 4096: a tile or a block
+ * that begins inside an operand then ends below 2^31, the range of the kernels' indices. */
+#define TGC_MAX_SIZE 2147479552
 
 /*
  * tgc_linear -- matrix product with bias, activation and residual in its epilogue:
@@ -577,8 +580,8 @@ typedef enum tgc_act {
  *
  * Requirements: K > 0; K % 8 == 0 and N % 8 == 0, row strides % 8 == 0 and every
  * pointer 16-byte aligned (offsets 4-byte): TGC_ERR_ALIGN.  Row strides at least
- * the row length, M, N, K < 2^31 and ngroups * N < 2^31: TGC_ERR_INVALID_ARG.  M == 0 or N == 0
- * returns TGC_OK.  Asynchronous on `stream`, no allocation, no workspace; can be
+ * the row length, M, N, K <= TGC_MAX_SIZE and ngroups * N < 2^31: TGC_ERR_INVALID_ARG.  M == 0 or
+ * N == 0 returns TGC_OK.  Asynchronous on `stream`, no allocation, no workspace; can be
  * captured in a CUDA graph after one uncaptured call on the device.
  */
 typedef struct tgc_linear_args {
@@ -670,7 +673,7 @@ typedef enum tgc_norm { TGC_NORM_NONE = 0, TGC_NORM_RMS = 1, TGC_NORM_LAYER = 2 
  * dtype     TGC_BF16, TGC_F16 or TGC_F32, of every tensor.  Pointers need their
  *           element's alignment (16-byte aligned rows run faster).
  * Errors: TGC_ERR_INVALID_ARG (null y, neither r nor h, gates not a divisor of M,
- * D not in [1, TGC_NORM_MAX_D], M >= 2^31, eps, ...), TGC_ERR_DTYPE, TGC_ERR_ALIGN.  M == 0
+ * D not in [1, TGC_NORM_MAX_D], M > TGC_MAX_SIZE, eps, ...), TGC_ERR_DTYPE, TGC_ERR_ALIGN.  M == 0
  * returns TGC_OK.  Asynchronous on `stream`.
  */
 typedef struct tgc_block_norm_args {

@@ -1,13 +1,15 @@
 """The transformer-block operators at the edges of what they accept, without a GPU: index arithmetic for
-offsets that decrease, compiled for the host from the kernels' own header."""
+offsets that decrease, compiled for the host from the kernels' own header; the largest sizes."""
+import ctypes
 import os
 import subprocess
 
 import pytest
 
-from tile_gather_comm_gb300 import _build
+from tile_gather_comm_gb300 import _build, _lib
 
 CSRC = _build.CSRC
+FAKE = 1 << 20  # an aligned address that is never dereferenced
 
 
 def _run(tmp_path, body, headers):
@@ -73,3 +75,28 @@ def test_the_tile_table_ends_where_its_list_does(tile, M, groups, offsets, tmp_p
     printf("%lld %lld\\n", (long long)wrong, (long long)(cut + (base < sum)));""", ["groups.cuh"])
     assert wrong == 0
     assert cut == 0 or "groups" not in offsets
+
+
+@pytest.mark.parametrize("name", ["M", "K", "N"])
+@pytest.mark.parametrize("past", [8, 2048, 4096 - 8])
+def test_sizes_a_tile_short_of_32_bits_are_refused(name, past):
+    """Between the limit and 2^31 a tile's end leaves 32 bits; 8 is the smallest step of K and N."""
+    L, size = _lib.lib(), {"M": 8, "K": 8, "N": 8, name: _lib.MAX_SIZE + past}
+    assert f"#define TGC_MAX_SIZE {_lib.MAX_SIZE}\n" in open(os.path.join(_build.INCLUDE, "tgc.h")).read()
+    fwd = _lib.LinearArgs(x=FAKE, w=FAKE, y=FAKE, dtype=3, **size)
+    assert L.tgc_linear(ctypes.byref(fwd)) == _lib.TGC_ERR_INVALID_ARG
+    bwd = dict(dy=FAKE, x=FAKE, w=FAKE, dx=FAKE, dw=FAKE, dbias=FAKE, dtype=3, workspace=FAKE, workspace_bytes=1 << 60)
+    assert L.tgc_linear_bwd(ctypes.byref(_lib.LinearBwdArgs(**bwd, **size))) == _lib.TGC_ERR_INVALID_ARG
+    query = L.tgc_linear_bwd_workspace_bytes
+    assert query(ctypes.byref(_lib.LinearBwdArgs(**bwd, **size))) == 0
+    size[name] = _lib.MAX_SIZE  # accepted
+    assert query(ctypes.byref(_lib.LinearBwdArgs(**bwd, **size))) >= 4 * size["N"]
+
+
+@pytest.mark.parametrize("past", [1, 3000, 4095])
+def test_norm_rows_a_block_short_of_32_bits_are_refused(past):
+    L, M = _lib.lib(), _lib.MAX_SIZE + past
+    kw = dict(M=M, D=1, pre=1, eps=1e-5, dtype=3, res_scale=1, branch_scale=1)
+    assert L.tgc_block_norm(ctypes.byref(_lib.BlockNormArgs(y=FAKE, h=FAKE, **kw))) == _lib.TGC_ERR_INVALID_ARG
+    bwd = _lib.BlockNormBwdArgs(r=FAKE, dh=FAKE, dy=FAKE, workspace=FAKE, workspace_bytes=1 << 60, **kw)
+    assert L.tgc_block_norm_bwd(ctypes.byref(bwd)) == _lib.TGC_ERR_INVALID_ARG

@@ -39,6 +39,7 @@ ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 NORMS = {"none": 0, "rms": 1, "layer": 2}
 MAX_GROUPS = 1024              # TGC_MAX_GROUPS
 NORM_MAX_D = 16384             # TGC_NORM_MAX_D
+MAX_SIZE = (1 << 31) - 4096    # TGC_MAX_SIZE
 MAX_RANKS = 64
 TRACE_WORDS = 16
 TRACE = dict(start=0, wait_ns=1, waited_tiles=2, copy_first=3, copy_last=4, pieces=5, end=6, tiles=7,

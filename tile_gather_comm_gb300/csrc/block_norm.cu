@@ -972,7 +972,7 @@ static int launch_norm(const NormParams &p, const TeamShape &s, cudaStream_t str
 static int norm_impl(tgc_block_norm_args a) {
     const int es = norm_elem(a.dtype);
     if (es == 0) return TGC_ERR_DTYPE;
-    if (a.M < 0 || a.M >= (int64_t(1) << 31) || a.D < 1 || a.D > TGC_NORM_MAX_D) return TGC_ERR_INVALID_ARG;
+    if (a.M < 0 || a.M > TGC_MAX_SIZE || a.D < 1 || a.D > TGC_NORM_MAX_D) return TGC_ERR_INVALID_ARG;
     if (!norm_kind(a.post) || !norm_kind(a.pre)) return TGC_ERR_INVALID_ARG;
     if (a.gate == nullptr ? a.gates != 0 : (a.gates < 1 || a.M % a.gates != 0)) return TGC_ERR_INVALID_ARG;
     if (a.post == TGC_NORM_NONE && (a.post_weight != nullptr || a.post_bias != nullptr)) return TGC_ERR_INVALID_ARG;
@@ -1047,7 +1047,7 @@ static NormPlan norm_plan(const tgc_block_norm_bwd_args &a) {
 static int norm_bwd_check(tgc_block_norm_bwd_args &a, bool *vec) {
     const int es = norm_elem(a.dtype);
     if (es == 0) return TGC_ERR_DTYPE;
-    if (a.M < 0 || a.M >= (int64_t(1) << 31) || a.D < 1 || a.D > TGC_NORM_MAX_D) return TGC_ERR_INVALID_ARG;
+    if (a.M < 0 || a.M > TGC_MAX_SIZE || a.D < 1 || a.D > TGC_NORM_MAX_D) return TGC_ERR_INVALID_ARG;
     if (!norm_kind(a.post) || !norm_kind(a.pre)) return TGC_ERR_INVALID_ARG;
     if (a.gate == nullptr ? (a.gates != 0 || a.dgate != nullptr) : (a.gates < 1 || a.M % a.gates != 0))
         return TGC_ERR_INVALID_ARG;

@@ -171,15 +171,14 @@ __global__ void __launch_bounds__(256) bias_sum_kernel(const float *partial, T *
 static int check_common(tgc_dtype dtype, tgc_act act, int64_t M, int64_t K, int64_t N, const int32_t *offsets,
                         int ngroups) {
     if (M < 0 || K < 0 || N < 0) return TGC_ERR_INVALID_ARG;
-    const int64_t lim = int64_t(1) << 31;
-    if (M >= lim || K >= lim || N >= lim) return TGC_ERR_INVALID_ARG;
+    if (M > TGC_MAX_SIZE || K > TGC_MAX_SIZE || N > TGC_MAX_SIZE) return TGC_ERR_INVALID_ARG;
     if (dtype != TGC_BF16 && dtype != TGC_F16) return TGC_ERR_DTYPE;
     if (act < TGC_ACT_NONE || act > TGC_ACT_SILU) return TGC_ERR_INVALID_ARG;
     if (offsets == nullptr ? ngroups != 0 : (ngroups < 1 || ngroups > TGC_MAX_GROUPS)) return TGC_ERR_INVALID_ARG;
     if (!aligned(offsets, 4)) return TGC_ERR_ALIGN;
     if (K == 0) return TGC_ERR_INVALID_ARG;
     if (K % 8 != 0 || N % 8 != 0) return TGC_ERR_ALIGN;
-    if ((int64_t)(ngroups > 0 ? ngroups : 1) * N >= lim) return TGC_ERR_INVALID_ARG;
+    if ((int64_t)(ngroups > 0 ? ngroups : 1) * N >= (int64_t(1) << 31)) return TGC_ERR_INVALID_ARG;
     return TGC_OK;
 }
 
