@@ -100,3 +100,18 @@ def test_norm_rows_a_block_short_of_32_bits_are_refused(past):
     assert L.tgc_block_norm(ctypes.byref(_lib.BlockNormArgs(y=FAKE, h=FAKE, **kw))) == _lib.TGC_ERR_INVALID_ARG
     bwd = _lib.BlockNormBwdArgs(r=FAKE, dh=FAKE, dy=FAKE, workspace=FAKE, workspace_bytes=1 << 60, **kw)
     assert L.tgc_block_norm_bwd(ctypes.byref(bwd)) == _lib.TGC_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("M", [2122219135, 2133429024, 2140000000, _lib.MAX_SIZE])
+@pytest.mark.parametrize("D", [1, 8, 64])
+def test_the_norm_gradients_deal_out_the_most_rows(M, D):
+    """The partial sums go by the number of workers, which a million rows reach as well as any more do."""
+    L = _lib.lib()
+
+    def need(rows, **kw):
+        a = _lib.BlockNormBwdArgs(r=FAKE, dh=FAKE, dy=FAKE, dpre_weight=FAKE, M=rows, D=D, pre=1, eps=1e-5, dtype=3,
+                                  res_scale=1, branch_scale=1, **kw)
+        return L.tgc_block_norm_bwd_workspace_bytes(ctypes.byref(a))
+    assert 0 < need(M) <= need(1 << 20)
+    one = dict(gate=FAKE, gates=1, y=FAKE, dgate=FAKE)
+    assert need(M) < need(M, **one) <= need(1 << 20, **one)

@@ -1030,10 +1030,10 @@ static NormPlan norm_plan(const tgc_block_norm_bwd_args &a) {
     q.segments = a.gate != nullptr ? (int)a.gates : 1;
     q.rows_per_gate = (int)(a.M / q.segments);
     int64_t upg = (target + q.segments - 1) / q.segments;
-    const int64_t most = (q.rows_per_gate + 1) / 2;
+    const int64_t per_gate = q.rows_per_gate, most = (per_gate + 1) / 2;
     if (upg > most) upg = most;
-    q.unit_rows = (int)((q.rows_per_gate + upg - 1) / upg);
-    q.units_per_gate = (q.rows_per_gate + q.unit_rows - 1) / q.unit_rows;
+    q.unit_rows = (int)((per_gate + upg - 1) / upg);
+    q.units_per_gate = (int)((per_gate + q.unit_rows - 1) / q.unit_rows);
     q.units = q.units_per_gate * q.segments;
     q.workers = q.units < target ? q.units : (int)target;
     auto up = [](size_t v) { return (v + 127) / 128 * 128; };
