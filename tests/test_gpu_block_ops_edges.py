@@ -1,8 +1,13 @@
-"""What the transformer-block operators do at the edges of what they accept, on the GPU: offsets that decrease."""
+"""What the transformer-block operators do at the edges of what they accept, on the GPU: offsets that decrease,
+host threads that call at the same time."""
+import ctypes
+import threading
+
 import pytest
 import torch
 
 import tile_gather_comm_gb300 as tgc
+from tile_gather_comm_gb300 import _lib
 from tests.helpers import requires_gpu
 
 pytestmark = pytest.mark.gpu
@@ -48,3 +53,44 @@ def test_offsets_that_decrease_stay_inside_the_workspace(M, groups, act):
     y = torch.empty(M, N, device="cuda", dtype=BF)
     tgc.tgc_linear(x, w, y, offsets=offsets)
     assert torch.equal(y, (x.double() @ w1.double().t()).to(BF))
+
+
+# ---------------------------------------------------------------- host threads
+
+
+def test_host_threads_with_rows_of_two_widths():
+    """Two threads, each with a width of its own and a stream of its own: every call is accepted."""
+    L, rounds, M = _lib.lib(), 4000, 200
+    bad, done = [], []
+
+    def work(D, backward):
+        y, r, h, dr, dh = (torch.ones(M, D, device="cuda", dtype=BF) for _ in range(5))
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        kw = dict(M=M, D=D, post=1, pre=1, eps=1e-5, dtype=3, res_scale=1.0, branch_scale=1.0, stream=s.cuda_stream)
+        p = lambda t: t.data_ptr()  # noqa: E731
+        if backward:
+            a = _lib.BlockNormBwdArgs(y=p(y), r=p(r), dr=p(dr), dh=p(dh), dx=p(h), **kw)
+            f = L.tgc_block_norm_bwd
+        else:
+            a = _lib.BlockNormArgs(y=p(y), r=p(r), h=p(h), **kw)
+            f = L.tgc_block_norm
+        torch.cuda.synchronize()
+        start.wait()
+        for i in range(rounds):
+            rc = f(ctypes.byref(a))
+            if rc != _lib.TGC_OK:
+                bad.append((D, backward, rc))
+            if i % 200 == 199:
+                s.synchronize()
+        done.append((y, r, h, dr, dh))
+
+    for backward, widths in ((True, (4104, 8192)), (False, (6400, 8192))):
+        start = threading.Barrier(2)
+        ts = [threading.Thread(target=work, args=(D, backward)) for D in widths]
+        for t in ts:
+            t.start()
+        for t in ts:
+            t.join()
+    torch.cuda.synchronize()
+    assert len(done) == 4 and not bad, (len(bad), bad[:3])

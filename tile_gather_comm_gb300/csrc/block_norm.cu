@@ -15,6 +15,7 @@
 // Measured, bf16, 8192 x 4096, rms norms, gate and residual: forward 48.6 us (5.5 TB/s, 60 % of the
 // issue slots), backward 84 us and 8 to 9 for the sums over rows (89 together, the launches overlap):
 // 4.5 TB/s, held back by its own instructions, about 43 an element at 16 warps an SM.
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 #include <type_traits>
@@ -933,19 +934,41 @@ static TeamShape team_shape(int64_t D, int es, bool vec, bool backward) {
     return s;
 }
 
+constexpr int kMaxTeam = 512;  // threads of a block that has dynamic shared memory, at most
+
+// Lets a kernel have the dynamic shared memory that its widest rows take, once per device.  The limit
+// belongs to the kernel, not to a call: were it this call's size, another host thread's narrower rows
+// could lower it before this call's launch.
+template <auto KERNEL, int BYTES>
+static int allow_smem() {
+    static std::atomic<bool> done[64];
+    if (BYTES <= 40 * 1024) return TGC_OK;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (dev < 64 && done[dev].load(std::memory_order_acquire)) return TGC_OK;
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (dev < 64) done[dev].store(true, std::memory_order_release);
+    return TGC_OK;
+}
+
+template <typename T, int V, int NV, bool BIAS, bool STAGED>
+static int launch_norm_form(const NormParams &p, dim3 grid, dim3 block, cudaStream_t stream) {
+    constexpr int kThread = STAGED ? V * NV * 4 * kFwdRows<NV> * (int)sizeof(T) : 0;  // two stages of y and x
+    const int rc = allow_smem<norm_kernel<T, V, NV, BIAS, STAGED>, kMaxTeam * kThread>();
+    if (rc != TGC_OK) return rc;
+    const cudaError_t e = launch_overlapped(norm_kernel<T, V, NV, BIAS, STAGED>, grid, block,
+                                            (size_t)(block.x * block.y) * kThread, 1, stream, p);
+    return e == cudaSuccess ? TGC_OK : cuda_fail(e);
+}
+
 template <typename T, int V, int NV, bool STAGED>
 static int launch_norm_nv(const NormParams &p, bool bias, dim3 grid, dim3 block, cudaStream_t stream) {
     if constexpr (STAGED)
         if (p.M <= p.workers) return launch_norm_nv<T, V, NV, false>(p, bias, grid, block, stream);
-    auto kernel = bias ? norm_kernel<T, V, NV, true, STAGED> : norm_kernel<T, V, NV, false, STAGED>;
-    // two stages of y and x
-    const int smem = STAGED ? (int)(block.x * block.y) * V * NV * 4 * kFwdRows<NV> * (int)sizeof(T) : 0;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return cuda_fail(e);
-    }
-    const cudaError_t e = launch_overlapped(kernel, grid, block, (size_t)smem, 1, stream, p);
-    return e == cudaSuccess ? TGC_OK : cuda_fail(e);
+    return bias ? launch_norm_form<T, V, NV, true, STAGED>(p, grid, block, stream)
+                : launch_norm_form<T, V, NV, false, STAGED>(p, grid, block, stream);
 }
 
 template <typename T>
@@ -1080,19 +1103,22 @@ static int norm_bwd_check(tgc_block_norm_bwd_args &a, bool *vec) {
     return TGC_OK;
 }
 
-template <typename T, int V, int NV>
-static int launch_norm_bwd_nv(const NormBwdParams &p, bool full, dim3 grid, dim3 block, cudaStream_t stream) {
+template <typename T, int V, int NV, bool FULL>
+static int launch_norm_bwd_form(const NormBwdParams &p, dim3 grid, dim3 block, cudaStream_t stream) {
     // Two fp32 factors a column (128 KiB at the widest row) unless they are in registers, and two
     // stages of four inputs.
-    const int columns = (int)(block.y * block.x) * V * NV, rows = full ? kBwdRows<NV, true> : kBwdRows<NV, false>;
-    const int smem = columns * ((NV == 1 ? 0 : 8) + (kStaged<V, NV> ? 8 * rows * (int)sizeof(T) : 0));
-    auto kernel = full ? norm_bwd_kernel<T, V, NV, true> : norm_bwd_kernel<T, V, NV, false>;
-    if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return cuda_fail(e);
-    }
-    const cudaError_t e = launch_overlapped(kernel, grid, block, (size_t)smem, 1, stream, p);
+    constexpr int kThread = V * NV * ((NV == 1 ? 0 : 8) + (kStaged<V, NV> ? 8 * kBwdRows<NV, FULL> * (int)sizeof(T) : 0));
+    const int rc = allow_smem<norm_bwd_kernel<T, V, NV, FULL>, kMaxTeam * kThread>();
+    if (rc != TGC_OK) return rc;
+    const cudaError_t e = launch_overlapped(norm_bwd_kernel<T, V, NV, FULL>, grid, block,
+                                            (size_t)(block.x * block.y) * kThread, 1, stream, p);
     return e == cudaSuccess ? TGC_OK : cuda_fail(e);
+}
+
+template <typename T, int V, int NV>
+static int launch_norm_bwd_nv(const NormBwdParams &p, bool full, dim3 grid, dim3 block, cudaStream_t stream) {
+    return full ? launch_norm_bwd_form<T, V, NV, true>(p, grid, block, stream)
+                : launch_norm_bwd_form<T, V, NV, false>(p, grid, block, stream);
 }
 
 template <typename T>
