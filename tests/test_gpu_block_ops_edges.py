@@ -1,6 +1,7 @@
 """What the transformer-block operators do at the edges of what they accept, on the GPU: offsets that decrease,
-host threads that call at the same time."""
+host threads that call at the same time, infinities where a term has no factor for them."""
 import ctypes
+import math
 import threading
 
 import pytest
@@ -11,7 +12,7 @@ from tile_gather_comm_gb300 import _lib
 from tests.helpers import requires_gpu
 
 pytestmark = pytest.mark.gpu
-BF = torch.bfloat16
+BF, F16, F32 = torch.bfloat16, torch.float16, torch.float32
 
 
 @pytest.fixture(autouse=True)
@@ -94,3 +95,29 @@ def test_host_threads_with_rows_of_two_widths():
             t.join()
     torch.cuda.synchronize()
     assert len(done) == 4 and not bad, (len(bad), bad[:3])
+
+
+# ---------------------------------------------------------------- block norm
+
+
+@pytest.mark.parametrize("D", [64, 777, 1191, 2501, 4096, 8192, 16384])
+@pytest.mark.parametrize("dtype", [BF, F16, F32])
+@pytest.mark.parametrize("pre", ["none", "rms", "layer"])
+def test_without_a_post_norm_dy_does_not_depend_on_y(D, dtype, pre):
+    """r = a x + c gate y: dy = c gate t whatever y holds, with and without the gate's gradient."""
+    g, M, gates = gen(D), 6, 2
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda").to(dtype)  # noqa: E731
+    y, r, dr, dh, gate = n(M, D), n(M, D), n(M, D), n(M, D) if pre != "none" else None, n(gates, D)
+    y[1, 3], y[4, D - 1], y[5, 0] = math.inf, -math.inf, math.nan
+    kw = dict(gate=gate, pre=pre, branch_scale=0.5, res_scale=0.75)
+    dy, alone, dg, dgf = (torch.full_like(t, 7.0) for t in (y, y, gate, gate))
+    tgc.tgc_block_norm_bwd(y, r, dr, dh, dy=dy, dgate=dg, **kw)
+    tgc.tgc_block_norm_bwd(None, r, dr, dh, dy=alone, **kw)
+    assert bool(alone.isfinite().all())
+    assert torch.equal(dy, alone)
+    # and the gate's gradient is what it would be without those columns' values
+    finite = torch.where(y.isfinite(), y, torch.zeros_like(y))
+    tgc.tgc_block_norm_bwd(finite, r, dr, dh, dgate=dgf, **kw)
+    keep = torch.ones(D, dtype=torch.bool, device="cuda")
+    keep[3] = keep[D - 1] = keep[0] = False
+    assert torch.equal(dg[:, keep], dgf[:, keep])

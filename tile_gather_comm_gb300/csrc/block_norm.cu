@@ -740,36 +740,40 @@ __global__ void __launch_bounds__(kBwdMax<VEC, NV>) norm_bwd_kernel(const NormBw
                 // t = dr + R q - (R s1) - (R s0) rhat;  dy = Y b t - (Y e1) - (Y e0) yhat
                 const L lR = every<L>(R), lY = every<L>(Y), k_r = every<L>(-R * s0), k_y = every<L>(-Y * e0);
                 const L l1 = every<L>(-R * s1), le = every<L>(-Y * e1), rs = every<L>(p.res_scale);
+                // Without a post norm y is no part of dy, not even times zero: it may be infinite.
+                auto columns = [&](auto with_post) {
 #pragma unroll
-                for (int k = 0; k < NV; ++k) {
-                    if constexpr (!LEAN) {
-                        pr[rr][k].forget(); pd[rr][k].forget(); py[rr][k].forget(); pt[rr][k].forget();
-                    }
-                    refill(k, true);
-                    const int c = c0 + k * step;
-                    if (c >= p.D) continue;
-                    L w[NP], b[NP], ox[NP], oy[NP];
-                    factors(k, w, b);
-#pragma unroll
-                    for (int i = 0; i < NP; ++i) {
-                        L r = pr[rr][k % HELD].get(i), y = py[rr][k % HELD].get(i);
-                        if (FULL) { r = add(r, mean_r); y = add(y, mean_y); }
-                        const L rh = mul(lR, r), yh = mul(lY, y), dh = pd[rr][k % HELD].get(i);
-                        L t = fma(lR, mul(dh, w[i]), fma(k_r, rh, pt[rr][k % HELD].get(i)));
-                        if (FULL) t = add(t, l1);
-                        ox[i] = mul(rs, t);
-                        a_s[k][i] = fma(t, yh, a_s[k][i]);
-                        a_pre[k][i] = fma(dh, rh, a_pre[k][i]);
-                        oy[i] = fma(mul(lY, b[i]), t, mul(k_y, yh));
-                        if constexpr (FULL) {
-                            oy[i] = add(oy[i], le);
-                            a_t[k][i] = add(a_t[k][i], t);
-                            a_preb[k][i] = add(a_preb[k][i], dh);
+                    for (int k = 0; k < NV; ++k) {
+                        if constexpr (!LEAN) {
+                            pr[rr][k].forget(); pd[rr][k].forget(); py[rr][k].forget(); pt[rr][k].forget();
                         }
+                        refill(k, true);
+                        const int c = c0 + k * step;
+                        if (c >= p.D) continue;
+                        L w[NP], b[NP], ox[NP], oy[NP];
+                        factors(k, w, b);
+#pragma unroll
+                        for (int i = 0; i < NP; ++i) {
+                            L r = pr[rr][k % HELD].get(i), y = py[rr][k % HELD].get(i);
+                            if (FULL) { r = add(r, mean_r); y = add(y, mean_y); }
+                            const L rh = mul(lR, r), yh = mul(lY, y), dh = pd[rr][k % HELD].get(i);
+                            L t = fma(lR, mul(dh, w[i]), fma(k_r, rh, pt[rr][k % HELD].get(i)));
+                            if (FULL) t = add(t, l1);
+                            ox[i] = mul(rs, t);
+                            a_s[k][i] = fma(t, yh, a_s[k][i]);
+                            a_pre[k][i] = fma(dh, rh, a_pre[k][i]);
+                            oy[i] = decltype(with_post)::value ? fma(mul(lY, b[i]), t, mul(k_y, yh)) : mul(b[i], t);
+                            if constexpr (FULL) {
+                                oy[i] = add(oy[i], le);
+                                a_t[k][i] = add(a_t[k][i], t);
+                                a_preb[k][i] = add(a_preb[k][i], dh);
+                            }
+                        }
+                        if (p.dx != nullptr) store_pack<T, VEC>(p.dx, (m + rr) * p.lddx + c, ox);
+                        if (p.dy != nullptr) store_pack<T, VEC>(p.dy, (m + rr) * p.lddy + c, oy);
                     }
-                    if (p.dx != nullptr) store_pack<T, VEC>(p.dx, (m + rr) * p.lddx + c, ox);
-                    if (p.dy != nullptr) store_pack<T, VEC>(p.dy, (m + rr) * p.lddy + c, oy);
-                }
+                };
+                if (post) columns(std::true_type{}); else columns(std::false_type{});
             }
         }
         // The unit's share of the gate's and the post norm's gradients; the latter gather in the
