@@ -1,14 +1,15 @@
 """What the transformer-block operators do at the edges of what they accept, on the GPU: offsets that decrease,
-host threads that call at the same time, infinities where a term has no factor for them."""
+host threads that call at the same time, infinities where a term has no factor for them, waits."""
 import ctypes
 import math
+import os
 import threading
 
 import pytest
 import torch
 
 import tile_gather_comm_gb300 as tgc
-from tile_gather_comm_gb300 import _lib
+from tile_gather_comm_gb300 import _build, _lib
 from tests.helpers import requires_gpu
 
 pytestmark = pytest.mark.gpu
@@ -121,3 +122,46 @@ def test_without_a_post_norm_dy_does_not_depend_on_y(D, dtype, pre):
     keep = torch.ones(D, dtype=torch.bool, device="cuda")
     keep[3] = keep[D - 1] = keep[0] = False
     assert torch.equal(dg[:, keep], dgf[:, keep])
+
+
+# ---------------------------------------------------------------- waits
+
+
+@pytest.fixture(scope="module")
+def short_waits():
+    """The library with its limits on waits made so short that a pass outlasts them: a millisecond for the products."""
+    requires_gpu()
+    path = _build.build_variant(os.path.join(_build.PKG, "_build", "variant_short_waits"),
+                                {"TGC_LINEAR_TIMEOUT_NS": 1000000})
+    return _lib.load_library(path)
+
+
+def test_a_reduction_may_outlast_the_limit_of_a_wait(short_waits):
+    """Reductions of 65536 steps and more of a tile, several milliseconds each: a wait for all of it counts from the
+    last step.  Whole numbers, so sums below 2^24 are exact."""
+    L, g = short_waits, gen(21)
+    ints = lambda *s: torch.randint(-1, 2, s, generator=g, device="cuda", dtype=torch.int8).to(BF)  # noqa: E731
+    stream = torch.cuda.current_stream().cuda_stream
+
+    def status(rc):
+        assert rc == _lib.TGC_OK
+        return L.tgc_async_status(stream)
+
+    # few tiles: the depth is split over the CTAs of a cluster
+    M, K, N = 8, 1 << 25, 8
+    x, w = ints(M, K), ints(N, K)
+    y = torch.empty(M, N, device="cuda", dtype=BF)
+    a = _lib.LinearArgs(x=x.data_ptr(), w=w.data_ptr(), y=y.data_ptr(), M=M, K=K, N=N, dtype=3, stream=stream)
+    assert status(L.tgc_linear(ctypes.byref(a))) == _lib.TGC_OK
+    assert torch.equal(y, (x.float() @ w.float().t()).to(BF))
+    del x, w
+    # experts' weight gradients: one CTA or a pair for each tile, rows of another group behind the last step
+    for M, K, N in (((1 << 22) + 7, 64, 64), ((1 << 21) + 7, 512, 512)):
+        x, dy = ints(M, K), ints(M, N)
+        x[M - 9:], dy[M - 9:] = math.nan, math.nan
+        off = torch.tensor([0, M - 9], device="cuda", dtype=torch.int32)
+        dw = torch.empty(1, N, K, device="cuda", dtype=BF)
+        b = _lib.LinearBwdArgs(dy=dy.data_ptr(), x=x.data_ptr(), dw=dw.data_ptr(), M=M, K=K, N=N, dtype=3,
+                               offsets=off.data_ptr(), ngroups=1, stream=stream)
+        assert status(L.tgc_linear_bwd(ctypes.byref(b))) == _lib.TGC_OK
+        assert torch.equal(dw[0], (dy[:M - 9].float().t() @ x[:M - 9].float()).to(BF))

@@ -55,20 +55,6 @@ struct LCfg {
                                   (TGC_MAX_GROUPS + 8) * 4 + 512;
 };
 
-template <bool CLUSTER = false>
-__device__ __forceinline__ bool lin_wait(uint64_t *bar, uint32_t parity, const LinearParams &p) {
-    const uint32_t a = smem_addr(bar);
-    auto ready = [&] { return CLUSTER ? mbar_try_wait_cluster(a, parity) : mbar_try_wait(a, parity); };
-    if (ready()) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (uint64_t it = 1; it < (1ull << 40); ++it) {
-        if (ready()) return true;
-        if ((it & 63) == 0 && globaltimer_ns() - t0 > p.timeout_ns) break;
-    }
-    raise_status(p.fault, kStatusTimeout);
-    return false;
-}
-
 // kWgrad with groups: does step kb of the tile hold rows that are not the group's?
 __device__ __forceinline__ bool needs_repair(const LinearParams &p, const Tile &tl, int kb) {
     return p.offsets != nullptr && kb == tl.num_kb - 1 && (kb + 1) * kBK != tl.red;
@@ -159,7 +145,7 @@ __device__ void lin_role_tma(const LinearMaps &maps, const LinearParams &p, cons
 template <int CG, int MODE, int TN>
 __device__ void lin_role_mma(const LinearParams &p, const int *tile0, uint8_t *sA, uint8_t *sB, uint64_t *full,
                              uint64_t *fixed, uint64_t *empty, uint64_t *tfull, uint64_t *tempty, uint64_t *drain,
-                             uint32_t tmem_base) {
+                             uint32_t *progress, uint32_t tmem_base) {
     using C = LCfg<CG, MODE, TN>;
     const uint32_t idesc = make_idesc_16_f32(p.f16 != 0, C::kAMn, C::kBMn, C::kTM, TN);
     uint32_t it = 0, tc = 0, fixes = 0;  // fixes: per stage, the parity of its next repair
@@ -193,6 +179,7 @@ __device__ void lin_role_mma(const LinearParams &p, const int *tile0, uint8_t *s
             }
             if (CG == 1) mma_commit(&empty[s]);
             else mma_commit_pair_mc(&empty[s], (uint16_t)0x3);
+            if ((it & 15) == 0) publish_progress(progress, it + 1);
         }
         if (ok) {
             if (CG == 1) mma_commit(&tfull[acc]);
@@ -207,7 +194,7 @@ __device__ void lin_role_mma(const LinearParams &p, const int *tile0, uint8_t *s
 // kWgrad with groups: zero the rows of a group's last stage that are not the group's.
 template <int CG, int MODE, int TN>
 __device__ void lin_role_fix(const LinearParams &p, const int *tile0, uint8_t *sA, uint8_t *sB, uint64_t *raw,
-                             uint64_t *fixed, int lane) {
+                             uint64_t *fixed, uint32_t progress, int lane) {
     using C = LCfg<CG, MODE, TN>;
     uint32_t it = 0, phases = 0;  // phases: per stage, the parity of its next cut step
     const int tiles = num_tiles<MODE>(p, tile0);
@@ -220,7 +207,7 @@ __device__ void lin_role_fix(const LinearParams &p, const int *tile0, uint8_t *s
         const uint32_t s = (it - 1) % C::kStages, ph = (phases >> s) & 1u;
         phases ^= 1u << s;
         bool ok = true;
-        if (lane == 0) ok = lin_wait(&raw[s], ph, p);
+        if (lane == 0) ok = lin_wait(&raw[s], ph, p, progress);
         if (__shfl_sync(0xffffffffu, ok ? 1 : 0, 0) == 0) return;
         __syncwarp();
         // a row of a box is 128 bytes whatever the swizzle; 8 lanes zero one
@@ -243,8 +230,8 @@ __device__ void lin_role_fix(const LinearParams &p, const int *tile0, uint8_t *s
 
 template <int CG, int MODE, int TN>
 __device__ void lin_role_epilogue(const LinearMaps &maps, const LinearParams &p, const int *tile0, uint8_t *sC,
-                                  float *sBias, uint64_t *tfull, uint64_t *tempty, uint32_t tmem_base, uint32_t crank, int warp,
-                                  int lane) {
+                                  float *sBias, uint64_t *tfull, uint64_t *tempty, uint32_t progress, uint32_t tmem_base,
+                                  uint32_t crank, int warp, int lane) {
     using C = LCfg<CG, MODE, TN>;
     const int ew = warp - kEpiWarp0, q = warp & 3;  // q: the TMEM lane quarter a warp may read
     const int col0 = (ew >> 2) * (TN / 2);
@@ -291,7 +278,7 @@ __device__ void lin_role_epilogue(const LinearMaps &maps, const LinearParams &p,
             __syncwarp();
         }
         bool ok = true;
-        if (lane == 0) ok = lin_wait(&tfull[acc], aph, p);
+        if (lane == 0) ok = lin_wait(&tfull[acc], aph, p, progress);
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;  // warp-uniform: tcgen05.ld is .sync.aligned
         if (!ok) break;
         tc_fence_after();
@@ -396,8 +383,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     uint64_t *tfull = raw + C::kStages;
     uint64_t *tempty = tfull + 2;
     uint64_t *drain = tempty + 2;
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
-    static_assert((4 * C::kStages + 5) * 8 + 4 <= 512, "barrier area");
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1), *progress = tmem_holder + 1;
+    static_assert((4 * C::kStages + 5) * 8 + 8 <= 512, "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t crank = CG == 2 ? cluster_ctarank() : 0u;
@@ -413,6 +400,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             mbar_init(&tempty[a], kEpiWarps * CG);
         }
         mbar_init(drain, 1);
+        *progress = 0u;
         fence_mbarrier_init();
         fence_proxy_async_shared();
         prefetch_tensormap(&maps.a);
@@ -429,6 +417,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     if (CG == 1) __syncthreads(); else cluster_sync();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
+    const uint32_t progress0 = CG == 2 ? mapa_shared(smem_addr(progress), 0) : smem_addr(progress);  // the MMAs' steps
 
     if (warp == 0) {
         if (lane == 0) lin_role_tma<CG, MODE, TN, true, MODE == kFwd>(maps, p, tile0, sA, sB, full, empty, raw, crank);
@@ -437,13 +426,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             lin_role_tma<CG, MODE, TN, false, true>(maps, p, tile0, sA, sB, full, empty, raw, crank);
     } else if (warp == 1) {
         if (lane == 0 && crank == 0)
-            lin_role_mma<CG, MODE, TN>(p, tile0, sA, sB, full, fixed, empty, tfull, tempty, drain, tmem_base);
+            lin_role_mma<CG, MODE, TN>(p, tile0, sA, sB, full, fixed, empty, tfull, tempty, drain, progress, tmem_base);
     } else if (warp == 2) {
         if (MODE == kWgrad && p.offsets != nullptr)
-            lin_role_fix<CG, MODE, TN>(p, tile0, sA, sB, raw, fixed, lane);
+            lin_role_fix<CG, MODE, TN>(p, tile0, sA, sB, raw, fixed, progress0, lane);
     } else if (warp >= kEpiWarp0) {
-        lin_role_epilogue<CG, MODE, TN>(maps, p, tile0, sC, sBias, tfull, tempty, tmem_base, crank,
-                                          warp, lane);
+        lin_role_epilogue<CG, MODE, TN>(maps, p, tile0, sC, sBias, tfull, tempty, progress0, tmem_base,
+                                          crank, warp, lane);
     }
     // in a pair the even CTA's MMAs read the odd one's shared memory: neither leaves before both are done
     __syncwarp();
@@ -552,7 +541,7 @@ int lin_params(LinearParams *p, const LinearProduct &q, int tile_n) {
     p->act = q.act;
     p->f16 = q.f16;
     p->early = q.early;
-    p->timeout_ns = 4ull * 1000 * 1000 * 1000;
+    p->timeout_ns = TGC_LINEAR_TIMEOUT_NS;
     return device_fault_word(&p->fault);
 }
 

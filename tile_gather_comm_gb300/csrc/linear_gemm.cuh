@@ -25,6 +25,12 @@ namespace tgc {
 
 enum : int { kFwd = 0, kDgrad = 1, kWgrad = 2 };
 
+// A wait inside the products ends without success after this long; where it is for a whole reduction,
+// which may take longer than that, after this long without a step of it.
+#ifndef TGC_LINEAR_TIMEOUT_NS
+#define TGC_LINEAR_TIMEOUT_NS 4000000000ull
+#endif
+
 constexpr int kRowBox = 32;  // rows of the small boxes that load a partial tile of rows
 
 struct LinearParams {
@@ -99,6 +105,30 @@ struct Tile {
     int red0, red;     // kWgrad: first row and number of rows of the reduction
     int num_kb;        // 64-deep steps of the reduction, at least one
 };
+
+// Waits for the phase of `bar` with this parity; false, and the fault marked, when the limit passed.
+// progress != 0: address (shared::cluster) of a count of steps that starts the limit anew whenever it moves.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool lin_wait(uint64_t *bar, uint32_t parity, const LinearParams &p, uint32_t progress = 0) {
+    const uint32_t a = smem_addr(bar);
+    auto ready = [&] { return CLUSTER ? mbar_try_wait_cluster(a, parity) : mbar_try_wait(a, parity); };
+    if (ready()) return true;
+    uint64_t t0 = globaltimer_ns();
+    uint32_t seen = progress != 0 ? read_progress(progress) : 0u;
+    for (uint64_t it = 1; it < (1ull << 40); ++it) {
+        if (ready()) return true;
+        if ((it & 63) != 0) continue;
+        const uint64_t now = globaltimer_ns();
+        const uint32_t steps = progress != 0 ? read_progress(progress) : 0u;
+        if (steps != seen) {
+            seen = steps;
+            t0 = now;
+        }
+        if (now - t0 > p.timeout_ns) break;
+    }
+    raise_status(p.fault, kStatusTimeout);
+    return false;
+}
 
 // Cumulative tile rows of the groups, built by one warp at kernel start: tile0[e] is the first
 // tile row of group e, tile0[ngroups] their number (p.listed where groups overlap and have more).

@@ -58,6 +58,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     uint64_t *done = empty + kSplitMaxStages;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(done + 1);
     __shared__ Tile s_tile;
+    __shared__ uint32_t s_steps;  // whose products have been issued
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part_id = (int)(blockIdx.x % (unsigned)q.parts), t = (int)(blockIdx.x / (unsigned)q.parts);
@@ -67,6 +68,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
             mbar_init(&empty[s], 1);
         }
         mbar_init(done, 1);
+        s_steps = 0u;
         fence_mbarrier_init();
         fence_proxy_async_shared();
         prefetch_tensormap(MODE == kWgrad ? &maps.a : &maps.a_small);
@@ -121,17 +123,6 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
     const int kb0 = (int)((int64_t)tl.num_kb * part_id / q.parts), kb1 = (int)((int64_t)tl.num_kb * (part_id + 1) / q.parts);
     bool ok = true;
     if (rows > 0) {  // the same for the whole cluster
-        auto wait = [&](uint64_t *bar, uint32_t parity) {
-            const uint32_t a = smem_addr(bar);
-            if (mbar_try_wait(a, parity)) return true;
-            const uint64_t t0 = globaltimer_ns();
-            for (uint64_t it = 1; it < (1ull << 40); ++it) {
-                if (mbar_try_wait(a, parity)) return true;
-                if ((it & 63) == 0 && globaltimer_ns() - t0 > p.timeout_ns) break;
-            }
-            raise_status(p.fault, kStatusTimeout);
-            return false;
-        };
         if (warp == 0 && lane == 0) {
             const int box_bytes = kAMn ? (int)kBoxMn : q.row_box * kBK * 2;
             const int boxes = kAMn ? 2 : (rows + q.row_box - 1) / q.row_box;
@@ -139,7 +130,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
             int s = 0;
             uint32_t ph = 1;
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (!wait(&empty[s], ph)) break;
+                if (!lin_wait(&empty[s], ph, p)) break;
                 mbar_arrive_expect_tx(&full[s], tx);
                 uint8_t *a = sA + s * q.a_bytes, *b = sB + s * kBBytes;
                 const int r0 = kb * kBK;
@@ -167,7 +158,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
             int s = 0;
             uint32_t ph = 0;
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (!wait(&full[s], ph)) break;
+                if (!lin_wait(&full[s], ph, p)) break;
                 tc_fence_after();
                 const uint64_t ad = kAMn ? make_sw128_mnmajor_desc(a0 + s * q.a_bytes, kBoxMn)
                                          : make_sw128_kmajor_desc(a0 + s * q.a_bytes);
@@ -178,6 +169,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
                     mma_bf16_ss(tmem, ad + (uint64_t)(k * (kAMn ? 2048 >> 4 : 32 >> 4)),
                                 bd + (uint64_t)(k * (kBMn ? 2048 >> 4 : 32 >> 4)), idesc, kb > kb0 || k > 0 ? 1u : 0u);
                 mma_commit(&empty[s]);
+                if ((kb & 15) == 0) publish_progress(&s_steps, (uint32_t)(kb - kb0 + 1));
                 if (++s == q.stages) { s = 0; ph ^= 1u; }
             }
             mma_commit(done);
@@ -185,7 +177,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
         __syncwarp();
         // Every load this CTA issued has landed once the MMAs that read it have completed, so the
         // ring is free.  TMEM lane = row of the tile.
-        if (lane == 0) ok = wait(done, 0);
+        if (lane == 0) ok = lin_wait(done, 0, p, smem_addr(&s_steps));
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         tc_fence_after();
         const int qrow = (warp & 3) * 32, row = qrow + lane;

@@ -188,6 +188,17 @@ __device__ __forceinline__ void mbar_drain_wait(uint64_t *bar, uint32_t parity, 
     }
 }
 
+// A count of steps in shared memory that one thread publishes now and then and others, of the same CTA or of the
+// cluster (a shared::cluster address), look at to see whether it still moves.  Orders nothing.
+__device__ __forceinline__ void publish_progress(uint32_t *word, uint32_t steps) {
+    asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(smem_addr(word)), "r"(steps) : "memory");
+}
+__device__ __forceinline__ uint32_t read_progress(uint32_t cluster_addr) {
+    uint32_t v;
+    asm volatile("ld.volatile.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
 // ---------------------------------------------------------------- L2 cache policies
 
 // 64-bit L2 policies for the .L2::cache_hint forms of the bulk / tensor copies.
