@@ -129,10 +129,11 @@ def test_without_a_post_norm_dy_does_not_depend_on_y(D, dtype, pre):
 
 @pytest.fixture(scope="module")
 def short_waits():
-    """The library with its limits on waits made so short that a pass outlasts them: a millisecond for the products."""
+    """The library with its limits on waits made so short that a pass outlasts them: a millisecond for the products,
+    nothing for the norms' rows."""
     requires_gpu()
     path = _build.build_variant(os.path.join(_build.PKG, "_build", "variant_short_waits"),
-                                {"TGC_LINEAR_TIMEOUT_NS": 1000000})
+                                {"TGC_LINEAR_TIMEOUT_NS": 1000000, "TGC_ROW_TIMEOUT_NS": 0})
     return _lib.load_library(path)
 
 
@@ -165,3 +166,37 @@ def test_a_reduction_may_outlast_the_limit_of_a_wait(short_waits):
                                offsets=off.data_ptr(), ngroups=1, stream=stream)
         assert status(L.tgc_linear_bwd(ctypes.byref(b))) == _lib.TGC_OK
         assert torch.equal(dw[0], (dy[:M - 9].float().t() @ x[:M - 9].float()).to(BF))
+
+
+@pytest.mark.parametrize("D", [256, 4096, 8192])
+@pytest.mark.parametrize("full", [False, True])
+def test_norms_whose_wait_expires_end_and_say_so(short_waits, D, full):
+    """Rows that have not landed at the first look: the kernels go on without them, let them land, end and mark
+    the fault; every later call is right."""
+    g, M = gen(D), 20000
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF)  # noqa: E731
+    y, x, r, h, dr, dh, dx, dy = (n(M, D) for _ in range(8))
+    dw, db = (torch.empty(D, device="cuda", dtype=BF) for _ in range(2))
+    ws = torch.empty(1 << 25, device="cuda", dtype=torch.uint8)
+    stream = torch.cuda.current_stream().cuda_stream
+    p = lambda t: t.data_ptr()  # noqa: E731
+    kw = dict(M=M, D=D, post=2 if full else 1, pre=1, eps=1e-5, dtype=3, res_scale=1.0, branch_scale=1.0, stream=stream)
+    fwd = dict(y=p(y), x=p(x), pre_bias=p(db) if full else None)
+    bwd = dict(y=p(y), r=p(r), dr=p(dr), dh=p(dh), workspace=p(ws), workspace_bytes=ws.numel(), dpre_weight=p(dw),
+               dpre_bias=p(db) if full else None)
+    db.zero_()
+    seen = []
+    for _ in range(3):
+        rc = short_waits.tgc_block_norm(ctypes.byref(_lib.BlockNormArgs(r=p(dx), h=p(dy), **fwd, **kw)))
+        assert rc == _lib.TGC_OK
+        seen.append(short_waits.tgc_async_status(stream))
+        rc = short_waits.tgc_block_norm_bwd(ctypes.byref(_lib.BlockNormBwdArgs(dx=p(dx), dy=p(dy), **bwd, **kw)))
+        assert rc == _lib.TGC_OK
+        seen.append(short_waits.tgc_async_status(stream))
+    assert set(seen) <= {_lib.TGC_OK, _lib.TGC_ERR_TIMEOUT}
+    assert D < 4096 or seen[0] == seen[1] == _lib.TGC_ERR_TIMEOUT
+    tgc.tgc_block_norm(y, dx, dy, x=x, post="layer" if full else "rms", pre="rms", pre_bias=db if full else None)
+    tgc.tgc_async_status()
+    v = y.float() - (y.float().mean(1, keepdim=True) if full else 0)
+    want = x.float() + v * torch.rsqrt((v * v).mean(1, keepdim=True) + 1e-5)
+    assert bool(((dx.float() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-4).all())

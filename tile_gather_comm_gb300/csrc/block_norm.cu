@@ -198,16 +198,34 @@ constexpr int kFwdRows = NV == 1 ? 2 : 1;  // staged rows the forward kernel wor
 template <int NV, bool FULL>
 constexpr int kBwdRows = NV == 1 && !FULL ? 2 : 1;  // rows the backward kernel works on at a time
 
-// Waits for the phase with this parity; gives up after about two seconds and marks the fault.
-__device__ __forceinline__ void row_wait(uint64_t *bar, uint32_t parity, int *fault) {
-    const uint32_t a = smem_addr(bar);
-    if (mbar_try_wait(a, parity)) return;
+#ifndef TGC_ROW_TIMEOUT_NS
+#define TGC_ROW_TIMEOUT_NS 2000000000ull
+#endif
+
+// Waits for the rows of a turn.  If they do not land within the limit the fault is marked and *dead set to
+// 1 + turn: from then on the team waits no more and asks for no more rows, but goes through those that
+// remain, with wrong results.  A barrier of the team lies between the wait of a turn and its ask, so no
+// rows beyond the next turn's have been asked for then.  A limit of nothing (tests build the kernels so)
+// looks once.
+__device__ __forceinline__ void row_wait(uint64_t *bars, uint32_t turn, volatile uint32_t *dead, int *fault) {
+    const uint32_t a = smem_addr(&bars[turn & 1u]), parity = (turn >> 1) & 1u;
+    constexpr bool kLook = TGC_ROW_TIMEOUT_NS == 0;
+    if (kLook ? mbar_test_wait(a, parity) : mbar_try_wait(a, parity)) return;
+    if (*dead != 0) return;
     const uint64_t t0 = globaltimer_ns();
-    for (uint64_t it = 1; it < (1ull << 40); ++it) {
+    for (uint64_t it = 1; !kLook && it < (1ull << 40); ++it) {
         if (mbar_try_wait(a, parity)) return;
-        if ((it & 63) == 0 && globaltimer_ns() - t0 > 2000000000ull) break;
+        if ((it & 63) == 0 && (*dead != 0 || globaltimer_ns() - t0 > TGC_ROW_TIMEOUT_NS)) break;
     }
     raise_status(fault, kStatusTimeout);
+    *dead = turn + 1;
+}
+
+// At a kernel's end: what a dead team asked for has time to land before shared memory is given up.
+__device__ __forceinline__ void drain_rows(uint64_t *bars, const volatile uint32_t *dead) {
+    const uint32_t d = *dead;
+    if (d == 0) return;
+    for (uint32_t t = d - 1; t <= d; ++t) mbar_drain_wait(&bars[t & 1u], (t >> 1) & 1u, 200000000ull);
 }
 
 // ---------------------------------------------------------------- forward
@@ -234,13 +252,16 @@ __global__ void __launch_bounds__(kFwdMax<T, VEC, NV>, NV == 1 ? 2 : 1) norm_ker
     constexpr int ROWS = STAGED ? kFwdRows<NV> : 1;
     __shared__ float smem[2][ROWS][32];
     __shared__ uint64_t bars[4][2];
+    __shared__ uint32_t deads[4];
     extern __shared__ __align__(16) uint8_t staged[];  // a team's own: two stages of ROWS rows of y and x
     int buf = 0;
     const int worker = blockIdx.x * blockDim.y + threadIdx.y;
     uint64_t *const bar = bars[threadIdx.y];
+    volatile uint32_t *const dead = &deads[threadIdx.y];
     if (STAGED && threadIdx.x == 0) {
         mbar_init(&bar[0], 1);
         mbar_init(&bar[1], 1);
+        *dead = 0u;
         fence_mbarrier_init();
     }
     if (STAGED && blockDim.y == 1) __syncthreads(); else __syncwarp();
@@ -290,7 +311,7 @@ __global__ void __launch_bounds__(kFwdMax<T, VEC, NV>, NV == 1 ? 2 : 1) norm_ker
     for (int m = m0; m < m1; m += ROWS, ++turn) {
         const uint32_t stage = turn & 1u;
         const uint8_t *const here = stages + stage * ROWS * 2 * row_bytes;
-        if constexpr (STAGED) row_wait(&bar[stage], (turn >> 1) & 1u, p.fault);
+        if constexpr (STAGED) row_wait(bar, turn, dead, p.fault);
         L v[ROWS][NV][NP];  // columns past the row's end, and rows past the last, stay zeros
 #pragma unroll
         for (int rr = 0; rr < ROWS; ++rr)
@@ -399,7 +420,7 @@ __global__ void __launch_bounds__(kFwdMax<T, VEC, NV>, NV == 1 ? 2 : 1) norm_ker
         if constexpr (STAGED) {
             // past the sum (or the barrier) every thread has read this stage
             __syncwarp();
-            if (threadIdx.x == 0) ask(m + 2 * ROWS, (int)stage);
+            if (threadIdx.x == 0 && *dead == 0) ask(m + 2 * ROWS, (int)stage);
         }
         if (p.pre == TGC_NORM_NONE) continue;
 #pragma unroll
@@ -411,6 +432,7 @@ __global__ void __launch_bounds__(kFwdMax<T, VEC, NV>, NV == 1 ? 2 : 1) norm_ker
                 if (c0 + k * step < p.D) store_pack<T, VEC>(p.h, (m + rr) * p.ldh + c0 + k * step, v[rr][k]);
         }
     }
+    if (STAGED && threadIdx.x == 0) drain_rows(bar, dead);
 }
 
 // ---------------------------------------------------------------- backward
@@ -463,6 +485,7 @@ __global__ void __launch_bounds__(kBwdMax<VEC, NV>) norm_bwd_kernel(const NormBw
     __shared__ alignas(16) float smem[2][NS][32];
     __shared__ float means[2][2][32];
     __shared__ uint64_t bars[4][2];
+    __shared__ uint32_t deads[4];
     // A team's own: the columns' factors in fp32 (w_pre, and b of the unit being worked on), unless
     // in registers; then, where rows are staged, two stages of ROWS rows of r, dh, y and dr.
     extern __shared__ __align__(16) float dynamic[];
@@ -481,6 +504,7 @@ __global__ void __launch_bounds__(kBwdMax<VEC, NV>) norm_bwd_kernel(const NormBw
     float *const fb = fw + (REGS ? 0 : step * NV);
     uint8_t *const stages = reinterpret_cast<uint8_t *>(fb + (REGS ? 0 : step * NV));
     uint64_t *const bar = bars[threadIdx.y];
+    volatile uint32_t *const dead = &deads[threadIdx.y];
     L a_s[NV][NP], a_pre[NV][NP], a_t[FULL ? NV : 1][NP], a_preb[FULL ? NV : 1][NP];
     L rw[NP], rb[NP];  // the factors, where they are in registers
     auto clear = [](auto &a) {
@@ -579,6 +603,7 @@ __global__ void __launch_bounds__(kBwdMax<VEC, NV>) norm_bwd_kernel(const NormBw
         if (threadIdx.x == 0) {
             mbar_init(&bar[0], 1);
             mbar_init(&bar[1], 1);
+            *dead = 0u;
             fence_mbarrier_init();
         }
         if (blockDim.y == 1) __syncthreads(); else __syncwarp();
@@ -629,7 +654,7 @@ __global__ void __launch_bounds__(kBwdMax<VEC, NV>) norm_bwd_kernel(const NormBw
         for (int m = m0; m < m1; m += ROWS) {
             const uint32_t stage = turn & 1u;
             P pr[ROWS][HELD], pd[ROWS][HELD], py[ROWS][HELD], pt[ROWS][HELD];
-            if constexpr (STAGED) row_wait(&bar[stage], (turn >> 1) & 1u, p.fault);
+            if constexpr (STAGED) row_wait(bar, turn, dead, p.fault);
             auto fetch = [&](P (&to)[HELD], int rr, int j, int k0) {
 #pragma unroll
                 for (int k = 0; k < HELD; ++k) {
@@ -719,7 +744,7 @@ __global__ void __launch_bounds__(kBwdMax<VEC, NV>) norm_bwd_kernel(const NormBw
             if constexpr (STAGED) {
                 // Past the sum every thread has its part of these rows in registers: the stage is free.
                 __syncwarp();
-                if (threadIdx.x == 0) ask((int)stage);
+                if (threadIdx.x == 0 && *dead == 0) ask((int)stage);
                 ++turn;
             }
 #pragma unroll
@@ -827,6 +852,7 @@ __global__ void __launch_bounds__(kBwdMax<VEC, NV>) norm_bwd_kernel(const NormBw
     };
     put(2, a_pre);
     if constexpr (FULL) put(3, a_preb);
+    if (STAGED && threadIdx.x == 0) drain_rows(bar, dead);
 }
 
 // Adds the partials of one output vector: blockIdx.y 0..3 the parameter vectors, then one a gate.
