@@ -133,7 +133,17 @@ def short_waits():
     nothing for the norms' rows."""
     requires_gpu()
     path = _build.build_variant(os.path.join(_build.PKG, "_build", "variant_short_waits"),
-                                {"TGC_LINEAR_TIMEOUT_NS": 1000000, "TGC_ROW_TIMEOUT_NS": 0})
+                                {"TGC_LINEAR_TIMEOUT_NS": 1000000, "TGC_ROW_TIMEOUT_NS": 0},
+                                ["linear_gemm.cu", "linear_split.cu", "block_norm.cu"])
+    return _lib.load_library(path)
+
+
+@pytest.fixture(scope="module")
+def one_look():
+    """The library with products that give up where the first look at a barrier finds it open."""
+    requires_gpu()
+    path = _build.build_variant(os.path.join(_build.PKG, "_build", "variant_one_look"), {"TGC_LINEAR_TIMEOUT_NS": 0},
+                                ["linear_gemm.cu", "linear_split.cu"])
     return _lib.load_library(path)
 
 
@@ -200,3 +210,34 @@ def test_norms_whose_wait_expires_end_and_say_so(short_waits, D, full):
     v = y.float() - (y.float().mean(1, keepdim=True) if full else 0)
     want = x.float() + v * torch.rsqrt((v * v).mean(1, keepdim=True) + 1e-5)
     assert bool(((dx.float() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-4).all())
+
+
+@pytest.mark.parametrize("M,K,N,groups", [(4, 4096, 1024, 0), (2048, 2048, 2048, 0), (2048, 1024, 1024, 3), (300, 512, 264, 0)])
+def test_products_whose_wait_expires_end_and_say_so(one_look, M, K, N, groups):
+    """Loads that have not landed at the first look: the kernels give up, let them land, end and mark the
+    fault; every later call is right."""
+    L, g = one_look, gen(M + N)
+    ints = lambda *s: torch.randint(-1, 2, s, generator=g, device="cuda", dtype=torch.int8).to(BF)  # noqa: E731
+    lead = (groups,) if groups else ()
+    x, w, dy = ints(M, K), ints(*lead, N, K), ints(M, N)
+    off = torch.tensor([0, M // 3 + 5, M // 3 + 5, M - 7], device="cuda", dtype=torch.int32) if groups else None
+    y, dx, dw = torch.zeros_like(dy), torch.zeros_like(x), torch.zeros_like(w)
+    stream = torch.cuda.current_stream().cuda_stream
+    p = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
+    kw = dict(M=M, K=K, N=N, dtype=3, offsets=p(off), ngroups=groups, stream=stream)
+    assert L.tgc_linear(ctypes.byref(_lib.LinearArgs(x=p(x), w=p(w), y=p(y), **kw))) == _lib.TGC_OK
+    assert L.tgc_async_status(stream) == _lib.TGC_ERR_TIMEOUT
+    for out in (dict(dx=p(dx)), dict(dw=p(dw)), dict(dx=p(dx), dw=p(dw))):
+        a = _lib.LinearBwdArgs(dy=p(dy), x=p(x), w=p(w), **out, **kw)
+        assert L.tgc_linear_bwd(ctypes.byref(a)) == _lib.TGC_OK
+        assert L.tgc_async_status(stream) == _lib.TGC_ERR_TIMEOUT
+    assert L.tgc_async_status(stream) == _lib.TGC_OK  # read, and cleared
+    tgc.tgc_linear(x, w, y, offsets=off)
+    tgc.tgc_linear_bwd(dy, x, w, dx=dx, dw=dw, offsets=off)
+    tgc.tgc_async_status()
+    spans = list(zip(off.tolist(), off.tolist()[1:])) if groups else [(0, M)]
+    for e, (i, j) in enumerate(spans):
+        we, dwe = (w[e], dw[e]) if groups else (w, dw)
+        assert torch.equal(y[i:j], (x[i:j].float() @ we.float().t()).to(BF))
+        assert torch.equal(dx[i:j], (dy[i:j].float() @ we.float()).to(BF))
+        assert torch.equal(dwe, (dy[i:j].float().t() @ x[i:j].float()).to(BF))

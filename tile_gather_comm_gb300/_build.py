@@ -75,14 +75,15 @@ def _compile_ops() -> None:
     os.replace(tmp, OPS)
 
 
-def build_variant(out_dir: str, defines: dict) -> str:
+def build_variant(out_dir: str, defines: dict, sources: list | None = None) -> str:
     """Build the library with compile-time settings changed (e.g. {"TGC_COPY_LSU": 0})
-    into out_dir/libtgc.so and return its path; the in-tree library is not touched."""
+    into out_dir/libtgc.so and return its path; the in-tree library is not touched.
+    ``sources``: the only files that the settings concern; the others' objects are the in-tree build's."""
     flags = [f"-D{k}={v}" for k, v in sorted(defines.items())]
-    return _compile(out_dir, os.path.join(out_dir, "libtgc.so"), flags, False, False)
+    return _compile(out_dir, os.path.join(out_dir, "libtgc.so"), flags, False, False, sources or SOURCES)
 
 
-def _compile(out_dir: str, lib_path: str, extra: list, verbose: bool, ptxas_info: bool) -> str:
+def _compile(out_dir: str, lib_path: str, extra: list, verbose: bool, ptxas_info: bool, sources=SOURCES) -> str:
     os.makedirs(out_dir, exist_ok=True)
     common = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-Wall", "-I", INCLUDE, "-I", CSRC, *extra]
@@ -99,8 +100,9 @@ def _compile(out_dir: str, lib_path: str, extra: list, verbose: bool, ptxas_info
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(len(SOURCES)) as ex:
-        objs = list(ex.map(compile_one, SOURCES))
+    kept = [os.path.join(PKG, "_build", os.path.splitext(s)[0] + ".o") for s in SOURCES if s not in sources]
+    with concurrent.futures.ThreadPoolExecutor(len(sources)) as ex:
+        objs = list(ex.map(compile_one, sources)) + kept
     tmp = lib_path + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

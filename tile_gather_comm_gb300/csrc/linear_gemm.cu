@@ -39,7 +39,6 @@ constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
 constexpr int kBoxBytes = 32 * 32 * 2;  // an epilogue warp's staging box: 32 rows x 32 columns
 constexpr int kBiasBytes = 128 * 4;     // its columns' bias in fp32
 constexpr uint32_t kLinTmemCols = 512;
-constexpr uint64_t kLinDrainNs = 200ull * 1000 * 1000;
 
 template <int CG, int MODE, int TN>
 struct LCfg {
@@ -189,6 +188,13 @@ __device__ void lin_role_mma(const LinearParams &p, const int *tile0, uint8_t *s
     if (CG == 1) mma_commit(drain);  // arrives once every MMA issued above has completed
     else mma_commit_pair_mc(drain, (uint16_t)0x1);
     mbar_drain_wait(drain, 0, kLinDrainNs);
+    if (!ok) {
+        // The loads of the steps that now take none have time to land before shared memory is given up:
+        // those counted here (a pair's on the even CTA), then those counted on raw.
+        for (uint32_t n = 0; n < (uint32_t)C::kStages; ++n, ++it)
+            mbar_drain_wait(&full[it % C::kStages], (it / C::kStages) & 1u, kLinDrainNs);
+        spin_for_ns(200000);
+    }
 }
 
 // kWgrad with groups: zero the rows of a group's last stage that are not the group's.

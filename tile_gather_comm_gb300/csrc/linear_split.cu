@@ -157,8 +157,10 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
             const uint32_t a0 = smem_addr(sA), b0 = smem_addr(sB);
             int s = 0;
             uint32_t ph = 0;
+            bool fed = true;
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (!lin_wait(&full[s], ph, p)) break;
+                fed = lin_wait(&full[s], ph, p);
+                if (!fed) break;
                 tc_fence_after();
                 const uint64_t ad = kAMn ? make_sw128_mnmajor_desc(a0 + s * q.a_bytes, kBoxMn)
                                          : make_sw128_kmajor_desc(a0 + s * q.a_bytes);
@@ -173,6 +175,13 @@ __global__ void __launch_bounds__(kSplitThreads, 2)
                 if (++s == q.stages) { s = 0; ph ^= 1u; }
             }
             mma_commit(done);
+            if (!fed) {  // what is under way has time to end before the ring and TMEM are used otherwise
+                mbar_drain_wait(done, 0, kLinDrainNs);
+                for (int n = 0; n < q.stages; ++n) {
+                    mbar_drain_wait(&full[s], ph, kLinDrainNs);
+                    if (++s == q.stages) { s = 0; ph ^= 1u; }
+                }
+            }
         }
         __syncwarp();
         // Every load this CTA issued has landed once the MMAs that read it have completed, so the
