@@ -1,5 +1,6 @@
 """What the transformer-block operators do at the edges of what they accept, on the GPU: offsets that decrease,
-host threads that call at the same time, infinities where a term has no factor for them, waits."""
+host threads that call at the same time, infinities where a term has no factor for them, waits, activations
+far from zero."""
 import ctypes
 import math
 import os
@@ -14,6 +15,7 @@ from tests.helpers import requires_gpu
 
 pytestmark = pytest.mark.gpu
 BF, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+U = {BF: 2.0 ** -8, F16: 2.0 ** -10}  # a unit in the last place
 
 
 @pytest.fixture(autouse=True)
@@ -241,3 +243,30 @@ def test_products_whose_wait_expires_end_and_say_so(one_look, M, K, N, groups):
         assert torch.equal(y[i:j], (x[i:j].float() @ we.float().t()).to(BF))
         assert torch.equal(dx[i:j], (dy[i:j].float() @ we.float()).to(BF))
         assert torch.equal(dwe, (dy[i:j].float().t() @ x[i:j].float()).to(BF))
+
+
+# ---------------------------------------------------------------- activations
+
+FAR = [50.0, 1e3, 1e9, 1e15, 1e19, 2e19, 1e20, 1e30, 3e38]
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("M", [4, 300])
+def test_activations_far_from_zero(act, M):
+    """|z| >= 50: act(z) is z, or next to nothing, and its derivative 1, or next to nothing."""
+    K = 8
+    values = torch.tensor([v * s for v in FAR for s in (1, -1)], device="cuda")
+    N = (len(values) + 7) // 8 * 8
+    values = torch.cat([values, torch.full((N - len(values),), 60.0, device="cuda")]).to(BF)
+    v64 = values.double()
+    gate = torch.sigmoid(v64) if act == "silu" else (v64 > 0).double()
+    want, slope = v64 * gate, gate * (1 + v64 * (1 - gate)) if act == "silu" else gate
+    x, w = torch.zeros(M, K, device="cuda", dtype=BF), torch.zeros(N, K, device="cuda", dtype=BF)
+    x[:, 0], w[:, 0] = 1.0, values
+    y, z = (torch.empty(M, N, device="cuda", dtype=BF) for _ in range(2))
+    tgc.tgc_linear(x, w, y, act=act, z=z)
+    assert torch.equal(z, values.expand(M, N))
+    assert bool(((y.double() - want).abs() <= U[BF] * want.abs()).all())
+    dy, db = torch.ones(M, N, device="cuda", dtype=BF), torch.empty(N, device="cuda", dtype=BF)
+    tgc.tgc_linear_bwd(dy, x, w, z=z, act=act, dbias=db)
+    assert bool(((db.double() - M * slope).abs() <= U[BF] * M * slope.abs()).all())

@@ -104,7 +104,10 @@ __device__ __forceinline__ F2 act_grad_of(F2 z) {
         return fma(mul(z, every<F2>(kInvSqrt2Pi)), e, phi);
     }
     if constexpr (ACT == TGC_ACT_GELU_TANH) {
-        const F2 zz = mul(z, z), s = tanh_gate(z, zz);
+        // z^2 is cut off where fp32 ends (|z| > 1.8e19): s is 0 or 1 long before, and the term that the
+        // slope enters has to be zero there, not zero times infinity.
+        const float2 sq = split(mul(z, z));
+        const F2 zz = f2(fminf(sq.x, 1e30f), fminf(sq.y, 1e30f)), s = tanh_gate(z, zz);
         const F2 slope = fma(zz, every<F2>(3.0f * kTanhK2), every<F2>(kTanhK1));
         return fma(mul(mul(z, s), fma(s, minus, one)), slope, s);
     }
