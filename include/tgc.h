@@ -537,7 +537,8 @@ void tgc_gemm_tile_shape(int *bm, int *bn, int *bk);
 
 /* Activations of the linear operator (z -> act(z), in fp32):
  *   RELU       max(z, 0)  (NaN stays NaN; derivative 1 where z > 0, else 0)
- *   GELU       z * Phi(z), Phi the normal distribution function
+ *   GELU       z * Phi(z), Phi the normal distribution function, within 2^-21 (absolute: below z = -5
+ *              the result, under 2e-6, keeps its size but not the last bits of its type)
  *   GELU_TANH  0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))
  *   SILU       z / (1 + exp(-z)) */
 typedef enum tgc_act {

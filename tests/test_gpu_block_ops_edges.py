@@ -270,3 +270,19 @@ def test_activations_far_from_zero(act, M):
     dy, db = torch.ones(M, N, device="cuda", dtype=BF), torch.empty(N, device="cuda", dtype=BF)
     tgc.tgc_linear_bwd(dy, x, w, z=z, act=act, dbias=db)
     assert bool(((db.double() - M * slope).abs() <= U[BF] * M * slope.abs()).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+def test_gelu_of_negative_values(dtype):
+    """Phi(z) is off by 2^-21 at most: 0.75e-7 by its formula; half of 2^-22 by the exponential, as Phi <= 1/2
+    here; 2^-22 times a slope below 0.6 by the reciprocal; five roundings of values below 0.75 by the polynomial."""
+    z = torch.linspace(-12, 0, 4096, device="cuda").to(dtype)
+    M, K, N = 8, 8, len(z)
+    x, w = torch.zeros(M, K, device="cuda", dtype=dtype), torch.zeros(N, K, device="cuda", dtype=dtype)
+    x[:, 0], w[:, 0] = 1.0, z
+    y = torch.empty(M, N, device="cuda", dtype=dtype)
+    tgc.tgc_linear(x, w, y, act="gelu")
+    z64 = z.double()
+    ref = z64 * 0.5 * torch.special.erfc(-z64 / math.sqrt(2))
+    err = (y.double() - ref).abs()
+    assert bool((err <= U[dtype] * ref.abs() + 2.0 ** -21 * z64.abs() + (2.0 ** -24 if dtype == F16 else 0)).all())

@@ -55,9 +55,12 @@ __device__ __forceinline__ F2 sigmoid_f2(F2 v) {
 
 // The normal distribution function Phi(z) and e = exp(-z^2 / 2), which gelu and its derivative
 // both need.  Phi by Abramowitz and Stegun 7.1.26: erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2),
-// t = 1 / (1 + p x), x >= 0, off by at most 1.5e-7 (so Phi by 0.75e-7): a tenth of what rounding
-// the result to 16 bits does, for one exponential that the derivative shares.  erff instead took
-// the backward's elementwise pass from memory-bound to 168 us for 8192 x 14336 (floor 104 us).
+// t = 1 / (1 + p x), x >= 0, off by at most 1.5e-7, so Phi by 0.75e-7; with fp32's roundings by 2.5e-7 (near
+// 0).  One exponential, which the derivative shares.  The bound is absolute, as that of 0.5 (1 + erf) in
+// fp32: below z = -3 Phi falls faster than its error.  gelu(-4) = -1.3e-4 is off by half a unit of f16's
+// last place, and of bf16's 2^-8 gelu(-5) = -1.4e-6 is off by 0.4, gelu(-7) = -9e-12 by 1.7 and gelu(-10) =
+// -8e-23 by 5.  erff instead took the backward's elementwise pass from memory-bound to 168 us for 8192 x
+// 14336 (floor 104 us).
 __device__ __forceinline__ F2 normal_cdf(F2 z, F2 *e) {
     const F2 x = F2{z.v & 0x7fffffff7fffffffull};
     *e = exp2_f2(mul(mul(z, z), every<F2>(-0.5f * kLog2e)));
