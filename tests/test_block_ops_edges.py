@@ -1,5 +1,6 @@
 """The transformer-block operators at the edges of what they accept, without a GPU: index arithmetic for
-offsets that decrease, compiled for the host from the kernels' own header; the largest sizes."""
+offsets that decrease, compiled for the host from the kernels' own header; the largest sizes; a binding
+that was built for another torch."""
 import ctypes
 import os
 import subprocess
@@ -115,3 +116,13 @@ def test_the_norm_gradients_deal_out_the_most_rows(M, D):
     assert 0 < need(M) <= need(1 << 20)
     one = dict(gate=FAKE, gates=1, y=FAKE, dgate=FAKE)
     assert need(M) < need(M, **one) <= need(1 << 20, **one)
+
+
+@pytest.mark.parametrize("written,current", [(None, False), ("Python 3.12\\ntorch 1.0\\n", False), ("", False), (True, True)])
+def test_a_binding_for_another_python_or_torch_is_out_of_date(written, current, tmp_path, monkeypatch):
+    _build.build()
+    stamp = tmp_path / "ops.stamp"
+    if written is not None:
+        stamp.write_text(open(_build.OPS_STAMP, encoding="utf-8").read() if written is True else written)
+    monkeypatch.setattr(_build, "OPS_STAMP", str(stamp))
+    assert _build.up_to_date() is current

@@ -20,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libtgc.so")
 OPS = os.path.join(PKG, "_ops.so")
+OPS_STAMP = os.path.join(PKG, "_build", "ops.stamp")  # the Python and torch that _ops.so was built against
 SOURCES = ["api.cu", "tgather.cu", "gemm.cu", "noalloc.cu", "ipc.cu", "linear.cu", "linear_gemm.cu", "linear_split.cu", "block_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -38,21 +39,35 @@ def _inputs():
     return files
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(OPS):
+def _newer_than_inputs(path: str) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path) for f in _inputs())
+
+
+def _ops_needs() -> str:
+    import torch
+    return f"Python {sys.version}\ntorch {torch.__version__}\n"
+
+
+def _ops_up_to_date() -> bool:
+    """Newer than its sources, and built against this Python and this torch: another's ABI may differ."""
+    if not _newer_than_inputs(OPS) or not os.path.exists(OPS_STAMP):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(OPS))
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    with open(OPS_STAMP, encoding="utf-8") as f:
+        return f.read() == _ops_needs()
+
+
+def up_to_date() -> bool:
+    return _newer_than_inputs(LIB) and _ops_up_to_date()
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
     with concurrent.futures.ThreadPoolExecutor(1) as ex:
-        ops = ex.submit(_compile_ops)
-        lib = _compile(os.path.join(PKG, "_build"), LIB, [], verbose, ptxas_info)
-        ops.result()
-    return lib
+        ops = ex.submit(_compile_ops) if force or not _ops_up_to_date() else None
+        if force or not _newer_than_inputs(LIB):
+            _compile(os.path.join(PKG, "_build"), LIB, [], verbose, ptxas_info)
+        if ops is not None:
+            ops.result()
+    return LIB
 
 
 def _compile_ops() -> None:
@@ -73,6 +88,9 @@ def _compile_ops() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, OPS)
+    os.makedirs(os.path.dirname(OPS_STAMP), exist_ok=True)
+    with open(OPS_STAMP, "w", encoding="utf-8") as f:
+        f.write(_ops_needs())
 
 
 def build_variant(out_dir: str, defines: dict, sources: list | None = None) -> str:
