@@ -566,7 +566,7 @@ typedef enum tgc_act {
  * residual  device (M, N) or NULL; may be y itself (same address and ldy).
  * y         device (M, N), written; must overlap no input except as above.
  * z         device (M, N) or NULL: receives the pre-activation z (what the
- *           backward pass needs).
+ *           backward pass needs); must overlap nothing else.
  * ldx, ldw, ldres, ldy, ldz   elements from one row to the next; 0 = dense.
  * w_stride  elements from one expert's weight to the next; 0 = N * ldw.
  * dtype     TGC_BF16 or TGC_F16, of every tensor.
@@ -576,7 +576,8 @@ typedef enum tgc_act {
  *           [offsets[0], offsets[ngroups]) are neither used nor written.  Values
  *           outside [0, M] are taken as the nearer bound, and a group that ends
  *           before it begins as empty, so no value makes the kernel leave the
- *           tensors.
+ *           tensors.  Where decreasing offsets make groups overlap, the rows of
+ *           later groups may be left out.
  * ngroups   1..TGC_MAX_GROUPS with offsets; 0 without.
  *
  * Requirements: K > 0; K % 8 == 0 and N % 8 == 0, row strides % 8 == 0 and every
@@ -615,7 +616,8 @@ int tgc_linear(const tgc_linear_args *args);
  * for dw, w for dx.  dw and dbias of an expert without rows are written as zeros.
  * Sums are fp32 in an order that does not change between calls; dz is rounded to `dtype`
  * before the products (the tensor cores' operand type), dbias is summed from the
- * unrounded values.
+ * unrounded values.  dx, dw, dbias and the workspace must overlap no input and not each
+ * other: the gradients are computed side by side.
  * Strides, alignment, limits and offsets as in tgc_linear; lddx 0 = K, dw dense
  * (its row stride is K, its expert stride N * K).  N > 0.  M == 0 writes zeros to dw
  * and dbias.
@@ -748,8 +750,9 @@ size_t tgc_block_norm_bwd_workspace_bytes(const tgc_block_norm_bwd_args *args);
 
 /*
  * Every wait inside the kernels of tgc_linear, tgc_block_norm and their gradients is
- * bounded.  Should one expire (the GPU stopped delivering a copy), its kernel ends
- * with wrong results and marks a word of the device.  tgc_async_status synchronises
+ * bounded, those for a whole reduction from its last step on.  Should one expire (the
+ * GPU stopped delivering a copy), its kernel ends with wrong results and marks a word
+ * of the device.  tgc_async_status synchronises
  * `stream`, clears that word and returns what it held: TGC_OK or TGC_ERR_TIMEOUT.
  */
 int tgc_async_status(cudaStream_t stream);

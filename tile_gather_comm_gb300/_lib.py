@@ -444,7 +444,8 @@ def tgc_linear(x, w, y, *, bias=None, act: str = "none", residual=None, z=None, 
 def tgc_linear_bwd(dy, x, w, *, z=None, act: str = "none", dx=None, dw=None, dbias=None, offsets=None,
                    workspace=None, stream=None, check: bool = True) -> int:
     """Gradients of tgc_linear into dx, dw and dbias (each optional): dz = dy * act'(z),
-    dx = dz @ w, dw = dz^T @ x, dbias = dz summed over rows.  The residual's gradient is dy.
+    dx = dz @ w, dw = dz^T @ x, dbias = dz summed over rows.  The residual's gradient is dy.  The
+    outputs must overlap no input and not each other.
     ``workspace``: a contiguous CUDA tensor of tgc_linear_bwd_workspace_bytes' size, by default
     taken from torch's allocator.  Asynchronous on ``stream``."""
     rc = (_ops or _native()).linear_bwd(dy, x, w, z, ACTS[act], dx, dw, dbias, offsets, workspace, _address(stream))

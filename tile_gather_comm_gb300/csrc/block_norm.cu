@@ -12,9 +12,10 @@
 // registers of its team of threads from the first load to the last store, so the several
 // passes a norm needs (mean, deviations, the gradient's two means) touch no memory.  A team
 // is a warp (rows of up to 32 vectors; no barrier at all) or a whole block.
-// Measured, bf16, 8192 x 4096, rms norms, gate and residual: forward 48.6 us (5.5 TB/s, 60 % of the
-// issue slots), backward 84 us and 8 to 9 for the sums over rows (89 together, the launches overlap):
-// 4.5 TB/s, held back by its own instructions, about 43 an element at 16 warps an SM.
+// Measured, bf16, 8192 x 4096, rms norms, gate and residual: forward 48.7 us (5.5 TB/s, 67 % of the
+// issue slots), backward 85 us and 8 to 10 for the sums over rows (90 together, the launches overlap):
+// 4.5 TB/s and 44 % of the issue slots, neither of them full.  A team of 16 warps is all that an SM's
+// registers hold, and for each pair of rows all of it waits at one barrier for the sums.
 #include <atomic>
 #include <cstdint>
 #include <cstring>
@@ -1209,10 +1210,7 @@ static int norm_bwd_impl(tgc_block_norm_bwd_args a) {
     for (int i = 0; i < 4; ++i) p.want[i] = outs[i] != nullptr;
     p.need_y = a.post != TGC_NORM_NONE || a.dgate != nullptr;
     p.res_scale = a.res_scale; p.branch_scale = a.branch_scale; p.eps = a.eps; p.inv_d = 1.0f / (float)a.D;
-    if (a.M > 0) {
-        const int rc = device_fault_word(&p.fault);
-        if (rc != TGC_OK) return rc;
-    }
+    TGC_TRY(device_fault_word(&p.fault));
     NormSumParams n{};
     n.partial = p.partial; n.gate_partial = p.gate_partial; n.dgate = a.dgate;
     for (int i = 0; i < 4; ++i) n.out[i] = outs[i];

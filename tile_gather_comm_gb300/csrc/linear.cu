@@ -31,6 +31,10 @@ static bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintp
 // dz = dy act'(z) and, in the same pass, the column sums of each chunk of kChunk rows (chunks
 // never cross a group): a block takes a strip of 32 vectors of 8 columns, 8 row lanes, each lane
 // 8 rows a chunk with all its loads under way before the first is used.
+// dz is rounded to the operands' 16 bits because the tensor cores take no wider type at their rate: the
+// gradients' error against 64 bits goes from 1.7e-3 to 2.3e-3 of the norm in bf16 (2.1e-4 to 2.9e-4 in f16)
+// against dz in fp32, which two products of a high and a low part would cost twice the time for.  The
+// bias gradient sums the unrounded values.
 // Bound by memory: dy and z read once, dz written once, partial sums M/kChunk x N fp32.
 // Measured: 8192 x 14336 bf16 gelu 104 us with the bias gradient (705 MB, the copy rate).
 constexpr int kChunk = 64;

@@ -21,9 +21,9 @@
 //               through shared memory and TMA stores; boxes that a group's end cuts are stored by
 //               the lanes whose rows exist
 // Measured, bf16, 8192 x 4096 x 14336: plain 492 us in a burst (1955 TFLOP/s) and 570 in a loop of a
-// second (1689); with bias, gelu and z 609 to 620 a pass.  At 2048 rows the tensor pipe is active 79 % of
+// second (1689); with bias, gelu and z 597 to 627 a pass.  At 2048 rows the tensor pipe is active 79 % of
 // the time forward, 76 % for the input gradient, 83 % for the weight gradient.  16 experts of 4096 x
-// 4096 over 16384 uneven rows: 389 to 408 us with tanh-gelu and z, 71 tile rows where even groups fill 64.
+// 4096 over 16384 uneven rows: 386 to 411 us with tanh-gelu and z, 71 tile rows where even groups fill 64.
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -585,13 +585,16 @@ static int lin_launch(const LinearProduct &q, int dev, int sms, cudaStream_t str
 // A form's time in SM cycles is the largest of three bounds and what nothing overlaps:
 //   l2     what L2 hands out: 2.83 / SMs cycles for every 128-byte row of an operand tile that any SM
 //          takes in; rows that do not start on a 128-byte line (they take two) 1.09 times that
-//   hbm    every operand once, 2120 bytes a cycle
+//   hbm    every operand once, 2120 bytes a cycle.  That is below what many CTAs stream (48 rows over 16
+//          experts: 6.9 TB/s): where it is the largest bound, forms tie on it and the first of them is
+//          taken, 112 CTAs for a token of 4096 x 14336 and 128 for 48 x 14336 x 4096, on 152 SMs
 //   sm     the busiest SM's steps -- the products (2 cycles a column of the tile) or the rows it takes
 //          in -- and, for the persistent kernel, no less than an epilogue a tile
 //   extra  start, the last epilogue, and the split kernel's exchange
 // The constants were fitted to 13,900 timings (190 shapes of 1..8192 x 64..14336 x 64..14336, three
 // products, every form): the form taken is 2.5 % slower than the best on the geometric mean, where
-// one persistent form for all rows above 128 and the split kernel below was 18 % slower.
+// one persistent form for all rows above 128 and the split kernel below was 18 % slower.  No grouped shape
+// was among them.
 struct LinearForm {
     int cg, tn;  // the persistent kernel's; cg 0: the split kernel's tn and parts
     int parts;

@@ -3,14 +3,16 @@
 // partial sums through distributed shared memory.
 //
 // With few rows the product streams the weight once and is bound by HBM (one row: 1 flop a byte);
-// what matters is that every SM loads, with enough bytes in flight.  So: small tiles, two CTAs on
-// an SM (about 110 KiB each, all of it stages), the reduction cut into as many parts as fill the
-// SMs, and A's stage no larger than the rows there are (the MMA reads 128 rows of shared memory
+// what matters is that the SMs load, with enough bytes in flight.  So: small tiles, CTAs of about
+// 110 KiB, all of it stages, of which two fit an SM, the reduction cut into parts where there are
+// few tiles, and A's stage no larger than the rows there are (the MMA reads 128 rows of shared memory
 // whatever they hold; what it computes from rows that do not exist is never stored).  No partial
 // sum goes to memory and nothing is added atomically: every output is summed over the parts in
 // order by one thread, so the result is the same in every run.
-// Measured: 1 x 4096 x 14336 bf16 23.7 to 24.2 us a call among others (4.9 TB/s; 28.9 alone from a cold L2),
-// 48 x 14336 x 4096 f16 with a residual 29 us.  Their bytes take 17.4 and 17.7 at the copy rate.
+// Measured, with the forms that lin_choose takes: 1 x 4096 x 14336 bf16 23.7 to 24.4 us a call among others
+// (4.8 TB/s; 29 alone from a cold L2) on 112 CTAs, a tile of 128 columns each and its whole reduction; 48 x
+// 14336 x 4096 f16 with a residual 29 us on 32 tiles of 4 parts; 48 rows over 16 experts of 4096 x 14336
+// 218 to 224 us (6.9 TB/s) on 1792 CTAs.  Their bytes take 17.6, 17.9 and 228 at the copy rate.
 #include <cstdint>
 #include <cstring>
 #include <mutex>
