@@ -1,7 +1,8 @@
 /*
  * tgc.h -- C ABI of libtgc.so: TGATHER row-concat gather, chunked AllGather
  * fused with a bf16 MatMul, and the transformer-block operators around that
- * product (linear, experts, block norm), for one sm_103a GPU.
+ * product (linear, experts, block norm; rotary positions, a paged key-value
+ * cache and its attention), for one sm_103a GPU.
  *
  * Sources (web pages):
  *   [TG]  "CANN PTO-ISA TGATHER 指令深度解析：跨 Rank 行拼接 Gather 的实现原理与开发指南"
@@ -747,6 +748,253 @@ int tgc_block_norm_bwd(const tgc_block_norm_bwd_args *args);
 /* Bytes of workspace tgc_block_norm_bwd needs for these arguments (pointers are only
  * tested for NULL); 0 for none or for arguments it would refuse. */
 size_t tgc_block_norm_bwd_workspace_bytes(const tgc_block_norm_bwd_args *args);
+
+/* ------------------------------------------------------------------------ */
+/* Attention: rotary positions, the paged key-value cache, single tokens     */
+/* ------------------------------------------------------------------------ */
+
+/* The cache.  Keys and values of every layer lie in pools of pages; a page holds page_size tokens,
+ * all heads.  A sequence s owns pages table[s, 0 .. ceil(lens[s] / page_size)), its token j lies at
+ * place j % page_size of page table[s, j / page_size].  The bookkeeping lives on the device, so
+ * nothing here synchronises with the host and every call can be captured in a CUDA graph (after one
+ * uncaptured call on the device):
+ *   refs   int32 (num_pages)              sequences that hold the page; 0: free
+ *   table  int32 (num_seqs, max_pages)    page numbers, -1 beyond a sequence's pages; rows table_ld
+ *                                         apart (0 = max_pages)
+ *   lens   int32 (num_seqs)               tokens of each sequence
+ * A page that is not full belongs to one sequence, so appending never writes into another's tokens
+ * (tgc_kv_fork keeps it so).  Page numbers outside [0, num_pages), sequence numbers outside
+ * [0, num_seqs) and lengths outside [0, max_pages * page_size] never make a kernel leave its tensors:
+ * each call says what it makes of them.  Calls that read or change the same cache are ordered by
+ * the caller (one stream, or events). */
+
+/* Which elements of a head turn together: (i, i + R/2), or neighbours (2i, 2i + 1). */
+typedef enum tgc_rope_layout { TGC_ROPE_HALF = 0, TGC_ROPE_INTERLEAVED = 1 } tgc_rope_layout;
+
+#define TGC_ROPE_MAX_D 1024
+#define TGC_ROPE_MAX_HEADS 65536  /* of q, k and v together */
+
+/*
+ * tgc_rope -- rotary positions: the first R elements of every head are R/2 pairs (a, b), and
+ *     a' = scale * (a cos w - b sin w),  b' = scale * (b cos w + a sin w),
+ *     w = pos[t] * freqs[i]  for pair i of token t;
+ * elements from R on are copied.  q and k (fewer heads) in one launch.  The angle is taken in 64
+ * bits modulo a whole turn, so far positions lose nothing; sine, cosine and the products are fp32,
+ * the result is rounded once.  Zero-initialise the struct; 0 / NULL means the default.
+ *
+ * q, q_out   device (T, heads_q, D), `dtype`.  q_out may be q (same address and strides), and must
+ *            overlap nothing else that is read or written.
+ * k, k_out   device (T, heads_k, D), or NULL with heads_k = 0; as q.
+ * q_t, q_h, ...  elements from one token, one head to the next; 0 = dense (heads side by side).
+ * pos        device int32 (T).  A token with a negative position is padding: its rows of q and k are
+ *            not read and those of q_out and k_out not written.
+ * freqs      device double (R/2), radians a position (tgc_rope_freqs makes them).
+ * R          even, 2 <= R <= D <= TGC_ROPE_MAX_D.
+ * scale      factor on the rotated elements; 0 = 1.
+ * dtype      TGC_BF16, TGC_F16 or TGC_F32.  Pointers need their element's alignment (16-byte aligned
+ *            rows and R/2 in whole 16-byte vectors run faster).
+ * Errors: TGC_ERR_INVALID_ARG (T > TGC_MAX_SIZE, heads in all not in [1, TGC_ROPE_MAX_HEADS], ...),
+ * TGC_ERR_DTYPE, TGC_ERR_ALIGN.  T == 0 returns TGC_OK.  Asynchronous on `stream`.
+ */
+typedef struct tgc_rope_args {
+    const void *q;
+    const void *k;
+    void *q_out;
+    void *k_out;
+    const int32_t *pos;
+    const double *freqs;
+    int64_t T, heads_q, heads_k, D, R;
+    int64_t q_t, q_h, k_t, k_h, qo_t, qo_h, ko_t, ko_h;
+    float scale;
+    tgc_rope_layout layout;
+    tgc_dtype dtype;
+    cudaStream_t stream;
+} tgc_rope_args;
+
+int tgc_rope(const tgc_rope_args *args);
+/* Its gradients: q and k hold the gradients of q_out and k_out, and those of q and k are written to
+ * q_out and k_out (the rotation by -w, times scale; elements from R on are copied). */
+int tgc_rope_bwd(const tgc_rope_args *args);
+
+/* How the frequencies base^(-2i / R), i < R/2, are stretched for a context `factor` times longer than
+ * the `trained` tokens that a model has seen:
+ *   NONE    not at all
+ *   LINEAR  divided by factor (positions interpolated)
+ *   NTK     base * factor^(R / (R - 2)) in place of base: the fastest pair stays, the slowest is divided by factor
+ *   YARN    pairs that make more than beta_fast turns over `trained` tokens stay, those that make fewer than
+ *           beta_slow are divided by factor, a straight ramp in the number of turns between them; scale 0.1 ln(factor) + 1 */
+typedef enum tgc_rope_scaling {
+    TGC_ROPE_NONE = 0, TGC_ROPE_LINEAR = 1, TGC_ROPE_NTK = 2, TGC_ROPE_YARN = 3
+} tgc_rope_scaling;
+
+/* Writes R/2 frequencies to the HOST array `freqs` and, where `scale` is not NULL, the factor on the
+ * rotated elements (1 except for YARN).  base > 1, factor >= 1, trained > 0 and beta_fast > beta_slow > 0 where they
+ * are used; TGC_ERR_INVALID_ARG otherwise.  NTK with R = 2 has one pair, whose frequency is 1 in any base.  Needs no GPU. */
+int tgc_rope_freqs(double *freqs, double *scale, int64_t R, double base, tgc_rope_scaling scaling, double factor,
+                   double trained, double beta_fast, double beta_slow);
+
+/*
+ * tgc_kv_append -- the new tokens' keys and values into their pages, the keys (and the queries)
+ * rotated on the way as tgc_rope does:
+ *     K[page, place, h] = rope(k[t, h]),  V[page, place, h] = v[t, h],  q_out[t, h] = rope(q[t, h]),
+ *     page = table[s, pos[t] / page_size],  place = pos[t] % page_size,  s = seqs[t].
+ * Tokens of prompts and single tokens alike, in one launch.
+ *
+ * k, v       device (T, heads_k, D), `dtype`; k_t, k_h, v_t, v_h elements between tokens and heads (0 = dense).
+ * q, q_out   device (T, heads_q, D) or both NULL with heads_q = 0; q_out may be q.
+ * k_pages, v_pages  device (num_pages, page_size, heads_k, D), page_s, token_s, head_s elements
+ *            between pages, tokens and heads of both (0 = dense), in either order of tokens and heads.
+ * table      as above; pos int32 (T); seqs int32 (T) or NULL: token t is sequence t's (T <= num_seqs).
+ * freqs, R, scale, layout  as tgc_rope; NULL with R = 0: nothing is rotated (q is copied).
+ * A token with a negative position is padding (nothing of it is read or written).  One whose page is
+ * not in the table (past max_pages, a number outside the pool, a sequence that is none) has its
+ * query rotated and its key and value dropped.  Tokens of one call have places of their own: where
+ * two have the same, the page holds elements of either.
+ * dtype, alignment, limits as tgc_rope; max_pages * page_size <= TGC_MAX_SIZE.
+ */
+typedef struct tgc_kv_append_args {
+    const void *k;
+    const void *v;
+    const void *q;
+    void *q_out;
+    void *k_pages;
+    void *v_pages;
+    const int32_t *table;
+    const int32_t *pos;
+    const int32_t *seqs;
+    const double *freqs;
+    int64_t T, heads_q, heads_k, D, R;
+    int64_t num_pages, page_size, num_seqs, max_pages, table_ld;
+    int64_t k_t, k_h, v_t, v_h, q_t, q_h, qo_t, qo_h;
+    int64_t page_s, token_s, head_s;
+    float scale;
+    tgc_rope_layout layout;
+    tgc_dtype dtype;
+    cudaStream_t stream;
+} tgc_kv_append_args;
+
+int tgc_kv_append(const tgc_kv_append_args *args);
+
+#define TGC_ATTENTION_MAX_D 256
+
+/*
+ * tgc_paged_attention -- attention of one new token of every sequence over its cached keys:
+ *     x_j = scale * q[s, h] . K_j      (softcap > 0:  x_j = softcap * tanh(x_j / softcap))
+ *     out[s, h] = sum_j p_j V_j,  p = softmax(x),  lse[s, h] = log(sum_j exp(x_j)),
+ *     j in [max(0, lens[s] - window), lens[s])   (window = 0: from 0)
+ * with head h reading key head h / (heads_q / heads_k).  The new token's own key is one of them: it is appended
+ * first and counted in lens.  A sequence without tokens gets zeros and lse = -inf.
+ * Scores, softmax and sums are fp32 (the probabilities enter the product with V as two 16-bit parts,
+ * so nothing of them is lost to 16 bits), out is rounded once.  The same inputs give the same
+ * bits on every call with the same sizes.  Zero-initialise the struct.
+ *
+ * q, out     device (num_seqs, heads_q, D), `dtype`; q_s, q_h, o_s, o_h elements between sequences
+ *            and heads (0 = dense).  out may be q.
+ * lse        device float (num_seqs, heads_q), dense, or NULL.
+ * k_pages, v_pages, page_s, token_s, head_s, table, table_ld   as tgc_kv_append.
+ * lens       device int32 (num_seqs); taken as 0 below 0 and as max_pages * page_size above it.
+ * Keys on pages whose number is outside [0, num_pages) are left out like masked ones.  What lies
+ * behind a sequence's last key in its page is not read, whatever it holds; a value that is infinite
+ * or NaN in range makes its column of out NaN.
+ * scale      0 = 1 / sqrt(D).
+ * Requirements: heads_q a multiple of heads_k, D <= TGC_ATTENTION_MAX_D (TGC_ERR_INVALID_ARG); TGC_BF16 or
+ * TGC_F16 (TGC_ERR_DTYPE); D and every stride in whole 16 bytes, every pointer 16-byte aligned (lse, table,
+ * lens: 4-byte) (TGC_ERR_ALIGN).  max_pages * page_size <= TGC_MAX_SIZE; num_seqs * heads_q < 2^31.
+ * workspace  device memory of tgc_paged_attention_workspace_bytes() bytes, 128-byte aligned, for the
+ *            parts of split sequences; no initialisation, meaningless after the call.  Calls that may run at
+ *            the same time (graphs on several streams among them) need one each.
+ * Asynchronous on `stream`.
+ */
+typedef struct tgc_paged_attention_args {
+    const void *q;
+    void *out;
+    float *lse;
+    const void *k_pages;
+    const void *v_pages;
+    const int32_t *table;
+    const int32_t *lens;
+    int64_t num_seqs, heads_q, heads_k, D;
+    int64_t num_pages, page_size, max_pages, table_ld;
+    int64_t q_s, q_h, o_s, o_h;
+    int64_t page_s, token_s, head_s;
+    float scale;
+    float softcap;
+    int64_t window;
+    tgc_dtype dtype;
+    void *workspace;
+    size_t workspace_bytes;
+    cudaStream_t stream;
+} tgc_paged_attention_args;
+
+int tgc_paged_attention(const tgc_paged_attention_args *args);
+/* Bytes of workspace for these arguments on the current device (pointers are not looked at); 0 for none or for arguments
+ * that would be refused. */
+size_t tgc_paged_attention_workspace_bytes(const tgc_paged_attention_args *args);
+
+#define TGC_KV_MAX_POOLS 256
+
+/*
+ * The cache's upkeep.  One struct for the five calls; each uses the fields it names, the others are
+ * ignored.  Pools are host arrays of device pointers (copied into kernel parameters), dense pages of
+ * page_bytes bytes, a multiple of 16, 16-byte aligned.  Every list is a device int32 array of n entries.
+ *
+ * tgc_kv_copy     pools, from, npools, page_bytes, num_pages, from_pages, src, dst, n:
+ *                 page src[i] of from[p] is copied to page dst[i] of pools[p], for every pool p.  from may
+ *                 be pools.  Entries whose src is outside [0, from_pages) or dst outside [0, num_pages) are
+ *                 left out.  No page may be both a source and a destination of one call, nor twice a
+ *                 destination with different sources (parts of either would be left).
+ * tgc_kv_reserve  refs, table, lens, dst, add, ok, n: sequence dst[i] grows by add[i] tokens: lens
+ *                 is raised and pages for them entered.
+ * tgc_kv_fork     pools, npools, page_bytes, refs, table, lens, src, dst, ok, n: sequence dst[i], which has to
+ *                 be empty, becomes a copy of sequence src[i]: whole pages are shared (refs + 1), a last
+ *                 page that is not full is copied into a page of its own.
+ * tgc_kv_free     refs, table, lens, dst, n: sequence dst[i] gives its pages back (refs - 1) and is empty.
+ *                 Sequences that are empty, listed twice or none are fine.
+ * tgc_kv_compact  pools, npools, page_bytes, refs, table, used: pages in use move down until they are
+ *                 [0, used[0]): those at or above the number in use go, in order, into the free ones
+ *                 below it; refs and the table follow.  What moved keeps its old bytes too.
+ *
+ * New pages are the lowest free numbers, given out in the list's order.  An entry gets all its pages or
+ * none: ok[i] (may be NULL) is 1 where it did; 0, with the sequence left as it was, where the pages of the entries
+ * up to and with it are more than there are free, and for entries that cannot be (a number that is no sequence, a
+ * negative add, more than max_pages, a child that is not empty or is its own parent, a sequence grown or
+ * a child named earlier in the list); these last ask for no pages.
+ *
+ * ok         device int32 (n) or NULL.      used   device int32 (1) or NULL.
+ * num_pages, num_seqs * max_pages and max_pages * page_size at most TGC_MAX_SIZE; n at most TGC_MAX_SIZE.
+ * Errors: TGC_ERR_INVALID_ARG, TGC_ERR_ALIGN, TGC_ERR_WORKSPACE.  n == 0 returns TGC_OK.
+ * workspace  (reserve, fork, compact) device memory of tgc_kv_workspace_bytes() bytes, 128-byte aligned, no
+ *            initialisation.  Asynchronous on `stream`.
+ */
+typedef struct tgc_kv_args {
+    int32_t *refs;
+    int32_t *table;
+    int32_t *lens;
+    int64_t num_pages, page_size, num_seqs, max_pages, table_ld;
+    const int32_t *src;
+    const int32_t *dst;
+    const int32_t *add;
+    int32_t *ok;
+    int32_t *used;
+    int64_t n;
+    void *const *pools;
+    const void *const *from;
+    int npools;
+    int64_t page_bytes;
+    int64_t from_pages;
+    void *workspace;
+    size_t workspace_bytes;
+    cudaStream_t stream;
+} tgc_kv_args;
+
+int tgc_kv_copy(const tgc_kv_args *args);
+int tgc_kv_reserve(const tgc_kv_args *args);
+int tgc_kv_fork(const tgc_kv_args *args);
+int tgc_kv_free(const tgc_kv_args *args);
+int tgc_kv_compact(const tgc_kv_args *args);
+/* Bytes of workspace that tgc_kv_reserve, tgc_kv_fork and tgc_kv_compact need for n entries, num_pages and
+ * num_seqs (one size for the three; 0 for arguments that would be refused). */
+size_t tgc_kv_workspace_bytes(const tgc_kv_args *args);
 
 /*
  * Every wait inside the kernels of tgc_linear, tgc_block_norm and their gradients is

@@ -1,5 +1,5 @@
 """Binding of libtgc.so: argument marshalling only, by ctypes, and natively (_ops.so) for the
-transformer-block operators, whose small calls the ctypes form would have held up.
+transformer-block, attention and cache operators, whose small calls the ctypes form would have held up.
 
 Every function here has the name of the C entry point it calls (include/tgc.h)
 and does nothing but turn torch tensors / Python values into pointers and
@@ -40,6 +40,12 @@ NORMS = {"none": 0, "rms": 1, "layer": 2}
 MAX_GROUPS = 1024              # TGC_MAX_GROUPS
 NORM_MAX_D = 16384             # TGC_NORM_MAX_D
 MAX_SIZE = (1 << 31) - 4096    # TGC_MAX_SIZE
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+ROPE_MAX_D = 1024              # TGC_ROPE_MAX_D
+ROPE_MAX_HEADS = 65536         # TGC_ROPE_MAX_HEADS
+ATTENTION_MAX_D = 256          # TGC_ATTENTION_MAX_D
+KV_MAX_POOLS = 256             # TGC_KV_MAX_POOLS
 MAX_RANKS = 64
 TRACE_WORDS = 16
 TRACE = dict(start=0, wait_ns=1, waited_tiles=2, copy_first=3, copy_last=4, pieces=5, end=6, tiles=7,
@@ -130,6 +136,52 @@ class BlockNormBwdArgs(ctypes.Structure):
     ]
 
 
+class RopeArgs(ctypes.Structure):
+    _fields_ = [
+        ("q", _vp), ("k", _vp), ("q_out", _vp), ("k_out", _vp), ("pos", _vp), ("freqs", _vp),
+        ("T", _i64), ("heads_q", _i64), ("heads_k", _i64), ("D", _i64), ("R", _i64),
+        ("q_t", _i64), ("q_h", _i64), ("k_t", _i64), ("k_h", _i64),
+        ("qo_t", _i64), ("qo_h", _i64), ("ko_t", _i64), ("ko_h", _i64),
+        ("scale", ctypes.c_float), ("layout", ctypes.c_int), ("dtype", ctypes.c_int), ("stream", _vp),
+    ]
+
+
+class KvAppendArgs(ctypes.Structure):
+    _fields_ = [
+        ("k", _vp), ("v", _vp), ("q", _vp), ("q_out", _vp), ("k_pages", _vp), ("v_pages", _vp),
+        ("table", _vp), ("pos", _vp), ("seqs", _vp), ("freqs", _vp),
+        ("T", _i64), ("heads_q", _i64), ("heads_k", _i64), ("D", _i64), ("R", _i64),
+        ("num_pages", _i64), ("page_size", _i64), ("num_seqs", _i64), ("max_pages", _i64), ("table_ld", _i64),
+        ("k_t", _i64), ("k_h", _i64), ("v_t", _i64), ("v_h", _i64),
+        ("q_t", _i64), ("q_h", _i64), ("qo_t", _i64), ("qo_h", _i64),
+        ("page_s", _i64), ("token_s", _i64), ("head_s", _i64),
+        ("scale", ctypes.c_float), ("layout", ctypes.c_int), ("dtype", ctypes.c_int), ("stream", _vp),
+    ]
+
+
+class PagedAttentionArgs(ctypes.Structure):
+    _fields_ = [
+        ("q", _vp), ("out", _vp), ("lse", _vp), ("k_pages", _vp), ("v_pages", _vp), ("table", _vp), ("lens", _vp),
+        ("num_seqs", _i64), ("heads_q", _i64), ("heads_k", _i64), ("D", _i64),
+        ("num_pages", _i64), ("page_size", _i64), ("max_pages", _i64), ("table_ld", _i64),
+        ("q_s", _i64), ("q_h", _i64), ("o_s", _i64), ("o_h", _i64),
+        ("page_s", _i64), ("token_s", _i64), ("head_s", _i64),
+        ("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", _i64),
+        ("dtype", ctypes.c_int), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t), ("stream", _vp),
+    ]
+
+
+class KvArgs(ctypes.Structure):
+    _fields_ = [
+        ("refs", _vp), ("table", _vp), ("lens", _vp),
+        ("num_pages", _i64), ("page_size", _i64), ("num_seqs", _i64), ("max_pages", _i64), ("table_ld", _i64),
+        ("src", _vp), ("dst", _vp), ("add", _vp), ("ok", _vp), ("used", _vp), ("n", _i64),
+        ("pools", ctypes.POINTER(_vp)), ("from_", ctypes.POINTER(_vp)), ("npools", ctypes.c_int),
+        ("page_bytes", _i64), ("from_pages", _i64),
+        ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t), ("stream", _vp),
+    ]
+
+
 class TGCError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -187,13 +239,22 @@ def load_library(path: str) -> ctypes.CDLL:
     L.tgc_gemm_tile_shape.argtypes = [ctypes.POINTER(ctypes.c_int)] * 3
     L.tgc_gemm_tile_shape.restype = None
     for name, args in (("tgc_linear", LinearArgs), ("tgc_linear_bwd", LinearBwdArgs),
-                       ("tgc_block_norm", BlockNormArgs), ("tgc_block_norm_bwd", BlockNormBwdArgs)):
+                       ("tgc_block_norm", BlockNormArgs), ("tgc_block_norm_bwd", BlockNormBwdArgs),
+                       ("tgc_rope", RopeArgs), ("tgc_rope_bwd", RopeArgs), ("tgc_kv_append", KvAppendArgs),
+                       ("tgc_paged_attention", PagedAttentionArgs), ("tgc_kv_copy", KvArgs),
+                       ("tgc_kv_reserve", KvArgs), ("tgc_kv_fork", KvArgs), ("tgc_kv_free", KvArgs),
+                       ("tgc_kv_compact", KvArgs)):
         getattr(L, name).argtypes = [ctypes.POINTER(args)]
         getattr(L, name).restype = ctypes.c_int
     for name, args in (("tgc_linear_bwd_workspace_bytes", LinearBwdArgs),
-                       ("tgc_block_norm_bwd_workspace_bytes", BlockNormBwdArgs)):
+                       ("tgc_block_norm_bwd_workspace_bytes", BlockNormBwdArgs),
+                       ("tgc_paged_attention_workspace_bytes", PagedAttentionArgs),
+                       ("tgc_kv_workspace_bytes", KvArgs)):
         getattr(L, name).argtypes = [ctypes.POINTER(args)]
         getattr(L, name).restype = ctypes.c_size_t
+    L.tgc_rope_freqs.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double), _i64, ctypes.c_double,
+                                 ctypes.c_int] + [ctypes.c_double] * 4
+    L.tgc_rope_freqs.restype = ctypes.c_int
     L.tgc_async_status.argtypes = [_vp]
     L.tgc_async_status.restype = ctypes.c_int
     L.tgc_status_string.argtypes = [ctypes.c_int]
@@ -422,7 +483,9 @@ def _native():
                               "`python -c 'import __graft_entry__ as g; g.build()'`") from e
         m.bind(*[ctypes.cast(getattr(L, n), _vp).value for n in (
             "tgc_linear", "tgc_linear_bwd", "tgc_linear_bwd_workspace_bytes", "tgc_block_norm", "tgc_block_norm_bwd",
-            "tgc_block_norm_bwd_workspace_bytes")])
+            "tgc_block_norm_bwd_workspace_bytes", "tgc_rope", "tgc_rope_bwd", "tgc_kv_append", "tgc_paged_attention",
+            "tgc_paged_attention_workspace_bytes", "tgc_kv_copy", "tgc_kv_reserve", "tgc_kv_fork", "tgc_kv_free",
+            "tgc_kv_compact", "tgc_kv_workspace_bytes")])
         _ops = m
     return _ops
 
@@ -490,6 +553,116 @@ def tgc_block_norm_bwd_workspace_bytes(y, r, dr, dh, *, gate=None, post: str = "
     return (_ops or _native()).block_norm_bwd_bytes(
         y, r, dr, dh, gate, NORMS[post], post_weight, post_bias, NORMS[pre], pre_weight, res_scale, branch_scale, eps,
         dx, dy, dgate, dpost_weight, dpost_bias, dpre_weight, dpre_bias, None, None)
+
+
+# ----------------------------------------------------------------------------- attention and the paged cache
+
+def tgc_rope_freqs(rotary_dim: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
+                   trained: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """(freqs, scale) for tgc_rope and tgc_kv_append: float64 radians a position on ``device`` for the
+    rotary_dim / 2 pairs, base^(-2i / rotary_dim) stretched for a context ``factor`` times ``trained``
+    tokens ("none", "linear", "ntk" or "yarn"), and the factor on the rotated elements."""
+    buf, scale = (ctypes.c_double * max(1, rotary_dim // 2))(), ctypes.c_double()
+    _check(lib().tgc_rope_freqs(buf, ctypes.byref(scale), rotary_dim, base, ROPE_SCALINGS[scaling], factor, trained,
+                                beta_fast, beta_slow), "tgc_rope_freqs")
+    return torch.tensor(list(buf), dtype=torch.float64, device=device), scale.value
+
+
+def tgc_rope(q, q_out, pos, freqs, *, k=None, k_out=None, layout: str = "half", scale: float = 1.0, stream=None,
+             check: bool = True) -> int:
+    """Rotary positions of the first 2 * len(freqs) elements of every head: q (tokens, heads, D) into
+    q_out and k (fewer heads) into k_out, by the angle pos[token] * freqs[pair], times ``scale``; pairs
+    are (i, i + half) or, "interleaved", neighbours.  An output may be its input.  Tokens with a
+    negative position are left out.  Asynchronous on ``stream``."""
+    rc = (_ops or _native()).rope(q, q_out, pos, freqs, k, k_out, ROPE_LAYOUTS[layout], scale, _address(stream))
+    return _check(rc, "tgc_rope") if check else rc
+
+
+def tgc_rope_bwd(dq_out, dq, pos, freqs, *, dk_out=None, dk=None, layout: str = "half", scale: float = 1.0, stream=None,
+                 check: bool = True) -> int:
+    """Gradients of tgc_rope: those of q_out and k_out turned back, into dq and dk.  Asynchronous on ``stream``."""
+    rc = (_ops or _native()).rope_bwd(dq_out, dq, pos, freqs, dk_out, dk, ROPE_LAYOUTS[layout], scale, _address(stream))
+    return _check(rc, "tgc_rope_bwd") if check else rc
+
+
+def tgc_kv_append(k, v, k_pages, v_pages, table, pos, *, seqs=None, q=None, q_out=None, freqs=None, layout: str = "half",
+                  scale: float = 1.0, stream=None, check: bool = True) -> int:
+    """The tokens' keys, rotated, and values into their pages (pages, page size, heads, D): token t is
+    token pos[t] of sequence seqs[t] (t itself without ``seqs``); q rotated into q_out on the way.
+    Without ``freqs`` nothing is rotated.  Asynchronous on ``stream``."""
+    rc = (_ops or _native()).kv_append(k, v, k_pages, v_pages, table, pos, seqs, q, q_out, freqs, ROPE_LAYOUTS[layout],
+                                       scale, _address(stream))
+    return _check(rc, "tgc_kv_append") if check else rc
+
+
+def tgc_paged_attention(q, out, k_pages, v_pages, table, lens, *, lse=None, scale: float = 0.0, window: int = 0,
+                        softcap: float = 0.0, workspace=None, stream=None, check: bool = True) -> int:
+    """Attention of one new token of every sequence, q (sequences, heads, D), over its lens[s] cached
+    tokens (the last ``window`` of them where it is not 0), scores capped by a tanh where ``softcap``
+    is not 0; ``scale`` 0 is D^-0.5.  lse (sequences, heads) receives the scores' log-sum-exp.  The table's width
+    bounds the lengths, so slicing it (table[:, :n]) lets a call with short sequences plan for them.
+    ``workspace``: as for tgc_linear_bwd.  Asynchronous on ``stream``."""
+    rc = (_ops or _native()).paged_attention(q, out, k_pages, v_pages, table, lens, lse, scale, window, softcap, workspace,
+                                             _address(stream))
+    return _check(rc, "tgc_paged_attention") if check else rc
+
+
+def tgc_paged_attention_workspace_bytes(q, out, k_pages, v_pages, table, lens, *, lse=None, scale: float = 0.0,
+                                        window: int = 0, softcap: float = 0.0) -> int:
+    """Bytes of ``workspace`` the same call of tgc_paged_attention takes."""
+    return (_ops or _native()).paged_attention_bytes(q, out, k_pages, v_pages, table, lens, lse, scale, window, softcap,
+                                                     None, None)
+
+
+def tgc_kv_copy(pools, from_pools, dst, src, *, stream=None, check: bool = True) -> int:
+    """Page src[i] of every pool in from_pools to page dst[i] of the pool beside it in pools (lists of
+    contiguous tensors (pages, ...)).  Asynchronous on ``stream``."""
+    rc = (_ops or _native()).kv_copy(pools, from_pools, dst, src, _address(stream))
+    return _check(rc, "tgc_kv_copy") if check else rc
+
+
+def tgc_kv_reserve(refs, table, lens, seqs, add, page_size: int, *, ok=None, workspace=None, stream=None,
+                   check: bool = True) -> int:
+    """Sequence seqs[i] grows by add[i] tokens: lens is raised and pages for them, the lowest free ones, entered
+    in the table; ok[i] says whether there were enough.  Asynchronous on ``stream``."""
+    rc = (_ops or _native()).kv_reserve(refs, table, lens, seqs, add, page_size, ok, workspace, _address(stream))
+    return _check(rc, "tgc_kv_reserve") if check else rc
+
+
+def tgc_kv_fork(pools, refs, table, lens, src, dst, page_size: int, *, ok=None, workspace=None, stream=None,
+                check: bool = True) -> int:
+    """The empty sequence dst[i] becomes a copy of sequence src[i]: full pages are shared, a part-filled
+    last page is copied in every pool.  Asynchronous on ``stream``."""
+    rc = (_ops or _native()).kv_fork(pools, refs, table, lens, src, dst, page_size, ok, workspace, _address(stream))
+    return _check(rc, "tgc_kv_fork") if check else rc
+
+
+def tgc_kv_free(refs, table, lens, seqs, *, stream=None, check: bool = True) -> int:
+    """The sequences give their pages back and are empty.  Asynchronous on ``stream``."""
+    rc = (_ops or _native()).kv_free(refs, table, lens, seqs, _address(stream))
+    return _check(rc, "tgc_kv_free") if check else rc
+
+
+def tgc_kv_compact(pools, refs, table, used=None, *, workspace=None, stream=None, check: bool = True) -> int:
+    """Moves the pages in use down to [0, used[0]), in every pool, and lets refs and the table follow.
+    Asynchronous on ``stream``."""
+    rc = (_ops or _native()).kv_compact(pools, refs, table, used, workspace, _address(stream))
+    return _check(rc, "tgc_kv_compact") if check else rc
+
+
+def tgc_kv_reserve_workspace_bytes(refs, table, lens, seqs, add, page_size: int) -> int:
+    """Bytes of ``workspace`` the same call of tgc_kv_reserve takes."""
+    return (_ops or _native()).kv_reserve_bytes(refs, table, lens, seqs, add, page_size, None, None, None)
+
+
+def tgc_kv_fork_workspace_bytes(pools, refs, table, lens, src, dst, page_size: int) -> int:
+    """Bytes of ``workspace`` the same call of tgc_kv_fork takes."""
+    return (_ops or _native()).kv_fork_bytes(pools, refs, table, lens, src, dst, page_size, None, None, None)
+
+
+def tgc_kv_compact_workspace_bytes(pools, refs, table) -> int:
+    """Bytes of ``workspace`` the same call of tgc_kv_compact takes."""
+    return (_ops or _native()).kv_compact_bytes(pools, refs, table, None, None, None)
 
 
 def tgc_async_status(stream=None) -> None:

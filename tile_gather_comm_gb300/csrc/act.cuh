@@ -25,6 +25,23 @@ __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2hal
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// Two values as a word of one of the 16-bit types (round to nearest even), the first in the low half, and back.
+__device__ __forceinline__ uint32_t pack16(F2 v, bool f16) {
+    const float2 f = split(v);
+    uint32_t r;
+    if (f16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(f.y), "f"(f.x));
+    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(f.y), "f"(f.x));
+    return r;
+}
+
+__device__ __forceinline__ F2 unpack16(uint32_t w, bool f16) {
+    if (f16) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+        return f2(f.x, f.y);
+    }
+    return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
 // The activations work on pairs (packed fp32): beside the products the epilogue's arithmetic is not
 // free -- 13 single instructions an element more took 13 % off the tensor pipe of a 4096 x 4096 x
 // 14336 product, whose other limits they do not touch.

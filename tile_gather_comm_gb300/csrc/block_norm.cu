@@ -16,7 +16,6 @@
 // issue slots), backward 85 us and 8 to 10 for the sums over rows (90 together, the launches overlap):
 // 4.5 TB/s and 44 % of the issue slots, neither of them full.  A team of 16 warps is all that an SM's
 // registers hold, and for each pair of rows all of it waits at one barrier for the sums.
-#include <atomic>
 #include <cstdint>
 #include <cstring>
 #include <type_traits>
@@ -966,23 +965,6 @@ static TeamShape team_shape(int64_t D, int es, bool vec, bool backward) {
 }
 
 constexpr int kMaxTeam = 512;  // threads of a block that has dynamic shared memory, at most
-
-// Lets a kernel have the dynamic shared memory that its widest rows take, once per device.  The limit
-// belongs to the kernel, not to a call: were it this call's size, another host thread's narrower rows
-// could lower it before this call's launch.
-template <auto KERNEL, int BYTES>
-static int allow_smem() {
-    static std::atomic<bool> done[64];
-    if (BYTES <= 40 * 1024) return TGC_OK;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return cuda_fail(e);
-    if (dev < 64 && done[dev].load(std::memory_order_acquire)) return TGC_OK;
-    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
-    if (e != cudaSuccess) return cuda_fail(e);
-    if (dev < 64) done[dev].store(true, std::memory_order_release);
-    return TGC_OK;
-}
 
 template <typename T, int V, int NV, bool BIAS, bool STAGED>
 static int launch_norm_form(const NormParams &p, dim3 grid, dim3 block, cudaStream_t stream) {

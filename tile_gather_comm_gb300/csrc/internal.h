@@ -2,6 +2,7 @@
 // libtgc.so (not part of the public ABI).
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -53,6 +54,23 @@ inline cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Lets a kernel have BYTES of dynamic shared memory, the most that any of its launches takes, once per device.  The limit
+// belongs to the kernel, not to a call: were it this call's size, another host thread's narrower rows
+// could lower it before this call's launch.
+template <auto KERNEL, int BYTES>
+inline int allow_smem() {
+    static std::atomic<bool> done[64];
+    if (BYTES <= 40 * 1024) return TGC_OK;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (dev < 64 && done[dev].load(std::memory_order_acquire)) return TGC_OK;
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (dev < 64) done[dev].store(true, std::memory_order_release);
+    return TGC_OK;
 }
 
 // Launch the TGATHER kernel; arguments already validated.

@@ -205,22 +205,6 @@ __device__ __forceinline__ Tile get_tile(const LinearParams &p, const int *tile0
     return r;
 }
 
-__device__ __forceinline__ uint32_t pack16(F2 v, bool f16) {
-    const float2 f = split(v);
-    uint32_t r;
-    if (f16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(f.y), "f"(f.x));
-    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(f.y), "f"(f.x));
-    return r;
-}
-
-__device__ __forceinline__ F2 unpack16(uint32_t w, bool f16) {
-    if (f16) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-        return f2(f.x, f.y);
-    }
-    return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-
 // Four words of 16-bit pairs added to eight fp32 values.
 __device__ __forceinline__ void add16(F2 (&v)[4], const uint4 &w, bool f16) {
     v[0] = add(v[0], unpack16(w.x, f16));
