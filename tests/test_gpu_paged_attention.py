@@ -286,6 +286,6 @@ def test_the_binding_refuses():
             call()
     for call in (lambda: tgc.tgc_paged_attention(q[:, :3], q[:, :3], kp, kp, table, n), lambda: tgc.tgc_paged_attention(q, q, kp, kp, table, n, window=-1),
                  lambda: tgc.tgc_paged_attention(q.float(), q.float(), kp.float(), kp.float(), table, n),
-                 lambda: tgc.tgc_paged_attention(q, q, kp, kp, table, n, workspace=torch.zeros(8, device="cuda", dtype=torch.uint8))):
+                 lambda: tgc.tgc_paged_attention(q, q, kp, kp, table.repeat(1, 3000), n, workspace=torch.zeros(8, device="cuda", dtype=torch.uint8))):
         with pytest.raises(tgc.TGCError):
             call()

@@ -5,25 +5,34 @@
 // Every key and value is read once and used for the G query heads that share it: 4 G flops for 4
 // bytes, so HBM is the bound and the design is about keeping loads in flight.
 //
-// Split: the keys of every (sequence, key head) -- an item -- are cut into units of 64 keys; all units of
-// all items lie end to end and every CTA takes an equal run of them, whatever the lengths are.  An
-// item that ends up in several CTAs is joined by a second kernel from the parts (maximum, sum,
-// unnormalised output) that they leave in the workspace; a CTA leaves two parts at most, so the
-// workspace does not grow with the lengths.  The lengths are read on the device.
+// A CTA's 4 warps work for themselves: of each unit of keys a warp takes its quarter (a step), copies it
+// with cp.async into its own ring of stages, and keeps its own running maximum, sum and output in
+// registers; they meet at an item's end.  No barrier in the loop; a page may end anywhere, as each key
+// finds its own page.  The copies run ahead of the products across the end of an item, so they do not
+// pause while the warps meet.
 //
-// A CTA's 4 warps work for themselves: of each unit a warp takes 16 keys, copies them with cp.async into
-// its own ring of stages, and keeps its own running maximum, sum and output in registers; they
-// meet at the item's end.  No barrier in the loop, and a page may end anywhere, as each key finds its
-// own page.
-//
-// Products: mma.sync m16n8k16, the heads that share a key (padded to 16) as rows.  One new token has
-// 1 to 16 rows; tcgen05 takes 64 or 128 at least, and its scores would go through TMEM to the
-// registers that need them here.  The bound is HBM, not the products.
+// Products: mma.sync m16n8k16 with keys (then elements of the values) as rows and the heads that share a key
+// as columns, padded to 8: scores^T = K Q^T, out^T = V^T P^T.  The scores come out with a key a lane group,
+// and movmatrix turns 8 x 8 of them into the second product's operand.  tcgen05 takes 64 or 128 rows of one
+// operand from shared memory alike, but its scores and outputs live in TMEM and would cross to registers and
+// back for every step; the bound is HBM, not the products.
 // The probabilities enter the second product as a high and a low 16-bit part: rounding them to
 // 16 bits once would add about as much error as rounding the output does.
+// The running maximum follows the scores only when one passes it by kSlack powers of two: until then the
+// probabilities are larger than 1, which costs no bits, and no lane needs another's maximum.
+//
+// Two ways to deal the work:
+//  - runs: the keys of every (sequence, key head) -- an item -- are cut into units; all units of all items
+//    lie end to end and every CTA takes an equal run of them, whatever the lengths are.  An item that ends up
+//    in several CTAs is joined by a second kernel from the parts (maximum, sum, unnormalised output) that
+//    they leave in the workspace; a CTA leaves two parts at most, so the workspace does not grow with the
+//    lengths.
+//  - clusters: an item is a cluster's, cut evenly over its CTAs, which join through distributed shared
+//    memory: one launch and no workspace, for calls with few and short items (attn_plan says which).
+// Both read the lengths on the device.
 #include <cmath>
 #include <cstdint>
-#include <cstring>
+#include <type_traits>
 
 #include <cuda_runtime.h>
 
@@ -36,9 +45,9 @@ namespace tgc {
 
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = kAttnWarps * 32;
-constexpr int kStep = 16;                     // keys of a warp's step
-constexpr int kUnit = kAttnWarps * kStep;     // keys of a unit
-constexpr int kMinUnits = 4;                  // units of a CTA at least: shorter runs cost more in joining than they save
+constexpr int kMinUnits = 4;                  // units of a CTA's run at least
+constexpr int kMaxCluster = 8;
+constexpr float kSlack = 8.0f;                // powers of two
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct AttnParams {
@@ -48,16 +57,17 @@ struct AttnParams {
     const int32_t *table, *lens;
     KvTable kv;
     int heads_q, heads_k, group, D;
-    int row_blocks;  // of a group, R rows each
+    int row_blocks;  // of a group, R heads each
     int64_t q_s, q_h, o_s, o_h, page_s, token_s, head_s;
     float scale;     // times log2(e) unless capped
     float cap, cap_inv;  // cap log2(e), scale / cap; cap 0: none
     int window;
-    int adv_pages, adv_tokens;  // kUnit keys on: pages and places
+    int cluster;  // CTAs of a cluster
+    int adv_pages, adv_tokens;  // a unit on: pages and places
     // workspace: parts (2 a CTA), and for each item the CTAs that share it
     float *part_out;   // (2 grid, R, D)
     float2 *part_ml;   // (2 grid, R): maximum (log2 units), sum
-    int2 *shared_by;   // (items): first and last CTA; (-1, -1): one alone
+    int2 *shared_by;   // (items): first and last CTA; (-1, -1): one alone, or no keys
 };
 
 // The keys of sequence s in range: [begin, end).
@@ -68,7 +78,8 @@ __device__ __forceinline__ KeyRange key_range(const AttnParams &p, int s) {
     const int end = p.kv.tokens(p.lens[s]);
     return {p.window > 0 && end > p.window ? end - p.window : 0, end};
 }
-__device__ __forceinline__ int units_of(KeyRange r) { return (r.end - r.begin + kUnit - 1) / kUnit; }
+template <int UNIT>
+__device__ __forceinline__ int units_of(KeyRange r) { return (r.end - r.begin + UNIT - 1) / UNIT; }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
     const int bytes = valid ? 16 : 0;  // the rest is filled with zeros
@@ -104,6 +115,13 @@ __device__ __forceinline__ float exp2_approx(float v) {
     return v;
 }
 
+// An 8 x 8 matrix of 16-bit elements, two in a row a lane, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
 // A 16-byte chunk's place in a row of a stage: rows of DP elements, chunks of 8 rows turned against one another
 // so that ldmatrix, which reads one chunk of 8 rows, meets every bank once.
 template <int DP>
@@ -111,354 +129,485 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
     return (uint32_t)(row * DP * 2 + ((chunk ^ (row & 7)) << 4));
 }
 
-template <int DP, int MT>
+// DP: elements of a head, padded to 64, 128 or 256.  NT: query heads of an item, in eights.
+template <int DP, int NT>
 struct AttnShape {
-    static constexpr int kRows = 16 * MT;
-    static constexpr int kTile = kStep * DP * 2;      // bytes of a step's keys (or values)
-    static constexpr int kStages = DP == 64 ? 6 : DP == 128 ? 3 : 3;
-    static constexpr int kQBytes = kRows * DP * 2;
-    static constexpr int kRing = kAttnWarps * kStages * 2 * kTile;
-    static constexpr int kJoin = kAttnWarps * kRows * (DP + 2) * 4;  // the warps' outputs, in the ring's place
-    static constexpr int kSmem = kQBytes + (kRing > kJoin ? kRing : kJoin);
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kKeys = DP == 64 ? 32 : 16;  // of a warp's step
+    static constexpr int kUnit = kAttnWarps * kKeys;
+    static constexpr int kTile = kKeys * DP * 2;      // bytes of a step's keys (or values)
+    static constexpr int kStages = 3;
+    static constexpr int kWarpRing = kStages * 2 * kTile;
+    static constexpr int kSmem = kAttnWarps * kWarpRing;
+    // Outputs of so many heads fit a stage; more take turns.
+    static constexpr int kRound = kRows * DP * 4 <= 2 * kTile ? kRows : 2 * kTile / (DP * 4);
+    // Where a CTA of a cluster that took `steps` steps leaves its part of the heads from r0 on: not in the stage where its
+    // warps' parts meet, the last it used.
+    __device__ static int cta_part(int steps, int r0) {
+        return r0 / kRound * kWarpRing + (steps + kStages) % kStages * 2 * kTile;
+    }
+};
+static_assert(AttnShape<128, 4>::kRound == 16 && AttnShape<64, 4>::kRound == 32 && AttnShape<256, 2>::kRound == 16, "whole eights");
+
+// Where a run stands: its place in the row of all units, and the item there.
+struct RunAt {
+    int64_t at, seq_begin;  // units before it; units before its sequence
+    int seq, item, unit, units;  // item of the sequence; unit of the item, of so many
+    int begin, end;              // keys of the sequence in range
 };
 
-// The rows' results: normalised to `out`, or as a part to the workspace.
-template <bool F16, int DP, int MT>
+// The pair at `local`'s place in CTA `rank` of this cluster.
+__device__ __forceinline__ float2 load_cluster(const void *local, int rank) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                 : "=f"(v.x), "=f"(v.y) : "r"(mapa_shared(smem_addr(local), (uint32_t)rank)) : "memory");
+    return v;
+}
+
+// Normalises a row's two neighbouring outputs and stores them.
+template <bool F16>
+__device__ __forceinline__ void store_out(const AttnParams &p, int seq, int head, int c, float m, float l, float2 o) {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + seq * p.o_s + head * p.o_h + c) =
+        pack16(f2(o.x * inv, o.y * inv), F16);
+    if (c == 0 && p.lse != nullptr)
+        p.lse[(int64_t)seq * p.heads_q + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+template <bool F16, int DP, int NT, bool CLUSTER>
 __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_kernel(const AttnParams p) {
-    using S = AttnShape<DP, MT>;
+    using S = AttnShape<DP, NT>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t s_scan[kAttnWarps];
     __shared__ int64_t s_before;
     __shared__ int s_seq;
     __shared__ uint32_t s_mask[kAttnWarps][S::kStages];
-    const int tid = (int)threadIdx.x, warp = tid / 32, lane = tid % 32;
-    uint8_t *q_s = smem, *ring = smem + S::kQBytes;
+    __shared__ float2 s_ml[kAttnWarps][S::kRows];
+    __shared__ float2 s_cta_ml[S::kRows];
+    const int tid = (int)threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane >> 2, t4 = lane & 3;
+    uint8_t *const ring = smem + warp * S::kWarpRing;
+    const uint32_t ring_at = smem_addr(ring);
+    const int chunks = p.D / 8;
 
-    // What lies beyond D in the stages stays zero, so it adds nothing to any product.
-    if (p.D < DP)
-        for (int i = tid; i < S::kRing / 16; i += kAttnThreads) reinterpret_cast<uint4 *>(ring)[i] = make_uint4(0, 0, 0, 0);
+    // Products are 16 deep: where D ends inside 16, the rest of the keys' rows has to be zero.
+    auto clear_tail = [&](int stage) {
+        if (chunks % 2 != 0 && lane < S::kKeys)
+            *reinterpret_cast<uint4 *>(ring + stage * 2 * S::kTile + chunk_at<DP>(lane, chunks)) = make_uint4(0, 0, 0, 0);
+    };
+#pragma unroll
+    for (int i = 0; i < S::kStages; ++i) clear_tail(i);
     stream_wait();
     stream_release();
 
     // ---- this CTA's run of units
     const int heads = p.heads_k * p.row_blocks;  // items of a sequence
-    const int share = (p.kv.num_seqs + kAttnThreads - 1) / kAttnThreads;
-    int64_t mine = 0;
-    for (int i = 0; i < share; ++i) {
-        const int s = tid * share + i;
-        if (s < p.kv.num_seqs) mine += units_of(key_range(p, s));
-    }
-    int64_t upto = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, upto, d);
-        if (lane >= d) upto += v;
-    }
-    if (lane == 31) s_scan[warp] = upto;
-    __syncthreads();
-    int64_t base = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) {
-        if (w < warp) base += s_scan[w];
-        total += s_scan[w];
-    }
-    upto += base;
-    total *= heads;
-    int64_t per = (total + gridDim.x - 1) / gridDim.x;
-    if (per < kMinUnits) per = kMinUnits;
-    int64_t at = per * blockIdx.x;
-    const int64_t stop = at + per < total ? at + per : total;
-
-    // Sequences without keys: zeros.
-    for (int s = (int)blockIdx.x; s < p.kv.num_seqs; s += (int)gridDim.x) {
-        if (units_of(key_range(p, s)) != 0) continue;
-        for (int i = tid; i < p.heads_q * p.D; i += kAttnThreads)
-            static_cast<uint16_t *>(p.out)[s * p.o_s + i / p.D * p.o_h + i % p.D] = 0;
-        if (p.lse != nullptr)
-            for (int i = tid; i < p.heads_q; i += kAttnThreads) p.lse[(int64_t)s * p.heads_q + i] = -INFINITY;
-    }
-    if (at >= stop) return;
-
-    // The sequence in which the run starts: in the share of the thread whose units hold it.
-    if ((upto - mine) * heads <= at && at < upto * heads) {
-        int64_t before = upto - mine;
-        int s = tid * share;
-        for (;; ++s) {
-            const int n = units_of(key_range(p, s));
-            if (at < (before + n) * heads) break;
-            before += n;
+    int64_t stop = 0, per = 0;
+    RunAt r{};  // where the copies stand
+    int rank = 0, ranks = 1;
+    if constexpr (CLUSTER) {
+        rank = (int)cluster_ctarank();
+        ranks = p.cluster;
+        const int all = (int)blockIdx.x / ranks;
+        r.seq = all / heads;
+        r.item = all % heads;
+        const KeyRange k = key_range(p, r.seq);
+        r.begin = k.begin;
+        r.end = k.end;
+        r.units = units_of<S::kUnit>(k);
+        const int each = (r.units + ranks - 1) / ranks;
+        r.unit = each * rank < r.units ? each * rank : r.units;
+        r.at = r.unit;
+        stop = r.unit + each < r.units ? r.unit + each : r.units;
+    } else {
+        const int share = (p.kv.num_seqs + kAttnThreads - 1) / kAttnThreads;
+        int64_t mine = 0;
+        for (int i = 0; i < share; ++i) {
+            const int s = tid * share + i;
+            if (s < p.kv.num_seqs) mine += units_of<S::kUnit>(key_range(p, s));
         }
-        s_seq = s;
-        s_before = before * heads;
-    }
-    __syncthreads();
-    int seq = s_seq;
-    int64_t seq_begin = s_before;  // global number of the sequence's first unit
-
-    const int chunks = p.D / 8;
-    const uint32_t ring_at = smem_addr(ring) + (uint32_t)(warp * S::kStages * 2 * S::kTile);
-    const uint32_t q_at = smem_addr(q_s);
-
-    while (at < stop) {
-        const KeyRange range = key_range(p, seq);
-        const int units = units_of(range);
-        if (at >= seq_begin + (int64_t)units * heads) {  // this sequence is done (or has no keys)
-            seq_begin += (int64_t)units * heads;
-            ++seq;
-            continue;
+        int64_t upto = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += v;
         }
-        const int item = (int)((at - seq_begin) / units), unit0 = (int)((at - seq_begin) - (int64_t)item * units);
-        const int unit1 = stop - at < units - unit0 ? unit0 + (int)(stop - at) : units;
-        const int head_k = item / p.row_blocks, row0 = item % p.row_blocks * S::kRows;
-        const int rows = p.group - row0 < S::kRows ? p.group - row0 : S::kRows;
-        const int64_t item_begin = seq_begin + (int64_t)item * units;
+        if (lane == 31) s_scan[warp] = upto;
+        __syncthreads();
+        int64_t base = 0, total = 0;
+#pragma unroll
+        for (int w = 0; w < kAttnWarps; ++w) {
+            if (w < warp) base += s_scan[w];
+            total += s_scan[w];
+        }
+        upto += base;
+        total *= heads;
+        per = (total + gridDim.x - 1) / gridDim.x;
+        if (per < kMinUnits) per = kMinUnits;
+        r.at = per * blockIdx.x;
+        stop = r.at + per < total ? r.at + per : total;
 
-        // ---- queries to shared memory, rows and columns beyond them zero
-        for (int i = tid; i < S::kRows * (DP / 8); i += kAttnThreads) {
-            const int r = i / (DP / 8), c = i % (DP / 8);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (r < rows && c < chunks)
-                v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + seq * p.q_s +
-                                                     (int64_t)(head_k * p.group + row0 + r) * p.q_h + c * 8);
-            *reinterpret_cast<uint4 *>(q_s + chunk_at<DP>(r, c)) = v;
+        // Sequences without keys: zeros.
+        for (int s = (int)blockIdx.x; s < p.kv.num_seqs; s += (int)gridDim.x) {
+            if (units_of<S::kUnit>(key_range(p, s)) != 0) continue;
+            for (int i = tid; i < p.heads_q * p.D; i += kAttnThreads)
+                static_cast<uint16_t *>(p.out)[s * p.o_s + i / p.D * p.o_h + i % p.D] = 0;
+            if (p.lse != nullptr)
+                for (int i = tid; i < p.heads_q; i += kAttnThreads) p.lse[(int64_t)s * p.heads_q + i] = -INFINITY;
+            for (int i = tid; i < heads; i += kAttnThreads) p.shared_by[(int64_t)s * heads + i] = make_int2(-1, -1);
+        }
+        if (r.at >= stop) return;
+
+        // The sequence in which the run starts: in the share of the thread whose units hold it.
+        if ((upto - mine) * heads <= r.at && r.at < upto * heads) {
+            int64_t before = upto - mine;
+            int s = tid * share;
+            for (;; ++s) {
+                const int n = units_of<S::kUnit>(key_range(p, s));
+                if (r.at < (before + n) * heads || s + 1 == p.kv.num_seqs) break;
+                before += n;
+            }
+            s_seq = s;
+            s_before = before * heads;
         }
         __syncthreads();
+        r.seq = s_seq;
+        r.seq_begin = s_before;
+        const KeyRange k = key_range(p, r.seq);
+        r.begin = k.begin;
+        r.end = k.end;
+        r.units = units_of<S::kUnit>(k);
+        const int64_t in_seq = r.at - r.seq_begin;
+        if (r.units == 0 || in_seq / r.units >= heads) return;  // only where the lengths change under the call
+        r.item = (int)(in_seq / r.units);
+        r.unit = (int)(in_seq - (int64_t)r.item * r.units);
+    }
 
-        // ---- the warp's loads: lane l < 16 finds the page of key l of a step, all lanes copy
-        const int steps = unit1 - unit0;
-        const uint16_t *kp = static_cast<const uint16_t *>(p.k) + (int64_t)head_k * p.head_s;
-        const uint16_t *vp = static_cast<const uint16_t *>(p.v) + (int64_t)head_k * p.head_s;
-        int key = range.begin + unit0 * kUnit + warp * kStep + (lane & 15);  // of the step to be issued
-        int page_i = key / p.kv.page_size, place = key - page_i * p.kv.page_size;
-        auto next_page = [&] { return key < range.end ? p.kv.page_at(p.table, seq, page_i) : -1; };
-        int page = next_page();
-        auto issue = [&](int step) {
-            const int stage = step % S::kStages;
-            const int64_t off = page < 0 ? -1 : page * p.page_s + place * p.token_s;
-            const uint32_t have = __ballot_sync(0xffffffffu, off >= 0) & 0xffffu;
+    // ---- the warp's copies: a lane finds the page of a key of the step, all lanes copy
+    const int my_key = warp * S::kKeys + lane % S::kKeys;
+    int key = 0, page_i = 0, place = 0, page = -1;  // of the unit to be copied next
+    int64_t head_off = 0;
+    auto find_page = [&] { page = key < r.end ? p.kv.page_at(p.table, r.seq, page_i) : -1; };
+    auto enter_item = [&] {
+        key = r.begin + r.unit * S::kUnit + my_key;
+        page_i = key / p.kv.page_size;
+        place = key - page_i * p.kv.page_size;
+        head_off = (int64_t)(r.item / p.row_blocks) * p.head_s;
+        find_page();
+    };
+    if (r.at < stop) enter_item();
+    RunAt c = r;  // where the products stand
+    int issued = 0;
+    // The next sequence that has keys; none only where the lengths change under the call.
+    auto next_seq = [&](RunAt &w) {
+        while (++w.seq < p.kv.num_seqs) {
+            const KeyRange k = key_range(p, w.seq);
+            w.begin = k.begin;
+            w.end = k.end;
+            w.units = units_of<S::kUnit>(k);
+            if (w.units > 0) return true;
+        }
+        return false;
+    };
+    auto copy_unit = [&] {
+        if (r.at < stop) {
+            const int stage = issued % S::kStages;
+            const int64_t off = page < 0 ? -1 : page * p.page_s + place * p.token_s + head_off;
+            const uint32_t have = __ballot_sync(0xffffffffu, off >= 0);
             if (lane == 0) s_mask[warp][stage] = have;
             const uint32_t to = ring_at + (uint32_t)(stage * 2 * S::kTile);
 #pragma unroll
-            for (int i = 0; i < kStep * (DP / 8) / 32; ++i) {
-                const int idx = i * 32 + lane, r = idx / (DP / 8), c = idx % (DP / 8);
-                const int64_t o = __shfl_sync(0xffffffffu, off, r);
-                if (c < chunks) {
-                    const int64_t from = o < 0 ? 0 : o + c * 8;
-                    cp_async16(to + chunk_at<DP>(r, c), kp + from, o >= 0);
-                    cp_async16(to + S::kTile + chunk_at<DP>(r, c), vp + from, o >= 0);
+            for (int i = 0; i < S::kKeys * (DP / 8) / 32; ++i) {
+                const int idx = i * 32 + lane, row = idx / (DP / 8), ch = idx % (DP / 8);
+                const int64_t o = __shfl_sync(0xffffffffu, off, row);
+                if (ch < chunks) {
+                    const int64_t from = o < 0 ? 0 : o + ch * 8;
+                    cp_async16(to + chunk_at<DP>(row, ch), static_cast<const uint16_t *>(p.k) + from, o >= 0);
+                    cp_async16(to + S::kTile + chunk_at<DP>(row, ch), static_cast<const uint16_t *>(p.v) + from, o >= 0);
                 }
             }
-            key += kUnit;
-            page_i += p.adv_pages;
-            place += p.adv_tokens;
-            if (place >= p.kv.page_size) {
-                place -= p.kv.page_size;
-                ++page_i;
+            ++r.at;
+            if (++r.unit < r.units) {
+                key += S::kUnit;
+                page_i += p.adv_pages;
+                place += p.adv_tokens;
+                if (place >= p.kv.page_size) {
+                    place -= p.kv.page_size;
+                    ++page_i;
+                }
+                find_page();
+            } else if (!CLUSTER && r.at < stop) {
+                r.unit = 0;
+                if (++r.item == heads) {
+                    r.item = 0;
+                    r.seq_begin += (int64_t)r.units * heads;
+                    if (!next_seq(r)) {
+                        r.at = stop;
+                        return;
+                    }
+                }
+                enter_item();
             }
-            page = next_page();
-        };
-#pragma unroll
-        for (int i = 0; i < S::kStages - 1; ++i) {
-            if (i < steps) issue(i);
-            cp_async_commit();
         }
+    };
+    auto issue = [&] {
+        copy_unit();
+        ++issued;
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < S::kStages - 1; ++i) issue();
 
-        // ---- the loop
-        constexpr bool kQInRegs = DP * MT <= 128;
-        uint32_t qf[kQInRegs ? MT : 1][kQInRegs ? DP / 16 : 1][4];
-        const uint32_t q_lane = (uint32_t)(lane & 15);
-        if constexpr (kQInRegs)
+    int step = 0;
+    do {
+        const int head_k = c.item / p.row_blocks, row0 = c.item % p.row_blocks * S::kRows;
+        const int rows = p.group - row0 < S::kRows ? p.group - row0 : S::kRows;
+        const int head0 = head_k * p.group + row0;
+        int todo = (int)(stop - c.at < c.units - c.unit ? stop - c.at : c.units - c.unit);
+        if (CLUSTER) todo = (int)(stop - c.at);
+
+        // queries as the first product's right operand: lane (g, t4) has elements 2 t4, 2 t4 + 1 of every 8 of head g
+        uint32_t qf[NT][DP / 16][2];
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+        for (int n = 0; n < NT; ++n) {
+            const uint16_t *from = static_cast<const uint16_t *>(p.q) + c.seq * p.q_s + (int64_t)(head0 + n * 8 + g) * p.q_h + t4 * 2;
 #pragma unroll
-                for (int kk = 0; kk < DP / 16; ++kk)
-                    ldmatrix4(qf[m][kk], q_at + chunk_at<DP>(m * 16 + (int)q_lane, kk * 2 + (lane >> 4)));
-        float acc[MT][DP / 8][4];
-        float top[MT][2], sum[MT][2];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-#pragma unroll
-            for (int j = 0; j < DP / 8; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.0f;
-            top[m][0] = top[m][1] = -INFINITY;
-            sum[m][0] = sum[m][1] = 0.0f;
+            for (int i = 0; i < DP / 8; ++i)
+                qf[n][i / 2][i % 2] = n * 8 + g < rows && i < chunks ? *reinterpret_cast<const uint32_t *>(from + i * 8) : 0u;
         }
-        for (int step = 0; step < steps; ++step) {
+        float acc[DP / 16][NT][4];  // elements g and g + 8 of every 16, heads 2 t4 and 2 t4 + 1 of every 8
+        float top[NT][2], sum[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int j = 0; j < DP / 16; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[j][n][e] = 0.0f;
+            top[n][0] = top[n][1] = -INFINITY;
+            sum[n][0] = sum[n][1] = 0.0f;
+        }
+        for (int left = todo; left > 0; --left, ++step) {
             cp_async_wait<S::kStages - 2>();
             __syncwarp();
             const int stage = step % S::kStages;
             const uint32_t k_at = ring_at + (uint32_t)(stage * 2 * S::kTile), v_at = k_at + S::kTile;
             const uint32_t have = s_mask[warp][stage];
-            if (step + S::kStages - 1 < steps) issue(step + S::kStages - 1);
-            cp_async_commit();
+            issue();
 
-            // scores: two tiles of 16 rows x 8 keys
-            float x[MT][2][4];
+            constexpr int MK = S::kKeys / 16;
+            float x[MK][NT][4];  // keys g and g + 8 of every 16
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int m = 0; m < MK; ++m)
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[m][j][e] = 0.0f;
+                    for (int e = 0; e < 4; ++e) x[m][n][e] = 0.0f;
 #pragma unroll
             for (int kk = 0; kk < DP / 16; ++kk) {
-                uint32_t b[4];  // keys 0-7 and 8-15, each the two halves of 16 elements
-                ldmatrix4(b, k_at + chunk_at<DP>((lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)));
+                if (kk * 2 >= chunks) break;
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    if constexpr (kQInRegs) {
-                        mma16<F16>(x[m][0], qf[m][kk], b[0], b[1]);
-                        mma16<F16>(x[m][1], qf[m][kk], b[2], b[3]);
-                    } else {
-                        uint32_t a[4];
-                        ldmatrix4(a, q_at + chunk_at<DP>(m * 16 + (int)q_lane, kk * 2 + (lane >> 4)));
-                        mma16<F16>(x[m][0], a, b[0], b[1]);
-                        mma16<F16>(x[m][1], a, b[2], b[3]);
-                    }
+                for (int m = 0; m < MK; ++m) {
+                    uint32_t a[4];
+                    ldmatrix4(a, k_at + chunk_at<DP>(m * 16 + (lane & 15), kk * 2 + (lane >> 4)));
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma16<F16>(x[m][n], a, qf[n][kk][0], qf[n][kk][1]);
                 }
             }
-            // softmax, in powers of two
-            uint32_t ph[MT][4], pl[MT][4];  // probabilities as the next product's operand: high and low parts
+            if (p.cap > 0.0f) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                if (p.cap > 0.0f) {
+                for (int m = 0; m < MK; ++m)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[m][j][e] = p.cap * tanhf(x[m][j][e] * p.cap_inv);
-                } else {
+                        for (int e = 0; e < 4; ++e) x[m][n][e] = p.cap * tanhf(x[m][n][e] * p.cap_inv);
+            } else {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
+                for (int m = 0; m < MK; ++m)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[m][j][e] *= p.scale;
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[m][n][e] *= p.scale;
+            }
+            if (have != 0xffffffffu) {
+#pragma unroll
+                for (int m = 0; m < MK; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (!(have >> (m * 16 + h * 8 + g) & 1u))
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) x[m][n][2 * h] = x[m][n][2 * h + 1] = -INFINITY;
+            }
+            // softmax in powers of two
+            float big[NT][2];
+            bool past = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float v = fmaxf(x[0][n][e], x[0][n][2 + e]);
+                    if (MK == 2) v = fmaxf(v, fmaxf(x[MK - 1][n][e], x[MK - 1][n][2 + e]));
+                    big[n][e] = v;
+                    past = past || v > top[n][e] + kSlack;
                 }
-                if (have != 0xffffu) {
+            if (__any_sync(0xffffffffu, past)) {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (!(have >> (j * 8 + (lane & 3) * 2 + (e & 1)) & 1u)) x[m][j][e] = -INFINITY;
-                }
-                float big[2];
-                bool rescale = false;
+                    for (int e = 0; e < 2; ++e) {
+                        float v = big[n][e];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    big[h] = fmaxf(fmaxf(x[m][0][2 * h], x[m][0][2 * h + 1]), fmaxf(x[m][1][2 * h], x[m][1][2 * h + 1]));
-                    big[h] = fmaxf(big[h], __shfl_xor_sync(0xffffffffu, big[h], 1));
-                    big[h] = fmaxf(big[h], __shfl_xor_sync(0xffffffffu, big[h], 2));
-                    rescale = rescale || big[h] > top[m][h];
-                }
-                if (__any_sync(0xffffffffu, rescale)) {
+                        for (int d = 4; d < 32; d *= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+                        v = fmaxf(top[n][e], v);
+                        const float f = v == -INFINITY ? 1.0f : exp2_approx(top[n][e] - v);
+                        top[n][e] = v;
+                        sum[n][e] *= f;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float now = fmaxf(top[m][h], big[h]);
-                        const float f = now == -INFINITY ? 1.0f : exp2_approx(top[m][h] - now);
-                        top[m][h] = now;
-                        sum[m][h] *= f;
-#pragma unroll
-                        for (int j = 0; j < DP / 8; ++j) {
-                            acc[m][j][2 * h] *= f;
-                            acc[m][j][2 * h + 1] *= f;
+                        for (int j = 0; j < DP / 16; ++j) {
+                            acc[j][n][e] *= f;
+                            acc[j][n][2 + e] *= f;
                         }
                     }
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float off = top[m][h] == -INFINITY ? 0.0f : top[m][h];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float a = exp2_approx(x[m][j][2 * h] - off), b = exp2_approx(x[m][j][2 * h + 1] - off);
-                        sum[m][h] += a + b;
-                        const F2 both = f2(a, b);
-                        const uint32_t hi = pack16(both, F16);
-                        const float2 r = split(unpack16(hi, F16));
-                        ph[m][j * 2 + h] = hi;
-                        pl[m][j * 2 + h] = pack16(f2(a - r.x, b - r.y), F16);
-                    }
-                }
             }
-            // outputs: 16 keys deep, tiles of 16 rows x 8 elements
+            uint32_t hi[MK][NT][2], lo[MK][NT][2];  // probabilities: keys 0-7 and 8-15 of every 16
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float off0 = top[n][0] == -INFINITY ? 0.0f : top[n][0], off1 = top[n][1] == -INFINITY ? 0.0f : top[n][1];
+#pragma unroll
+                for (int m = 0; m < MK; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float a = exp2_approx(x[m][n][2 * h] - off0), b = exp2_approx(x[m][n][2 * h + 1] - off1);
+                        sum[n][0] += a;
+                        sum[n][1] += b;
+                        const uint32_t w = pack16(f2(a, b), F16);
+                        const float2 back = split(unpack16(w, F16));
+                        hi[m][n][h] = transpose8(w);
+                        lo[m][n][h] = transpose8(pack16(f2(a - back.x, b - back.y), F16));
+                    }
+            }
 #pragma unroll
             for (int j = 0; j < DP / 16; ++j) {
-                uint32_t b[4];
-                ldmatrix4_trans(b, v_at + chunk_at<DP>(lane & 15, j * 2 + (lane >> 4)));
+                if (j * 2 >= chunks) break;
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    mma16<F16>(acc[m][2 * j], ph[m], b[0], b[1]);
-                    mma16<F16>(acc[m][2 * j + 1], ph[m], b[2], b[3]);
-                    mma16<F16>(acc[m][2 * j], pl[m], b[0], b[1]);
-                    mma16<F16>(acc[m][2 * j + 1], pl[m], b[2], b[3]);
+                for (int m = 0; m < MK; ++m) {
+                    uint32_t a[4];
+                    ldmatrix4_trans(a, v_at + chunk_at<DP>(m * 16 + (lane & 7) + ((lane >> 4) << 3), j * 2 + ((lane >> 3) & 1)));
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma16<F16>(acc[j][n], a, hi[m][n][0], hi[m][n][1]);
+                        mma16<F16>(acc[j][n], a, lo[m][n][0], lo[m][n][1]);
+                    }
                 }
             }
         }
 
-        // ---- the warps' parts meet in the ring's place
-        cp_async_wait<0>();
-        __syncthreads();
-        float *w_out = reinterpret_cast<float *>(ring);                         // (warps, rows, DP)
-        float2 *w_ml = reinterpret_cast<float2 *>(w_out + kAttnWarps * S::kRows * DP);  // (warps, rows)
+        // ---- the warps' parts meet: each in the stage that it used last, which its copies have not reached again
+        const int last_stage = (step + S::kStages - 1) % S::kStages;
+        auto part_of = [&](int w) { return reinterpret_cast<float *>(smem + w * S::kWarpRing + last_stage * 2 * S::kTile); };
+        // heads' rows of DP; pairs of heads turned against one another, so that a warp's stores meet every bank once
+        auto place_of = [](int row, int d) { return row * DP + (d ^ (((row >> 1) & 3) << 3)); };
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float l = sum[m][h];
-                l += __shfl_xor_sync(0xffffffffu, l, 1);
-                l += __shfl_xor_sync(0xffffffffu, l, 2);
-                const int r = m * 16 + h * 8 + (lane >> 2);
-                if ((lane & 3) == 0) w_ml[warp * S::kRows + r] = make_float2(top[m][h], l);
-                if (r < rows)
+            for (int e = 0; e < 2; ++e) {
+                float l = sum[n][e];
 #pragma unroll
-                    for (int j = 0; j < DP / 8; ++j)
-                        *reinterpret_cast<float2 *>(w_out + (warp * S::kRows + r) * DP + j * 8 + (lane & 3) * 2) =
-                            make_float2(acc[m][j][2 * h], acc[m][j][2 * h + 1]);
+                for (int d = 4; d < 32; d *= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
+                if (g == 0) s_ml[warp][n * 8 + t4 * 2 + e] = make_float2(top[n][e], l);
             }
-        __syncthreads();
-        const int64_t first = item_begin / per, last = (item_begin + units - 1) / per;
-        const bool whole = first == last;
+        const int64_t item_begin = c.at - c.unit;
+        const bool whole = CLUSTER ? ranks == 1 : item_begin / per == (item_begin + c.units - 1) / per;
         const int part = 2 * (int)blockIdx.x + (item_begin < per * blockIdx.x ? 0 : 1);
-        if (tid == 0 && unit0 == 0)
-            p.shared_by[(int64_t)seq * heads + item] = whole ? make_int2(-1, -1) : make_int2((int)first, (int)last);
-        for (int i = tid; i < rows * (p.D / 2); i += kAttnThreads) {
-            const int r = i / (p.D / 2), c = i % (p.D / 2) * 2;
-            float2 ml[kAttnWarps];
-            float m = -INFINITY;
+        if (!CLUSTER && tid == 0 && c.unit == 0)
+            p.shared_by[(int64_t)c.seq * heads + c.item] =
+                whole ? make_int2(-1, -1) : make_int2((int)(item_begin / per), (int)((item_begin + c.units - 1) / per));
 #pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) {
-                ml[w] = w_ml[w * S::kRows + r];
-                m = fmaxf(m, ml[w].x);
-            }
-            const float off = m == -INFINITY ? 0.0f : m;
-            float l = 0.0f;
-            float2 o = make_float2(0.0f, 0.0f);
+        for (int r0 = 0; r0 < S::kRows; r0 += S::kRound) {
+            __syncwarp();
 #pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) {
-                const float f = exp2_approx(ml[w].x - off);
-                const float2 v = *reinterpret_cast<const float2 *>(w_out + (w * S::kRows + r) * DP + c);
-                l += ml[w].y * f;
-                o.x += v.x * f;
-                o.y += v.y * f;
+            for (int n = r0 / 8; n < (r0 + S::kRound) / 8; ++n)
+#pragma unroll
+                for (int j = 0; j < DP / 16; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        part_of(warp)[place_of(n * 8 - r0 + t4 * 2 + (e & 1), j * 16 + g + (e >> 1) * 8)] = acc[j][n][e];
+            __syncthreads();
+            const int here = rows - r0 < S::kRound ? rows - r0 : S::kRound;
+            for (int i = tid; i < here * (p.D / 2); i += kAttnThreads) {
+                const int row = i / (p.D / 2), d = i % (p.D / 2) * 2;
+                float2 ml[kAttnWarps];
+                float m = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kAttnWarps; ++w) {
+                    ml[w] = s_ml[w][r0 + row];
+                    m = fmaxf(m, ml[w].x);
+                }
+                const float off = m == -INFINITY ? 0.0f : m;
+                float l = 0.0f;
+                float2 o = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int w = 0; w < kAttnWarps; ++w) {
+                    const float f = exp2_approx(ml[w].x - off);
+                    const float2 v = *reinterpret_cast<const float2 *>(part_of(w) + place_of(row, d));
+                    l += ml[w].y * f;
+                    o.x += v.x * f;
+                    o.y += v.y * f;
+                }
+                if (whole) {
+                    store_out<F16>(p, c.seq, head0 + r0 + row, d, m, l, o);
+                } else if (CLUSTER) {
+                    *reinterpret_cast<float2 *>(smem + S::cta_part(step, r0) + (row * DP + d) * 4) = o;
+                    if (d == 0) s_cta_ml[r0 + row] = make_float2(m, l);
+                } else {
+                    *reinterpret_cast<float2 *>(p.part_out + ((int64_t)part * S::kRows + r0 + row) * p.D + d) = o;
+                    if (d == 0) p.part_ml[part * S::kRows + r0 + row] = make_float2(m, l);
+                }
             }
-            const int head = head_k * p.group + row0 + r;
-            if (whole) {
-                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + seq * p.o_s + head * p.o_h + c) =
-                    pack16(f2(o.x * inv, o.y * inv), F16);
-                if (c == 0 && p.lse != nullptr)
-                    p.lse[(int64_t)seq * p.heads_q + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
-            } else {
-                *reinterpret_cast<float2 *>(p.part_out + ((int64_t)part * S::kRows + r) * p.D + c) = o;
-                if (c == 0) p.part_ml[part * S::kRows + r] = make_float2(m, l);
-            }
-        }
-        __syncthreads();
-        if (p.D < DP && at + (unit1 - unit0) < stop) {  // zeros again where the parts lay
-            for (int i = tid; i < S::kRing / 16; i += kAttnThreads)
-                reinterpret_cast<uint4 *>(ring)[i] = make_uint4(0, 0, 0, 0);
             __syncthreads();
         }
-        at += unit1 - unit0;
-    }
+        if constexpr (CLUSTER) {
+            if (ranks > 1) {
+                // the CTAs' parts meet: every CTA takes some of the outputs and reads all parts of them
+                cluster_sync();
+                const int each = (c.units + ranks - 1) / ranks;
+                for (int i = rank * kAttnThreads + tid; i < rows * (p.D / 2); i += ranks * kAttnThreads) {
+                    const int row = i / (p.D / 2), d = i % (p.D / 2) * 2, r0 = row / S::kRound * S::kRound;
+                    float2 ml[kMaxCluster], v[kMaxCluster];
+                    float m = -INFINITY;
+#pragma unroll
+                    for (int q = 0; q < kMaxCluster; ++q) {
+                        if (q >= ranks) break;
+                        const int before = each * q < c.units ? each * q : c.units;
+                        const int steps = c.units - before < each ? c.units - before : each;
+                        ml[q] = load_cluster(&s_cta_ml[row], q);
+                        v[q] = load_cluster(smem + S::cta_part(steps, r0) + ((row - r0) * DP + d) * 4, q);
+                        m = fmaxf(m, ml[q].x);
+                    }
+                    const float off = m == -INFINITY ? 0.0f : m;
+                    float l = 0.0f;
+                    float2 o = make_float2(0.0f, 0.0f);
+#pragma unroll
+                    for (int q = 0; q < kMaxCluster; ++q) {
+                        if (q >= ranks) break;
+                        const float f = exp2_approx(ml[q].x - off);
+                        l += ml[q].y * f;
+                        o.x += v[q].x * f;
+                        o.y += v[q].y * f;
+                    }
+                    store_out<F16>(p, c.seq, head0 + row, d, m, l, o);
+                }
+                cluster_sync();  // no CTA ends while another may still read its part
+            }
+            return;
+        }
+        clear_tail(last_stage);
+        // on to the next item
+        c.at += todo;
+        c.unit = 0;
+        if (c.at < stop && ++c.item == heads) {
+            c.item = 0;
+            if (!next_seq(c)) break;
+        }
+    } while (c.at < stop);
 }
 
 // One block a row (sequence, query head) joins the parts of an item that several CTAs share.
@@ -471,8 +620,6 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
     stream_wait();
     stream_release();
     const int head = (int)(blockIdx.x % (unsigned)p.heads_q), seq = (int)(blockIdx.x / (unsigned)p.heads_q);
-    const KeyRange range = key_range(p, seq);
-    if (range.end == range.begin) return;
     const int heads = p.heads_k * p.row_blocks, in_group = head % p.group;
     const int item = head / p.group * p.row_blocks + in_group / part_rows, row = in_group % part_rows;
     const int2 by = p.shared_by[(int64_t)seq * heads + item];
@@ -516,7 +663,6 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
     l = 0.0f;
 #pragma unroll
     for (int w = 0; w < kJoinThreads / 32; ++w) l += s_ml[1][w];
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     for (int c = tid; c < p.D / 2; c += kJoinThreads) {
         float2 v = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -524,11 +670,8 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
             v.x += s_out[w][c].x;
             v.y += s_out[w][c].y;
         }
-        *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + seq * p.o_s + head * p.o_h + 2 * c) =
-            pack16(f2(v.x * inv, v.y * inv), F16);
+        store_out<F16>(p, seq, head, 2 * c, m, l, v);
     }
-    if (tid == 0 && p.lse != nullptr)
-        p.lse[(int64_t)seq * p.heads_q + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // ---------------------------------------------------------------- host
@@ -554,45 +697,63 @@ static int attn_check(tgc_paged_attention_args &a) {
 }
 
 struct AttnPlan {
-    int dp, mt, row_blocks, grid;
+    int dp, nt, row_blocks, unit, grid, cluster;  // cluster: 0 where the work is dealt in runs
     int64_t items;
     bool join;
     size_t ml_off, shared_off, total;
 };
 
-// Rows of an MMA: 16 for up to 16 heads a key head, 32 for more where the registers hold their outputs (D <= 128).
-// Grid: two CTAs an SM (one for D > 128), no more than there can be runs of kMinUnits units.
+// Heads of an item, in eights: as many as share a key, up to 32 (16 for D > 128, whose outputs take twice the
+// registers).
+// Clusters where the items' CTAs are all resident at once, and a CTA has at most kClusterUnits units of its item; runs
+// otherwise.  Grid of runs: two CTAs an SM (one for D > 128), no more than there can be runs of kMinUnits units.
+constexpr int kClusterUnits = 16;
+
 static AttnPlan attn_plan(const tgc_paged_attention_args &a, int sms) {
     AttnPlan q{};
     const int64_t group = a.heads_q / a.heads_k;
     q.dp = a.D <= 64 ? 64 : a.D <= 128 ? 128 : 256;
-    q.mt = group > 16 && q.dp <= 128 ? 2 : 1;
-    q.row_blocks = (int)((group + 16 * q.mt - 1) / (16 * q.mt));
+    q.unit = q.dp == 64 ? AttnShape<64, 1>::kUnit : AttnShape<128, 1>::kUnit;
+    q.nt = group <= 8 ? 1 : group <= 16 || q.dp == 256 ? 2 : 4;
+    q.row_blocks = (int)((group + 8 * q.nt - 1) / (8 * q.nt));
     q.items = a.num_seqs * a.heads_k * q.row_blocks;
     int64_t most = a.max_pages * a.page_size;
     if (a.window > 0 && most > a.window) most = a.window;
-    const int64_t units = (most + kUnit - 1) / kUnit, room = (int64_t)sms * (q.dp <= 128 ? 2 : 1);
-    const int64_t runs = units > 0 ? (q.items * units + kMinUnits - 1) / kMinUnits : 1;
+    const int64_t units = (most + q.unit - 1) / q.unit, room = (int64_t)sms * (q.dp <= 128 ? 2 : 1);
+    int c = 1;
+    while (c < kMaxCluster && 2 * c * q.items <= room && c < units) c *= 2;
+    if (c * q.items <= room && (units + c - 1) / c <= kClusterUnits) {
+        q.cluster = c;
+        q.grid = (int)(c * q.items);
+        return q;
+    }
+    const int64_t runs = (q.items * units + kMinUnits - 1) / kMinUnits;
     q.grid = (int)(runs < 1 ? 1 : runs < room ? runs : room);
     q.join = q.grid > 1 && units > 1;  // items of one unit are never split
     auto up = [](size_t v) { return (v + 127) / 128 * 128; };
-    const size_t rows = (size_t)2 * q.grid * 16 * q.mt;
+    const size_t rows = (size_t)2 * q.grid * 8 * q.nt;
     q.ml_off = up(rows * (size_t)a.D * 4);
     q.shared_off = q.ml_off + up(rows * 8);
     q.total = q.shared_off + up((size_t)q.items * 8);
     return q;
 }
 
-template <bool F16, int DP, int MT>
-static int launch_attention(const AttnParams &p, const AttnPlan &q, cudaStream_t stream) {
-    using S = AttnShape<DP, MT>;
-    TGC_TRY((allow_smem<attention_kernel<F16, DP, MT>, S::kSmem>()));
-    cudaError_t e = launch_overlapped(attention_kernel<F16, DP, MT>, dim3((unsigned)q.grid), dim3(kAttnThreads),
-                                      (size_t)S::kSmem, 1, stream, p);
+template <bool F16, int DP, int NT, bool CLUSTER>
+static int launch_attention_form(const AttnParams &p, const AttnPlan &q, cudaStream_t stream) {
+    using S = AttnShape<DP, NT>;
+    TGC_TRY((allow_smem<attention_kernel<F16, DP, NT, CLUSTER>, S::kSmem>()));
+    cudaError_t e = launch_overlapped(attention_kernel<F16, DP, NT, CLUSTER>, dim3((unsigned)q.grid), dim3(kAttnThreads),
+                                      (size_t)S::kSmem, CLUSTER ? q.cluster : 1, stream, p);
     if (e == cudaSuccess && q.join)
         e = launch_overlapped(attention_join_kernel<F16>, dim3((unsigned)(p.kv.num_seqs * p.heads_q)), dim3(kJoinThreads), 0, 1,
                               stream, p, S::kRows);
     return e == cudaSuccess ? TGC_OK : cuda_fail(e);
+}
+
+template <bool F16, int DP, int NT>
+static int launch_attention(const AttnParams &p, const AttnPlan &q, cudaStream_t stream) {
+    return q.cluster > 0 ? launch_attention_form<F16, DP, NT, true>(p, q, stream)
+                         : launch_attention_form<F16, DP, NT, false>(p, q, stream);
 }
 
 static int attn_impl(tgc_paged_attention_args a) {
@@ -613,8 +774,10 @@ static int attn_impl(tgc_paged_attention_args a) {
     const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e);
     const AttnPlan q = attn_plan(a, sm_count(dev));
-    if (a.workspace == nullptr || a.workspace_bytes < q.total) return TGC_ERR_WORKSPACE;
-    if (reinterpret_cast<uintptr_t>(a.workspace) % 128 != 0) return TGC_ERR_ALIGN;
+    if (q.total > 0) {
+        if (a.workspace == nullptr || a.workspace_bytes < q.total) return TGC_ERR_WORKSPACE;
+        if (reinterpret_cast<uintptr_t>(a.workspace) % 128 != 0) return TGC_ERR_ALIGN;
+    }
     AttnParams p{};
     p.q = a.q; p.k = a.k_pages; p.v = a.v_pages; p.out = a.out; p.lse = a.lse; p.table = a.table; p.lens = a.lens;
     p.kv = KvTable{(int)a.num_pages, (int)a.page_size, (int)a.num_seqs, (int)a.max_pages, a.table_ld};
@@ -629,17 +792,25 @@ static int attn_impl(tgc_paged_attention_args a) {
         p.cap_inv = scale / a.softcap;
     }
     p.window = a.window > TGC_MAX_SIZE ? 0 : (int)a.window;
-    p.adv_pages = kUnit / (int)a.page_size;
-    p.adv_tokens = kUnit % (int)a.page_size;
+    p.cluster = q.cluster;
+    p.adv_pages = q.unit / (int)a.page_size;
+    p.adv_tokens = q.unit % (int)a.page_size;
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
     p.part_out = reinterpret_cast<float *>(ws);
     p.part_ml = reinterpret_cast<float2 *>(ws + q.ml_off);
     p.shared_by = reinterpret_cast<int2 *>(ws + q.shared_off);
     auto go = [&](auto f16) {
         constexpr bool F16 = decltype(f16)::value;
-        return q.dp == 64    ? (q.mt == 1 ? launch_attention<F16, 64, 1>(p, q, a.stream) : launch_attention<F16, 64, 2>(p, q, a.stream))
-               : q.dp == 128 ? (q.mt == 1 ? launch_attention<F16, 128, 1>(p, q, a.stream) : launch_attention<F16, 128, 2>(p, q, a.stream))
-                             : launch_attention<F16, 256, 1>(p, q, a.stream);
+        auto heads = [&](auto dp) {
+            constexpr int DP = decltype(dp)::value;
+            if (q.nt == 1) return launch_attention<F16, DP, 1>(p, q, a.stream);
+            if constexpr (DP < 256)
+                if (q.nt == 4) return launch_attention<F16, DP, 4>(p, q, a.stream);
+            return launch_attention<F16, DP, 2>(p, q, a.stream);
+        };
+        return q.dp == 64    ? heads(std::integral_constant<int, 64>{})
+               : q.dp == 128 ? heads(std::integral_constant<int, 128>{})
+                             : heads(std::integral_constant<int, 256>{});
     };
     return a.dtype == TGC_F16 ? go(std::true_type{}) : go(std::false_type{});
 }
