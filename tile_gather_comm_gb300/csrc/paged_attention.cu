@@ -24,8 +24,8 @@
 // Two ways to deal the work:
 //  - runs: the keys of every (sequence, key head) -- an item -- are cut into units; all units of all items
 //    lie end to end and every CTA takes an equal run of them, whatever the lengths are.  An item that ends up
-//    in several CTAs is joined by a second kernel from the parts (maximum, sum, unnormalised output) that
-//    they leave in the workspace; a CTA leaves two parts at most, so the workspace does not grow with the
+//    in several runs is joined by a second kernel from the parts (maximum, sum, unnormalised output) that
+//    they leave in the workspace; a run leaves two parts at most, so the workspace does not grow with the
 //    lengths.
 //  - clusters: an item is a cluster's, cut evenly over its CTAs, which join through distributed shared
 //    memory: one launch and no workspace, for calls with few and short items (attn_plan says which).
@@ -45,7 +45,7 @@ namespace tgc {
 
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = kAttnWarps * 32;
-constexpr int kMinUnits = 4;                  // units of a CTA's run at least
+constexpr int kMinUnits = 4;                  // units of a run at least (more than the copies run ahead)
 constexpr int kMaxCluster = 8;
 constexpr float kSlack = 8.0f;                // powers of two
 constexpr float kLn2 = 0.6931471805599453f;
@@ -64,10 +64,10 @@ struct AttnParams {
     int window;
     int cluster;  // CTAs of a cluster
     int adv_pages, adv_tokens;  // a unit on: pages and places
-    // workspace: parts (2 a CTA), and for each item the CTAs that share it
-    float *part_out;   // (2 grid, R, D)
-    float2 *part_ml;   // (2 grid, R): maximum (log2 units), sum
-    int2 *shared_by;   // (items): first and last CTA; (-1, -1): one alone, or no keys
+    // workspace: parts (2 a run), and for each item the runs that share it
+    float *part_out;   // (2 runs, R, D)
+    float2 *part_ml;   // (2 runs, R): maximum (log2 units), sum
+    int2 *shared_by;   // (items with keys): first and last run; (-1, -1): one alone
 };
 
 // The keys of sequence s in range: [begin, end).
@@ -110,6 +110,7 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ float exp2_approx(float v) {
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(v));
     return v;
@@ -156,6 +157,41 @@ struct RunAt {
     int begin, end;              // keys of the sequence in range
 };
 
+// Warp-collective: the sequence that holds unit `at`, looked for from r.seq (whose first unit is r.seq_begin) on, or from
+// the start where that is past it; then the item and unit.  False only where the lengths change under the call.
+template <int UNIT>
+__device__ __forceinline__ bool seek(const AttnParams &p, RunAt &r, int64_t at, int heads, int lane) {
+    if (at < r.seq_begin) r.seq = 0, r.seq_begin = 0;
+    for (; r.seq < p.kv.num_seqs; r.seq += 32) {
+        const int mine = r.seq + lane < p.kv.num_seqs ? units_of<UNIT>(key_range(p, r.seq + lane)) : 0;
+        int64_t upto = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += v;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, r.seq_begin + upto * heads > at);
+        if (past != 0) {
+            const int l = __ffs(past) - 1;
+            r.seq += l;
+            r.seq_begin += __shfl_sync(0xffffffffu, upto - mine, l) * heads;
+            break;
+        }
+        r.seq_begin += __shfl_sync(0xffffffffu, upto, 31) * heads;
+    }
+    if (r.seq >= p.kv.num_seqs) return false;
+    const KeyRange k = key_range(p, r.seq);
+    r.begin = k.begin;
+    r.end = k.end;
+    r.units = units_of<UNIT>(k);
+    r.at = at;
+    const int64_t in_seq = at - r.seq_begin;
+    if (r.units == 0 || in_seq / r.units >= heads) return false;
+    r.item = (int)(in_seq / r.units);
+    r.unit = (int)(in_seq - (int64_t)r.item * r.units);
+    return true;
+}
+
 // The pair at `local`'s place in CTA `rank` of this cluster.
 __device__ __forceinline__ float2 load_cluster(const void *local, int rank) {
     float2 v;
@@ -178,9 +214,8 @@ template <bool F16, int DP, int NT, bool CLUSTER>
 __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_kernel(const AttnParams p) {
     using S = AttnShape<DP, NT>;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t s_scan[kAttnWarps];
-    __shared__ int64_t s_before;
-    __shared__ int s_seq;
+    __shared__ int64_t s_sum[kAttnWarps];
+    __shared__ RunAt s_cur;  // where the products stand: one copy, so that all warps meet at the same items
     __shared__ uint32_t s_mask[kAttnWarps][S::kStages];
     __shared__ float2 s_ml[kAttnWarps][S::kRows];
     __shared__ float2 s_cta_ml[S::kRows];
@@ -199,10 +234,11 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
     stream_wait();
     stream_release();
 
-    // ---- this CTA's run of units
+    // ---- this CTA's run
     const int heads = p.heads_k * p.row_blocks;  // items of a sequence
-    int64_t stop = 0, per = 0;
-    RunAt r{};  // where the copies stand
+    int64_t stop = 0, per = 0;                   // end of the run; units of a run
+    int runs = 0;
+    RunAt r{};                                   // where the copies stand
     int rank = 0, ranks = 1;
     if constexpr (CLUSTER) {
         rank = (int)cluster_ctarank();
@@ -219,83 +255,65 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
         r.at = r.unit;
         stop = r.unit + each < r.units ? r.unit + each : r.units;
     } else {
-        const int share = (p.kv.num_seqs + kAttnThreads - 1) / kAttnThreads;
-        int64_t mine = 0;
-        for (int i = 0; i < share; ++i) {
-            const int s = tid * share + i;
-            if (s < p.kv.num_seqs) mine += units_of<S::kUnit>(key_range(p, s));
-        }
-        int64_t upto = mine;
+        int64_t mine = 0, total = 0;
+        for (int s = tid; s < p.kv.num_seqs; s += kAttnThreads) mine += units_of<S::kUnit>(key_range(p, s));
 #pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, upto, d);
-            if (lane >= d) upto += v;
-        }
-        if (lane == 31) s_scan[warp] = upto;
+        for (int d = 16; d > 0; d /= 2) mine += __shfl_xor_sync(0xffffffffu, mine, d);
+        if (lane == 0) s_sum[warp] = mine;
         __syncthreads();
-        int64_t base = 0, total = 0;
 #pragma unroll
-        for (int w = 0; w < kAttnWarps; ++w) {
-            if (w < warp) base += s_scan[w];
-            total += s_scan[w];
-        }
-        upto += base;
+        for (int w = 0; w < kAttnWarps; ++w) total += s_sum[w];
         total *= heads;
         per = (total + gridDim.x - 1) / gridDim.x;
         if (per < kMinUnits) per = kMinUnits;
-        r.at = per * blockIdx.x;
-        stop = r.at + per < total ? r.at + per : total;
-
-        // Sequences without keys: zeros.
-        for (int s = (int)blockIdx.x; s < p.kv.num_seqs; s += (int)gridDim.x) {
-            if (units_of<S::kUnit>(key_range(p, s)) != 0) continue;
-            for (int i = tid; i < p.heads_q * p.D; i += kAttnThreads)
-                static_cast<uint16_t *>(p.out)[s * p.o_s + i / p.D * p.o_h + i % p.D] = 0;
-            if (p.lse != nullptr)
-                for (int i = tid; i < p.heads_q; i += kAttnThreads) p.lse[(int64_t)s * p.heads_q + i] = -INFINITY;
-            for (int i = tid; i < heads; i += kAttnThreads) p.shared_by[(int64_t)s * heads + i] = make_int2(-1, -1);
-        }
-        if (r.at >= stop) return;
-
-        // The sequence in which the run starts: in the share of the thread whose units hold it.
-        if ((upto - mine) * heads <= r.at && r.at < upto * heads) {
-            int64_t before = upto - mine;
-            int s = tid * share;
-            for (;; ++s) {
-                const int n = units_of<S::kUnit>(key_range(p, s));
-                if (r.at < (before + n) * heads || s + 1 == p.kv.num_seqs) break;
-                before += n;
-            }
-            s_seq = s;
-            s_before = before * heads;
-        }
-        __syncthreads();
-        r.seq = s_seq;
-        r.seq_begin = s_before;
-        const KeyRange k = key_range(p, r.seq);
-        r.begin = k.begin;
-        r.end = k.end;
-        r.units = units_of<S::kUnit>(k);
-        const int64_t in_seq = r.at - r.seq_begin;
-        if (r.units == 0 || in_seq / r.units >= heads) return;  // only where the lengths change under the call
-        r.item = (int)(in_seq / r.units);
-        r.unit = (int)(in_seq - (int64_t)r.item * r.units);
+        // what is left over behind the last whole run is one too where it has kMinUnits, else a part of that
+        runs = (int)(total / per) + (total % per >= kMinUnits || (total > 0 && total < per) ? 1 : 0);
+        const int run = (int)blockIdx.x;
+        if (run >= runs) return;
+        stop = run + 1 < runs ? per * (run + 1) : total;
+        if (!seek<S::kUnit>(p, r, per * run, heads, lane)) r.at = stop;
     }
 
-    // ---- the warp's copies: a lane finds the page of a key of the step, all lanes copy
+    // ---- the warp's copies: a lane finds the page of a key of the step, all lanes copy.  Pages are looked up two units
+    // ahead: a miss takes longer than the copies of one.
     const int my_key = warp * S::kKeys + lane % S::kKeys;
-    int key = 0, page_i = 0, place = 0, page = -1;  // of the unit to be copied next
+    int key = 0, page_i = 0, place = 0;  // of the unit to be looked up next
+    int page[2], at_place[2];            // of the unit to be copied next and the one behind it
     int64_t head_off = 0;
-    auto find_page = [&] { page = key < r.end ? p.kv.page_at(p.table, r.seq, page_i) : -1; };
+    auto look_up = [&] {
+        page[0] = page[1];
+        at_place[0] = at_place[1];
+        page[1] = key < r.end ? p.kv.page_at(p.table, r.seq, page_i) : -1;
+        at_place[1] = place;
+        key += S::kUnit;
+        page_i += p.adv_pages;
+        place += p.adv_tokens;
+        if (place >= p.kv.page_size) {
+            place -= p.kv.page_size;
+            ++page_i;
+        }
+    };
     auto enter_item = [&] {
         key = r.begin + r.unit * S::kUnit + my_key;
         page_i = key / p.kv.page_size;
         place = key - page_i * p.kv.page_size;
-        head_off = (int64_t)(r.item / p.row_blocks) * p.head_s;
-        find_page();
+        const int head_k = r.item / p.row_blocks, row0 = r.item % p.row_blocks * S::kRows;
+        head_off = (int64_t)head_k * p.head_s;
+        look_up();
+        look_up();
+        // the item's queries on their way into L2
+        constexpr int kLines = DP / 64;
+        for (int i = lane; i < S::kRows * kLines; i += 32)
+            if (row0 + i / kLines < p.group && i % kLines * 64 < p.D)
+                prefetch_l2(static_cast<const uint16_t *>(p.q) + r.seq * p.q_s +
+                            (int64_t)(head_k * p.group + row0 + i / kLines) * p.q_h + i % kLines * 64);
     };
     if (r.at < stop) enter_item();
-    RunAt c = r;  // where the products stand
+    if (!CLUSTER) {
+        if (tid == 0) s_cur = r;
+        __syncthreads();
+    }
+    RunAt c = CLUSTER ? r : s_cur;
     int issued = 0;
     // The next sequence that has keys; none only where the lengths change under the call.
     auto next_seq = [&](RunAt &w) {
@@ -311,7 +329,7 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
     auto copy_unit = [&] {
         if (r.at < stop) {
             const int stage = issued % S::kStages;
-            const int64_t off = page < 0 ? -1 : page * p.page_s + place * p.token_s + head_off;
+            const int64_t off = page[0] < 0 ? -1 : page[0] * p.page_s + at_place[0] * p.token_s + head_off;
             const uint32_t have = __ballot_sync(0xffffffffu, off >= 0);
             if (lane == 0) s_mask[warp][stage] = have;
             const uint32_t to = ring_at + (uint32_t)(stage * 2 * S::kTile);
@@ -327,14 +345,7 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
             }
             ++r.at;
             if (++r.unit < r.units) {
-                key += S::kUnit;
-                page_i += p.adv_pages;
-                place += p.adv_tokens;
-                if (place >= p.kv.page_size) {
-                    place -= p.kv.page_size;
-                    ++page_i;
-                }
-                find_page();
+                look_up();
             } else if (!CLUSTER && r.at < stop) {
                 r.unit = 0;
                 if (++r.item == heads) {
@@ -358,12 +369,11 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
     for (int i = 0; i < S::kStages - 1; ++i) issue();
 
     int step = 0;
-    do {
+    while (CLUSTER || c.at < stop) {
         const int head_k = c.item / p.row_blocks, row0 = c.item % p.row_blocks * S::kRows;
         const int rows = p.group - row0 < S::kRows ? p.group - row0 : S::kRows;
         const int head0 = head_k * p.group + row0;
-        int todo = (int)(stop - c.at < c.units - c.unit ? stop - c.at : c.units - c.unit);
-        if (CLUSTER) todo = (int)(stop - c.at);
+        const int todo = (int)(stop - c.at < c.units - c.unit ? stop - c.at : c.units - c.unit);
 
         // queries as the first product's right operand: lane (g, t4) has elements 2 t4, 2 t4 + 1 of every 8 of head g
         uint32_t qf[NT][DP / 16][2];
@@ -515,11 +525,12 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
                 if (g == 0) s_ml[warp][n * 8 + t4 * 2 + e] = make_float2(top[n][e], l);
             }
         const int64_t item_begin = c.at - c.unit;
-        const bool whole = CLUSTER ? ranks == 1 : item_begin / per == (item_begin + c.units - 1) / per;
+        auto run_of = [&](int64_t unit) { return (int)(unit / per < runs ? unit / per : runs - 1); };
+        const int first = CLUSTER ? 0 : run_of(item_begin), last = CLUSTER ? ranks - 1 : run_of(item_begin + c.units - 1);
+        const bool whole = first == last;
         const int part = 2 * (int)blockIdx.x + (item_begin < per * blockIdx.x ? 0 : 1);
         if (!CLUSTER && tid == 0 && c.unit == 0)
-            p.shared_by[(int64_t)c.seq * heads + c.item] =
-                whole ? make_int2(-1, -1) : make_int2((int)(item_begin / per), (int)((item_begin + c.units - 1) / per));
+            p.shared_by[(int64_t)c.seq * heads + c.item] = whole ? make_int2(-1, -1) : make_int2(first, last);
 #pragma unroll
         for (int r0 = 0; r0 < S::kRows; r0 += S::kRound) {
             __syncwarp();
@@ -562,6 +573,16 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
                     if (d == 0) p.part_ml[part * S::kRows + r0 + row] = make_float2(m, l);
                 }
             }
+            if (!CLUSTER && tid == 0 && r0 + S::kRound == S::kRows) {
+                RunAt to = c;  // on to the next item
+                to.at += todo;
+                to.unit = 0;
+                if (to.at < stop && ++to.item == heads) {
+                    to.item = 0;
+                    if (!next_seq(to)) to.at = stop;
+                }
+                s_cur = to;
+            }
             __syncthreads();
         }
         if constexpr (CLUSTER) {
@@ -600,78 +621,90 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
             return;
         }
         clear_tail(last_stage);
-        // on to the next item
-        c.at += todo;
-        c.unit = 0;
-        if (c.at < stop && ++c.item == heads) {
-            c.item = 0;
-            if (!next_seq(c)) break;
-        }
-    } while (c.at < stop);
+        c = s_cur;
+    }
+    cp_async_wait<0>();
 }
 
-// One block a row (sequence, query head) joins the parts of an item that several CTAs share.
-constexpr int kJoinThreads = 128;
+// One block a row (sequence, query head) joins the parts of an item that several runs share: a warp takes every eighth
+// part, kJoinDeep at a time, with a maximum of its own; the warps meet in shared memory.
+constexpr int kJoinWarps = 8;
+constexpr int kJoinThreads = kJoinWarps * 32;
+constexpr int kJoinDeep = 4;
 
-template <bool F16>
+template <bool F16, int VEC>  // VEC: float2 a lane, 1, 2 or 4 for D up to 64, 128 or 256
 __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnParams p, const int part_rows) {
-    __shared__ float s_ml[2][kJoinThreads / 32];
-    __shared__ float2 s_out[kJoinThreads / 32][TGC_ATTENTION_MAX_D / 2];
+    __shared__ float2 s_ml[kJoinWarps];
+    __shared__ float2 s_out[kJoinWarps][VEC * 32];
     stream_wait();
     stream_release();
     const int head = (int)(blockIdx.x % (unsigned)p.heads_q), seq = (int)(blockIdx.x / (unsigned)p.heads_q);
     const int heads = p.heads_k * p.row_blocks, in_group = head % p.group;
     const int item = head / p.group * p.row_blocks + in_group / part_rows, row = in_group % part_rows;
-    const int2 by = p.shared_by[(int64_t)seq * heads + item];
-    if (by.x < 0) return;
-    // the first CTA's part is its second place unless the item began in an earlier one, so never here
-    const int n = by.y - by.x + 1, tid = (int)threadIdx.x, warp = tid / 32, lane = tid % 32;
-    auto part_at = [&](int i) { return (int64_t)(2 * (by.x + i) + (i == 0 ? 1 : 0)) * part_rows + row; };
-    float m = -INFINITY;
-    for (int i = tid; i < n; i += kJoinThreads) m = fmaxf(m, p.part_ml[part_at(i)].x);
-#pragma unroll
-    for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if (lane == 0) s_ml[0][warp] = m;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, s_ml[0][w]);
-    const float off = m == -INFINITY ? 0.0f : m;
-    // a warp takes every fourth part; a lane pairs of elements 32 apart
-    float l = 0.0f;
-    float2 o[TGC_ATTENTION_MAX_D / 64];
+    const int tid = (int)threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const volatile int *by_at = reinterpret_cast<const volatile int *>(p.shared_by + (int64_t)seq * heads + item);
+    const int first = by_at[0], last = by_at[1];  // both loads beside that of the length: they say nothing where it is 0
+    const KeyRange range = key_range(p, seq);
+    if (range.end == range.begin) {
+        for (int c = tid; c < p.D / 2; c += kJoinThreads) store_out<F16>(p, seq, head, 2 * c, 0.0f, 0.0f, make_float2(0.0f, 0.0f));
+        return;
+    }
+    if (first < 0) return;
+    float m = -INFINITY, l = 0.0f;
+    float2 o[VEC];
 #pragma unroll
     for (float2 &v : o) v = make_float2(0.0f, 0.0f);
-    for (int i = warp; i < n; i += kJoinThreads / 32) {
-        const float2 ml = p.part_ml[part_at(i)];
-        const float f = exp2_approx(ml.x - off);
-        const float *from = p.part_out + part_at(i) * p.D;
-        l += ml.y * f;
+    for (int i = first + warp; i <= last; i += kJoinWarps * kJoinDeep) {
+        float2 ml[kJoinDeep], v[kJoinDeep][VEC];
 #pragma unroll
-        for (int j = 0; j < TGC_ATTENTION_MAX_D / 64; ++j) {
-            const int c = (j * 32 + lane) * 2;
-            if (c < p.D) {
-                const float2 v = *reinterpret_cast<const float2 *>(from + c);
-                o[j].x += v.x * f;
-                o[j].y += v.y * f;
-            }
+        for (int u = 0; u < kJoinDeep; ++u) {
+            const int run = i + u * kJoinWarps;
+            ml[u] = make_float2(-INFINITY, 0.0f);
+            if (run > last) continue;
+            // the first run's part is in its second place, the others' in their first
+            const int64_t at = (int64_t)(2 * run + (run == first ? 1 : 0)) * part_rows + row;
+            ml[u] = p.part_ml[at];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j)
+                if ((j * 32 + lane) * 2 < p.D) v[u][j] = *reinterpret_cast<const float2 *>(p.part_out + at * p.D + (j * 32 + lane) * 2);
+        }
+        float now = m;
+#pragma unroll
+        for (int u = 0; u < kJoinDeep; ++u) now = fmaxf(now, ml[u].x);
+        const float off = now == -INFINITY ? 0.0f : now, f = exp2_approx(m - off);
+        m = now;
+        l *= f;
+#pragma unroll
+        for (float2 &w : o) w.x *= f, w.y *= f;
+#pragma unroll
+        for (int u = 0; u < kJoinDeep; ++u) {
+            if (i + u * kJoinWarps > last) continue;
+            const float g = exp2_approx(ml[u].x - off);
+            l += ml[u].y * g;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j)
+                if ((j * 32 + lane) * 2 < p.D) o[j].x += v[u][j].x * g, o[j].y += v[u][j].y * g;
         }
     }
-    if (lane == 0) s_ml[1][warp] = l;
+    if (lane == 0) s_ml[warp] = make_float2(m, l);
 #pragma unroll
-    for (int j = 0; j < TGC_ATTENTION_MAX_D / 64; ++j) s_out[warp][j * 32 + lane] = o[j];
+    for (int j = 0; j < VEC; ++j) s_out[warp][j * 32 + lane] = o[j];
     __syncthreads();
+    if (tid * 2 >= p.D) return;
+    m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, s_ml[w].x);
+    const float off = m == -INFINITY ? 0.0f : m;
+    float2 sum = make_float2(0.0f, 0.0f);
     l = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kJoinThreads / 32; ++w) l += s_ml[1][w];
-    for (int c = tid; c < p.D / 2; c += kJoinThreads) {
-        float2 v = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int w = 0; w < kJoinThreads / 32; ++w) {
-            v.x += s_out[w][c].x;
-            v.y += s_out[w][c].y;
-        }
-        store_out<F16>(p, seq, head, 2 * c, m, l, v);
+    for (int w = 0; w < kJoinWarps; ++w) {
+        const float f = exp2_approx(s_ml[w].x - off);
+        l += s_ml[w].y * f;
+        sum.x += s_out[w][tid].x * f;
+        sum.y += s_out[w][tid].y * f;
     }
+    store_out<F16>(p, seq, head, 2 * tid, m, l, sum);
 }
 
 // ---------------------------------------------------------------- host
@@ -699,14 +732,13 @@ static int attn_check(tgc_paged_attention_args &a) {
 struct AttnPlan {
     int dp, nt, row_blocks, unit, grid, cluster;  // cluster: 0 where the work is dealt in runs
     int64_t items;
-    bool join;
     size_t ml_off, shared_off, total;
 };
 
 // Heads of an item, in eights: as many as share a key, up to 32 (16 for D > 128, whose outputs take twice the
 // registers).
 // Clusters where the items' CTAs are all resident at once, and a CTA has at most kClusterUnits units of its item; runs
-// otherwise.  Grid of runs: two CTAs an SM (one for D > 128), no more than there can be runs of kMinUnits units.
+// otherwise.  Runs: one for each of two CTAs an SM (one for D > 128), no more than there can be of kMinUnits units.
 constexpr int kClusterUnits = 16;
 
 static AttnPlan attn_plan(const tgc_paged_attention_args &a, int sms) {
@@ -729,7 +761,6 @@ static AttnPlan attn_plan(const tgc_paged_attention_args &a, int sms) {
     }
     const int64_t runs = (q.items * units + kMinUnits - 1) / kMinUnits;
     q.grid = (int)(runs < 1 ? 1 : runs < room ? runs : room);
-    q.join = q.grid > 1 && units > 1;  // items of one unit are never split
     auto up = [](size_t v) { return (v + 127) / 128 * 128; };
     const size_t rows = (size_t)2 * q.grid * 8 * q.nt;
     q.ml_off = up(rows * (size_t)a.D * 4);
@@ -744,8 +775,8 @@ static int launch_attention_form(const AttnParams &p, const AttnPlan &q, cudaStr
     TGC_TRY((allow_smem<attention_kernel<F16, DP, NT, CLUSTER>, S::kSmem>()));
     cudaError_t e = launch_overlapped(attention_kernel<F16, DP, NT, CLUSTER>, dim3((unsigned)q.grid), dim3(kAttnThreads),
                                       (size_t)S::kSmem, CLUSTER ? q.cluster : 1, stream, p);
-    if (e == cudaSuccess && q.join)
-        e = launch_overlapped(attention_join_kernel<F16>, dim3((unsigned)(p.kv.num_seqs * p.heads_q)), dim3(kJoinThreads), 0, 1,
+    if (e == cudaSuccess && !CLUSTER)
+        e = launch_overlapped(attention_join_kernel<F16, DP / 64>, dim3((unsigned)(p.kv.num_seqs * p.heads_q)), dim3(kJoinThreads), 0, 1,
                               stream, p, S::kRows);
     return e == cudaSuccess ? TGC_OK : cuda_fail(e);
 }
