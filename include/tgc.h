@@ -787,8 +787,8 @@ typedef enum tgc_rope_layout { TGC_ROPE_HALF = 0, TGC_ROPE_INTERLEAVED = 1 } tgc
  * k, k_out   device (T, heads_k, D), or NULL with heads_k = 0; as q.
  * q_t, q_h, ...  elements from one token, one head to the next; 0 = dense (heads side by side).
  * pos        device int32 (T).  A token with a negative position is padding: its rows of q and k are
- *            not read and those of q_out and k_out not written.
- * freqs      device double (R/2), radians a position (tgc_rope_freqs makes them).
+ *            not used and those of q_out and k_out not written.
+ * freqs      device double (R/2), finite, radians a position (tgc_rope_freqs makes them).
  * R          even, 2 <= R <= D <= TGC_ROPE_MAX_D.
  * scale      factor on the rotated elements; 0 = 1.
  * dtype      TGC_BF16, TGC_F16 or TGC_F32.  Pointers need their element's alignment (16-byte aligned
@@ -846,7 +846,7 @@ int tgc_rope_freqs(double *freqs, double *scale, int64_t R, double base, tgc_rop
  *            between pages, tokens and heads of both (0 = dense), in either order of tokens and heads.
  * table      as above; pos int32 (T); seqs int32 (T) or NULL: token t is sequence t's (T <= num_seqs).
  * freqs, R, scale, layout  as tgc_rope; NULL with R = 0: nothing is rotated (q is copied).
- * A token with a negative position is padding (nothing of it is read or written).  One whose page is
+ * A token with a negative position is padding (nothing of it is used or written).  One whose page is
  * not in the table (past max_pages, a number outside the pool, a sequence that is none) has its
  * query rotated and its key and value dropped.  Tokens of one call have places of their own: where
  * two have the same, the page holds elements of either.

@@ -30,6 +30,7 @@
 //  - clusters: an item is a cluster's, cut evenly over its CTAs, which join through distributed shared
 //    memory: one launch and no workspace, for calls with few and short items (attn_plan says which).
 // Both read the lengths on the device.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -45,10 +46,14 @@ namespace tgc {
 
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = kAttnWarps * 32;
-constexpr int kMinUnits = 4;                  // units of a run at least (more than the copies run ahead)
 constexpr int kMaxCluster = 8;
 constexpr float kSlack = 8.0f;                // powers of two
 constexpr float kLn2 = 0.6931471805599453f;
+
+// The item that begins in a run and ends in a later one, `last`; -1: there is none.
+struct SplitItem {
+    int seq, item, last;
+};
 
 struct AttnParams {
     const void *q, *k, *v;
@@ -67,7 +72,7 @@ struct AttnParams {
     // workspace: parts (2 a run), and for each item the runs that share it
     float *part_out;   // (2 runs, R, D)
     float2 *part_ml;   // (2 runs, R): maximum (log2 units), sum
-    int2 *shared_by;   // (items with keys): first and last run; (-1, -1): one alone
+    SplitItem *split;  // (runs)
 };
 
 // The keys of sequence s in range: [begin, end).
@@ -77,6 +82,10 @@ struct KeyRange {
 __device__ __forceinline__ KeyRange key_range(const AttnParams &p, int s) {
     const int end = p.kv.tokens(p.lens[s]);
     return {p.window > 0 && end > p.window ? end - p.window : 0, end};
+}
+// a / b in 32 bits where both fit: 64-bit divisions take a few hundred cycles each, at every item's start and end.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 template <int UNIT>
 __device__ __forceinline__ int units_of(KeyRange r) { return (r.end - r.begin + UNIT - 1) / UNIT; }
@@ -139,7 +148,11 @@ struct AttnShape {
     static constexpr int kTile = kKeys * DP * 2;      // bytes of a step's keys (or values)
     static constexpr int kStages = 3;
     static constexpr int kWarpRing = kStages * 2 * kTile;
-    static constexpr int kSmem = kAttnWarps * kWarpRing;
+    static constexpr int kRings = kAttnWarps * kWarpRing;
+    // The queries of three items: one in work, two that the copies may have entered.  They come with the copies, as
+    // loads of their own would queue behind those at every item's start (0: no room beside the rings, loads).
+    static constexpr int kQueries = DP == 128 && NT == 4 ? 0 : kRows * DP * 2;
+    static constexpr int kSmem = kRings + 3 * kQueries;
     // Outputs of so many heads fit a stage; more take turns.
     static constexpr int kRound = kRows * DP * 4 <= 2 * kTile ? kRows : 2 * kTile / (DP * 4);
     // Where a CTA of a cluster that took `steps` steps leaves its part of the heads from r0 on: not in the stage where its
@@ -186,8 +199,10 @@ __device__ __forceinline__ bool seek(const AttnParams &p, RunAt &r, int64_t at, 
     r.units = units_of<UNIT>(k);
     r.at = at;
     const int64_t in_seq = at - r.seq_begin;
-    if (r.units == 0 || in_seq / r.units >= heads) return false;
-    r.item = (int)(in_seq / r.units);
+    if (r.units == 0) return false;
+    const int64_t item = quotient(in_seq, r.units);
+    if (item >= heads) return false;
+    r.item = (int)item;
     r.unit = (int)(in_seq - (int64_t)r.item * r.units);
     return true;
 }
@@ -200,14 +215,21 @@ __device__ __forceinline__ float2 load_cluster(const void *local, int rank) {
     return v;
 }
 
+__device__ __forceinline__ void store_lse(const AttnParams &p, int seq, int head, float m, float l) {
+    if (p.lse != nullptr) p.lse[(int64_t)seq * p.heads_q + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+template <bool F16>
+__device__ __forceinline__ void store_four(const AttnParams &p, int seq, int head, int c, F2 a, F2 b) {
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + seq * p.o_s + head * p.o_h + c) =
+        make_uint2(pack16(a, F16), pack16(b, F16));
+}
 // Normalises a row's two neighbouring outputs and stores them.
 template <bool F16>
 __device__ __forceinline__ void store_out(const AttnParams &p, int seq, int head, int c, float m, float l, float2 o) {
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + seq * p.o_s + head * p.o_h + c) =
         pack16(f2(o.x * inv, o.y * inv), F16);
-    if (c == 0 && p.lse != nullptr)
-        p.lse[(int64_t)seq * p.heads_q + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+    if (c == 0) store_lse(p, seq, head, m, l);
 }
 
 template <bool F16, int DP, int NT, bool CLUSTER>
@@ -237,7 +259,6 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
     // ---- this CTA's run
     const int heads = p.heads_k * p.row_blocks;  // items of a sequence
     int64_t stop = 0, per = 0;                   // end of the run; units of a run
-    int runs = 0;
     RunAt r{};                                   // where the copies stand
     int rank = 0, ranks = 1;
     if constexpr (CLUSTER) {
@@ -264,49 +285,65 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
 #pragma unroll
         for (int w = 0; w < kAttnWarps; ++w) total += s_sum[w];
         total *= heads;
-        per = (total + gridDim.x - 1) / gridDim.x;
-        if (per < kMinUnits) per = kMinUnits;
-        // what is left over behind the last whole run is one too where it has kMinUnits, else a part of that
-        runs = (int)(total / per) + (total % per >= kMinUnits || (total > 0 && total < per) ? 1 : 0);
+        per = quotient(total + gridDim.x - 1, gridDim.x);
+        // Sequences without keys: zeros.
+        for (int s = (int)blockIdx.x; s < p.kv.num_seqs; s += (int)gridDim.x) {
+            if (units_of<S::kUnit>(key_range(p, s)) != 0) continue;
+            for (int i = tid; i < p.heads_q * (p.D / 2); i += kAttnThreads)
+                store_out<F16>(p, s, i / (p.D / 2), i % (p.D / 2) * 2, 0.0f, 0.0f, make_float2(0.0f, 0.0f));
+        }
+        if (tid == 0) p.split[blockIdx.x].last = -1;
         const int run = (int)blockIdx.x;
-        if (run >= runs) return;
-        stop = run + 1 < runs ? per * (run + 1) : total;
+        if (per * run >= total) return;
+        stop = per * (run + 1) < total ? per * (run + 1) : total;
         if (!seek<S::kUnit>(p, r, per * run, heads, lane)) r.at = stop;
     }
 
-    // ---- the warp's copies: a lane finds the page of a key of the step, all lanes copy.  Pages are looked up two units
-    // ahead: a miss takes longer than the copies of one.
+    // ---- the warp's copies: a lane finds the page of a key of the step, all lanes copy.  Pages are looked up kAhead units
+    // before their copies: a load queues behind the copies under way, about two units' worth.
+    constexpr int kAhead = 3;
     const int my_key = warp * S::kKeys + lane % S::kKeys;
-    int key = 0, page_i = 0, place = 0;  // of the unit to be looked up next
-    int page[2], at_place[2];            // of the unit to be copied next and the one behind it
+    int key = 0, page_i = 0, look = 0;   // of the unit to be looked up next, with its place in the page
+    int page[kAhead], place = 0;         // of the units to be copied next; of the first of them
     int64_t head_off = 0;
-    auto look_up = [&] {
-        page[0] = page[1];
-        at_place[0] = at_place[1];
-        page[1] = key < r.end ? p.kv.page_at(p.table, r.seq, page_i) : -1;
-        at_place[1] = place;
-        key += S::kUnit;
-        page_i += p.adv_pages;
-        place += p.adv_tokens;
-        if (place >= p.kv.page_size) {
-            place -= p.kv.page_size;
-            ++page_i;
-        }
+    auto past = [&](int &at) {
+        at += p.adv_tokens;
+        const bool over = at >= p.kv.page_size;
+        if (over) at -= p.kv.page_size;
+        return over;
     };
+    auto look_up = [&] {
+#pragma unroll
+        for (int i = 1; i < kAhead; ++i) page[i - 1] = page[i];
+        page[kAhead - 1] = key < r.end ? p.kv.page_at(p.table, r.seq, page_i) : -1;
+        key += S::kUnit;
+        page_i += p.adv_pages + (past(look) ? 1 : 0);
+    };
+    int items = 0;       // that the copies have entered
+    bool fresh = false;  // nothing of the item is copied yet
     auto enter_item = [&] {
         key = r.begin + r.unit * S::kUnit + my_key;
         page_i = key / p.kv.page_size;
-        place = key - page_i * p.kv.page_size;
+        look = place = key - page_i * p.kv.page_size;
+        head_off = (int64_t)(r.item / p.row_blocks) * p.head_s;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) look_up();
+        fresh = true;
+    };
+    // The item's queries, a share a warp, with the copies of its first unit: two units ahead of the products, so in the
+    // place of an item that all warps are done with.
+    auto copy_queries = [&] {
         const int head_k = r.item / p.row_blocks, row0 = r.item % p.row_blocks * S::kRows;
-        head_off = (int64_t)head_k * p.head_s;
-        look_up();
-        look_up();
-        // the item's queries on their way into L2
-        constexpr int kLines = DP / 64;
-        for (int i = lane; i < S::kRows * kLines; i += 32)
-            if (row0 + i / kLines < p.group && i % kLines * 64 < p.D)
-                prefetch_l2(static_cast<const uint16_t *>(p.q) + r.seq * p.q_s +
-                            (int64_t)(head_k * p.group + row0 + i / kLines) * p.q_h + i % kLines * 64);
+        const uint32_t to = smem_addr(smem + S::kRings) + (uint32_t)(items % 3 * S::kQueries);
+        for (int i = tid; i < S::kRows * (DP / 8); i += kAttnThreads) {
+            const int row = i / (DP / 8), ch = i % (DP / 8);
+            const bool there = row0 + row < p.group && ch < chunks;
+            cp_async16(to + chunk_at<DP>(row, ch),
+                       static_cast<const uint16_t *>(p.q) + (there ? r.seq * p.q_s + (int64_t)(head_k * p.group + row0 + row) * p.q_h + ch * 8 : 0),
+                       there);
+        }
+        ++items;
+        fresh = false;
     };
     if (r.at < stop) enter_item();
     if (!CLUSTER) {
@@ -328,8 +365,9 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
     };
     auto copy_unit = [&] {
         if (r.at < stop) {
+            if (S::kQueries > 0 && fresh) copy_queries();
             const int stage = issued % S::kStages;
-            const int64_t off = page[0] < 0 ? -1 : page[0] * p.page_s + at_place[0] * p.token_s + head_off;
+            const int64_t off = page[0] < 0 ? -1 : page[0] * p.page_s + place * p.token_s + head_off;
             const uint32_t have = __ballot_sync(0xffffffffu, off >= 0);
             if (lane == 0) s_mask[warp][stage] = have;
             const uint32_t to = ring_at + (uint32_t)(stage * 2 * S::kTile);
@@ -346,6 +384,7 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
             ++r.at;
             if (++r.unit < r.units) {
                 look_up();
+                past(place);
             } else if (!CLUSTER && r.at < stop) {
                 r.unit = 0;
                 if (++r.item == heads) {
@@ -368,7 +407,7 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
 #pragma unroll
     for (int i = 0; i < S::kStages - 1; ++i) issue();
 
-    int step = 0;
+    int step = 0, done = 0;  // steps, items
     while (CLUSTER || c.at < stop) {
         const int head_k = c.item / p.row_blocks, row0 = c.item % p.row_blocks * S::kRows;
         const int rows = p.group - row0 < S::kRows ? p.group - row0 : S::kRows;
@@ -377,13 +416,32 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
 
         // queries as the first product's right operand: lane (g, t4) has elements 2 t4, 2 t4 + 1 of every 8 of head g
         uint32_t qf[NT][DP / 16][2];
+        if constexpr (S::kQueries > 0) {
+            if (CLUSTER && todo <= 0) cp_async_wait<0>();
+            else cp_async_wait<S::kStages - 2>();
+            __syncthreads();
+            const uint32_t q_at = smem_addr(smem + S::kRings) + (uint32_t)(done % 3 * S::kQueries);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const uint16_t *from = static_cast<const uint16_t *>(p.q) + c.seq * p.q_s + (int64_t)(head0 + n * 8 + g) * p.q_h + t4 * 2;
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < DP / 8; ++i)
-                qf[n][i / 2][i % 2] = n * 8 + g < rows && i < chunks ? *reinterpret_cast<const uint32_t *>(from + i * 8) : 0u;
+                for (int i = 0; i < DP / 32; ++i) {
+                    uint32_t a[4];
+                    ldmatrix4(a, q_at + chunk_at<DP>(n * 8 + (lane & 7), i * 4 + (lane >> 3)));
+                    qf[n][2 * i][0] = a[0];
+                    qf[n][2 * i][1] = a[1];
+                    qf[n][2 * i + 1][0] = a[2];
+                    qf[n][2 * i + 1][1] = a[3];
+                }
+        } else {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const uint16_t *from = static_cast<const uint16_t *>(p.q) + c.seq * p.q_s + (int64_t)(head0 + n * 8 + g) * p.q_h + t4 * 2;
+#pragma unroll
+                for (int i = 0; i < DP / 8; ++i)
+                    qf[n][i / 2][i % 2] = n * 8 + g < rows && i < chunks ? *reinterpret_cast<const uint32_t *>(from + i * 8) : 0u;
+            }
         }
+        ++done;
         float acc[DP / 16][NT][4];  // elements g and g + 8 of every 16, heads 2 t4 and 2 t4 + 1 of every 8
         float top[NT][2], sum[NT][2];
 #pragma unroll
@@ -525,12 +583,10 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
                 if (g == 0) s_ml[warp][n * 8 + t4 * 2 + e] = make_float2(top[n][e], l);
             }
         const int64_t item_begin = c.at - c.unit;
-        auto run_of = [&](int64_t unit) { return (int)(unit / per < runs ? unit / per : runs - 1); };
-        const int first = CLUSTER ? 0 : run_of(item_begin), last = CLUSTER ? ranks - 1 : run_of(item_begin + c.units - 1);
-        const bool whole = first == last;
-        const int part = 2 * (int)blockIdx.x + (item_begin < per * blockIdx.x ? 0 : 1);
-        if (!CLUSTER && tid == 0 && c.unit == 0)
-            p.shared_by[(int64_t)c.seq * heads + c.item] = whole ? make_int2(-1, -1) : make_int2(first, last);
+        const bool whole = CLUSTER ? ranks == 1 : c.unit == 0 && todo == c.units;
+        const int part = 2 * (int)blockIdx.x + (c.unit > 0 ? 0 : 1);
+        if (!CLUSTER && tid == 0 && c.unit == 0 && !whole)  // the item begins here and goes on in later runs
+            p.split[blockIdx.x] = SplitItem{c.seq, c.item, min((int)quotient(item_begin + c.units - 1, per), (int)gridDim.x - 1)};
 #pragma unroll
         for (int r0 = 0; r0 < S::kRows; r0 += S::kRound) {
             __syncwarp();
@@ -542,35 +598,44 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
                     for (int e = 0; e < 4; ++e)
                         part_of(warp)[place_of(n * 8 - r0 + t4 * 2 + (e & 1), j * 16 + g + (e >> 1) * 8)] = acc[j][n][e];
             __syncthreads();
-            const int here = rows - r0 < S::kRound ? rows - r0 : S::kRound;
-            for (int i = tid; i < here * (p.D / 2); i += kAttnThreads) {
-                const int row = i / (p.D / 2), d = i % (p.D / 2) * 2;
-                float2 ml[kAttnWarps];
-                float m = -INFINITY;
+            // a thread takes every kSpan-th four elements of a row: the warps' factors are computed once
+            constexpr int kSpan = kAttnThreads / S::kRound;
+            const int row = tid / kSpan;
+            if (r0 + row < rows) {
+                float f[kAttnWarps], m = -INFINITY, l = 0.0f;
 #pragma unroll
-                for (int w = 0; w < kAttnWarps; ++w) {
-                    ml[w] = s_ml[w][r0 + row];
-                    m = fmaxf(m, ml[w].x);
-                }
+                for (int w = 0; w < kAttnWarps; ++w) m = fmaxf(m, s_ml[w][r0 + row].x);
                 const float off = m == -INFINITY ? 0.0f : m;
-                float l = 0.0f;
-                float2 o = make_float2(0.0f, 0.0f);
 #pragma unroll
                 for (int w = 0; w < kAttnWarps; ++w) {
-                    const float f = exp2_approx(ml[w].x - off);
-                    const float2 v = *reinterpret_cast<const float2 *>(part_of(w) + place_of(row, d));
-                    l += ml[w].y * f;
-                    o.x += v.x * f;
-                    o.y += v.y * f;
+                    const float2 ml = s_ml[w][r0 + row];
+                    f[w] = exp2_approx(ml.x - off);
+                    l += ml.y * f[w];
                 }
-                if (whole) {
-                    store_out<F16>(p, c.seq, head0 + r0 + row, d, m, l, o);
-                } else if (CLUSTER) {
-                    *reinterpret_cast<float2 *>(smem + S::cta_part(step, r0) + (row * DP + d) * 4) = o;
-                    if (d == 0) s_cta_ml[r0 + row] = make_float2(m, l);
-                } else {
-                    *reinterpret_cast<float2 *>(p.part_out + ((int64_t)part * S::kRows + r0 + row) * p.D + d) = o;
-                    if (d == 0) p.part_ml[part * S::kRows + r0 + row] = make_float2(m, l);
+                const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+                if (tid % kSpan == 0) {
+                    if (whole) store_lse(p, c.seq, head0 + r0 + row, m, l);
+                    else if (CLUSTER) s_cta_ml[r0 + row] = make_float2(m, l);
+                    else p.part_ml[part * S::kRows + r0 + row] = make_float2(m, l);
+                }
+#pragma unroll
+                for (int d = tid % kSpan * 4; d < DP; d += kSpan * 4) {
+                    if (d >= p.D) break;
+                    F2 o[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
+#pragma unroll
+                    for (int w = 0; w < kAttnWarps; ++w) {
+                        const float4 v = *reinterpret_cast<const float4 *>(part_of(w) + place_of(row, d));
+                        o[0] = fma(f2(v.x, v.y), every<F2>(f[w]), o[0]);
+                        o[1] = fma(f2(v.z, v.w), every<F2>(f[w]), o[1]);
+                    }
+                    if (whole) {
+                        store_four<F16>(p, c.seq, head0 + r0 + row, d, mul(o[0], every<F2>(inv)), mul(o[1], every<F2>(inv)));
+                    } else {
+                        const float2 a = split(o[0]), b = split(o[1]);
+                        float *to = CLUSTER ? reinterpret_cast<float *>(smem + S::cta_part(step, r0)) + row * DP + d
+                                            : p.part_out + ((int64_t)part * S::kRows + r0 + row) * p.D + d;
+                        *reinterpret_cast<float4 *>(to) = make_float4(a.x, a.y, b.x, b.y);
+                    }
                 }
             }
             if (!CLUSTER && tid == 0 && r0 + S::kRound == S::kRows) {
@@ -626,35 +691,33 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
     cp_async_wait<0>();
 }
 
-// One block a row (sequence, query head) joins the parts of an item that several runs share: a warp takes every eighth
-// part, kJoinDeep at a time, with a maximum of its own; the warps meet in shared memory.
-constexpr int kJoinWarps = 8;
-constexpr int kJoinThreads = kJoinWarps * 32;
+// Joins the items that several runs share: a block for each run that such an item begins in (at most one does) and
+// kJoinRows of its heads.  kJoinWarps warps a head take parts in turn, kJoinDeep at a time, with a maximum of their own,
+// and meet in shared memory.
+constexpr int kJoinRows = 2;
+constexpr int kJoinWarps = 4;
+constexpr int kJoinThreads = kJoinRows * kJoinWarps * 32;
 constexpr int kJoinDeep = 4;
 
 template <bool F16, int VEC>  // VEC: float2 a lane, 1, 2 or 4 for D up to 64, 128 or 256
 __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnParams p, const int part_rows) {
-    __shared__ float2 s_ml[kJoinWarps];
-    __shared__ float2 s_out[kJoinWarps][VEC * 32];
+    __shared__ float2 s_ml[kJoinRows][kJoinWarps];
+    __shared__ float2 s_out[kJoinRows][kJoinWarps][VEC * 32];
     stream_wait();
     stream_release();
-    const int head = (int)(blockIdx.x % (unsigned)p.heads_q), seq = (int)(blockIdx.x / (unsigned)p.heads_q);
-    const int heads = p.heads_k * p.row_blocks, in_group = head % p.group;
-    const int item = head / p.group * p.row_blocks + in_group / part_rows, row = in_group % part_rows;
-    const int tid = (int)threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const volatile int *by_at = reinterpret_cast<const volatile int *>(p.shared_by + (int64_t)seq * heads + item);
-    const int first = by_at[0], last = by_at[1];  // both loads beside that of the length: they say nothing where it is 0
-    const KeyRange range = key_range(p, seq);
-    if (range.end == range.begin) {
-        for (int c = tid; c < p.D / 2; c += kJoinThreads) store_out<F16>(p, seq, head, 2 * c, 0.0f, 0.0f, make_float2(0.0f, 0.0f));
-        return;
-    }
-    if (first < 0) return;
+    const SplitItem it = p.split[blockIdx.x];
+    if (it.last < 0) return;
+    const int first = (int)blockIdx.x, last = it.last;
+    const int mine = (int)threadIdx.x / (kJoinWarps * 32), tid = (int)threadIdx.x % (kJoinWarps * 32);
+    const int warp = tid / 32, lane = tid % 32;
+    const int row0 = it.item % p.row_blocks * part_rows, row = (int)blockIdx.y * kJoinRows + mine;
+    const bool live = row < part_rows && row0 + row < p.group;
+    const int seq = it.seq, head = it.item / p.row_blocks * p.group + row0 + row;
     float m = -INFINITY, l = 0.0f;
     float2 o[VEC];
 #pragma unroll
     for (float2 &v : o) v = make_float2(0.0f, 0.0f);
-    for (int i = first + warp; i <= last; i += kJoinWarps * kJoinDeep) {
+    for (int i = first + warp; i <= last && live; i += kJoinWarps * kJoinDeep) {
         float2 ml[kJoinDeep], v[kJoinDeep][VEC];
 #pragma unroll
         for (int u = 0; u < kJoinDeep; ++u) {
@@ -686,23 +749,23 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
                 if ((j * 32 + lane) * 2 < p.D) o[j].x += v[u][j].x * g, o[j].y += v[u][j].y * g;
         }
     }
-    if (lane == 0) s_ml[warp] = make_float2(m, l);
+    if (lane == 0) s_ml[mine][warp] = make_float2(m, l);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) s_out[warp][j * 32 + lane] = o[j];
+    for (int j = 0; j < VEC; ++j) s_out[mine][warp][j * 32 + lane] = o[j];
     __syncthreads();
-    if (tid * 2 >= p.D) return;
+    if (!live || tid * 2 >= p.D) return;
     m = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, s_ml[w].x);
+    for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, s_ml[mine][w].x);
     const float off = m == -INFINITY ? 0.0f : m;
     float2 sum = make_float2(0.0f, 0.0f);
     l = 0.0f;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) {
-        const float f = exp2_approx(s_ml[w].x - off);
-        l += s_ml[w].y * f;
-        sum.x += s_out[w][tid].x * f;
-        sum.y += s_out[w][tid].y * f;
+        const float f = exp2_approx(s_ml[mine][w].x - off);
+        l += s_ml[mine][w].y * f;
+        sum.x += s_out[mine][w][tid].x * f;
+        sum.y += s_out[mine][w][tid].y * f;
     }
     store_out<F16>(p, seq, head, 2 * tid, m, l, sum);
 }
@@ -732,13 +795,13 @@ static int attn_check(tgc_paged_attention_args &a) {
 struct AttnPlan {
     int dp, nt, row_blocks, unit, grid, cluster;  // cluster: 0 where the work is dealt in runs
     int64_t items;
-    size_t ml_off, shared_off, total;
+    size_t ml_off, split_off, total;
 };
 
 // Heads of an item, in eights: as many as share a key, up to 32 (16 for D > 128, whose outputs take twice the
 // registers).
 // Clusters where the items' CTAs are all resident at once, and a CTA has at most kClusterUnits units of its item; runs
-// otherwise.  Runs: one for each of two CTAs an SM (one for D > 128), no more than there can be of kMinUnits units.
+// otherwise.  Runs: one for each of two CTAs an SM (one for D > 128), no more than there can be units.
 constexpr int kClusterUnits = 16;
 
 static AttnPlan attn_plan(const tgc_paged_attention_args &a, int sms) {
@@ -759,13 +822,13 @@ static AttnPlan attn_plan(const tgc_paged_attention_args &a, int sms) {
         q.grid = (int)(c * q.items);
         return q;
     }
-    const int64_t runs = (q.items * units + kMinUnits - 1) / kMinUnits;
+    const int64_t runs = q.items * units;
     q.grid = (int)(runs < 1 ? 1 : runs < room ? runs : room);
     auto up = [](size_t v) { return (v + 127) / 128 * 128; };
     const size_t rows = (size_t)2 * q.grid * 8 * q.nt;
     q.ml_off = up(rows * (size_t)a.D * 4);
-    q.shared_off = q.ml_off + up(rows * 8);
-    q.total = q.shared_off + up((size_t)q.items * 8);
+    q.split_off = q.ml_off + up(rows * 8);
+    q.total = q.split_off + up((size_t)q.grid * sizeof(SplitItem));
     return q;
 }
 
@@ -776,8 +839,9 @@ static int launch_attention_form(const AttnParams &p, const AttnPlan &q, cudaStr
     cudaError_t e = launch_overlapped(attention_kernel<F16, DP, NT, CLUSTER>, dim3((unsigned)q.grid), dim3(kAttnThreads),
                                       (size_t)S::kSmem, CLUSTER ? q.cluster : 1, stream, p);
     if (e == cudaSuccess && !CLUSTER)
-        e = launch_overlapped(attention_join_kernel<F16, DP / 64>, dim3((unsigned)(p.kv.num_seqs * p.heads_q)), dim3(kJoinThreads), 0, 1,
-                              stream, p, S::kRows);
+        e = launch_overlapped(attention_join_kernel<F16, DP / 64>,
+                              dim3((unsigned)q.grid, (unsigned)((std::min(p.group, S::kRows) + kJoinRows - 1) / kJoinRows)),
+                              dim3(kJoinThreads), 0, 1, stream, p, S::kRows);
     return e == cudaSuccess ? TGC_OK : cuda_fail(e);
 }
 
@@ -829,7 +893,7 @@ static int attn_impl(tgc_paged_attention_args a) {
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
     p.part_out = reinterpret_cast<float *>(ws);
     p.part_ml = reinterpret_cast<float2 *>(ws + q.ml_off);
-    p.shared_by = reinterpret_cast<int2 *>(ws + q.shared_off);
+    p.split = reinterpret_cast<SplitItem *>(ws + q.split_off);
     auto go = [&](auto f16) {
         constexpr bool F16 = decltype(f16)::value;
         auto heads = [&](auto dp) {

@@ -4,6 +4,7 @@
 //   (a, b) -> s (a cos w - b sin w), s (b cos w + a sin w),  w = pos freq     (backward: -w)
 //
 // A pair is read, turned and written by one thread, so a call may write over its own input.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -16,6 +17,13 @@
 #include "prims.cuh"
 
 namespace tgc {
+
+// i / d for i * d < 2^32: one multiplication by ceil(2^32 / d), whose excess adds less than 1 / d to the quotient.
+struct Divisor {
+    uint32_t d, m;
+    __device__ __forceinline__ int of(int i) const { return d == 1 ? i : (int)__umulhi((uint32_t)i, m); }
+};
+static Divisor divisor(int d) { return Divisor{(uint32_t)d, (uint32_t)(((uint64_t(1) << 32) + d - 1) / d)}; }
 
 struct RopeParams {
     // 0 queries, 1 keys, 2 values (never turned; only with a cache)
@@ -31,61 +39,118 @@ struct RopeParams {
     KvTable kv;
     const int32_t *table, *seqs;
     int64_t page_s, token_s;
-    int tokens, rows;  // of a block
+    int tokens, rows;                 // of a block
+    Divisor half, units, block_rows;  // pairs of a token, units of a row, rows of a block
 };
 
+// V elements as they lie in memory, read and written as two values at a time: kept as 16-bit elements they would take a
+// register each and be put together again for every store.
 template <typename T, int V>
 struct alignas(sizeof(T) * V) Vec {
-    T v[V];
+    uint32_t w[V * sizeof(T) / 4];
+    __device__ __forceinline__ F2 get(int i) const {
+        if constexpr (sizeof(T) == 4) return f2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        else return unpack16(w[i], std::is_same<T, __half>::value);
+    }
+    __device__ __forceinline__ void put(int i, F2 v) {
+        if constexpr (sizeof(T) == 4) {
+            const float2 f = split(v);
+            w[2 * i] = __float_as_uint(f.x);
+            w[2 * i + 1] = __float_as_uint(f.y);
+        } else {
+            w[i] = pack16(v, std::is_same<T, __half>::value);
+        }
+    }
+    // one of the first two elements
+    __device__ __forceinline__ void set(int i, T t) { reinterpret_cast<T *>(w)[i] = t; }
+    __device__ __forceinline__ T at(int i) const { return reinterpret_cast<const T *>(w)[i]; }
+};
+template <typename T>
+struct Vec<T, 1> {
+    T v;
+    __device__ __forceinline__ void set(int, T t) { v = t; }
+    __device__ __forceinline__ T at(int) const { return v; }
 };
 
-// One block: `tokens` tokens, `rows` of their heads.  First the sines and cosines of its tokens (one
-// for each token and pair, which the heads share), then the heads, a thread taking V pairs (half
-// layout: a vector of V from each half; interleaved: one vector of V / 2 pairs) or a vector of V
-// elements to copy at a time.
-//
-// The angle: pos * freq in fp64 (24 bits of position, 53 of frequency), taken modulo a turn by one
-// subtraction, its sine and cosine in fp32.  A thread's share of fp64 is four instructions for a pair
-// of a token; with 40 heads they are read 40 times from shared memory.
-constexpr int kRopeThreads = 256;
-constexpr int kRopeTokens = 4;  // of a block at most
+// A pair side by side, turned.
+__device__ __forceinline__ F2 turned(F2 v, float c, float s) {
+    const float2 f = split(v);
+    return fma(f2(f.y, f.x), f2(-s, s), mul(v, every<F2>(c)));
+}
 
-template <typename T, int V, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
-    extern __shared__ float2 s_turn[];  // tokens x R/2: scale (cos, sin)
+// One block: `tokens` tokens, `rows` of their heads.  First the sines and cosines of its tokens (one for each token
+// and pair, which the heads share), then the heads, a thread taking units of V pairs (half layout: a vector of V from
+// each half; interleaved: one vector of V / 2 pairs) or a vector of V elements to copy.
+//
+// The angle: freq / 2 pi, taken modulo 1, is held as a 64-bit fraction of a turn, and its product with the position
+// modulo 2^64 is the angle's: whole turns fall off the top.  What 31 bits of position make of the last bit of
+// freq is far below fp32's, in which sine and cosine are then taken.  fp64 is needed once a pair and
+// block.
+//
+// Bound by HBM where there are many tokens, by the launch where there are few.
+constexpr int kRopeThreads = 256;
+constexpr int kRopeTokens = 4;   // of a block at most
+constexpr int kRopeRows = 1024;  // rows of a block at most: with 1024 units a row, i * d stays below 2^32 (Divisor)
+
+// How a unit's elements lie: two vectors R/2 apart, of V pairs (half layout) or of V / 2 pairs each (interleaved); the
+// same with an odd R/2, where the second vector is not aligned and goes element by element (and the last unit
+// has one pair); one vector of V / 2 pairs; one pair of single elements.
+enum RopeForm { kHalf, kHalfOdd, kHalfOne, kNear, kNearSingle, kNearOne };
+
+// Units of a row that turn; those behind them copy V elements each.
+__host__ __device__ inline int rope_turning(RopeForm form, int v, int R) {
+    return form == kHalfOdd ? (R / 2 + 1) / 2 : form == kNearSingle ? R / v : R / 2 / v;
+}
+
+// Registers: 32 a thread, so that an SM holds 64 warps: with units taken several at a time in more registers fewer loads
+// were under way in all (8192 tokens of 40 heads of 128 bf16: 29.7 us; 2 units 33 to 37, 4 units 33 to 73).
+template <typename T, int V, RopeForm FORM>
+__global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const RopeParams p) {
+    constexpr bool INTERLEAVED = FORM == kNear || FORM == kNearSingle || FORM == kNearOne;
+    constexpr bool PAIR = FORM != kNearSingle;  // a unit that turns is two vectors
+    constexpr int kTwos = V > 1 ? V / 2 : 1;
+    using W = Vec<T, V>;
+    extern __shared__ uint64_t s_freq[];                          // R/2
+    float *s_cos = reinterpret_cast<float *>(s_freq + p.R / 2), *s_sin = s_cos + p.tokens * (p.R / 2);  // tokens x R/2, times scale
     __shared__ int64_t s_slot[kRopeTokens];
     __shared__ int s_pos[kRopeTokens];
     stream_wait();
     stream_release();
-    const int t0 = (int)blockIdx.x * p.tokens, half = p.R / 2;
-    const int tokens = p.T - t0 < p.tokens ? p.T - t0 : p.tokens;
+    const int tid = (int)threadIdx.x, half = p.R / 2;
+    const int t0 = (int)blockIdx.x * p.tokens, tokens = p.T - t0 < p.tokens ? p.T - t0 : p.tokens;
     const int all_rows = p.heads[0] + p.heads[1] + p.heads[2];
     const int row0 = (int)blockIdx.y * p.rows, rows = all_rows - row0 < p.rows ? all_rows - row0 : p.rows;
-    if ((int)threadIdx.x < tokens) {
-        const int t = t0 + (int)threadIdx.x, pos = p.pos[t];
+    const int turning = rope_turning(FORM, V, p.R), units = (int)p.units.d;
+    if (tid < tokens) {
+        const int t = t0 + tid, pos = p.pos[t];
         int64_t slot = -1;
         if (p.table != nullptr && pos >= 0) {
             const int page = p.kv.page_at(p.table, p.seqs != nullptr ? p.seqs[t] : t, pos / p.kv.page_size);
             if (page >= 0) slot = page * p.page_s + pos % p.kv.page_size * p.token_s;
         }
-        s_pos[threadIdx.x] = pos;
-        s_slot[threadIdx.x] = slot;
+        s_pos[tid] = pos;
+        s_slot[tid] = slot;
     }
-    for (int i = (int)threadIdx.x; i < tokens * half; i += kRopeThreads) {
-        const int t = i / half;
-        double turns = (double)p.pos[t0 + t] * p.freqs[i - t * half] * 0.15915494309189533577;  // 1 / (2 pi)
-        turns -= rint(turns);
-        float c, s;
-        sincospif(2.0f * (float)turns, &s, &c);
-        s_turn[i] = make_float2(c * p.scale, s * p.scale * p.sign);
+    for (int i = tid; i < half; i += kRopeThreads) {
+        double turns = p.freqs[i] * 0.15915494309189533577;  // 1 / (2 pi)
+        turns -= floor(turns);
+        s_freq[i] = turns < 1.0 ? (uint64_t)(turns * 18446744073709551616.0) : 0;  // 2^64
     }
     __syncthreads();
-    // Units of a row: those that turn, then those that copy the rest of the head.
-    const int turning = (INTERLEAVED && V > 1 ? p.R : half) / V;
-    const int units = turning + (p.D - p.R) / V;
+    for (int i = tid; i < tokens * half; i += kRopeThreads) {
+        const int t = p.half.of(i);
+        const uint64_t angle = s_freq[i - t * half] * (uint64_t)(uint32_t)s_pos[t];
+        float c, s;
+        sincospif((float)(int32_t)(angle >> 32) * 4.656612873077392578e-10f, &s, &c);  // 2^-31: half turns
+        s_cos[i] = c * p.scale;
+        s_sin[i] = s * p.scale * p.sign;
+    }
+    __syncthreads();
+    // the last block in y may have fewer rows than the divisor is for
+    const Divisor by_rows = rows == (int)p.block_rows.d ? p.block_rows : Divisor{(uint32_t)rows, 0xffffffffu / (uint32_t)rows + 1u};
     const int n = tokens * rows * units;
-    for (int i = (int)threadIdx.x; i < n; i += kRopeThreads) {
-        const int unit = i % units, row = i / units % rows + row0, t = i / units / rows;
+    for (int i = tid; i < n; i += kRopeThreads) {
+        const int r = p.units.of(i), unit = i - r * units, t = by_rows.of(r), row = r - t * rows + row0;
         const int set = row < p.heads[0] ? 0 : row < p.heads[0] + p.heads[1] ? 1 : 2;
         const int head = row - (set == 0 ? 0 : set == 1 ? p.heads[0] : p.heads[0] + p.heads[1]);
         if (s_pos[t] < 0) continue;
@@ -97,49 +162,68 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
         } else {
             out += (t0 + t) * p.out_t[set];
         }
-        using W = Vec<T, V>;
-        if (unit >= turning) {
-            const int e = p.R + (unit - turning) * V;
-            *reinterpret_cast<W *>(out + e) = *reinterpret_cast<const W *>(in + e);
-        } else if constexpr (INTERLEAVED && V > 1) {
-            const int e = unit * V;
-            W x = *reinterpret_cast<const W *>(in + e);
-            if (set < 2) {
+        const bool turns = unit < turning;
+        const int a = !turns ? p.R + (unit - turning) * V : FORM == kNearOne ? 2 * unit : unit * V;
+        const int b = a + (FORM == kNearOne ? 1 : half);  // the other vector of a unit that turns
+        const bool both = FORM != kHalfOdd || !turns || a + 1 < half;  // not one pair alone
+        W x, y;
+        if (both) x = *reinterpret_cast<const W *>(in + a);
+        else x.set(0, in[a]);
+        if (PAIR && turns) {
+            if constexpr (FORM == kHalfOdd) {
+                y.set(0, in[b]);
+                if (both) y.set(1, in[b + 1]);
+            } else {
+                y = *reinterpret_cast<const W *>(in + b);
+            }
+        }
+        if (turns && set < 2) {
+            const float *c = s_cos + t * half, *s = s_sin + t * half;
+            if constexpr (V == 1) {
+                const float va = to_f32(x.v), vb = to_f32(y.v);
+                x.v = from_f32<T>(va * c[unit] - vb * s[unit]);
+                y.v = from_f32<T>(vb * c[unit] + va * s[unit]);
+            } else {
 #pragma unroll
-                for (int j = 0; j < V / 2; ++j) {
-                    const float2 w = s_turn[t * half + e / 2 + j];
-                    const float a = to_f32(x.v[2 * j]), b = to_f32(x.v[2 * j + 1]);
-                    x.v[2 * j] = from_f32<T>(a * w.x - b * w.y);
-                    x.v[2 * j + 1] = from_f32<T>(b * w.x + a * w.y);
+                for (int j = 0; j < kTwos; ++j) {
+                    if constexpr (!INTERLEAVED) {  // two pairs
+                        const F2 va = x.get(j), vb = y.get(j);
+                        const int at = unit * V + 2 * j;
+                        const F2 cc = f2(c[at], c[both ? at + 1 : at]), ss = f2(s[at], s[both ? at + 1 : at]);
+                        x.put(j, fma(vb, mul(ss, every<F2>(-1.0f)), mul(va, cc)));
+                        y.put(j, fma(va, ss, mul(vb, cc)));
+                    } else {  // one in each vector
+                        const int at = unit * kTwos + j;
+                        x.put(j, turned(x.get(j), c[at], s[at]));
+                        if constexpr (PAIR) y.put(j, turned(y.get(j), c[at + half / 2], s[at + half / 2]));
+                    }
                 }
             }
-            *reinterpret_cast<W *>(out + e) = x;
-        } else {
-            const int ea = unit * V * (INTERLEAVED ? 2 : 1), eb = ea + (INTERLEAVED ? 1 : half);
-            W x = *reinterpret_cast<const W *>(in + ea), y = *reinterpret_cast<const W *>(in + eb);
-            if (set < 2) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float2 w = s_turn[t * half + unit * V + j];
-                    const float a = to_f32(x.v[j]), b = to_f32(y.v[j]);
-                    x.v[j] = from_f32<T>(a * w.x - b * w.y);
-                    y.v[j] = from_f32<T>(b * w.x + a * w.y);
-                }
+        }
+        if (both) *reinterpret_cast<W *>(out + a) = x;
+        else out[a] = x.at(0);
+        if (PAIR && turns) {
+            if constexpr (FORM == kHalfOdd) {
+                out[b] = y.at(0);
+                if (both) out[b + 1] = y.at(1);
+            } else {
+                *reinterpret_cast<W *>(out + b) = y;
             }
-            *reinterpret_cast<W *>(out + ea) = x;
-            *reinterpret_cast<W *>(out + eb) = y;
         }
     }
 }
 
 static int elem_bytes(tgc_dtype t) { return t == TGC_F32 ? 4 : t == TGC_BF16 || t == TGC_F16 ? 2 : 0; }
 
-// The widest vector, in elements, that pointers, strides and the parts of a head all keep: 16 bytes, 2
-// elements or 1.
-static int rope_vector(const RopeParams &p, bool interleaved, int es, const void *k_pages, const void *v_pages,
-                       int64_t head_s) {
+struct RopeShape {
+    RopeForm form;
+    int v;  // elements of a vector
+};
+
+// The widest vectors that pointers, strides and the parts of a head all keep: 16 bytes, two elements, one.
+static RopeShape rope_shape(const RopeParams &p, bool interleaved, int es, const void *k_pages, const void *v_pages, int64_t head_s) {
     for (const int v : {16 / es, 2}) {
-        bool fits = p.D % v == 0 && p.R % v == 0 && (interleaved || p.R / 2 % v == 0);
+        bool fits = p.D % v == 0 && p.R % v == 0;
         auto at = [&](const void *q, int64_t a, int64_t b) {
             fits = fits && reinterpret_cast<uintptr_t>(q) % (v * es) == 0 && a % v == 0 && b % v == 0;
         };
@@ -152,43 +236,47 @@ static int rope_vector(const RopeParams &p, bool interleaved, int es, const void
             at(k_pages, p.page_s, p.token_s);
             at(v_pages, head_s, 0);
         }
-        if (fits) return v;
+        if (!fits) continue;
+        if (p.R / 2 % v == 0 && (v > 2 || !interleaved)) return {interleaved ? kNear : kHalf, v};
+        if (v == 2) return {interleaved ? kNearSingle : kHalfOdd, 2};
     }
-    return 1;
+    return {interleaved ? kNearOne : kHalfOne, 1};
 }
 
-template <typename T, bool INTERLEAVED>
-static cudaError_t launch_rope_typed(const RopeParams &p, int v, dim3 grid, size_t smem, cudaStream_t stream) {
+template <typename T>
+static cudaError_t launch_rope_typed(const RopeParams &p, RopeShape f, dim3 grid, size_t smem, cudaStream_t stream) {
     constexpr int W = 16 / sizeof(T);
-    return v == W   ? launch_overlapped(rope_kernel<T, W, INTERLEAVED>, grid, dim3(kRopeThreads), smem, 1, stream, p)
-           : v == 2 ? launch_overlapped(rope_kernel<T, 2, INTERLEAVED>, grid, dim3(kRopeThreads), smem, 1, stream, p)
-                    : launch_overlapped(rope_kernel<T, 1, INTERLEAVED>, grid, dim3(kRopeThreads), smem, 1, stream, p);
+    auto go = [&](auto kernel) { return launch_overlapped(kernel, grid, dim3(kRopeThreads), smem, 1, stream, p); };
+    switch (f.form) {
+        case kHalf: return f.v == W ? go(rope_kernel<T, W, kHalf>) : go(rope_kernel<T, 2, kHalf>);
+        case kHalfOdd: return go(rope_kernel<T, 2, kHalfOdd>);
+        case kHalfOne: return go(rope_kernel<T, 1, kHalfOne>);
+        case kNear: return go(rope_kernel<T, W, kNear>);
+        case kNearSingle: return go(rope_kernel<T, 2, kNearSingle>);
+        default: return go(rope_kernel<T, 1, kNearOne>);
+    }
 }
 
-static int launch_rope(RopeParams &p, bool interleaved, tgc_dtype dtype, int v, cudaStream_t stream) {
+static int launch_rope(RopeParams &p, RopeShape f, tgc_dtype dtype, cudaStream_t stream) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e);
-    const int sms = sm_count(dev), rows = p.heads[0] + p.heads[1] + p.heads[2];
-    const int units = ((interleaved && v > 1 ? p.R : p.R / 2) + p.D - p.R) / v;
+    const int sms = sm_count(dev), rows = p.heads[0] + p.heads[1] + p.heads[2], half = p.R / 2;
+    const int units = rope_turning(f.form, f.v, p.R) + (p.D - p.R) / f.v;
     // Many tokens: up to 4 a block, so that its threads each have a sine to take.  Few: one a block, its rows cut
     // so that a thread has one unit.
     p.tokens = 1;
-    while (p.tokens < kRopeTokens && 2 * p.tokens * (p.R / 2) <= kRopeThreads && p.T / (2 * p.tokens) >= 8 * sms) p.tokens *= 2;
-    p.rows = rows;
-    if (p.T < 4 * sms) {
-        p.rows = (kRopeThreads + units - 1) / units;
-        if (p.rows > rows) p.rows = rows;
-        if ((rows + p.rows - 1) / p.rows > 65535) p.rows = (rows + 65534) / 65535;
-    }
+    while (p.tokens < kRopeTokens && p.T / (2 * p.tokens) >= 8 * sms) p.tokens *= 2;
+    p.rows = rows < kRopeRows ? rows : kRopeRows;
+    if (p.T < 4 * sms) p.rows = std::min(p.rows, (kRopeThreads + units - 1) / units);
+    p.half = divisor(half > 0 ? half : 1);
+    p.units = divisor(units);
+    p.block_rows = divisor(p.rows);
     const dim3 grid((unsigned)((p.T + p.tokens - 1) / p.tokens), (unsigned)((rows + p.rows - 1) / p.rows));
-    const size_t smem = (size_t)p.tokens * (size_t)(p.R / 2) * sizeof(float2);
-    auto go = [&](auto type) {
-        using T = decltype(type);
-        return interleaved ? launch_rope_typed<T, true>(p, v, grid, smem, stream)
-                           : launch_rope_typed<T, false>(p, v, grid, smem, stream);
-    };
-    e = dtype == TGC_BF16 ? go(__nv_bfloat16{}) : dtype == TGC_F16 ? go(__half{}) : go(0.0f);
+    const size_t smem = (size_t)(p.tokens + 1) * (size_t)half * sizeof(float2);
+    e = dtype == TGC_BF16  ? launch_rope_typed<__nv_bfloat16>(p, f, grid, smem, stream)
+        : dtype == TGC_F16 ? launch_rope_typed<__half>(p, f, grid, smem, stream)
+                           : launch_rope_typed<float>(p, f, grid, smem, stream);
     return e == cudaSuccess ? TGC_OK : cuda_fail(e);
 }
 
@@ -251,7 +339,7 @@ static int rope_impl(tgc_rope_args a, float sign) {
     p.T = (int)a.T; p.D = (int)a.D; p.R = (int)a.R;
     p.scale = a.scale; p.sign = sign;
     const bool interleaved = a.layout == TGC_ROPE_INTERLEAVED;
-    return launch_rope(p, interleaved, a.dtype, rope_vector(p, interleaved, es, nullptr, nullptr, 0), a.stream);
+    return launch_rope(p, rope_shape(p, interleaved, es, nullptr, nullptr, 0), a.dtype, a.stream);
 }
 
 static int append_impl(tgc_kv_append_args a) {
@@ -286,7 +374,7 @@ static int append_impl(tgc_kv_append_args a) {
     p.kv = KvTable{(int)a.num_pages, (int)a.page_size, (int)a.num_seqs, (int)a.max_pages, a.table_ld};
     p.page_s = a.page_s; p.token_s = a.token_s;
     const bool interleaved = a.layout == TGC_ROPE_INTERLEAVED;
-    return launch_rope(p, interleaved, a.dtype, rope_vector(p, interleaved, es, a.k_pages, a.v_pages, a.head_s), a.stream);
+    return launch_rope(p, rope_shape(p, interleaved, es, a.k_pages, a.v_pages, a.head_s), a.dtype, a.stream);
 }
 
 }  // namespace tgc
