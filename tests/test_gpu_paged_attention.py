@@ -90,7 +90,13 @@ CASES = [  # lens, key heads, group, D, page
     ([20000], 1, 4, 64, 16), ([9000, 1, 12000], 2, 8, 128, 128), ([511] * 9, 4, 3, 144, 3), ([1] * 300, 1, 1, 64, 4)]
 
 
-@pytest.mark.parametrize("lens,Hk,group,D,page", CASES)
+# many items, or long ones, with more than 8 heads a key or more than 128 elements a head
+WIDE = [([20000, 300], 1, 16, 128, 16), ([9000, 1, 8000], 2, 32, 96, 24), ([700, 5] * 85, 2, 12, 64, 16),
+        ([500, 0, 1, 127, 128, 129] * 30, 2, 9, 72, 7), ([300] * 160, 1, 4, 256, 16), ([12000], 1, 16, 256, 33),
+        ([130, 0, 257] * 60, 1, 40, 200, 5), ([25000], 1, 33, 128, 64), ([1, 2, 3] * 110, 1, 20, 8, 1)]
+
+
+@pytest.mark.parametrize("lens,Hk,group,D,page", CASES + WIDE)
 @pytest.mark.parametrize("dtype", list(DT))
 @pytest.mark.parametrize("window,cap", [(0, 0.0), (100, 0.0), (37, 5.0)])
 def test_attention(lens, Hk, group, D, page, dtype, window, cap):
