@@ -17,10 +17,10 @@
 // for one of them: 768 for 16 keys of up to 8 heads x 128, whose bytes take HBM 1400 a quarter; with 16 heads the
 // products are the bound (64 x 1850 tokens, 2 x 16 heads x 128: 44 us, bytes 23).
 // The same on tcgen05 -- 128 keys or elements as rows, heads as columns, scores and outputs in TMEM, warps of
-// their own for copies, products and softmax -- was built and measured: 66 us there, 98 against 111 with
-// 256 elements a head, 220 against 162 for 170 x 70 tokens.  A product of 128 rows takes it 130 clocks whatever its
+// their own for copies, products and softmax -- was built and measured: 66 us there, 98 against 86 with 256
+// elements a head, 220 against 126 for 170 sequences of 70 tokens.  A product of 128 rows takes it 130 clocks whatever its
 // 16 to 64 columns, also where neighbouring ones do not depend on each other: 2100 for 128 keys, and the way from
-// scores to probabilities to outputs cannot hide behind it.
+// scores to probabilities to outputs does not hide behind it.
 // The probabilities enter the second product as a high and a low 16-bit part: rounding them to
 // 16 bits once would add about as much error as rounding the output does.
 // The running maximum follows the scores only when one passes it by kSlack powers of two: until then the
@@ -151,22 +151,30 @@ struct AttnShape {
     static constexpr int kKeys = DP == 64 ? 32 : 16;  // of a warp's step
     static constexpr int kUnit = kAttnWarps * kKeys;
     static constexpr int kTile = kKeys * DP * 2;      // bytes of a step's keys (or values)
+    // A warp's ring: three slots, of a step's keys and values; with wide heads of either alone (keys, values, keys, ...), so
+    // that two CTAs fit an SM: alone, its one warp a quarter waits for each of its own products.
+    static constexpr bool kAlone = DP == 256;
     static constexpr int kStages = 3;
-    static constexpr int kWarpRing = kStages * 2 * kTile;
+    static constexpr int kSlot = kAlone ? kTile : 2 * kTile;
+    static constexpr int kWarpRing = kStages * kSlot;
+    __device__ static int keys_at(int step) { return (kAlone ? 2 * step : step) % kStages * kSlot; }
+    __device__ static int values_at(int step) { return kAlone ? (2 * step + 1) % kStages * kSlot : keys_at(step) + kTile; }
+    // The slot that the last of `steps` steps left last: no copy has reached it again.
+    __device__ static int last_slot(int steps) { return (kAlone ? 2 * steps + 2 : steps + 2) % kStages; }
     static constexpr int kRings = kAttnWarps * kWarpRing;
     // The queries of three items: one in work, two that the copies may have entered.  They come with the copies, as
     // loads of their own would queue behind those at every item's start (0: no room beside the rings, loads).
-    static constexpr int kQueries = DP == 128 && NT == 4 ? 0 : kRows * DP * 2;
+    static constexpr int kQueries = (DP == 128 && NT == 4) || (DP == 256 && NT == 2) ? 0 : kRows * DP * 2;
     static constexpr int kSmem = kRings + 3 * kQueries;
-    // Outputs of so many heads fit a stage; more take turns.
-    static constexpr int kRound = kRows * DP * 4 <= 2 * kTile ? kRows : 2 * kTile / (DP * 4);
-    // Where a CTA of a cluster that took `steps` steps leaves its part of the heads from r0 on: not in the stage where its
-    // warps' parts meet, the last it used.
+    // Outputs of so many heads fit a slot; more take turns.
+    static constexpr int kRound = kRows * DP * 4 <= kSlot ? kRows : kSlot / (DP * 4);
+    // Where a CTA of a cluster that took `steps` steps leaves its part of the heads from r0 on: not in the slot where its
+    // warps' parts meet.
     __device__ static int cta_part(int steps, int r0) {
-        return r0 / kRound * kWarpRing + (steps + kStages) % kStages * 2 * kTile;
+        return r0 / kRound * kWarpRing + (last_slot(steps) + 1) % kStages * kSlot;
     }
 };
-static_assert(AttnShape<128, 4>::kRound == 16 && AttnShape<64, 4>::kRound == 32 && AttnShape<256, 2>::kRound == 16, "whole eights");
+static_assert(AttnShape<128, 4>::kRound == 16 && AttnShape<64, 4>::kRound == 32 && AttnShape<256, 2>::kRound == 8, "whole eights");
 
 // Where a run stands: its place in the row of all units, and the item there.
 struct RunAt {
@@ -238,7 +246,7 @@ __device__ __forceinline__ void store_out(const AttnParams &p, int seq, int head
 }
 
 template <bool F16, int DP, int NT, bool CLUSTER>
-__global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnParams p) {
     using S = AttnShape<DP, NT>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t s_sum[kAttnWarps];
@@ -252,9 +260,9 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
     const int chunks = p.D / 8;
 
     // Products are 16 deep: where D ends inside 16, the rest of the keys' rows has to be zero.
-    auto clear_tail = [&](int stage) {
+    auto clear_tail = [&](int slot) {
         if (chunks % 2 != 0 && lane < S::kKeys)
-            *reinterpret_cast<uint4 *>(ring + stage * 2 * S::kTile + chunk_at<DP>(lane, chunks)) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(ring + slot * S::kSlot + chunk_at<DP>(lane, chunks)) = make_uint4(0, 0, 0, 0);
     };
 #pragma unroll
     for (int i = 0; i < S::kStages; ++i) clear_tail(i);
@@ -356,7 +364,6 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
         __syncthreads();
     }
     RunAt c = CLUSTER ? r : s_cur;
-    int issued = 0;
     // The next sequence that has keys; none only where the lengths change under the call.
     auto next_seq = [&](RunAt &w) {
         while (++w.seq < p.kv.num_seqs) {
@@ -368,49 +375,55 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
         }
         return false;
     };
-    auto copy_unit = [&] {
-        if (r.at < stop) {
-            if (S::kQueries > 0 && fresh) copy_queries();
-            const int stage = issued % S::kStages;
-            const int64_t off = page[0] < 0 ? -1 : page[0] * p.page_s + place * p.token_s + head_off;
-            const uint32_t have = __ballot_sync(0xffffffffu, off >= 0);
-            if (lane == 0) s_mask[warp][stage] = have;
-            const uint32_t to = ring_at + (uint32_t)(stage * 2 * S::kTile);
+    int64_t off = -1;  // of this lane's key in the pools, of the unit in work
+    auto copy_rows = [&](const void *pool, int to) {
 #pragma unroll
-            for (int i = 0; i < S::kKeys * (DP / 8) / 32; ++i) {
-                const int idx = i * 32 + lane, row = idx / (DP / 8), ch = idx % (DP / 8);
-                const int64_t o = __shfl_sync(0xffffffffu, off, row);
-                if (ch < chunks) {
-                    const int64_t from = o < 0 ? 0 : o + ch * 8;
-                    cp_async16(to + chunk_at<DP>(row, ch), static_cast<const uint16_t *>(p.k) + from, o >= 0);
-                    cp_async16(to + S::kTile + chunk_at<DP>(row, ch), static_cast<const uint16_t *>(p.v) + from, o >= 0);
-                }
-            }
-            ++r.at;
-            if (++r.unit < r.units) {
-                look_up();
-                past(place);
-            } else if (!CLUSTER && r.at < stop) {
-                r.unit = 0;
-                if (++r.item == heads) {
-                    r.item = 0;
-                    r.seq_begin += (int64_t)r.units * heads;
-                    if (!next_seq(r)) {
-                        r.at = stop;
-                        return;
-                    }
-                }
-                enter_item();
-            }
+        for (int i = 0; i < S::kKeys * (DP / 8) / 32; ++i) {
+            const int idx = i * 32 + lane, row = idx / (DP / 8), ch = idx % (DP / 8);
+            const int64_t o = __shfl_sync(0xffffffffu, off, row);
+            if (ch < chunks)
+                cp_async16(ring_at + (uint32_t)to + chunk_at<DP>(row, ch), static_cast<const uint16_t *>(pool) + (o < 0 ? 0 : o + ch * 8), o >= 0);
         }
     };
-    auto issue = [&] {
-        copy_unit();
-        ++issued;
-        cp_async_commit();
+    auto copy_keys = [&](int unit) {  // the unit's number in the run
+        off = -1;
+        if (r.at < stop) {
+            if (S::kQueries > 0 && fresh) copy_queries();
+            if (page[0] >= 0) off = page[0] * p.page_s + place * p.token_s + head_off;
+            const uint32_t have = __ballot_sync(0xffffffffu, off >= 0);
+            if (lane == 0) s_mask[warp][unit % S::kStages] = have;
+            copy_rows(p.k, S::keys_at(unit));
+        }
     };
-#pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) issue();
+    auto copy_values = [&](int unit) {  // and on to the next unit
+        if (r.at >= stop) return;
+        copy_rows(p.v, S::values_at(unit));
+        ++r.at;
+        if (++r.unit < r.units) {
+            look_up();
+            past(place);
+        } else if (!CLUSTER && r.at < stop) {
+            r.unit = 0;
+            if (++r.item == heads) {
+                r.item = 0;
+                r.seq_begin += (int64_t)r.units * heads;
+                if (!next_seq(r)) {
+                    r.at = stop;
+                    return;
+                }
+            }
+            enter_item();
+        }
+    };
+    // The copies stay two units ahead (kAlone: a unit's keys and another's values, and the keys after them).
+    copy_keys(0);
+    if (S::kAlone) cp_async_commit();
+    copy_values(0);
+    cp_async_commit();
+    copy_keys(1);
+    if (!S::kAlone) copy_values(1);
+    cp_async_commit();
+    constexpr int kBehind = S::kAlone ? 2 : 1;  // groups that may be under way while the next one's data are used
 
     int step = 0, done = 0;  // steps, items
     while (CLUSTER || c.at < stop) {
@@ -423,7 +436,7 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
         uint32_t qf[NT][DP / 16][2];
         if constexpr (S::kQueries > 0) {
             if (CLUSTER && todo <= 0) cp_async_wait<0>();
-            else cp_async_wait<S::kStages - 2>();
+            else cp_async_wait<kBehind>();
             __syncthreads();
             const uint32_t q_at = smem_addr(smem + S::kRings) + (uint32_t)(done % 3 * S::kQueries);
 #pragma unroll
@@ -459,12 +472,15 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
             sum[n][0] = sum[n][1] = 0.0f;
         }
         for (int left = todo; left > 0; --left, ++step) {
-            cp_async_wait<S::kStages - 2>();
+            cp_async_wait<kBehind>();
             __syncwarp();
-            const int stage = step % S::kStages;
-            const uint32_t k_at = ring_at + (uint32_t)(stage * 2 * S::kTile), v_at = k_at + S::kTile;
-            const uint32_t have = s_mask[warp][stage];
-            issue();
+            const uint32_t k_at = ring_at + (uint32_t)S::keys_at(step), v_at = ring_at + (uint32_t)S::values_at(step);
+            const uint32_t have = s_mask[warp][step % S::kStages];
+            if (!S::kAlone) {
+                copy_keys(step + 2);
+                copy_values(step + 2);
+                cp_async_commit();
+            }
 
             constexpr int MK = S::kKeys / 16;
             float x[MK][NT][4];  // keys g and g + 8 of every 16
@@ -484,6 +500,11 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
 #pragma unroll
                     for (int n = 0; n < NT; ++n) mma16<F16>(x[m][n], a, qf[n][kk][0], qf[n][kk][1]);
                 }
+            }
+            if (S::kAlone) {  // the next values in place of these keys
+                __syncwarp();
+                copy_values(step + 1);
+                cp_async_commit();
             }
             if (p.cap > 0.0f) {
 #pragma unroll
@@ -557,6 +578,10 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
                         lo[m][n][h] = transpose8(pack16(f2(a - back.x, b - back.y), F16));
                     }
             }
+            if (S::kAlone) {
+                cp_async_wait<kBehind>();
+                __syncwarp();
+            }
 #pragma unroll
             for (int j = 0; j < DP / 16; ++j) {
                 if (j * 2 >= chunks) break;
@@ -571,11 +596,16 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
                     }
                 }
             }
+            if (S::kAlone && left > 1) {  // keys in place of these values; after the item's end, where it is this
+                __syncwarp();
+                copy_keys(step + 2);
+                cp_async_commit();
+            }
         }
 
-        // ---- the warps' parts meet: each in the stage that it used last, which its copies have not reached again
-        const int last_stage = (step + S::kStages - 1) % S::kStages;
-        auto part_of = [&](int w) { return reinterpret_cast<float *>(smem + w * S::kWarpRing + last_stage * 2 * S::kTile); };
+        // ---- the warps' parts meet: each in the slot that it used last, which its copies have not reached again
+        const int last = S::last_slot(step);
+        auto part_of = [&](int w) { return reinterpret_cast<float *>(smem + w * S::kWarpRing + last * S::kSlot); };
         // heads' rows of DP; pairs of heads turned against one another, so that a warp's stores meet every bank once
         auto place_of = [](int row, int d) { return row * DP + (d ^ (((row >> 1) & 3) << 3)); };
 #pragma unroll
@@ -690,7 +720,12 @@ __global__ void __launch_bounds__(kAttnThreads, DP <= 128 ? 2 : 1) attention_ker
             }
             return;
         }
-        clear_tail(last_stage);
+        clear_tail(last);
+        if (S::kAlone) {
+            __syncwarp();
+            copy_keys(step + 1);
+            cp_async_commit();
+        }
         c = s_cur;
     }
     cp_async_wait<0>();
@@ -805,9 +840,11 @@ struct AttnPlan {
 
 // Heads of an item, in eights: as many as share a key, up to 32 (16 for D > 128, whose outputs take twice the
 // registers).
-// Clusters where the items' CTAs are all resident at once, and a CTA has at most kClusterUnits units of its item; runs
-// otherwise.  Runs: one for each of two CTAs an SM (one for D > 128), no more than there can be units.
-constexpr int kClusterUnits = 16;
+// Clusters where the items' CTAs are all resident at once, a CTA has at most kClusterUnits units of its item and not many
+// more than a run would have; runs otherwise.  With 8 heads of 128 x 4 a key, clusters and runs take 5.8 and 7.7 us for
+// 200 tokens, 7.6 and 8.4 for 900, 9.6 and 9.3 for 2000, 13.6 and 11.6 for 4000 (8 units where a run has 2), 13.9 and 15.7 for
+// 16 x 1000 (8 and 7), 12.0 and 18.3 for 32 x 500.  Runs: one for each of two CTAs an SM, no more than there can be units.
+constexpr int kClusterUnits = 16, kClusterBehind = 3;
 
 static AttnPlan attn_plan(const tgc_paged_attention_args &a, int sms) {
     AttnPlan q{};
@@ -819,10 +856,11 @@ static AttnPlan attn_plan(const tgc_paged_attention_args &a, int sms) {
     q.items = a.num_seqs * a.heads_k * q.row_blocks;
     int64_t most = a.max_pages * a.page_size;
     if (a.window > 0 && most > a.window) most = a.window;
-    const int64_t units = (most + q.unit - 1) / q.unit, room = (int64_t)sms * (q.dp <= 128 ? 2 : 1);
+    const int64_t units = (most + q.unit - 1) / q.unit, room = (int64_t)sms * 2;
     int c = 1;
     while (c < kMaxCluster && 2 * c * q.items <= room && c < units) c *= 2;
-    if (c * q.items <= room && (units + c - 1) / c <= kClusterUnits) {
+    const int64_t each = (units + c - 1) / c;
+    if (c * q.items <= room && each <= kClusterUnits && each - (q.items * units + room - 1) / room <= kClusterBehind) {
         q.cluster = c;
         q.grid = (int)(c * q.items);
         return q;
