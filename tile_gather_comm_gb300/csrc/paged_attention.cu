@@ -6,7 +6,7 @@
 // bytes, so HBM is the bound and the design is about keeping loads in flight.
 //
 // A CTA's 4 warps work for themselves: of each unit of keys a warp takes its quarter (a step), copies it
-// with cp.async into its own ring of stages, and keeps its own running maximum, sum and output in
+// with cp.async into its own ring of slots, and keeps its own running maximum, sum and output in
 // registers; they meet at an item's end.  No barrier in the loop; a page may end anywhere, as each key
 // finds its own page.  The copies run ahead of the products across the end of an item, so they do not
 // pause while the warps meet.
@@ -124,7 +124,6 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ float exp2_approx(float v) {
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(v));
     return v;
@@ -137,7 +136,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     return r;
 }
 
-// A 16-byte chunk's place in a row of a stage: rows of DP elements, chunks of 8 rows turned against one another
+// A 16-byte chunk's place in a row of a slot: rows of DP elements, chunks of 8 rows turned against one another
 // so that ldmatrix, which reads one chunk of 8 rows, meets every bank once.
 template <int DP>
 __device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
