@@ -191,6 +191,35 @@ def test_bad_pages_and_lengths():
     check(out[:1], None, q[:1], keys, D ** -0.5)
 
 
+def test_nothing_to_attend_to():
+    """No sequences; a table without pages; a pool without pages; all lengths zero, in runs and in clusters."""
+    ints = dict(device="cuda", dtype=torch.int32)
+    kp = torch.full((3, 4, 2, 64), float("nan"), device="cuda", dtype=torch.bfloat16)
+    for S, table, pool, n in ((0, torch.zeros(0, 2, **ints), kp, 0), (3, torch.zeros(3, 0, **ints), kp, 5),
+                              (3, torch.zeros(3, 2, **ints), kp[:0], 5), (3, torch.zeros(3, 2, **ints), kp, 0),
+                              (400, torch.zeros(400, 2, **ints), kp, 0), (400, torch.zeros(400, 0, **ints), kp, 9)):
+        q = torch.randn(S, 4, 64, device="cuda").bfloat16()
+        out, lse = torch.full_like(q, 7.0), torch.full((S, 4), 7.0, device="cuda")
+        tgc.tgc_paged_attention(q, out, pool, pool, table, torch.full((S,), n, **ints), lse=lse)
+        assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+
+
+def test_many_sequences():
+    """More sequences than threads look at in one go, most of them empty."""
+    g = gen(12)
+    lens = [0] * 3000
+    for s in (0, 5, 31, 32, 700, 1500, 2998, 2999):
+        lens[s] = 1 + s % 97
+    kp, vp, table, n, keys = cache(lens, 16, 2, 64, torch.bfloat16, g)
+    q = torch.randn(3000, 4, 64, generator=g, device="cuda").bfloat16()
+    out, lse = torch.full_like(q, 7.0), torch.full((3000, 4), 7.0, device="cuda")
+    tgc.tgc_paged_attention(q, out, kp, vp, table, n, lse=lse)
+    some = [s for s in range(3000) if lens[s]]
+    check(out[some], lse[some], q[some], [keys[s] for s in some], 0.125)
+    gone = [s for s in range(3000) if not lens[s]]
+    assert bool((out[gone] == 0).all()) and bool((lse[gone] == -math.inf).all())
+
+
 def test_large_scores_and_infinities():
     """Scores of thousands do not overflow; a row whose scores fall from step to step keeps its first maximum."""
     g = gen(6)

@@ -201,6 +201,20 @@ def test_append(T, S, Hq, Hk, D, R, page, dtype, layout, heads_first):
         assert bool((qo[~live] == 9.0).all())
 
 
+def test_the_most_heads_and_none():
+    freqs, _ = tgc.tgc_rope_freqs(2)
+    q = torch.randn(1, 65536, 1024, generator=gen(), device="cuda").half()
+    out, pos = torch.empty_like(q), torch.tensor([5], device="cuda", dtype=torch.int32)
+    tgc.tgc_rope(q, out, pos, freqs)
+    for h in (slice(0, 40), slice(32700, 32800), slice(65500, 65536)):
+        check(out[:, h], q[:, h], pos, freqs, "half")
+    nothing = torch.zeros(0, dtype=torch.int32, device="cuda")
+    tgc.tgc_rope(q[:0], q[:0], nothing, freqs)
+    kp = torch.full((2, 4, 3, 8), 7.0, device="cuda")
+    tgc.tgc_kv_append(kp[0, :0], kp[0, :0], kp, kp.clone(), torch.zeros(1, 2, device="cuda", dtype=torch.int32), nothing)
+    assert bool((kp == 7).all())
+
+
 def test_a_far_page_of_a_large_pool():
     """Pages more than 2^31 elements from the pool's start."""
     D, Hk, page = 128, 8, 64

@@ -269,6 +269,7 @@ static int launch_rope(RopeParams &p, RopeShape f, tgc_dtype dtype, cudaStream_t
     while (p.tokens < kRopeTokens && p.T / (2 * p.tokens) >= 8 * sms) p.tokens *= 2;
     p.rows = rows < kRopeRows ? rows : kRopeRows;
     if (p.T < 4 * sms) p.rows = std::min(p.rows, (kRopeThreads + units - 1) / units);
+    p.rows = std::max(p.rows, (rows + 65534) / 65535);  // a grid has 65535 blocks in y at most
     p.half = divisor(half > 0 ? half : 1);
     p.units = divisor(units);
     p.block_rows = divisor(p.rows);
