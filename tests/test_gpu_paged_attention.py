@@ -241,6 +241,29 @@ def test_large_scores_and_infinities():
         assert bool(((lse[0].double() - want_lse).abs() <= want_lse.abs() * 2 ** -22).all())
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("at", [0, 500, 999])
+def test_small_probabilities_count(dtype, at):
+    """One key, whose value is zero, weighs e^17.7 as much as each of the others: what is left of those 999 is below fp16's
+    normal range, and is the output."""
+    g = gen(at)
+    n, D, page, S = 1000, 64, 16, 200
+    kp, vp, table, lens, keys = cache([n] * S, page, 1, D, DT[dtype], g)
+    j = torch.arange(n, device="cuda")
+    for s, kv in enumerate(keys):
+        kv[0] = 0.0
+        kv[0, at, 0, 0] = 17.6875 if dtype == "f16" else 17.75
+        kv[1] = kv[1].abs() * 64
+        kv[1, at] = 0.0
+        where = table[s, j // page].long()
+        kp[where, j % page], vp[where, j % page] = kv[0], kv[1]
+    q = torch.zeros(S, 2, D, device="cuda", dtype=DT[dtype])
+    q[:, :, 0] = 1.0
+    out, lse = torch.empty_like(q), torch.empty(S, 2, device="cuda")
+    tgc.tgc_paged_attention(q, out, kp, vp, table, lens, lse=lse, scale=1.0)
+    check(out, lse, q, keys, 1.0)
+
+
 def test_same_bits_streams_and_graphs():
     g = gen(8)
     lens, Hk, group, D, page = [3000, 10, 5000, 777, 0, 64], 4, 4, 128, 16

@@ -23,13 +23,15 @@
 // scores to probabilities to outputs does not hide behind it.
 // The probabilities enter the second product as a high and a low 16-bit part: rounding them to
 // 16 bits once would add about as much error as rounding the output does.
-// The running maximum follows the scores only when one passes it by kSlack powers of two: until then the
-// probabilities are larger than 1, which costs no bits, and no lane needs another's maximum.
+// Probabilities are taken relative to a reference that follows the running maximum only when a score passes
+// it by Slack::kOver powers of two: until then they are larger, which costs no bits, and no lane needs another's
+// maximum.  fp16 has few exponents, so there the reference stays kLift powers of two below the maximum: what is lost
+// beneath fp16's smallest number is then at most 2^-36 of the largest key's weight a key, not 2^-25.
 //
 // Two ways to deal the work:
 //  - runs: the keys of every (sequence, key head) -- an item -- are cut into units; all units of all items
 //    lie end to end and every CTA takes an equal run of them, whatever the lengths are.  An item that ends up
-//    in several runs is joined by a second kernel from the parts (maximum, sum, unnormalised output) that
+//    in several runs is joined by a second kernel from the parts (reference, sum, unnormalised output) that
 //    they leave in the workspace; a run leaves two parts at most, so the workspace does not grow with the
 //    lengths.
 //  - clusters: an item is a cluster's, cut evenly over its CTAs, which join through distributed shared
@@ -52,7 +54,6 @@ namespace tgc {
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = kAttnWarps * 32;
 constexpr int kMaxCluster = 8;
-constexpr float kSlack = 8.0f;                // powers of two
 constexpr float kLn2 = 0.6931471805599453f;
 
 // The item that begins in a run and ends in a later one, `last`; -1: there is none.
@@ -76,7 +77,7 @@ struct AttnParams {
     int adv_pages, adv_tokens;  // a unit on: pages and places
     // workspace: parts (2 a run), and for each item the runs that share it
     float *part_out;   // (2 runs, R, D)
-    float2 *part_ml;   // (2 runs, R): maximum (log2 units), sum
+    float2 *part_ml;   // (2 runs, R): reference (log2 units), sum
     SplitItem *split;  // (runs)
 };
 
@@ -142,6 +143,13 @@ template <int DP>
 __device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
     return (uint32_t)(row * DP * 2 + ((chunk ^ (row & 7)) << 4));
 }
+
+// Powers of two: the reference is set kLift below the maximum, and again when that passes it by kOver (probabilities up
+// to 2^kOver then; fp16 ends at 2^16).
+template <bool F16>
+struct Slack {
+    static constexpr float kLift = F16 ? 11.0f : 0.0f, kOver = F16 ? 15.0f : 8.0f;
+};
 
 // DP: elements of a head, padded to 64, 128 or 256.  NT: query heads of an item, in eights.
 template <int DP, int NT>
@@ -539,7 +547,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnPa
                     float v = fmaxf(x[0][n][e], x[0][n][2 + e]);
                     if (MK == 2) v = fmaxf(v, fmaxf(x[MK - 1][n][e], x[MK - 1][n][2 + e]));
                     big[n][e] = v;
-                    past = past || v > top[n][e] + kSlack;
+                    past = past || v > top[n][e] + Slack<F16>::kOver;
                 }
             if (__any_sync(0xffffffffu, past)) {
 #pragma unroll
@@ -549,7 +557,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnPa
                         float v = big[n][e];
 #pragma unroll
                         for (int d = 4; d < 32; d *= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-                        v = fmaxf(top[n][e], v);
+                        v = fmaxf(top[n][e], v - Slack<F16>::kLift);
                         const float f = v == -INFINITY ? 1.0f : exp2_approx(top[n][e] - v);
                         top[n][e] = v;
                         sum[n][e] *= f;
