@@ -115,6 +115,11 @@ def test_attention_refusals(kw, rc):
     assert _attention(**kw) == rc
 
 
+def test_attention_wants_a_table_for_an_empty_pool():
+    """Lengths lead into the table whether or not its numbers can be pages."""
+    assert _attention(num_pages=0, k_pages=None, v_pages=None, table=None) == INV
+
+
 def _kv(name, **kw):
     pools = (ctypes.c_void_p * 2)(FAKE, 2 * FAKE)
     d = dict(refs=FAKE, table=FAKE, lens=FAKE, num_pages=9, page_size=16, num_seqs=3, max_pages=5, src=FAKE, dst=FAKE,

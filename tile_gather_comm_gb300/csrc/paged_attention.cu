@@ -905,8 +905,8 @@ static int attn_impl(tgc_paged_attention_args a) {
     TGC_TRY(attn_check(a));
     if (a.num_seqs == 0) return TGC_OK;
     if (a.q == nullptr || a.out == nullptr || a.lens == nullptr) return TGC_ERR_INVALID_ARG;
-    if (a.max_pages > 0 && a.num_pages > 0 && (a.table == nullptr || a.k_pages == nullptr || a.v_pages == nullptr))
-        return TGC_ERR_INVALID_ARG;
+    if (a.max_pages > 0 && a.table == nullptr) return TGC_ERR_INVALID_ARG;  // read whatever the pool holds
+    if (a.max_pages > 0 && a.num_pages > 0 && (a.k_pages == nullptr || a.v_pages == nullptr)) return TGC_ERR_INVALID_ARG;
     if (a.q == a.out && ((a.num_seqs > 1 && a.q_s != a.o_s) || (a.heads_q > 1 && a.q_h != a.o_h))) return TGC_ERR_INVALID_ARG;
     uintptr_t bits = 0;
     for (const void *v : {a.q, (const void *)a.out, a.k_pages, a.v_pages}) bits |= reinterpret_cast<uintptr_t>(v);
