@@ -876,6 +876,7 @@ typedef struct tgc_kv_append_args {
 int tgc_kv_append(const tgc_kv_append_args *args);
 
 #define TGC_ATTENTION_MAX_D 256
+#define TGC_ATTENTION_MAX_HEADS 65536  /* of q */
 
 /*
  * tgc_paged_attention -- attention of one new token of every sequence over its cached keys:
@@ -897,8 +898,8 @@ int tgc_kv_append(const tgc_kv_append_args *args);
  * behind a sequence's last key in its page is not read, whatever it holds; a value that is infinite
  * or NaN in range makes its column of out NaN.
  * scale      0 = 1 / sqrt(D).
- * Requirements: heads_q a multiple of heads_k, D <= TGC_ATTENTION_MAX_D (TGC_ERR_INVALID_ARG); TGC_BF16 or
- * TGC_F16 (TGC_ERR_DTYPE); D and every stride in whole 16 bytes, every pointer 16-byte aligned (lse, table,
+ * Requirements: heads_q a multiple of heads_k and at most TGC_ATTENTION_MAX_HEADS, D <= TGC_ATTENTION_MAX_D
+ * (TGC_ERR_INVALID_ARG); TGC_BF16 or TGC_F16 (TGC_ERR_DTYPE); D and every stride in whole 16 bytes, every pointer 16-byte aligned (lse, table,
  * lens: 4-byte) (TGC_ERR_ALIGN).  max_pages * page_size <= TGC_MAX_SIZE; num_seqs * heads_q < 2^31.
  * workspace  device memory of tgc_paged_attention_workspace_bytes() bytes, 128-byte aligned, for the
  *            parts of split sequences; no initialisation, meaningless after the call.  Calls that may run at

@@ -41,7 +41,7 @@ def test_ctypes_structs_match_the_header(cls, cname, tmp_path):
 
 def test_constants_match_the_header():
     text = open(os.path.join(ROOT, "include", "tgc.h"), encoding="utf-8").read()
-    for name in ("ROPE_MAX_D", "ROPE_MAX_HEADS", "ATTENTION_MAX_D", "KV_MAX_POOLS"):
+    for name in ("ROPE_MAX_D", "ROPE_MAX_HEADS", "ATTENTION_MAX_D", "ATTENTION_MAX_HEADS", "KV_MAX_POOLS"):
         assert f"#define TGC_{name} {getattr(_lib, name)}" in text
     for name, v in _lib.ROPE_LAYOUTS.items():
         assert f"TGC_ROPE_{name.upper()} = {v}" in text
@@ -113,6 +113,11 @@ def _attention(**kw):
 ])
 def test_attention_refusals(kw, rc):
     assert _attention(**kw) == rc
+
+
+def test_attention_refuses_more_heads_than_its_indices_hold():
+    for heads in (65537, 1 << 26):  # times D / 2: past 32 bits
+        assert _attention(heads_q=heads, heads_k=1, D=256, num_seqs=1) == INV
 
 
 def test_attention_wants_a_table_for_an_empty_pool():

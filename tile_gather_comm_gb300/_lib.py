@@ -45,6 +45,7 @@ ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 ROPE_MAX_D = 1024              # TGC_ROPE_MAX_D
 ROPE_MAX_HEADS = 65536         # TGC_ROPE_MAX_HEADS
 ATTENTION_MAX_D = 256          # TGC_ATTENTION_MAX_D
+ATTENTION_MAX_HEADS = 65536    # TGC_ATTENTION_MAX_HEADS
 KV_MAX_POOLS = 256             # TGC_KV_MAX_POOLS
 MAX_RANKS = 64
 TRACE_WORDS = 16

@@ -830,7 +830,7 @@ static int attn_check(tgc_paged_attention_args &a) {
     if (a.num_seqs < 0 || a.heads_q < 1 || a.heads_k < 1 || a.heads_q % a.heads_k != 0 || a.D < 1 ||
         a.D > TGC_ATTENTION_MAX_D)
         return TGC_ERR_INVALID_ARG;
-    if (a.heads_q > TGC_MAX_SIZE || (a.num_seqs > 0 && a.heads_q > TGC_MAX_SIZE / a.num_seqs)) return TGC_ERR_INVALID_ARG;
+    if (a.heads_q > TGC_ATTENTION_MAX_HEADS || (a.num_seqs > 0 && a.heads_q > TGC_MAX_SIZE / a.num_seqs)) return TGC_ERR_INVALID_ARG;
     if (a.window < 0 || !std::isfinite(a.scale) || !std::isfinite(a.softcap) || a.softcap < 0.0f) return TGC_ERR_INVALID_ARG;
     TGC_TRY(kv_table_check(a.num_pages, a.page_size, a.num_seqs, a.max_pages, &a.table_ld));
     TGC_TRY(kv_pages_check(a.num_pages, a.page_size, a.heads_k, a.D, &a.page_s, &a.token_s, &a.head_s));
