@@ -152,6 +152,23 @@ def test_many_pages_and_entries():
     c.same()
 
 
+@pytest.mark.parametrize("n", [4, 1100])
+def test_the_most_pages(n):
+    """2^31 - 4096 pages, all but four of them taken: those are found, at the start and the end, and the entry that
+    wants more makes the search run to the pool's very end."""
+    pages = 2 ** 31 - 4096
+    ints = dict(device="cuda", dtype=torch.int32)
+    refs, table, lens = torch.ones(pages, **ints), torch.full((4, 4), -1, **ints), torch.zeros(4, **ints)
+    refs[5] = 0
+    refs[-3:] = 0
+    seqs, add = torch.full((n,), -1, **ints), torch.zeros(n, **ints)
+    seqs[:3], add[:3], ok = torch.tensor([0, 1, 2], **ints), torch.tensor([2, 2, 1], **ints), torch.full((n,), -1, **ints)
+    tgc.tgc_kv_reserve(refs, table, lens, seqs, add, 1, ok=ok)
+    assert table[:, :2].tolist() == [[5, pages - 3], [pages - 2, pages - 1], [-1, -1], [-1, -1]]
+    assert ok.tolist() == [1, 1] + [0] * (n - 2) and lens.tolist() == [2, 2, 0, 0]
+    assert bool((refs == 1).all())
+
+
 @pytest.mark.parametrize("page_bytes", [16, 48, 512, 4096, 4112, 40960])
 @pytest.mark.parametrize("npools", [1, 5, 256])
 def test_copy(page_bytes, npools):
@@ -207,6 +224,50 @@ def test_streams_and_graphs():
         graph.replay()
     assert c.lens.tolist()[:2] == [18, 14] and ok.tolist() == [1, 1]
     assert int((c.table >= 0).sum()) == 5 + 4 and int(c.refs.sum()) == 9
+
+
+def test_every_call_on_another_stream_and_captured():
+    """Reserve, free, fork, compact and a copy: the same on the current stream, on another one and replayed, each time
+    from the same cache, and the model's."""
+    caches = [Cache(600, 40, 20, 4, npools=3, width=16, seed=4) for _ in range(3)]
+    rng = random.Random(4)
+    adds, gone = [rng.randrange(60) for _ in range(40)], rng.sample(range(40), 15)
+    add2 = [rng.randrange(9) for _ in range(40)]
+    lists = {k: caches[0].ints(v) for k, v in dict(seqs=list(range(40)), adds=adds, gone=gone, src=[s for s in range(40) if s not in gone][:15],
+                                                  add2=add2, a=[0, 1, 2], b=[597, 598, 599]).items()}
+    side = torch.cuda.Stream()
+
+    def work(c, **on):
+        own = (lambda n: dict(workspace=torch.empty(n, device="cuda", dtype=torch.uint8))) if on.pop("captured", False) else (lambda n: {})
+        grow = (c.refs, c.table, c.lens, lists["seqs"], lists["adds"], 4)
+        tgc.tgc_kv_reserve(*grow, **on, **own(1 << 20))
+        tgc.tgc_kv_free(c.refs, c.table, c.lens, lists["gone"], **on)
+        tgc.tgc_kv_fork(c.pools, c.refs, c.table, c.lens, lists["src"], lists["gone"], 4, **on, **own(1 << 20))
+        tgc.tgc_kv_reserve(c.refs, c.table, c.lens, lists["seqs"], lists["add2"], 4, **on, **own(1 << 20))
+        tgc.tgc_kv_compact(c.pools, c.refs, c.table, **on, **own(1 << 20))
+        tgc.tgc_kv_copy(c.pools, c.pools, lists["b"], lists["a"], **on)
+
+    work(caches[0])
+    torch.cuda.synchronize()
+    work(caches[1], stream=side)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        work(caches[2], captured=True)
+    graph.replay()
+    torch.cuda.synchronize()
+    c = caches[0]
+    for o in caches[1:]:
+        assert torch.equal(c.refs, o.refs) and torch.equal(c.table, o.table) and torch.equal(c.lens, o.lens)
+        assert all(torch.equal(x, y) for x, y in zip(c.pools, o.pools))
+    m = Cache(600, 40, 20, 4, npools=3, width=16, seed=4)
+    m.reserve(list(range(40)), adds)
+    m.free(gone)
+    m.fork([s for s in range(40) if s not in gone][:15], gone)
+    m.reserve(list(range(40)), add2)
+    m.compact()
+    m.same()
+    assert torch.equal(m.table, c.table) and torch.equal(m.lens, c.lens) and torch.equal(m.refs, c.refs)
 
 
 def test_the_binding_refuses():

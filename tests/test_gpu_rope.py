@@ -215,6 +215,43 @@ def test_the_most_heads_and_none():
     assert bool((kp == 7).all())
 
 
+def test_another_stream_and_a_graph():
+    """Rotation, its gradients and appending on another stream and replayed from a graph: the same bits."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    ints = dict(device="cuda", dtype=torch.int32)
+    T, H, K, D = 37, 6, 2, 64
+    rows = torch.randn(T, H + 2 * K, D, generator=g, device="cuda").bfloat16()
+    pos, seqs = torch.randint(0, 60, (T,), generator=g, **ints), torch.arange(T, **ints)
+    table = torch.randperm(T * 4, generator=g, device="cuda").to(torch.int32).view(T, 4)
+    freqs, _ = tgc.tgc_rope_freqs(D, device="cuda")
+
+    def work(stream=None):
+        o = [torch.zeros(T, H, D, device="cuda", dtype=torch.bfloat16) for _ in range(3)]
+        pools = [torch.zeros(T * 4, 16, K, D, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+        here = torch.cuda.current_stream()
+        if stream is not None:
+            stream.wait_stream(here)
+        on = {} if stream is None else dict(stream=stream)
+        tgc.tgc_rope(rows[:, :H], o[0], pos, freqs, **on)
+        tgc.tgc_rope_bwd(o[0], o[1], pos, freqs, **on)
+        tgc.tgc_kv_append(rows[:, H:H + K], rows[:, H + K:], *pools, table, pos, seqs=seqs, q=rows[:, :H], q_out=o[2], freqs=freqs, **on)
+        if stream is not None:
+            here.wait_stream(stream)
+        return o + pools
+
+    want = work()
+    assert torch.equal(want[0], want[2]) and bool(want[3].any())
+    for a, b in zip(want, work(torch.cuda.Stream())):
+        assert torch.equal(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = work()
+    for _ in range(2):
+        graph.replay()
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
+
+
 def test_a_far_page_of_a_large_pool():
     """Pages more than 2^31 elements from the pool's start."""
     D, Hk, page = 128, 8, 64

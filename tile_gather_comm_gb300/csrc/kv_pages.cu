@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kSegThreads) grant_kernel(const KvParams p) {
             if (used >> i & 1u) continue;
             int lo = 0, hi = p.n - 1;  // the first entry with upto > rank
             while (lo < hi) {
-                const int mid = (lo + hi) / 2;
+                const int mid = lo + (hi - lo) / 2;
                 if (p.w.upto[mid] > rank) hi = mid;
                 else lo = mid + 1;
             }
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kSegThreads) grant_kernel(const KvParams p) {
     }
     // a warp an entry
     const int warps = (int)gridDim.x * (kSegThreads / 32), lane = (int)threadIdx.x % 32;
-    for (int e = (int)blockIdx.x * (kSegThreads / 32) + (int)threadIdx.x / 32; e < p.n; e += warps) {
+    for (int64_t e = (int64_t)blockIdx.x * (kSegThreads / 32) + threadIdx.x / 32; e < p.n; e += warps) {
         const bool good = p.w.flag[e] != 0 && p.w.upto[e] <= free;
         if (lane == 0 && p.ok != nullptr) p.ok[e] = good;
         if (!good) continue;
@@ -332,8 +332,9 @@ __global__ void __launch_bounds__(kGrowThreads) grow_kernel(const KvParams p) {
         if (r < rank) before += c;
         total += c;
     }
-    for (int base = page0; base < page1 && before < asked; base += kGrowThreads * kGrowEach) {
-        const int first = base + tid * kGrowEach;
+    // 64 bits: the step past the last pages of the largest pool leaves 32
+    for (int64_t base = page0; base < page1 && before < asked; base += kGrowThreads * kGrowEach) {
+        const int64_t first = base + tid * kGrowEach;
         unsigned bits = 0;
 #pragma unroll
         for (int i = 0; i < kGrowEach; ++i)
@@ -349,7 +350,7 @@ __global__ void __launch_bounds__(kGrowThreads) grow_kernel(const KvParams p) {
                 else lo = mid + 1;
             }
             if (s_upto[lo] > total) continue;
-            const int page = first + __ffs(bits) - 1;
+            const int page = (int)first + __ffs(bits) - 1;
             p.table[s_dst[lo] * p.kv.ld + s_have[lo] + (order - (lo > 0 ? s_upto[lo - 1] : 0))] = page;
             p.refs[page] = 1;
             if (FORK) p.w.to[lo] = page;
