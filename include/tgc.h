@@ -965,7 +965,8 @@ size_t tgc_paged_attention_workspace_bytes(const tgc_paged_attention_args *args)
  * num_pages, num_seqs * max_pages and max_pages * page_size at most TGC_MAX_SIZE; n at most TGC_MAX_SIZE.
  * Errors: TGC_ERR_INVALID_ARG, TGC_ERR_ALIGN, TGC_ERR_WORKSPACE.  n == 0 returns TGC_OK.
  * workspace  (reserve, fork, compact) device memory of tgc_kv_workspace_bytes() bytes, 128-byte aligned, no
- *            initialisation.  Asynchronous on `stream`.
+ *            initialisation, meaningless after the call.  Calls that may run at the same time (on caches of
+ *            their own) need one each.  Asynchronous on `stream`.
  */
 typedef struct tgc_kv_args {
     int32_t *refs;
