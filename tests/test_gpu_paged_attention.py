@@ -96,7 +96,13 @@ WIDE = [([20000, 300], 1, 16, 128, 16), ([9000, 1, 8000], 2, 32, 96, 24), ([700,
         ([130, 0, 257] * 60, 1, 40, 200, 5), ([25000], 1, 33, 128, 64), ([1, 2, 3] * 110, 1, 20, 8, 1)]
 
 
-@pytest.mark.parametrize("lens,Hk,group,D,page", CASES + WIDE)
+# many items of key heads by fours
+FOURS = [([1] * 200, 4, 1, 64, 1), ([700, 5, 0, 33, 32, 31, 64] * 12, 4, 3, 40, 16), ([1, 2, 15, 16, 17] * 30, 8, 8, 128, 5),
+         ([6000, 1, 9000, 16] * 4, 16, 1, 64, 24), ([0, 0, 3000] * 11, 4, 8, 120, 16), ([257, 0, 1000] * 6, 12, 5, 72, 7),
+         ([50] * 170, 32, 1, 8, 64), ([20000, 3, 1200, 7] * 8, 4, 4, 128, 64), ([0] * 60 + [900] * 4 + [0] * 60, 8, 2, 96, 16)]
+
+
+@pytest.mark.parametrize("lens,Hk,group,D,page", CASES + WIDE + FOURS)
 @pytest.mark.parametrize("dtype", list(DT))
 @pytest.mark.parametrize("window,cap", [(0, 0.0), (100, 0.0), (37, 5.0)])
 def test_attention(lens, Hk, group, D, page, dtype, window, cap):
@@ -189,6 +195,28 @@ def test_bad_pages_and_lengths():
     lens[0] = 2 ** 31 - 1
     tgc.tgc_paged_attention(q[:1], out[:1], kp, vp, table, lens)
     check(out[:1], None, q[:1], keys, D ** -0.5)
+
+
+def test_bad_pages_of_many_sequences():
+    """The same where every warp has a key head of its own, heads and tokens in either order."""
+    g = gen(14)
+    Hk, group, D, page = 8, 3, 64, 16
+    for heads_first in (False, True):
+        lens = [(s * 53) % 400 for s in range(48)]
+        kp, vp, table, n, keys = cache(lens, page, Hk, D, torch.bfloat16, g, heads_first=heads_first)
+        q = torch.randn(48, Hk * group, D, generator=g, device="cuda").bfloat16()
+        bad = torch.rand(table.shape, generator=g, device="cuda") < 0.3
+        table[bad] = torch.tensor([-1, kp.shape[0], 2 ** 31 - 1, -(2 ** 31)], device="cuda", dtype=torch.int32)[
+            torch.randint(0, 4, (int(bad.sum()),), generator=g, device="cuda")]
+        out, lse = torch.full_like(q, 7.0), torch.full((48, Hk * group), 7.0, device="cuda")
+        tgc.tgc_paged_attention(q, out, kp, vp, table, n, lse=lse)
+        for s in range(48):
+            gone = bad[s].repeat_interleave(page)[:lens[s]]
+            want, want_lse, tol, tol_lse = expect(q[s], keys[s], D ** -0.5, gone=gone)
+            assert bool(((out[s].double() - want).abs() <= tol + 2 ** -8 * (want.abs() + tol)).all()), s
+            assert torch.equal(torch.isinf(lse[s]), torch.isinf(want_lse))
+            live = ~torch.isinf(want_lse)
+            assert bool(((lse[s].double() - want_lse).abs()[live] <= tol_lse[live]).all()), s
 
 
 def test_nothing_to_attend_to():

@@ -5,9 +5,9 @@
 // Every key and value is read once and used for the G query heads that share it: 4 G flops for 4
 // bytes, so HBM is the bound and the design is about keeping loads in flight.
 //
-// A CTA's 4 warps work for themselves: of each unit of keys a warp takes its quarter (a step), copies it
-// with cp.async into its own ring of slots, and keeps its own running maximum, sum and output in
-// registers; they meet at an item's end.  No barrier in the loop; a page may end anywhere, as each key
+// A CTA's 4 warps work for themselves: of each unit of keys a warp takes its quarter, or all of its own
+// head (a step), copies it with cp.async into its own ring of slots, and keeps its own reference, sum and
+// output in registers; where they share an item, they meet at its end.  No barrier in the loop; a page may end anywhere, as each key
 // finds its own page.  The copies run ahead of the products across the end of an item, so they do not
 // pause while the warps meet.
 //
@@ -34,6 +34,8 @@
 //    in several runs is joined by a second kernel from the parts (reference, sum, unnormalised output) that
 //    they leave in the workspace; a run leaves two parts at most, so the workspace does not grow with the
 //    lengths.
+//    An item is a key head, whose keys the 4 warps share, or (own runs) 4 key heads side by side, one a warp: rows 4 times as
+//    long for the copies, no meeting of warps, no barrier at all, but 4 times the parts where items are split.
 //  - clusters: an item is a cluster's, cut evenly over its CTAs, which join through distributed shared
 //    memory: one launch and no workspace, for calls with few and short items (attn_plan says which).
 // Both read the lengths on the device.
@@ -75,9 +77,9 @@ struct AttnParams {
     int window;
     int cluster;  // CTAs of a cluster
     int adv_pages, adv_tokens;  // a unit on: pages and places
-    // workspace: parts (2 a run), and for each item the runs that share it
-    float *part_out;   // (2 runs, R, D)
-    float2 *part_ml;   // (2 runs, R): reference (log2 units), sum
+    // workspace: parts (2 a run, of 4 heads with own runs), and for each item the runs that share it
+    float *part_out;   // (2 runs, 1 or 4, R, D)
+    float2 *part_ml;   // (2 runs, 1 or 4, R): reference (log2 units), sum
     SplitItem *split;  // (runs)
 };
 
@@ -173,6 +175,8 @@ struct AttnShape {
     // loads of their own would queue behind those at every item's start (0: no room beside the rings, loads).
     static constexpr int kQueries = (DP == 128 && NT == 4) || (DP == 256 && NT == 2) ? 0 : kRows * DP * 2;
     static constexpr int kSmem = kRings + 3 * kQueries;
+    // With a key head a warp: the queries of two items of each warp, as those of the one in work are in registers.
+    static constexpr int kOwnSmem = kRings + 2 * kAttnWarps * kRows * DP * 2;
     // Outputs of so many heads fit a slot; more take turns.
     static constexpr int kRound = kRows * DP * 4 <= kSlot ? kRows : kSlot / (DP * 4);
     // Where a CTA of a cluster that took `steps` steps leaves its part of the heads from r0 on: not in the slot where its
@@ -181,6 +185,15 @@ struct AttnShape {
         return r0 / kRound * kWarpRing + (last_slot(steps) + 1) % kStages * kSlot;
     }
 };
+
+// How the work is dealt: see the top.
+enum AttnForm { kRuns, kOwnRuns, kClusters };
+// Shapes whose queries fit beside the rings, two CTAs an SM; with 16 heads a key (x 64) the products are the bound, and 43.6 and
+// 43.1 us the same (200 x 1000 tokens).
+template <int DP, int NT>
+constexpr bool kOwnFits = DP <= 128 && NT == 1;
+static_assert(AttnShape<128, 1>::kOwnSmem <= 112 * 1024 && AttnShape<64, 1>::kOwnSmem <= 112 * 1024, "two CTAs an SM");
+
 static_assert(AttnShape<128, 4>::kRound == 16 && AttnShape<64, 4>::kRound == 32 && AttnShape<256, 2>::kRound == 8, "whole eights");
 
 // Where a run stands: its place in the row of all units, and the item there.
@@ -252,15 +265,18 @@ __device__ __forceinline__ void store_out(const AttnParams &p, int seq, int head
     if (c == 0) store_lse(p, seq, head, m, l);
 }
 
-template <bool F16, int DP, int NT, bool CLUSTER>
+template <bool F16, int DP, int NT, AttnForm FORM>
 __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnParams p) {
     using S = AttnShape<DP, NT>;
+    constexpr bool CLUSTER = FORM == kClusters, OWN = FORM == kOwnRuns;
+    constexpr int UNIT = OWN ? S::kKeys : S::kUnit, ITEMS = OWN ? kAttnWarps : 1;  // keys of a unit; key heads (or parts of their groups) of an item
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t s_sum[kAttnWarps];
     __shared__ RunAt s_cur;  // where the products stand: one copy, so that all warps meet at the same items
     __shared__ uint32_t s_mask[kAttnWarps][S::kStages];
     __shared__ float2 s_ml[kAttnWarps][S::kRows];
     __shared__ float2 s_cta_ml[S::kRows];
+    __shared__ int3 s_items[kAttnWarps][4];  // OWN: sequence, item and units of those that the copies have entered last
     const int tid = (int)threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane >> 2, t4 = lane & 3;
     uint8_t *const ring = smem + warp * S::kWarpRing;
     const uint32_t ring_at = smem_addr(ring);
@@ -277,7 +293,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnPa
     stream_release();
 
     // ---- this CTA's run
-    const int heads = p.heads_k * p.row_blocks;  // items of a sequence
+    const int heads = p.heads_k * p.row_blocks / ITEMS;  // items of a sequence
     int64_t stop = 0, per = 0;                   // end of the run; units of a run
     RunAt r{};                                   // where the copies stand
     int rank = 0, ranks = 1;
@@ -290,14 +306,14 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnPa
         const KeyRange k = key_range(p, r.seq);
         r.begin = k.begin;
         r.end = k.end;
-        r.units = units_of<S::kUnit>(k);
+        r.units = units_of<UNIT>(k);
         const int each = (r.units + ranks - 1) / ranks;
         r.unit = each * rank < r.units ? each * rank : r.units;
         r.at = r.unit;
         stop = r.unit + each < r.units ? r.unit + each : r.units;
     } else {
         int64_t mine = 0, total = 0;
-        for (int s = tid; s < p.kv.num_seqs; s += kAttnThreads) mine += units_of<S::kUnit>(key_range(p, s));
+        for (int s = tid; s < p.kv.num_seqs; s += kAttnThreads) mine += units_of<UNIT>(key_range(p, s));
 #pragma unroll
         for (int d = 16; d > 0; d /= 2) mine += __shfl_xor_sync(0xffffffffu, mine, d);
         if (lane == 0) s_sum[warp] = mine;
@@ -308,7 +324,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnPa
         per = quotient(total + gridDim.x - 1, gridDim.x);
         // Sequences without keys: zeros.
         for (int s = (int)blockIdx.x; s < p.kv.num_seqs; s += (int)gridDim.x) {
-            if (units_of<S::kUnit>(key_range(p, s)) != 0) continue;
+            if (units_of<UNIT>(key_range(p, s)) != 0) continue;
             for (int i = tid; i < p.heads_q * (p.D / 2); i += kAttnThreads)
                 store_out<F16>(p, s, i / (p.D / 2), i % (p.D / 2) * 2, 0.0f, 0.0f, make_float2(0.0f, 0.0f));
         }
@@ -316,13 +332,13 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnPa
         const int run = (int)blockIdx.x;
         if (per * run >= total) return;
         stop = per * (run + 1) < total ? per * (run + 1) : total;
-        if (!seek<S::kUnit>(p, r, per * run, heads, lane)) r.at = stop;
+        if (!seek<UNIT>(p, r, per * run, heads, lane)) r.at = stop;
     }
 
     // ---- the warp's copies: a lane finds the page of a key of the step, all lanes copy.  Pages are looked up kAhead units
     // before their copies: a load queues behind the copies under way, about two units' worth.
     constexpr int kAhead = 3;
-    const int my_key = warp * S::kKeys + lane % S::kKeys;
+    const int my_key = (OWN ? 0 : warp * S::kKeys) + lane % S::kKeys;
     int key = 0, page_i = 0, look = 0;   // of the unit to be looked up next, with its place in the page
     int page[kAhead], place = 0;         // of the units to be copied next; of the first of them
     int64_t head_off = 0;
@@ -336,26 +352,34 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnPa
 #pragma unroll
         for (int i = 1; i < kAhead; ++i) page[i - 1] = page[i];
         page[kAhead - 1] = key < r.end ? p.kv.page_at(p.table, r.seq, page_i) : -1;
-        key += S::kUnit;
+        key += UNIT;
         page_i += p.adv_pages + (past(look) ? 1 : 0);
     };
-    int items = 0;       // that the copies have entered
+    int items = 0;       // whose queries are copied
+    int entered = 0;     // that the copies have entered
     bool fresh = false;  // nothing of the item is copied yet
     auto enter_item = [&] {
-        key = r.begin + r.unit * S::kUnit + my_key;
+        // OWN: the products are at most three items behind
+        if (OWN && lane == 0) s_items[warp][entered % 4] = make_int3(r.seq, r.item, r.units);
+        ++entered;
+        key = r.begin + r.unit * UNIT + my_key;
         page_i = key / p.kv.page_size;
         look = place = key - page_i * p.kv.page_size;
-        head_off = (int64_t)(r.item / p.row_blocks) * p.head_s;
+        head_off = (int64_t)((OWN ? r.item * ITEMS + warp : r.item) / p.row_blocks) * p.head_s;
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) look_up();
         fresh = true;
     };
     // The item's queries, a share a warp, with the copies of its first unit: two units ahead of the products, so in the
     // place of an item that all warps are done with.
+    constexpr int kQueries = OWN ? S::kRows * DP * 2 : S::kQueries;
+    auto queries_of = [&](int item) {  // the item's number in the run
+        return smem_addr(smem + S::kRings) + (uint32_t)((OWN ? warp * 2 + item % 2 : item % 3) * kQueries);
+    };
     auto copy_queries = [&] {
-        const int head_k = r.item / p.row_blocks, row0 = r.item % p.row_blocks * S::kRows;
-        const uint32_t to = smem_addr(smem + S::kRings) + (uint32_t)(items % 3 * S::kQueries);
-        for (int i = tid; i < S::kRows * (DP / 8); i += kAttnThreads) {
+        const int item = OWN ? r.item * ITEMS + warp : r.item, head_k = item / p.row_blocks, row0 = item % p.row_blocks * S::kRows;
+        const uint32_t to = queries_of(items);
+        for (int i = OWN ? lane : tid; i < S::kRows * (DP / 8); i += OWN ? 32 : kAttnThreads) {
             const int row = i / (DP / 8), ch = i % (DP / 8);
             const bool there = row0 + row < p.group && ch < chunks;
             cp_async16(to + chunk_at<DP>(row, ch),
@@ -366,18 +390,18 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnPa
         fresh = false;
     };
     if (r.at < stop) enter_item();
-    if (!CLUSTER) {
+    if (FORM == kRuns) {
         if (tid == 0) s_cur = r;
         __syncthreads();
     }
-    RunAt c = CLUSTER ? r : s_cur;
+    RunAt c = FORM == kRuns ? s_cur : r;
     // The next sequence that has keys; none only where the lengths change under the call.
     auto next_seq = [&](RunAt &w) {
         while (++w.seq < p.kv.num_seqs) {
             const KeyRange k = key_range(p, w.seq);
             w.begin = k.begin;
             w.end = k.end;
-            w.units = units_of<S::kUnit>(k);
+            w.units = units_of<UNIT>(k);
             if (w.units > 0) return true;
         }
         return false;
@@ -395,7 +419,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnPa
     auto copy_keys = [&](int unit) {  // the unit's number in the run
         off = -1;
         if (r.at < stop) {
-            if (S::kQueries > 0 && fresh) copy_queries();
+            if (kQueries > 0 && fresh) copy_queries();
             if (page[0] >= 0) off = page[0] * p.page_s + place * p.token_s + head_off;
             const uint32_t have = __ballot_sync(0xffffffffu, off >= 0);
             if (lane == 0) s_mask[warp][unit % S::kStages] = have;
@@ -433,19 +457,28 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnPa
     constexpr int kBehind = S::kAlone ? 2 : 1;  // groups that may be under way while the next one's data are used
 
     int step = 0, done = 0;  // steps, items
-    while (CLUSTER || c.at < stop) {
-        const int head_k = c.item / p.row_blocks, row0 = c.item % p.row_blocks * S::kRows;
+    while (CLUSTER || (OWN ? done < entered : c.at < stop)) {
+        if constexpr (OWN) {
+            __syncwarp();
+            const int3 it = s_items[warp][done % 4];
+            c.seq = it.x;
+            c.item = it.y;
+            c.units = it.z;
+        }
+        const int my_item = OWN ? c.item * ITEMS + warp : c.item;
+        const int head_k = my_item / p.row_blocks, row0 = my_item % p.row_blocks * S::kRows;
         const int rows = p.group - row0 < S::kRows ? p.group - row0 : S::kRows;
         const int head0 = head_k * p.group + row0;
         const int todo = (int)(stop - c.at < c.units - c.unit ? stop - c.at : c.units - c.unit);
 
         // queries as the first product's right operand: lane (g, t4) has elements 2 t4, 2 t4 + 1 of every 8 of head g
         uint32_t qf[NT][DP / 16][2];
-        if constexpr (S::kQueries > 0) {
+        if constexpr (kQueries > 0) {
             if (CLUSTER && todo <= 0) cp_async_wait<0>();
             else cp_async_wait<kBehind>();
-            __syncthreads();
-            const uint32_t q_at = smem_addr(smem + S::kRings) + (uint32_t)(done % 3 * S::kQueries);
+            if constexpr (OWN) __syncwarp();
+            else __syncthreads();
+            const uint32_t q_at = queries_of(done);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -610,7 +643,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnPa
             }
         }
 
-        // ---- the warps' parts meet: each in the slot that it used last, which its copies have not reached again
+        // ---- the item's end, in the slot that each warp used last, which its copies have not reached again
         const int last = S::last_slot(step);
         auto part_of = [&](int w) { return reinterpret_cast<float *>(smem + w * S::kWarpRing + last * S::kSlot); };
         // heads' rows of DP; pairs of heads turned against one another, so that a warp's stores meet every bank once
@@ -624,11 +657,43 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnPa
                 for (int d = 4; d < 32; d *= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
                 if (g == 0) s_ml[warp][n * 8 + t4 * 2 + e] = make_float2(top[n][e], l);
             }
-        const int64_t item_begin = c.at - c.unit;
+        const int64_t item_begin = c.at - c.unit;  // OWN: a warp's output is whole, and only stored by rows
         const bool whole = CLUSTER ? ranks == 1 : c.unit == 0 && todo == c.units;
         const int part = 2 * (int)blockIdx.x + (c.unit > 0 ? 0 : 1);
         if (!CLUSTER && tid == 0 && c.unit == 0 && !whole)  // the item begins here and goes on in later runs
             p.split[blockIdx.x] = SplitItem{c.seq, c.item, min((int)quotient(item_begin + c.units - 1, per), (int)gridDim.x - 1)};
+        if constexpr (OWN) {
+            __syncwarp();
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n * 8 + t4 * 2 + (e & 1) < rows)
+#pragma unroll
+                        for (int j = 0; j < DP / 16; ++j)
+                            part_of(warp)[place_of(n * 8 + t4 * 2 + (e & 1), j * 16 + g + (e >> 1) * 8)] = acc[j][n][e];
+            __syncwarp();
+            for (int i = lane; i < rows * (DP / 4); i += 32) {
+                const int row = i / (DP / 4), d = i % (DP / 4) * 4;
+                if (d >= p.D) continue;
+                const float2 ml = s_ml[warp][row];
+                const float4 v = *reinterpret_cast<const float4 *>(part_of(warp) + place_of(row, d));
+                if (whole) {
+                    const F2 inv = every<F2>(ml.y == 0.0f ? 0.0f : 1.0f / ml.y);
+                    if (d == 0) store_lse(p, c.seq, head0 + row, ml.x, ml.y);
+                    store_four<F16>(p, c.seq, head0 + row, d, mul(f2(v.x, v.y), inv), mul(f2(v.z, v.w), inv));
+                } else {
+                    const int64_t at = (int64_t)(part * ITEMS + warp) * S::kRows + row;
+                    if (d == 0) p.part_ml[at] = ml;
+                    *reinterpret_cast<float4 *>(p.part_out + at * p.D + d) = v;
+                }
+            }
+            __syncwarp();
+            clear_tail(last);
+            c.at += todo;
+            c.unit = 0;
+            continue;
+        }
 #pragma unroll
         for (int r0 = 0; r0 < S::kRows; r0 += S::kRound) {
             __syncwarp();
@@ -747,7 +812,7 @@ constexpr int kJoinThreads = kJoinRows * kJoinWarps * 32;
 constexpr int kJoinDeep = 4;
 
 template <bool F16, int VEC>  // VEC: float2 a lane, 1, 2 or 4 for D up to 64, 128 or 256
-__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnParams p, const int part_rows) {
+__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnParams p, const int part_rows, const int own) {
     __shared__ float2 s_ml[kJoinRows][kJoinWarps];
     __shared__ float2 s_out[kJoinRows][kJoinWarps][VEC * 32];
     stream_wait();
@@ -757,9 +822,11 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
     const int first = (int)blockIdx.x, last = it.last;
     const int mine = (int)threadIdx.x / (kJoinWarps * 32), tid = (int)threadIdx.x % (kJoinWarps * 32);
     const int warp = tid / 32, lane = tid % 32;
-    const int row0 = it.item % p.row_blocks * part_rows, row = (int)blockIdx.y * kJoinRows + mine;
+    // kOwnRuns: an item is `own` of what is one elsewhere
+    const int item = it.item * own + (int)blockIdx.z;
+    const int row0 = item % p.row_blocks * part_rows, row = (int)blockIdx.y * kJoinRows + mine;
     const bool live = row < part_rows && row0 + row < p.group;
-    const int seq = it.seq, head = it.item / p.row_blocks * p.group + row0 + row;
+    const int seq = it.seq, head = item / p.row_blocks * p.group + row0 + row;
     float m = -INFINITY, l = 0.0f;
     float2 o[VEC];
 #pragma unroll
@@ -772,7 +839,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
             ml[u] = make_float2(-INFINITY, 0.0f);
             if (run > last) continue;
             // the first run's part is in its second place, the others' in their first
-            const int64_t at = (int64_t)(2 * run + (run == first ? 1 : 0)) * part_rows + row;
+            const int64_t at = ((int64_t)(2 * run + (run == first ? 1 : 0)) * own + (int)blockIdx.z) * part_rows + row;
             ml[u] = p.part_ml[at];
 #pragma unroll
             for (int j = 0; j < VEC; ++j)
@@ -841,6 +908,7 @@ static int attn_check(tgc_paged_attention_args &a) {
 
 struct AttnPlan {
     int dp, nt, row_blocks, unit, grid, cluster;  // cluster: 0 where the work is dealt in runs
+    int own;                                      // key heads of an item of kOwnRuns, 1 otherwise
     int64_t items;
     size_t ml_off, split_off, total;
 };
@@ -851,10 +919,14 @@ struct AttnPlan {
 // more than a run would have; runs otherwise.  With 8 heads of 128 x 4 a key, clusters and runs take 5.8 and 7.7 us for
 // 200 tokens, 7.6 and 8.4 for 900, 9.6 and 9.3 for 2000, 13.6 and 11.6 for 4000 (8 units where a run has 2), 13.9 and 15.7 for
 // 16 x 1000 (8 and 7), 12.0 and 18.3 for 32 x 500.  Runs: one for each of two CTAs an SM, no more than there can be units.
+// Own runs from as many items on as a head has elements (the parts grow with those): 64 x 8192 tokens, 8 x 4 heads x 128, 192.5
+// against 200.9 us, 16 x 4000 34.8 and 39.9, 8 x 20000 the same 75, 1 x 32000 38.0 and 33.4; 48 x 2000 of 5000, 16 heads x 64,
+// 63.7 and 72.1, 64 x 4000 101.5 and 121.7, 8 x 30000 of 8 heads 58.2 and 64.3.
 constexpr int kClusterUnits = 16, kClusterBehind = 3;
 
 static AttnPlan attn_plan(const tgc_paged_attention_args &a, int sms) {
     AttnPlan q{};
+    q.own = 1;
     const int64_t group = a.heads_q / a.heads_k;
     q.dp = a.D <= 64 ? 64 : a.D <= 128 ? 128 : 256;
     q.unit = q.dp == 64 ? AttnShape<64, 1>::kUnit : AttnShape<128, 1>::kUnit;
@@ -874,31 +946,38 @@ static AttnPlan attn_plan(const tgc_paged_attention_args &a, int sms) {
     }
     const int64_t runs = q.items * units;
     q.grid = (int)(runs < 1 ? 1 : runs < room ? runs : room);
+    if (q.dp <= 128 && q.nt == 1 && a.heads_k % kAttnWarps == 0 && q.items >= q.dp) {
+        q.own = kAttnWarps;
+        q.unit /= kAttnWarps;
+    }
     auto up = [](size_t v) { return (v + 127) / 128 * 128; };
-    const size_t rows = (size_t)2 * q.grid * 8 * q.nt;
+    const size_t rows = (size_t)2 * q.grid * q.own * 8 * q.nt;
     q.ml_off = up(rows * (size_t)a.D * 4);
     q.split_off = q.ml_off + up(rows * 8);
     q.total = q.split_off + up((size_t)q.grid * sizeof(SplitItem));
     return q;
 }
 
-template <bool F16, int DP, int NT, bool CLUSTER>
+template <bool F16, int DP, int NT, AttnForm FORM>
 static int launch_attention_form(const AttnParams &p, const AttnPlan &q, cudaStream_t stream) {
     using S = AttnShape<DP, NT>;
-    TGC_TRY((allow_smem<attention_kernel<F16, DP, NT, CLUSTER>, S::kSmem>()));
-    cudaError_t e = launch_overlapped(attention_kernel<F16, DP, NT, CLUSTER>, dim3((unsigned)q.grid), dim3(kAttnThreads),
-                                      (size_t)S::kSmem, CLUSTER ? q.cluster : 1, stream, p);
-    if (e == cudaSuccess && !CLUSTER)
+    constexpr int kSmem = FORM == kOwnRuns ? S::kOwnSmem : S::kSmem;
+    TGC_TRY((allow_smem<attention_kernel<F16, DP, NT, FORM>, kSmem>()));
+    cudaError_t e = launch_overlapped(attention_kernel<F16, DP, NT, FORM>, dim3((unsigned)q.grid), dim3(kAttnThreads),
+                                      (size_t)kSmem, FORM == kClusters ? q.cluster : 1, stream, p);
+    if (e == cudaSuccess && FORM != kClusters)
         e = launch_overlapped(attention_join_kernel<F16, DP / 64>,
-                              dim3((unsigned)q.grid, (unsigned)((std::min(p.group, S::kRows) + kJoinRows - 1) / kJoinRows)),
-                              dim3(kJoinThreads), 0, 1, stream, p, S::kRows);
+                              dim3((unsigned)q.grid, (unsigned)((std::min(p.group, S::kRows) + kJoinRows - 1) / kJoinRows), (unsigned)q.own),
+                              dim3(kJoinThreads), 0, 1, stream, p, S::kRows, q.own);
     return e == cudaSuccess ? TGC_OK : cuda_fail(e);
 }
 
 template <bool F16, int DP, int NT>
 static int launch_attention(const AttnParams &p, const AttnPlan &q, cudaStream_t stream) {
-    return q.cluster > 0 ? launch_attention_form<F16, DP, NT, true>(p, q, stream)
-                         : launch_attention_form<F16, DP, NT, false>(p, q, stream);
+    if (q.cluster > 0) return launch_attention_form<F16, DP, NT, kClusters>(p, q, stream);
+    if constexpr (kOwnFits<DP, NT>)
+        if (q.own > 1) return launch_attention_form<F16, DP, NT, kOwnRuns>(p, q, stream);
+    return launch_attention_form<F16, DP, NT, kRuns>(p, q, stream);
 }
 
 static int attn_impl(tgc_paged_attention_args a) {
