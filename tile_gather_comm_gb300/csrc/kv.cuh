@@ -15,10 +15,13 @@ struct KvTable {
 
     __host__ __device__ bool is_seq(int s) const { return s >= 0 && s < num_seqs; }
     __host__ __device__ bool is_page(int page) const { return page >= 0 && page < num_pages; }
+    // What the table has at place `i` of sequence `s`, a page only where is_page says so; -1 outside.
+    __host__ __device__ int entry_at(const int32_t *table, int s, int i) const {
+        return is_seq(s) && i >= 0 && i < max_pages ? table[s * ld + i] : -1;
+    }
     // The page that holds place `i` of sequence `s`, or -1.
     __host__ __device__ int page_at(const int32_t *table, int s, int i) const {
-        if (!is_seq(s) || i < 0 || i >= max_pages) return -1;
-        const int page = table[s * ld + i];
+        const int page = entry_at(table, s, i);
         return is_page(page) ? page : -1;
     }
     // A length as the cache can hold it.

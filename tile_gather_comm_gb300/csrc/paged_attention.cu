@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnPa
     auto look_up = [&] {
 #pragma unroll
         for (int i = 1; i < kAhead; ++i) page[i - 1] = page[i];
-        page[kAhead - 1] = key < r.end ? p.kv.page_at(p.table, r.seq, page_i) : -1;
+        page[kAhead - 1] = key < r.end ? p.kv.entry_at(p.table, r.seq, page_i) : -1;  // looked at when it is used: the load is not waited for
         key += UNIT;
         page_i += p.adv_pages + (past(look) ? 1 : 0);
     };
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnPa
         off = -1;
         if (r.at < stop) {
             if (kQueries > 0 && fresh) copy_queries();
-            if (page[0] >= 0) off = page[0] * p.page_s + place * p.token_s + head_off;
+            if (p.kv.is_page(page[0])) off = page[0] * p.page_s + place * p.token_s + head_off;
             const uint32_t have = __ballot_sync(0xffffffffu, off >= 0);
             if (lane == 0) s_mask[warp][unit % S::kStages] = have;
             copy_rows(p.k, S::keys_at(unit));
