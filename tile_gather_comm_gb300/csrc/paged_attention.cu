@@ -87,10 +87,11 @@ struct AttnParams {
 struct KeyRange {
     int begin, end;
 };
-__device__ __forceinline__ KeyRange key_range(const AttnParams &p, int s) {
-    const int end = p.kv.tokens(p.lens[s]);
+__device__ __forceinline__ KeyRange range_of(const AttnParams &p, int len) {
+    const int end = p.kv.tokens(len);
     return {p.window > 0 && end > p.window ? end - p.window : 0, end};
 }
+__device__ __forceinline__ KeyRange key_range(const AttnParams &p, int s) { return range_of(p, p.lens[s]); }
 // a / b in 32 bits where both fit: 64-bit divisions take a few hundred cycles each, at every item's start and end.
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
     return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
@@ -272,11 +273,13 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnPa
     constexpr int UNIT = OWN ? S::kKeys : S::kUnit, ITEMS = OWN ? kAttnWarps : 1;  // keys of a unit; key heads (or parts of their groups) of an item
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t s_sum[kAttnWarps];
-    __shared__ RunAt s_cur;  // where the products stand: one copy, so that all warps meet at the same items
     __shared__ uint32_t s_mask[kAttnWarps][S::kStages];
     __shared__ float2 s_ml[kAttnWarps][S::kRows];
     __shared__ float2 s_cta_ml[S::kRows];
-    __shared__ int3 s_items[kAttnWarps][4];  // OWN: sequence, item and units of those that the copies have entered last
+    // Sequence, item and units of the items entered last: the products read them at an item's start, when six are at most.
+    // Warps that share items all read warp 0's, so that they meet at the same ones.
+    constexpr int kItemRing = 8;
+    __shared__ int3 s_items[kAttnWarps][kItemRing];
     const int tid = (int)threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane >> 2, t4 = lane & 3;
     uint8_t *const ring = smem + warp * S::kWarpRing;
     const uint32_t ring_at = smem_addr(ring);
@@ -335,76 +338,104 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnPa
         if (!seek<UNIT>(p, r, per * run, heads, lane)) r.at = stop;
     }
 
-    // ---- the warp's copies: a lane finds the page of a key of the step, all lanes copy.  Pages are looked up kAhead units
-    // before their copies: a load queues behind the copies under way, about two units' worth.
-    constexpr int kAhead = 3;
+    // ---- the warp's copies: a lane finds the page of a key of the step, all lanes copy.  r runs kAhead units before the
+    // copies, across the ends of items, and looks the pages up: a load queues behind the copies under way, about two units'
+    // worth.  With wide heads, or 32, a unit's products take longer than that, and there are no registers for more.
+    constexpr int kAhead = S::kAlone || NT == 4 ? 1 : 3;
     const int my_key = (OWN ? 0 : warp * S::kKeys) + lane % S::kKeys;
-    int key = 0, page_i = 0, look = 0;   // of the unit to be looked up next, with its place in the page
-    int page[kAhead], place = 0;         // of the units to be copied next; of the first of them
-    int64_t head_off = 0;
+    int key = 0, page_i = 0, look = 0, key_head = 0;  // of the unit to be looked up next, with its place in the page
+    int page[kAhead], place[kAhead], head[kAhead];    // of the units to be copied next; head is ~ its number where an item begins
+    int entered = 0;     // items that r has entered
+    if (lane < kItemRing) s_items[warp][lane] = make_int3(0, 0, 1);
+    __syncwarp();
+    bool fresh = false;  // nothing of the last one is looked up yet
     auto past = [&](int &at) {
         at += p.adv_tokens;
         const bool over = at >= p.kv.page_size;
         if (over) at -= p.kv.page_size;
         return over;
     };
-    auto look_up = [&] {
-#pragma unroll
-        for (int i = 1; i < kAhead; ++i) page[i - 1] = page[i];
-        page[kAhead - 1] = key < r.end ? p.kv.entry_at(p.table, r.seq, page_i) : -1;  // looked at when it is used: the load is not waited for
-        key += UNIT;
-        page_i += p.adv_pages + (past(look) ? 1 : 0);
-    };
-    int items = 0;       // whose queries are copied
-    int entered = 0;     // that the copies have entered
-    bool fresh = false;  // nothing of the item is copied yet
     auto enter_item = [&] {
-        // OWN: the products are at most three items behind
-        if (OWN && lane == 0) s_items[warp][entered % 4] = make_int3(r.seq, r.item, r.units);
+        if (lane == 0) s_items[warp][entered % kItemRing] = make_int3(r.seq, r.item, r.units);
         ++entered;
         key = r.begin + r.unit * UNIT + my_key;
         page_i = key / p.kv.page_size;
-        look = place = key - page_i * p.kv.page_size;
-        head_off = (int64_t)((OWN ? r.item * ITEMS + warp : r.item) / p.row_blocks) * p.head_s;
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) look_up();
+        look = key - page_i * p.kv.page_size;
+        key_head = (OWN ? r.item * ITEMS + warp : r.item) / p.row_blocks;
         fresh = true;
     };
-    // The item's queries, a share a warp, with the copies of its first unit: two units ahead of the products, so in the
+    // The next sequence that has keys; none only where the lengths change under the call.  A lane has the length of one of
+    // the next 32: a load here would wait behind the copies.
+    int lens_from = r.seq + 1, its_len = 0;
+    auto load_lens = [&] { its_len = lens_from + lane < p.kv.num_seqs ? p.lens[lens_from + lane] : 0; };
+    if (!CLUSTER) load_lens();
+    auto next_seq = [&] {
+        while (++r.seq < p.kv.num_seqs) {
+            if (r.seq == lens_from + 32) {
+                lens_from = r.seq;
+                load_lens();
+            }
+            const KeyRange k = range_of(p, __shfl_sync(0xffffffffu, its_len, r.seq - lens_from));
+            r.begin = k.begin;
+            r.end = k.end;
+            r.units = units_of<UNIT>(k);
+            if (r.units > 0) return true;
+        }
+        return false;
+    };
+    auto look_up = [&] {
+#pragma unroll
+        for (int i = 1; i < kAhead; ++i) {
+            page[i - 1] = page[i];
+            place[i - 1] = place[i];
+            head[i - 1] = head[i];
+        }
+        page[kAhead - 1] = r.at < stop && key < r.end ? p.kv.entry_at(p.table, r.seq, page_i) : -1;  // looked at when it is used: the load is not waited for
+        place[kAhead - 1] = look;
+        head[kAhead - 1] = fresh ? ~key_head : key_head;
+        if (r.at >= stop) return;
+        fresh = false;
+        key += UNIT;
+        page_i += p.adv_pages + (past(look) ? 1 : 0);
+        ++r.at;
+        if (++r.unit == r.units && !CLUSTER && r.at < stop) {
+            r.unit = 0;
+            if (++r.item == heads) {
+                r.item = 0;
+                if (!next_seq()) {
+                    r.at = stop;
+                    return;
+                }
+            }
+            enter_item();
+        }
+    };
+    RunAt c = r;            // where the products stand
+    int64_t copied = r.at;  // units before the one to be copied next
+    if (r.at < stop) enter_item();
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) look_up();
+    if (FORM == kRuns) __syncthreads();
+    // An item's queries, a share a warp, with the copies of its first unit: two units ahead of the products, so in the
     // place of an item that all warps are done with.
     constexpr int kQueries = OWN ? S::kRows * DP * 2 : S::kQueries;
     auto queries_of = [&](int item) {  // the item's number in the run
         return smem_addr(smem + S::kRings) + (uint32_t)((OWN ? warp * 2 + item % 2 : item % 3) * kQueries);
     };
+    int items = 0;  // whose queries are copied
     auto copy_queries = [&] {
-        const int item = OWN ? r.item * ITEMS + warp : r.item, head_k = item / p.row_blocks, row0 = item % p.row_blocks * S::kRows;
+        __syncwarp();
+        const int3 it = s_items[warp][items % kItemRing];
+        const int item = OWN ? it.y * ITEMS + warp : it.y, head_k = item / p.row_blocks, row0 = item % p.row_blocks * S::kRows;
         const uint32_t to = queries_of(items);
         for (int i = OWN ? lane : tid; i < S::kRows * (DP / 8); i += OWN ? 32 : kAttnThreads) {
             const int row = i / (DP / 8), ch = i % (DP / 8);
             const bool there = row0 + row < p.group && ch < chunks;
             cp_async16(to + chunk_at<DP>(row, ch),
-                       static_cast<const uint16_t *>(p.q) + (there ? r.seq * p.q_s + (int64_t)(head_k * p.group + row0 + row) * p.q_h + ch * 8 : 0),
+                       static_cast<const uint16_t *>(p.q) + (there ? it.x * p.q_s + (int64_t)(head_k * p.group + row0 + row) * p.q_h + ch * 8 : 0),
                        there);
         }
         ++items;
-        fresh = false;
-    };
-    if (r.at < stop) enter_item();
-    if (FORM == kRuns) {
-        if (tid == 0) s_cur = r;
-        __syncthreads();
-    }
-    RunAt c = FORM == kRuns ? s_cur : r;
-    // The next sequence that has keys; none only where the lengths change under the call.
-    auto next_seq = [&](RunAt &w) {
-        while (++w.seq < p.kv.num_seqs) {
-            const KeyRange k = key_range(p, w.seq);
-            w.begin = k.begin;
-            w.end = k.end;
-            w.units = units_of<UNIT>(k);
-            if (w.units > 0) return true;
-        }
-        return false;
     };
     int64_t off = -1;  // of this lane's key in the pools, of the unit in work
     auto copy_rows = [&](const void *pool, int to) {
@@ -418,33 +449,20 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnPa
     };
     auto copy_keys = [&](int unit) {  // the unit's number in the run
         off = -1;
-        if (r.at < stop) {
-            if (kQueries > 0 && fresh) copy_queries();
-            if (p.kv.is_page(page[0])) off = page[0] * p.page_s + place * p.token_s + head_off;
+        if (copied < stop) {
+            const bool first = head[0] < 0;
+            if (kQueries > 0 && first) copy_queries();
+            if (p.kv.is_page(page[0])) off = page[0] * p.page_s + place[0] * p.token_s + (first ? ~head[0] : head[0]) * p.head_s;
             const uint32_t have = __ballot_sync(0xffffffffu, off >= 0);
             if (lane == 0) s_mask[warp][unit % S::kStages] = have;
             copy_rows(p.k, S::keys_at(unit));
         }
     };
     auto copy_values = [&](int unit) {  // and on to the next unit
-        if (r.at >= stop) return;
+        if (copied >= stop) return;
         copy_rows(p.v, S::values_at(unit));
-        ++r.at;
-        if (++r.unit < r.units) {
-            look_up();
-            past(place);
-        } else if (!CLUSTER && r.at < stop) {
-            r.unit = 0;
-            if (++r.item == heads) {
-                r.item = 0;
-                r.seq_begin += (int64_t)r.units * heads;
-                if (!next_seq(r)) {
-                    r.at = stop;
-                    return;
-                }
-            }
-            enter_item();
-        }
+        ++copied;
+        look_up();
     };
     // The copies stay two units ahead (kAlone: a unit's keys and another's values, and the keys after them).
     copy_keys(0);
@@ -457,10 +475,10 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnPa
     constexpr int kBehind = S::kAlone ? 2 : 1;  // groups that may be under way while the next one's data are used
 
     int step = 0, done = 0;  // steps, items
-    while (CLUSTER || (OWN ? done < entered : c.at < stop)) {
-        if constexpr (OWN) {
+    while (CLUSTER || c.at < stop) {
+        if constexpr (!CLUSTER) {
             __syncwarp();
-            const int3 it = s_items[warp][done % 4];
+            const int3 it = s_items[OWN ? warp : 0][done % kItemRing];
             c.seq = it.x;
             c.item = it.y;
             c.units = it.z;
@@ -745,16 +763,6 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnPa
                     }
                 }
             }
-            if (!CLUSTER && tid == 0 && r0 + S::kRound == S::kRows) {
-                RunAt to = c;  // on to the next item
-                to.at += todo;
-                to.unit = 0;
-                if (to.at < stop && ++to.item == heads) {
-                    to.item = 0;
-                    if (!next_seq(to)) to.at = stop;
-                }
-                s_cur = to;
-            }
             __syncthreads();
         }
         if constexpr (CLUSTER) {
@@ -798,7 +806,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attention_kernel(const AttnPa
             copy_keys(step + 1);
             cp_async_commit();
         }
-        c = s_cur;
+        c.at += todo;
+        c.unit = 0;
     }
     cp_async_wait<0>();
 }
