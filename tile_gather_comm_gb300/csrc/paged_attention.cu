@@ -15,9 +15,9 @@
 // as columns, padded to 8: scores^T = K Q^T, out^T = V^T P^T.  The scores come out with a key a lane group,
 // and movmatrix turns 8 x 8 of them into the second product's operand.  A quarter of an SM takes 32 clocks
 // for one of them: 768 for 16 keys of up to 8 heads x 128, whose bytes take HBM 1400 a quarter; with 16 heads the
-// products are the bound (64 x 1850 tokens, 2 x 16 heads x 128: 44 us, bytes 23).
+// products are the bound (64 x 1850 tokens, 2 x 16 heads x 128: 42 us, bytes 23).
 // The same on tcgen05 -- 128 keys or elements as rows, heads as columns, scores and outputs in TMEM, warps of
-// their own for copies, products and softmax -- was built and measured: 66 us there, 98 against 86 with 256
+// their own for copies, products and softmax -- was built and measured: 66 us there, 98 against 83 with 256
 // elements a head, 220 against 126 for 170 sequences of 70 tokens.  A product of 128 rows takes it 130 clocks whatever its
 // 16 to 64 columns, also where neighbouring ones do not depend on each other: 2100 for 128 keys, and the way from
 // scores to probabilities to outputs does not hide behind it.
