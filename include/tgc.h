@@ -886,7 +886,7 @@ int tgc_kv_append(const tgc_kv_append_args *args);
  * with head h reading key head h / (heads_q / heads_k).  The new token's own key is one of them: it is appended
  * first and counted in lens.  A sequence without tokens gets zeros and lse = -inf.
  * Scores, softmax and sums are fp32 (the probabilities enter the product with V as two 16-bit parts,
- * so nothing of them is lost to 16 bits), out is rounded once.  The same inputs give the same
+ * which hold all that matters of them; with TGC_F16 at most 2^-36 of the largest one is lost a key), out is rounded once.  The same inputs give the same
  * bits on every call with the same sizes.  Zero-initialise the struct.
  *
  * q, out     device (num_seqs, heads_q, D), `dtype`; q_s, q_h, o_s, o_h elements between sequences
