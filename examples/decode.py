@@ -67,21 +67,26 @@ class Cache:
         tgc.tgc_kv_compact(self.pools, self.refs, self.table, self.used)
 
 
-def step(model, cache, tokens, live):
-    """One token of every sequence in ``live`` (int32) through the model; tokens has one for every sequence of
-    the cache.  Returns logits (sequences, vocabulary); rows of empty sequences mean nothing."""
+def step(model, cache, tokens, live, ok=None):
+    """One token of every sequence in ``live`` (int32, each once) through the model; tokens has one for every sequence of
+    the cache.  Returns logits (sequences, vocabulary).  A sequence that is not in ``live``, or that the cache has
+    no room for (``ok``, int32 beside ``live``, says which it had), keeps its tokens as they are; its row of the logits
+    means nothing."""
     S, H, K, E, D = len(tokens), model.heads, model.kv_heads, model.head, model.width
     new = lambda *shape: torch.empty(*shape, device=tokens.device, dtype=BF)  # noqa: E731
-    ok = torch.empty_like(live)
+    ok = torch.empty_like(live) if ok is None else ok
     cache.reserve(live, ok)
-    pos = cache.lens - 1  # -1 where a sequence is empty: nothing of it is appended
+    # the new token's position where there is one, -1 elsewhere: nothing of those is appended
+    at = live.long()
+    pos = torch.full_like(cache.lens, -1)
+    pos.scatter_(0, at, torch.where(ok > 0, cache.lens[at] - 1, -1))
     x = model.embed[tokens]
     for i, w in enumerate(model.layers):
         keys, values = cache.pools[2 * i:2 * i + 2]
         h, qkv, q, a, r, u = new(S, D), new(S, H + 2 * K, E), new(S, H, E), new(S, H, E), new(S, D), new(S, len(w["up"]))
         tgc.tgc_block_norm(x, None, h, pre="rms", pre_weight=w["norm1"])
         tgc.tgc_linear(h, w["qkv"], qkv.view(S, -1))
-        q.zero_()  # rows of empty sequences are left as they are
+        q.zero_()  # rows without a new token are left as they are
         tgc.tgc_kv_append(qkv[:, H:H + K], qkv[:, H + K:], keys, values, cache.table, pos, q=qkv[:, :H], q_out=q,
                           freqs=model.freqs, scale=model.rope_scale)
         tgc.tgc_paged_attention(q, a, keys, values, cache.table, cache.lens)
@@ -117,6 +122,7 @@ def main(argv=None):
     cache.fork(children % a.prompts, children)
     live = torch.arange(S, device=dev, dtype=torch.int32)
     logits = logits[live % a.prompts]
+    ok, refused = torch.empty_like(live), torch.zeros((), device=dev, dtype=torch.int64)
     texts = []
     for t in range(a.steps):
         p = torch.softmax(logits.float(), -1)
@@ -125,9 +131,13 @@ def main(argv=None):
         if t == a.steps // 2:  # every second sequence ends
             cache.free(live[1::2].contiguous())
             live = live[::2].contiguous()
+            ok = torch.empty_like(live)
             cache.compact()
             print(f"{len(live)} sequences go on in {int(cache.used)} pages")
-        logits = step(model, cache, tokens, live)
+        logits = step(model, cache, tokens, live, ok)
+        refused += (ok == 0).sum()
+    if int(refused):
+        raise RuntimeError(f"the cache had no room for {int(refused)} tokens")
     texts = torch.stack(texts, 1)
     for s in live.tolist():
         print(f"sequence {s:2d} ({int(cache.lens[s])} tokens): {texts[s].tolist()}")

@@ -1,0 +1,81 @@
+"""The attention and cache operators, and the example that decodes with them, at the edges of what they accept."""
+import importlib.util
+import os
+
+import pytest
+import torch
+
+from tests.helpers import requires_gpu
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+BF = torch.bfloat16
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    requires_gpu()
+
+
+def ints(v):
+    return torch.tensor(v, device="cuda", dtype=torch.int32)
+
+
+# ---------------------------------------------------------------- the decoding example
+
+
+def example():
+    spec = importlib.util.spec_from_file_location("decode", os.path.join(ROOT, "examples", "decode.py"))
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+def tokens_of(cache, s, n):
+    """The first n tokens' bytes of sequence s, in every pool."""
+    j = torch.arange(n, device="cuda")
+    at = cache.table[s, j // cache.page].long()
+    return [p[at, j % cache.page].view(torch.int16) for p in cache.pools]
+
+
+def same(a, b):
+    return all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_a_sequence_left_out_of_a_step_keeps_its_tokens():
+    """Six tokens of three sequences, then steps without the second: its length, its bytes, and, when it goes on, the
+    same logits as a cache in which nobody paused."""
+    m = example()
+    model = m.Model(seed=3)
+    paused, straight = (m.Cache(model, 16, 4, 4, 5) for _ in range(2))
+    for t in range(6):
+        for c in (paused, straight):
+            m.step(model, c, torch.full((4,), 3 * t + 1, device="cuda"), ints([0, 1, 2]))
+    before = tokens_of(paused, 1, 6)
+    for t in range(3):
+        m.step(model, paused, torch.full((4,), 99 + t, device="cuda"), ints([2, 0]))
+        assert paused.lens.tolist() == [7 + t, 6, 7 + t, 0]
+        assert same(tokens_of(paused, 1, 6), before)
+    got = m.step(model, paused, torch.full((4,), 42, device="cuda"), ints([1]))
+    want = m.step(model, straight, torch.full((4,), 42, device="cuda"), ints([1]))
+    assert torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("held", [8, 7])
+def test_a_step_that_finds_no_room_keeps_every_token(held):
+    """Two branches whose pages are full (shared, or one shared and one of each) and one free page: the first
+    branch has it, the second is told so, and nobody's old tokens change."""
+    m = example()
+    model = m.Model(seed=3)
+    cache = m.Cache(model, 3 if held == 8 else 4, 4, 2, 5)
+    for t in range(held):
+        m.step(model, cache, torch.full((2,), 3 * t + 1, device="cuda"), ints([0]))
+    cache.fork(ints([0]), ints([1]))
+    if held == 7:
+        m.step(model, cache, torch.tensor([50, 60], device="cuda"), ints([0, 1]))
+    before = [tokens_of(cache, s, 8) for s in range(2)]
+    ok = ints([-1, -1])
+    m.step(model, cache, torch.tensor([5, 77], device="cuda"), ints([0, 1]), ok)
+    assert ok.tolist() == [1, 0] and cache.lens.tolist() == [9, 8]
+    for s in range(2):
+        assert same(tokens_of(cache, s, 8), before[s])
