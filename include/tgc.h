@@ -897,7 +897,8 @@ int tgc_kv_append(const tgc_kv_append_args *args);
  * Keys on pages whose number is outside [0, num_pages) are left out like masked ones.  What lies
  * behind a sequence's last key in its page is not read, whatever it holds; a value that is infinite
  * or NaN in range makes its column of out NaN.
- * scale      0 = 1 / sqrt(D).
+ * scale      0 = 1 / sqrt(D).  scale * log2(e) and softcap * log2(e) are finite in fp32 (up to 2.35e38), and scale / softcap
+ *            neither infinite nor below fp32's normal numbers (TGC_ERR_INVALID_ARG).
  * Requirements: heads_q a multiple of heads_k and at most TGC_ATTENTION_MAX_HEADS, D <= TGC_ATTENTION_MAX_D
  * (TGC_ERR_INVALID_ARG); TGC_BF16 or TGC_F16 (TGC_ERR_DTYPE); D and every stride in whole 16 bytes, every pointer 16-byte aligned (lse, table,
  * lens: 4-byte) (TGC_ERR_ALIGN).  max_pages * page_size <= TGC_MAX_SIZE; num_seqs * heads_q < 2^31.

@@ -5,6 +5,7 @@ import os
 import pytest
 import torch
 
+import tile_gather_comm_gb300 as tgc
 from tests.helpers import requires_gpu
 
 pytestmark = pytest.mark.gpu
@@ -79,3 +80,28 @@ def test_a_step_that_finds_no_room_keeps_every_token(held):
     assert ok.tolist() == [1, 0] and cache.lens.tolist() == [9, 8]
     for s in range(2):
         assert same(tokens_of(cache, s, 8), before[s])
+
+
+# ---------------------------------------------------------------- attention
+
+
+@pytest.mark.parametrize("scale,cap", [(8.0, 2.3e38), (0.125, 1e37), (1.0, 1e-30), (0.125, 1e-38), (-0.5, 40.0)])
+@pytest.mark.parametrize("S", [1, 300])
+def test_the_largest_and_smallest_caps(scale, cap, S):
+    """A cap that no score comes near changes nothing; one that all pass by far leaves +-cap, 0 for softmax.  Products
+    of -1, 0 and 1: scores are exact before they are scaled, 2^9.6 in powers of two at most.  Quotient, product and the
+    cap's factor round by 2^-24 each and tanh by 2^-22: 2^-11.6 of a score and as much of the reference, times ln 2 2^-11.1
+    of a probability, twice (product and sum) 2^-10.1; what is left to 2^-9 is for the sums and parts."""
+    g = torch.Generator(device="cuda").manual_seed(S)
+    n, D, page = 70, 64, 16
+    kp = torch.randint(-1, 2, (S * 5, page, 1, D), generator=g, device="cuda").to(BF)
+    vp = torch.randn(S * 5, page, 1, D, generator=g, device="cuda").to(BF)
+    table = torch.arange(S * 5, device="cuda", dtype=torch.int32).view(S, 5)
+    q = torch.randint(-1, 2, (S, 2, D), generator=g, device="cuda").to(BF)
+    out = torch.empty_like(q)
+    tgc.tgc_paged_attention(q, out, kp, vp, table, ints([n] * S), scale=scale, softcap=cap)
+    k, v = (p[table.long()].reshape(S, 80, D)[:, :n].double() for p in (kp, vp))
+    x = q.double() @ k.transpose(1, 2) * scale
+    p = torch.softmax(cap * torch.tanh(x / cap), -1)
+    want, size = p @ v, p @ v.abs()
+    assert bool(((out.double() - want).abs() <= 2 ** -9 * size + 2 ** -8 * want.abs()).all())

@@ -901,6 +901,8 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
         if (rc_ != TGC_OK) return rc_;    \
     } while (0)
 
+static float attn_scale(const tgc_paged_attention_args &a) { return a.scale != 0.0f ? a.scale : 1.0f / std::sqrt((float)a.D); }
+
 static int attn_check(tgc_paged_attention_args &a) {
     if (a.dtype != TGC_BF16 && a.dtype != TGC_F16) return TGC_ERR_DTYPE;
     if (a.num_seqs < 0 || a.heads_q < 1 || a.heads_k < 1 || a.heads_q % a.heads_k != 0 || a.D < 1 ||
@@ -908,6 +910,9 @@ static int attn_check(tgc_paged_attention_args &a) {
         return TGC_ERR_INVALID_ARG;
     if (a.heads_q > TGC_ATTENTION_MAX_HEADS || (a.num_seqs > 0 && a.heads_q > TGC_MAX_SIZE / a.num_seqs)) return TGC_ERR_INVALID_ARG;
     if (a.window < 0 || !std::isfinite(a.scale) || !std::isfinite(a.softcap) || a.softcap < 0.0f) return TGC_ERR_INVALID_ARG;
+    // The kernel's factors: an infinite one meets zeros, and a ratio below fp32's normal range has lost bits.
+    if (!std::isfinite(attn_scale(a) * kLog2e)) return TGC_ERR_INVALID_ARG;
+    if (a.softcap > 0.0f && (!std::isfinite(a.softcap * kLog2e) || !std::isnormal(attn_scale(a) / a.softcap))) return TGC_ERR_INVALID_ARG;
     TGC_TRY(kv_table_check(a.num_pages, a.page_size, a.num_seqs, a.max_pages, &a.table_ld));
     TGC_TRY(kv_pages_check(a.num_pages, a.page_size, a.heads_k, a.D, &a.page_s, &a.token_s, &a.head_s));
     TGC_TRY(heads_check(a.num_seqs, a.heads_q, a.D, &a.q_s, &a.q_h));
@@ -1018,7 +1023,7 @@ static int attn_impl(tgc_paged_attention_args a) {
     p.row_blocks = q.row_blocks;
     p.q_s = a.q_s; p.q_h = a.q_h; p.o_s = a.o_s; p.o_h = a.o_h;
     p.page_s = a.page_s; p.token_s = a.token_s; p.head_s = a.head_s;
-    const float scale = a.scale != 0.0f ? a.scale : 1.0f / std::sqrt((float)a.D);
+    const float scale = attn_scale(a);
     p.scale = scale * kLog2e;
     if (a.softcap > 0.0f) {
         p.cap = a.softcap * kLog2e;
