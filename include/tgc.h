@@ -936,9 +936,11 @@ size_t tgc_paged_attention_workspace_bytes(const tgc_paged_attention_args *args)
 #define TGC_KV_MAX_POOLS 256
 
 /*
- * The cache's upkeep.  One struct for the five calls; each uses the fields it names, the others are
- * ignored.  Pools are host arrays of device pointers (copied into kernel parameters), dense pages of
- * page_bytes bytes, a multiple of 16, 16-byte aligned.  Every list is a device int32 array of n entries.
+ * The cache's upkeep.  One struct for the five calls; each uses the fields it names, and all but
+ * tgc_kv_copy the sizes that describe the cache, num_pages, page_size (at least 1, also where a call has no other use
+ * for it), num_seqs, max_pages and table_ld; the others are ignored.  Pools are host arrays of device pointers (copied
+ * into kernel parameters), dense pages of page_bytes bytes, a multiple of 16, 16-byte aligned; with npools = 0 no
+ * bytes are copied, and page_bytes and the arrays are ignored.  Every list is a device int32 array of n entries.
  *
  * tgc_kv_copy     pools, from, npools, page_bytes, num_pages, from_pages, src, dst, n:
  *                 page src[i] of from[p] is copied to page dst[i] of pools[p], for every pool p.  from may

@@ -28,3 +28,24 @@ def test_scales_and_caps_that_leave_fp32(scale, softcap, rc):
     if rc == INV:
         assert _attention(scale=scale, softcap=softcap) == INV
         assert _attention("tgc_paged_attention_workspace_bytes", scale=scale, softcap=softcap) == 0
+
+
+def _kv(name, **kw):
+    d = dict(refs=FAKE, table=FAKE, lens=FAKE, num_pages=9, page_size=16, num_seqs=3, max_pages=5, src=FAKE, dst=FAKE,
+             add=FAKE, ok=FAKE, used=FAKE, n=0, workspace=FAKE, workspace_bytes=1 << 20)
+    d.update(kw)
+    return getattr(_lib.lib(), "tgc_kv_" + name)(ctypes.byref(_lib.KvArgs(**d)))
+
+
+@pytest.mark.parametrize("name,kw,rc", [
+    ("fork", {}, OK), ("fork", dict(page_bytes=24), OK), ("fork", dict(page_bytes=-1), OK), ("compact", dict(num_pages=0, used=None), OK),
+    ("copy", dict(n=2), OK), ("copy", dict(n=2, page_bytes=8), OK), ("fork", dict(npools=1), INV), ("fork", dict(npools=-1), INV),
+    ("copy", dict(n=2, num_pages=-1), INV)])
+def test_without_pools_their_fields_are_ignored(name, kw, rc):
+    assert _kv(name, **kw) == rc
+
+
+@pytest.mark.parametrize("name", ["reserve", "fork", "free", "compact"])
+@pytest.mark.parametrize("kw", [dict(page_size=0), dict(num_pages=-1), dict(num_seqs=-1), dict(max_pages=-1), dict(table_ld=4)])
+def test_every_call_on_a_cache_wants_its_sizes(name, kw):
+    assert _kv(name, **kw) == INV

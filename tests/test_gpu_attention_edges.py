@@ -1,4 +1,5 @@
 """The attention and cache operators, and the example that decodes with them, at the edges of what they accept."""
+import ctypes
 import importlib.util
 import os
 
@@ -6,6 +7,7 @@ import pytest
 import torch
 
 import tile_gather_comm_gb300 as tgc
+from tile_gather_comm_gb300 import _lib
 from tests.helpers import requires_gpu
 
 pytestmark = pytest.mark.gpu
@@ -105,3 +107,30 @@ def test_the_largest_and_smallest_caps(scale, cap, S):
     p = torch.softmax(cap * torch.tanh(x / cap), -1)
     want, size = p @ v, p @ v.abs()
     assert bool(((out.double() - want).abs() <= 2 ** -9 * size + 2 ** -8 * want.abs()).all())
+
+
+# ---------------------------------------------------------------- the cache's upkeep
+
+
+def test_upkeep_without_pools():
+    """npools = 0: the same bookkeeping as with pools, and no bytes."""
+    tables = []
+    for pools in (True, False):
+        refs, lens = torch.zeros(40, device="cuda", dtype=torch.int32), ints([0] * 6)
+        table, ws = torch.full((6, 8), -1, device="cuda", dtype=torch.int32), torch.empty(1 << 16, device="cuda", dtype=torch.uint8)
+        src, dst, used = ints([0, 1, 1]), ints([4, 5, 3]), ints([-1])
+        tgc.tgc_kv_reserve(refs, table, lens, ints([0, 1, 2]), ints([13, 16, 30]), 4)
+        if pools:
+            pool = [torch.zeros(40, 4, 8, device="cuda", dtype=BF)]
+            tgc.tgc_kv_fork(pool, refs, table, lens, src, dst, 4)
+            tgc.tgc_kv_free(refs, table, lens, ints([0, 1]))
+            tgc.tgc_kv_compact(pool, refs, table, used)
+        else:
+            a = _lib.KvArgs(refs=refs.data_ptr(), table=table.data_ptr(), lens=lens.data_ptr(), num_pages=40, page_size=4,
+                            num_seqs=6, max_pages=8, src=src.data_ptr(), dst=dst.data_ptr(), n=3, workspace=ws.data_ptr(),
+                            workspace_bytes=ws.numel(), used=used.data_ptr(), stream=torch.cuda.current_stream().cuda_stream)
+            assert _lib.lib().tgc_kv_fork(ctypes.byref(a)) == _lib.TGC_OK
+            tgc.tgc_kv_free(refs, table, lens, ints([0, 1]))
+            assert _lib.lib().tgc_kv_compact(ctypes.byref(a)) == _lib.TGC_OK
+        tables.append([t.tolist() for t in (refs, table, lens, used)])
+    assert tables[0] == tables[1] and tables[0][3] == [8 + 3 + 1 + 4]

@@ -549,6 +549,8 @@ static int kv_pools(const tgc_kv_args &a, const void *const *from, int64_t from_
     if (a.npools < 0 || a.npools > TGC_KV_MAX_POOLS || (a.npools > 0 && (a.pools == nullptr || from == nullptr)))
         return TGC_ERR_INVALID_ARG;
     if (a.num_pages < 0 || a.num_pages > TGC_MAX_SIZE || from_pages < 0 || from_pages > TGC_MAX_SIZE) return TGC_ERR_INVALID_ARG;
+    *out = CopyParams{};
+    if (a.npools == 0) return TGC_OK;  // nothing to copy: page_bytes is not looked at
     // a pool ends below 2^59 bytes, the pieces of all pools below 2^31
     const int64_t most = a.num_pages > from_pages ? a.num_pages : from_pages;
     if (a.page_bytes < 1 || a.page_bytes > (int64_t(1) << 34) || most > (int64_t(1) << 59) / a.page_bytes) return TGC_ERR_INVALID_ARG;
