@@ -204,11 +204,10 @@ struct RunAt {
     int begin, end;              // keys of the sequence in range
 };
 
-// Warp-collective: the sequence that holds unit `at`, looked for from r.seq (whose first unit is r.seq_begin) on, or from
-// the start where that is past it; then the item and unit.  False only where the lengths change under the call.
+// Warp-collective: the sequence that holds unit `at`, looked for from the first on (r is zeroed), then the item and unit.
+// False only where the lengths change under the call.
 template <int UNIT>
 __device__ __forceinline__ bool seek(const AttnParams &p, RunAt &r, int64_t at, int heads, int lane) {
-    if (at < r.seq_begin) r.seq = 0, r.seq_begin = 0;
     for (; r.seq < p.kv.num_seqs; r.seq += 32) {
         const int mine = r.seq + lane < p.kv.num_seqs ? units_of<UNIT>(key_range(p, r.seq + lane)) : 0;
         int64_t upto = mine;
