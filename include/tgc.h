@@ -779,8 +779,8 @@ typedef enum tgc_rope_layout { TGC_ROPE_HALF = 0, TGC_ROPE_INTERLEAVED = 1 } tgc
  *     a' = scale * (a cos w - b sin w),  b' = scale * (b cos w + a sin w),
  *     w = pos[t] * freqs[i]  for pair i of token t;
  * elements from R on are copied.  q and k (fewer heads) in one launch.  The angle is taken in 64
- * bits modulo a whole turn, so far positions lose nothing; sine, cosine and the products are fp32,
- * the result is rounded once.  Zero-initialise the struct; 0 / NULL means the default.
+ * bits modulo a whole turn, off by 2^-64 turns a position: 2^-30 radians at the farthest one (for freqs up to
+ * 2^40); sine, cosine and the products are fp32, the result is rounded once.  Zero-initialise the struct; 0 / NULL means the default.
  *
  * q, q_out   device (T, heads_q, D), `dtype`.  q_out may be q (same address and strides), and must
  *            overlap nothing else that is read or written.

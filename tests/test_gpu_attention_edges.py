@@ -1,7 +1,9 @@
 """The attention and cache operators, and the example that decodes with them, at the edges of what they accept."""
 import ctypes
 import importlib.util
+import math
 import os
+from fractions import Fraction
 
 import pytest
 import torch
@@ -134,3 +136,29 @@ def test_upkeep_without_pools():
             assert _lib.lib().tgc_kv_compact(ctypes.byref(a)) == _lib.TGC_OK
         tables.append([t.tolist() for t in (refs, table, lens, used)])
     assert tables[0] == tables[1] and tables[0][3] == [8 + 3 + 1 + 4]
+
+
+# ---------------------------------------------------------------- positions
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("back", [False, True])
+def test_angles_keep_their_bits(layout, back):
+    """Fast and slow pairs at near and far positions against whole-number arithmetic.  The fraction of a turn is off by
+    2^-64 a position (2^-61.3 radians, with its product's 2^-106); the angle is rounded to fp32, 2^-24 of itself, and its
+    factor pi, sine and cosine by 2 units (2^-23 each): 2^-21 in all, of a small angle's sine relative to it."""
+    freqs = [1.0, 0.7310585786300049, 0.11, 0.5, math.pi, 100.3, 12345.678, -0.9, 1e-3, 1e-7, 1e-9, 3e-12, -1e-10, 2.0 ** 40 + 0.5, 0.0]
+    pos = [0, 1, 3, 4097, 999983, 16777217, 2 ** 31 - 1]
+    R = 2 * len(freqs)
+    q = torch.zeros(len(pos), 1, R, device="cuda")
+    a, b = (q[..., :R // 2], q[..., R // 2:]) if layout == "half" else (q[..., 0::2], q[..., 1::2])
+    a.fill_(1.0)  # (1, 0) turns into (cos, sin)
+    (tgc.tgc_rope_bwd if back else tgc.tgc_rope)(q, q, ints(pos), torch.tensor(freqs, dtype=torch.float64, device="cuda"), layout=layout)
+    turn = Fraction(2 * 31415926535897932384626433832795028841971693993751, 10 ** 49)
+    for t, p in enumerate(pos):
+        for i, f in enumerate(freqs):
+            w = Fraction(f) * p * (-1 if back else 1)
+            w = float(w - turn * round(w / turn))
+            far = p * 2 ** -61
+            assert abs(float(a[t, 0, i]) - math.cos(w)) <= 2 ** -21 + far, (p, f)
+            assert abs(float(b[t, 0, i]) - math.sin(w)) <= 2 ** -21 * min(1.0, abs(w)) + far, (p, f)

@@ -78,14 +78,29 @@ __device__ __forceinline__ F2 turned(F2 v, float c, float s) {
     return fma(f2(f.y, f.x), f2(-s, s), mul(v, every<F2>(c)));
 }
 
+// freq / 2 pi modulo a whole turn, in 2^-64 turns (signed: a negative one wraps).  1 / 2 pi in two terms, the rounding
+// of the first one's product added to the second's: off by about 2^-106 of itself before it is rounded to 2^-64,
+// where one product of doubles would be off by 2^-53, 2^-25 turns at 2^31 positions a radian apart.
+__device__ __forceinline__ uint64_t turn_fraction(double freq) {
+    constexpr double kHigh = 0x1.45f306dc9c883p+61, kLow = -0x1.6b01ec5417056p+7;  // their sum: 2^64 / (2 pi)
+    constexpr double kTurn = 0x1p64;
+    double high = __dmul_rn(freq, kHigh), low = __fma_rn(freq, kLow, __fma_rn(freq, kHigh, -high));
+    if (fabs(high) >= kTurn / 2) {  // half a turn a position, or more
+        high -= kTurn * rint(high / kTurn);
+        low -= kTurn * rint(low / kTurn);
+        if (high == kTurn / 2) high = -high;
+    }
+    return (uint64_t)__double2ll_rn(high) + (uint64_t)__double2ll_rn(low);
+}
+
 // One block: `tokens` tokens, `rows` of their heads.  First the sines and cosines of its tokens (one for each token
 // and pair, which the heads share), then the heads, a thread taking units of V pairs (half layout: a vector of V from
 // each half; interleaved: one vector of V / 2 pairs) or a vector of V elements to copy.
 //
-// The angle: freq / 2 pi, taken modulo 1, is held as a 64-bit fraction of a turn, and its product with the position
-// modulo 2^64 is the angle's: whole turns fall off the top.  What 31 bits of position make of the last bit of
-// freq is far below fp32's, in which sine and cosine are then taken.  fp64 is needed once a pair and
-// block.
+// The angle: freq / 2 pi, taken modulo 1, is held as a 64-bit fraction of a turn (turn_fraction), and its product with
+// the position modulo 2^64 is the angle's: whole turns fall off the top.  The fraction is off by one 2^-64 at most, so
+// the angle by 2^-33 turns at the farthest position; it is rounded to fp32 relative to itself, so that a small
+// one keeps its bits, and sine and cosine are taken in fp32.  fp64 is needed once a pair and block.
 //
 // Bound by HBM where there are many tokens, by the launch where there are few.
 constexpr int kRopeThreads = 256;
@@ -131,17 +146,13 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const RopeParams 
         s_pos[tid] = pos;
         s_slot[tid] = slot;
     }
-    for (int i = tid; i < half; i += kRopeThreads) {
-        double turns = p.freqs[i] * 0.15915494309189533577;  // 1 / (2 pi)
-        turns -= floor(turns);
-        s_freq[i] = turns < 1.0 ? (uint64_t)(turns * 18446744073709551616.0) : 0;  // 2^64
-    }
+    for (int i = tid; i < half; i += kRopeThreads) s_freq[i] = turn_fraction(p.freqs[i]);
     __syncthreads();
     for (int i = tid; i < tokens * half; i += kRopeThreads) {
         const int t = p.half.of(i);
         const uint64_t angle = s_freq[i - t * half] * (uint64_t)(uint32_t)s_pos[t];
         float c, s;
-        sincospif((float)(int32_t)(angle >> 32) * 4.656612873077392578e-10f, &s, &c);  // 2^-31: half turns
+        sincospif((float)(int64_t)angle * 0x1p-63f, &s, &c);  // half turns
         s_cos[i] = c * p.scale;
         s_sin[i] = s * p.scale * p.sign;
     }
