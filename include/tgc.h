@@ -765,8 +765,9 @@ size_t tgc_block_norm_bwd_workspace_bytes(const tgc_block_norm_bwd_args *args);
  * A page that is not full belongs to one sequence, so appending never writes into another's tokens
  * (tgc_kv_fork keeps it so).  Page numbers outside [0, num_pages), sequence numbers outside
  * [0, num_seqs) and lengths outside [0, max_pages * page_size] never make a kernel leave its tensors:
- * each call says what it makes of them.  Calls that read or change the same cache are ordered by
- * the caller (one stream, or events). */
+ * each call says what it makes of them.  Tables without entries and refs of no pages may be NULL, and so may pools of no
+ * pages in tgc_kv_append and tgc_paged_attention.  Calls that read or change the same cache are ordered by the caller
+ * (one stream, or events). */
 
 /* Which elements of a head turn together: (i, i + R/2), or neighbours (2i, 2i + 1). */
 typedef enum tgc_rope_layout { TGC_ROPE_HALF = 0, TGC_ROPE_INTERLEAVED = 1 } tgc_rope_layout;

@@ -162,3 +162,19 @@ def test_angles_keep_their_bits(layout, back):
             far = p * 2 ** -61
             assert abs(float(a[t, 0, i]) - math.cos(w)) <= 2 ** -21 + far, (p, f)
             assert abs(float(b[t, 0, i]) - math.sin(w)) <= 2 ** -21 * min(1.0, abs(w)) + far, (p, f)
+
+
+def test_append_where_no_page_can_be():
+    """An empty pool (its pointer is NULL), a table without pages, one without sequences: the queries are turned, and keys
+    and values dropped."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(3, 2, 8, generator=g, device="cuda")
+    freqs, _ = tgc.tgc_rope_freqs(8)
+    pos, want, seqs = ints([1, 2, 3]), torch.empty_like(x), ints([0, 0, 0])
+    tgc.tgc_rope(x, want, pos, freqs)
+    for pages, seq_n, wide in ((0, 3, 2), (2, 3, 0), (2, 0, 2), (0, 0, 0)):
+        pool = torch.zeros(pages, 4, 2, 8, device="cuda")
+        out = torch.full_like(x, 7.0)
+        tgc.tgc_kv_append(x, x, pool, pool, torch.zeros(seq_n, wide, device="cuda", dtype=torch.int32), pos, seqs=seqs, q=x,
+                          q_out=out, freqs=freqs)
+        assert torch.equal(out, want) and not bool(pool.any())

@@ -35,7 +35,8 @@ struct RopeParams {
     const double *freqs;
     int T, D, R;
     float scale, sign;
-    // the cache that keys and values go to; table == nullptr: none, keys go to out[1]
+    // the cache that keys and values go to; none: keys go to out[1]
+    bool cached;
     KvTable kv;
     const int32_t *table, *seqs;
     int64_t page_s, token_s;
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const RopeParams 
     if (tid < tokens) {
         const int t = t0 + tid, pos = p.pos[t];
         int64_t slot = -1;
-        if (p.table != nullptr && pos >= 0) {
+        if (p.cached && pos >= 0) {
             const int page = p.kv.page_at(p.table, p.seqs != nullptr ? p.seqs[t] : t, pos / p.kv.page_size);
             if (page >= 0) slot = page * p.page_s + pos % p.kv.page_size * p.token_s;
         }
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const RopeParams 
         if (s_pos[t] < 0) continue;
         const T *in = static_cast<const T *>(p.in[set]) + (t0 + t) * p.in_t[set] + head * p.in_h[set];
         T *out = static_cast<T *>(p.out[set]) + head * p.out_h[set];
-        if (set > 0 && p.table != nullptr) {
+        if (set > 0 && p.cached) {
             if (s_slot[t] < 0) continue;
             out += s_slot[t];
         } else {
@@ -241,9 +242,9 @@ static RopeShape rope_shape(const RopeParams &p, bool interleaved, int es, const
         for (int i = 0; i < 3; ++i)
             if (p.heads[i] > 0) {
                 at(p.in[i], p.in_t[i], p.in_h[i]);
-                if (p.table == nullptr || i == 0) at(p.out[i], p.out_t[i], p.out_h[i]);
+                if (!p.cached || i == 0) at(p.out[i], p.out_t[i], p.out_h[i]);
             }
-        if (p.table != nullptr) {
+        if (p.cached) {
             at(k_pages, p.page_s, p.token_s);
             at(v_pages, head_s, 0);
         }
@@ -362,9 +363,11 @@ static int append_impl(tgc_kv_append_args a) {
     if (a.seqs == nullptr && a.T > a.num_seqs) return TGC_ERR_INVALID_ARG;
     TGC_TRY(kv_pages_check(a.num_pages, a.page_size, a.heads_k, a.D, &a.page_s, &a.token_s, &a.head_s));
     if (a.T == 0) return TGC_OK;
-    if (a.pos == nullptr || a.table == nullptr || a.k_pages == nullptr || a.v_pages == nullptr || a.k == nullptr ||
-        a.v == nullptr)
-        return TGC_ERR_INVALID_ARG;
+    if (a.pos == nullptr || a.k == nullptr || a.v == nullptr) return TGC_ERR_INVALID_ARG;
+    // no place for a key without any of these: then the queries alone are turned
+    if (a.num_seqs > 0 && a.max_pages > 0) {
+        if (a.table == nullptr || (a.num_pages > 0 && (a.k_pages == nullptr || a.v_pages == nullptr))) return TGC_ERR_INVALID_ARG;
+    }
     TGC_TRY(heads_given(a.q, a.T, a.heads_q, a.D, es, &a.q_t, &a.q_h));
     TGC_TRY(heads_given(a.q_out, a.T, a.heads_q, a.D, es, &a.qo_t, &a.qo_h));
     TGC_TRY(heads_given(a.k, a.T, a.heads_k, a.D, es, &a.k_t, &a.k_h));
@@ -380,7 +383,7 @@ static int append_impl(tgc_kv_append_args a) {
     p.in_h[0] = a.q_h; p.in_h[1] = a.k_h; p.in_h[2] = a.v_h;
     p.out_t[0] = a.qo_t; p.out_h[0] = a.qo_h; p.out_h[1] = p.out_h[2] = a.head_s;
     p.heads[0] = (int)a.heads_q; p.heads[1] = p.heads[2] = (int)a.heads_k;
-    p.pos = a.pos; p.freqs = a.freqs; p.table = a.table; p.seqs = a.seqs;
+    p.pos = a.pos; p.freqs = a.freqs; p.cached = true; p.table = a.table; p.seqs = a.seqs;
     p.T = (int)a.T; p.D = (int)a.D; p.R = (int)a.R;
     p.scale = a.scale; p.sign = 1.0f;
     p.kv = KvTable{(int)a.num_pages, (int)a.page_size, (int)a.num_seqs, (int)a.max_pages, a.table_ld};
