@@ -830,7 +830,7 @@ typedef enum tgc_rope_scaling {
 
 /* Writes R/2 frequencies to the HOST array `freqs` and, where `scale` is not NULL, the factor on the
  * rotated elements (1 except for YARN).  base > 1, factor >= 1, trained > 0 and beta_fast > beta_slow > 0 where they
- * are used; TGC_ERR_INVALID_ARG otherwise.  NTK with R = 2 has one pair, whose frequency is 1 in any base.  Needs no GPU. */
+ * are used, and NTK's base finite; TGC_ERR_INVALID_ARG otherwise.  NTK with R = 2 has one pair, whose frequency is 1 in any base.  Needs no GPU. */
 int tgc_rope_freqs(double *freqs, double *scale, int64_t R, double base, tgc_rope_scaling scaling, double factor,
                    double trained, double beta_fast, double beta_slow);
 

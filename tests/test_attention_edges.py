@@ -3,6 +3,7 @@ import ctypes
 
 import pytest
 
+import tile_gather_comm_gb300 as tgc
 from tile_gather_comm_gb300 import _lib
 
 FAKE = 1 << 20  # an aligned address that is never dereferenced
@@ -49,3 +50,13 @@ def test_without_pools_their_fields_are_ignored(name, kw, rc):
 @pytest.mark.parametrize("kw", [dict(page_size=0), dict(num_pages=-1), dict(num_seqs=-1), dict(max_pages=-1), dict(table_ld=4)])
 def test_every_call_on_a_cache_wants_its_sizes(name, kw):
     assert _kv(name, **kw) == INV
+
+
+def test_a_base_stretched_past_64_bits_is_refused():
+    """R = 4: factor^2 times the base."""
+    with pytest.raises(tgc.TGCError):
+        tgc.tgc_rope_freqs(4, 10000.0, scaling="ntk", factor=1e153, device="cpu")
+    freqs, _ = tgc.tgc_rope_freqs(4, 10000.0, scaling="ntk", factor=1e150, device="cpu")
+    assert freqs[0] == 1 and freqs[1] * 1e152 == pytest.approx(1.0, rel=1e-12)
+    freqs, _ = tgc.tgc_rope_freqs(2, 10000.0, scaling="ntk", factor=1e300, device="cpu")
+    assert freqs.tolist() == [1.0]

@@ -419,6 +419,7 @@ extern "C" int tgc_rope_freqs(double *freqs, double *scale, int64_t R, double ba
                                      !(beta_fast > beta_slow) || !std::isfinite(beta_fast)))
         return TGC_ERR_INVALID_ARG;
     if (scaling == TGC_ROPE_NTK && R > 2) base *= std::pow(factor, (double)R / (double)(R - 2));
+    if (!std::isfinite(base)) return TGC_ERR_INVALID_ARG;  // it would leave every pair but the first standing still
     for (int64_t i = 0; i < R / 2; ++i) {
         double f = std::pow(base, -2.0 * (double)i / (double)R);
         if (scaling == TGC_ROPE_LINEAR) f /= factor;
