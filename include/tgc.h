@@ -897,7 +897,8 @@ int tgc_kv_append(const tgc_kv_append_args *args);
  * lens       device int32 (num_seqs); taken as 0 below 0 and as max_pages * page_size above it.
  * Keys on pages whose number is outside [0, num_pages) are left out like masked ones.  What lies
  * behind a sequence's last key in its page is not read, whatever it holds; a value that is infinite
- * or NaN in range makes its column of out NaN.
+ * or NaN in range makes its column of out NaN.  The values' weighted sum is fp32, no key's weight above 1 with TGC_BF16: it
+ * leaves fp32 where the values themselves, added up, do.
  * scale      0 = 1 / sqrt(D).  scale * log2(e) and softcap * log2(e) are finite in fp32 (up to 2.35e38), and scale / softcap
  *            neither infinite nor below fp32's normal numbers (TGC_ERR_INVALID_ARG).
  * Requirements: heads_q a multiple of heads_k and at most TGC_ATTENTION_MAX_HEADS, D <= TGC_ATTENTION_MAX_D

@@ -111,6 +111,28 @@ def test_the_largest_and_smallest_caps(scale, cap, S):
     assert bool(((out.double() - want).abs() <= 2 ** -9 * size + 2 ** -8 * want.abs()).all())
 
 
+@pytest.mark.parametrize("late", [0, 500, 900, 999])
+@pytest.mark.parametrize("S,Hk", [(400, 1), (40, 4), (1, 1)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_values_near_the_end_of_fp32(late, S, Hk, D):
+    """A key of e^5.25 times the others' weight (2^7.6: under any step of the reference) with values of 2^122 among zeros:
+    what comes out is finite, and so has to be the way there.  Scores are 0 and 5.25: off by 2^-22 in powers of two; the
+    parts of a probability by 2^-17, sums of 1000 by 2^-14, one rounding."""
+    n, page, wide = 1000, 16, 63
+    kp = torch.zeros(S * wide, page, Hk, D, device="cuda", dtype=BF)
+    vp = torch.zeros_like(kp)
+    table = torch.arange(S * wide, device="cuda", dtype=torch.int32).view(S, wide)
+    at = table[:, late // page].long()
+    kp[at, late % page, :, 0] = 5.25
+    vp[at, late % page] = 2.0 ** 122
+    q = torch.zeros(S, 2 * Hk, D, device="cuda", dtype=BF)
+    q[..., 0] = 1
+    out = torch.empty_like(q)
+    tgc.tgc_paged_attention(q, out, kp, vp, table, ints([n] * S), scale=1.0)
+    want = 2.0 ** 122 * math.exp(5.25) / (math.exp(5.25) + n - 1)
+    assert bool(((out.double() - want).abs() <= want * (2 ** -8 + 2 ** -13)).all())
+
+
 # ---------------------------------------------------------------- the cache's upkeep
 
 

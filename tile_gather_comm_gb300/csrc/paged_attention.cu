@@ -23,9 +23,10 @@
 // scores to probabilities to outputs does not hide behind it.
 // The probabilities enter the second product as a high and a low 16-bit part: rounding them to
 // 16 bits once would add about as much error as rounding the output does.
-// Probabilities are taken relative to a reference that follows the running maximum only when a score passes
-// it by Slack::kOver powers of two: until then they are larger, which costs no bits, and no lane needs another's
-// maximum.  fp16 has few exponents, so there the reference stays kLift powers of two below the maximum: what is lost
+// Probabilities are taken relative to a reference that follows the running maximum by steps (Slack): until the next one
+// they grow by up to kOver - kLift powers of two, which costs no bits, and no lane needs another's maximum.  In
+// bf16 the reference lies above the maximum, so that no probability passes 1: larger ones take values near fp32's end
+// past it.  fp16 has few exponents, so there it stays kLift powers of two below the maximum: what is lost
 // beneath fp16's smallest number is then at most 2^-36 of the largest key's weight a key, not 2^-25.
 //
 // Two ways to deal the work:
@@ -147,11 +148,11 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
     return (uint32_t)(row * DP * 2 + ((chunk ^ (row & 7)) << 4));
 }
 
-// Powers of two: the reference is set kLift below the maximum, and again when that passes it by kOver (probabilities up
-// to 2^kOver then; fp16 ends at 2^16).
+// Powers of two: the reference is set kLift below the maximum, and again when a score passes it by kOver (probabilities up
+// to 2^kOver then; fp16 ends at 2^16; bf16 has fp32's exponents below 1, and fp32's sums want 1 above).
 template <bool F16>
 struct Slack {
-    static constexpr float kLift = F16 ? 11.0f : 0.0f, kOver = F16 ? 15.0f : 8.0f;
+    static constexpr float kLift = F16 ? 11.0f : -8.0f, kOver = F16 ? 15.0f : 0.0f;
 };
 
 // DP: elements of a head, padded to 64, 128 or 256.  NT: query heads of an item, in eights.
