@@ -133,6 +133,27 @@ def test_values_near_the_end_of_fp32(late, S, Hk, D):
     assert bool(((out.double() - want).abs() <= want * (2 ** -8 + 2 ** -13)).all())
 
 
+@pytest.mark.parametrize("shape", [(6, 8, 1, 64), (1, 8, 2, 64), (6, 1, 2, 64)])
+def test_strides_of_one_entry_mean_nothing(shape):
+    """Keys and values whose strides differ only where a dimension has one entry."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    kp, vp = (torch.randn(shape, generator=g, device="cuda").to(BF) for _ in range(2))
+    strides = [s if n > 1 else 40 for n, s in zip(shape, vp.stride())]
+    odd = vp.as_strided(shape, strides)
+    table = ints([[0, min(3, shape[0] - 1), -1]])
+    n = ints([2 * shape[1]])
+    q = torch.randn(1, 2 * shape[2], 64, generator=g, device="cuda").to(BF)
+    want, out = torch.empty_like(q), torch.empty_like(q)
+    tgc.tgc_paged_attention(q, want, kp, vp, table, n)
+    tgc.tgc_paged_attention(q, out, kp, odd, table, n)
+    assert torch.equal(out, want)
+    x = torch.randn(1, shape[2], 64, generator=g, device="cuda").to(BF)
+    tgc.tgc_kv_append(x, x, kp, odd, table, ints([0]))
+    assert torch.equal(vp[0, 0], x[0]) and torch.equal(kp[0, 0], x[0])
+    with pytest.raises(ValueError):  # and where they mean something they have to be the same
+        tgc.tgc_paged_attention(q, out, kp, vp.transpose(1, 2).contiguous().transpose(1, 2) if shape[1] > 1 and shape[2] > 1 else vp[..., :32], table, n)
+
+
 # ---------------------------------------------------------------- the cache's upkeep
 
 

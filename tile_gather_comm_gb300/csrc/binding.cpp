@@ -371,8 +371,9 @@ struct Pages {
 
 Pages pages_of(const at::Tensor *k, const at::Tensor *v, at::ScalarType type) {
     if (k->dim() != 4 || k->scalar_type() != type) refuse("k_pages", "expected (pages, page size, heads, D) of the call's type");
-    if (v->scalar_type() != type || v->sizes() != k->sizes() || v->strides() != k->strides())
-        refuse("v_pages", "has another type, shape or strides than k_pages");
+    bool same = v->scalar_type() == type && v->sizes() == k->sizes();
+    for (int i = 0; same && i < 4; ++i) same = k->size(i) < 2 || v->stride(i) == k->stride(i);  // of one entry it means nothing
+    if (!same) refuse("v_pages", "has another type, shape or strides than k_pages");
     if (k->size(3) > 1 && k->stride(3) != 1) refuse("k_pages", "its last dimension must be contiguous");
     Pages p{k->data_ptr(), v->data_ptr(), k->size(0), k->size(1), k->size(2), k->size(3), 0, 0, 0};
     int64_t *const s[3] = {&p.page_s, &p.token_s, &p.head_s};
