@@ -221,3 +221,36 @@ def test_append_where_no_page_can_be():
         tgc.tgc_kv_append(x, x, pool, pool, torch.zeros(seq_n, wide, device="cuda", dtype=torch.int32), pos, seqs=seqs, q=x,
                           q_out=out, freqs=freqs)
         assert torch.equal(out, want) and not bool(pool.any())
+
+
+@pytest.mark.parametrize("seed", range(8))
+def test_corrupt_bookkeeping_moves_bytes_of_the_pool_alone(seed):
+    """Table entries, lengths and references that no history gives, and a pool between two pages that are not its own:
+    those stay, and every 16 bytes of the pool are some page's of it (a page may be a source and a destination at once
+    then, so not every page is one page's)."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    pages, seqs, wide, page = 32, 6, 8, 4
+
+    def mixed(n, low, high):
+        v = torch.randint(low, high, (n,), generator=g, device="cuda", dtype=torch.int32)
+        bad = torch.tensor([-1, -(2 ** 31), 2 ** 31 - 1, pages, pages + 1, -2], device="cuda", dtype=torch.int32)
+        pick = torch.randint(0, 24, (n,), generator=g, device="cuda")
+        return torch.where(pick < 6, bad[pick.clamp(max=5)], v)
+
+    refs, table, lens = mixed(pages, -2, 3), mixed(seqs * wide, 0, pages).view(seqs, wide), mixed(seqs, 0, wide * page)
+    lens[:2] = 0  # children that can be
+    pools = [torch.empty(pages + 2, page, 8, device="cuda", dtype=BF) for _ in range(2)]
+    for p in pools:
+        p.copy_(torch.arange(pages + 2, device="cuda")[:, None, None].expand_as(p))
+        p[0], p[-1] = -100, -200
+    inner = [p[1:-1] for p in pools]
+    tgc.tgc_kv_reserve(refs, table, lens, mixed(8, 2, seqs), mixed(8, 0, 9), page)
+    tgc.tgc_kv_fork(inner, refs, table, lens, mixed(7, 2, seqs), mixed(7, 0, seqs), page)
+    tgc.tgc_kv_compact(inner, refs, table)
+    tgc.tgc_kv_copy(inner, inner, mixed(4, 0, pages // 2), pages - 1 - mixed(4, 0, pages // 2))
+    tgc.tgc_kv_free(refs, table, lens, mixed(7, 0, seqs))
+    torch.cuda.synchronize()
+    for p, a in zip(pools, inner):
+        assert bool((p[0] == -100).all()) and bool((p[-1] == -200).all())
+        assert bool((a == a[..., :1]).all()) and bool((a >= 1).all()) and bool((a <= pages).all())
+        assert bool((a[:, 0, 0] != torch.arange(1, pages + 1, device="cuda")).any())  # something was moved
