@@ -886,8 +886,9 @@ int tgc_kv_append(const tgc_kv_append_args *args);
  *     j in [max(0, lens[s] - window), lens[s])   (window = 0: from 0)
  * with head h reading key head h / (heads_q / heads_k).  The new token's own key is one of them: it is appended
  * first and counted in lens.  A sequence without tokens gets zeros and lse = -inf.
- * Scores, softmax and sums are fp32 (the probabilities enter the product with V as two 16-bit parts,
- * which hold all that matters of them; with TGC_F16 at most 2^-36 of the largest one is lost a key), out is rounded once.  The same inputs give the same
+ * Scores, softmax and sums are fp32, out is rounded once.  The probabilities enter the product with V as two 16-bit parts:
+ * off by 2^-17 of each at most with TGC_BF16, where out's rounding is 2^-8 of it, by 2^-23 with TGC_F16 (out: 2^-11),
+ * and there by 2^-36 of the largest one a key.  The same inputs give the same
  * bits on every call with the same sizes.  Zero-initialise the struct.
  *
  * q, out     device (num_seqs, heads_q, D), `dtype`; q_s, q_h, o_s, o_h elements between sequences

@@ -154,6 +154,38 @@ def test_strides_of_one_entry_mean_nothing(shape):
         tgc.tgc_paged_attention(q, out, kp, vp.transpose(1, 2).contiguous().transpose(1, 2) if shape[1] > 1 and shape[2] > 1 else vp[..., :32], table, n)
 
 
+@pytest.mark.parametrize("dtype", [BF, torch.float16])
+def test_two_parts_of_a_probability(dtype):
+    """Hundreds of keys of one weight against 16 of another (one of every 32, so that every warp's reference comes of
+    them), whose values nearly cancel: what is left shows what the two 16-bit parts of a probability lose, 2^-17 of it in bf16 (8 bits, then 8 bits of a rest below 2^-8) and 2^-23 in fp16.
+    Beside that: scores are exact, times log2(e) off by 2^-24 of 2^3, the exponential by 2^-22, 25 sums of a lane and
+    of the lanes by 2^-24 each, 16 products of 16 keys by 2^-22 each: 2^-17 in all, and one rounding of the result."""
+    n, D, page, wide = 512, 64, 16, 32
+    scores = [float(torch.tensor(-k / 64).to(dtype)) for k in range(3, 250, 5)]
+    S = len(scores)
+    keys, values = torch.full((S, n), -64.0, dtype=torch.float64), torch.zeros(S, n, dtype=torch.float64)
+    for s, x in enumerate(scores):
+        _, m, c = min((abs(m * math.exp(x) - c), m, c) for m in range(200, 496)
+                      for c in [float(torch.tensor(m * math.exp(x)).to(dtype))])
+        light = torch.arange(n)[torch.arange(n) % 32 != 0][:m]
+        keys[s, ::32], values[s, ::32] = 0.0, -c / 16
+        keys[s, light], values[s, light] = x, 1.0
+    p = torch.softmax(keys, 1)
+    want, size = (p * values).sum(1), (p * values.abs()).sum(1)
+    assert float((want.abs() / size).max()) < 2 ** -10  # the result's own rounding: 2^-18 of size
+    kp = torch.zeros(S * wide, page, 1, D, device="cuda", dtype=dtype)
+    kp[..., 0] = keys.view(S * wide, page, 1).cuda().to(dtype)
+    vp = values.view(S * wide, page, 1, 1).cuda().to(dtype).expand(-1, -1, -1, D).contiguous()
+    q = torch.zeros(S, 1, D, device="cuda", dtype=dtype)
+    q[..., 0] = 1
+    out = torch.empty_like(q)
+    tgc.tgc_paged_attention(q, out, kp, vp, torch.arange(S * wide, device="cuda", dtype=torch.int32).view(S, wide), ints([n] * S), scale=1.0)
+    err = (out[:, 0].double() - want.cuda()[:, None]).abs().amax(1).cpu()
+    lost = {BF: 2 ** -17, torch.float16: 2 ** -23}[dtype]
+    assert dtype != BF or float((err / size).max()) > 2 ** -20  # what the parts lose is seen here
+    assert bool((err <= (lost + 2 ** -17) * size + torch.finfo(dtype).eps / 2 * want.abs() + 2 ** -25).all())
+
+
 # ---------------------------------------------------------------- the cache's upkeep
 
 

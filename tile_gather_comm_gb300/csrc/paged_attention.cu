@@ -22,7 +22,8 @@
 // 16 to 64 columns, also where neighbouring ones do not depend on each other: 2100 for 128 keys, and the way from
 // scores to probabilities to outputs does not hide behind it.
 // The probabilities enter the second product as a high and a low 16-bit part: rounding them to
-// 16 bits once would add about as much error as rounding the output does.
+// 16 bits once would add about as much error as rounding the output does.  Both parts lose 2^-17 of a probability at most in
+// bf16, 2^-23 in fp16; a third one would make the second product half as long again, for a 512th of the output's own rounding.
 // Probabilities are taken relative to a reference that follows the running maximum by steps (Slack): until the next one
 // they grow by up to kOver - kLift powers of two, which costs no bits, and no lane needs another's maximum.  In
 // bf16 the reference lies above the maximum, so that no probability passes 1: larger ones take values near fp32's end
