@@ -10,6 +10,7 @@ import torch
 
 import tile_gather_comm_gb300 as tgc
 from tile_gather_comm_gb300 import _lib
+from tests import test_gpu_paged_attention as attention
 from tests.helpers import requires_gpu
 
 pytestmark = pytest.mark.gpu
@@ -152,6 +153,21 @@ def test_strides_of_one_entry_mean_nothing(shape):
     assert torch.equal(vp[0, 0], x[0]) and torch.equal(kp[0, 0], x[0])
     with pytest.raises(ValueError):  # and where they mean something they have to be the same
         tgc.tgc_paged_attention(q, out, kp, vp.transpose(1, 2).contiguous().transpose(1, 2) if shape[1] > 1 and shape[2] > 1 else vp[..., :32], table, n)
+
+
+@pytest.mark.parametrize("lens,Hk,group,D,page", attention.FOURS + [([200, 0, 7, 33] * 6, 8, 8, 64, 8), ([300, 1] * 20, 4, 7, 104, 16)])
+@pytest.mark.parametrize("dtype", list(attention.DT))
+def test_key_heads_by_fours_under_wide_tables(lens, Hk, group, D, page, dtype):
+    """Tables wide enough that every warp takes a key head of its own, whatever the lengths are."""
+    g = attention.gen(sum(lens) + D)
+    items = len(lens) * Hk
+    wide = max(0, 2 * 304 * 1300 * group // items) // page + 1
+    kp, vp, table, n, keys = attention.cache(lens, page, Hk, D, attention.DT[dtype], g, wide=wide)
+    q = torch.randn(len(lens), Hk * group, D, generator=g, device="cuda").to(attention.DT[dtype])
+    for window, cap in ((0, 0.0), (37, 5.0)):
+        out, lse = torch.full_like(q, 7.0), torch.full((len(lens), Hk * group), 7.0, device="cuda")
+        tgc.tgc_paged_attention(q, out, kp, vp, table, n, lse=lse, window=window, softcap=cap)
+        attention.check(out, lse, q, keys, D ** -0.5, window, cap)
 
 
 @pytest.mark.parametrize("dtype", [BF, torch.float16])

@@ -934,10 +934,16 @@ struct AttnPlan {
 // more than a run would have; runs otherwise.  With 8 heads of 128 x 4 a key, clusters and runs take 5.8 and 7.7 us for
 // 200 tokens, 7.6 and 8.4 for 900, 9.6 and 9.3 for 2000, 13.6 and 11.6 for 4000 (8 units where a run has 2), 13.9 and 15.7 for
 // 16 x 1000 (8 and 7), 12.0 and 18.3 for 32 x 500.  Runs: one for each of two CTAs an SM, no more than there can be units.
-// Own runs from as many items on as a head has elements (the parts grow with those): 64 x 8192 tokens, 8 x 4 heads x 128, 192.5
-// against 200.9 us, 16 x 4000 34.8 and 39.9, 8 x 20000 the same 75, 1 x 32000 38.0 and 33.4; 48 x 2000 of 5000, 16 heads x 64,
-// 63.7 and 72.1, 64 x 4000 101.5 and 121.7, 8 x 30000 of 8 heads 58.2 and 64.3.
+// Own runs where what the four times longer rows and the meetings saved give is more than their four times as many parts
+// cost, which grow with the heads that share a key: where items * (most keys + kOwnEnd) is at least kOwnKeys a run and such
+// head.  1010 sizes (64, 80, 96, 128 elements, 1 to 8 heads a key, 16 to 2048 items of 200 to 24000 keys), own against
+// shared: 1.09 of the time within a quarter below the line, 0.98 within a third above it, 0.90 from four times it on:
+// of 128 elements, 384 items x 200 x 8 heads 21.9 us against 15.6, 256 x 1500 x 8 31.9 and 28.3 (below), 512 x 1500 x 1 43.4 and
+// 48.1 (above); of 64, 256 x 24000 x 8 138 and 149 (above).  And from as many items on as a head has elements: fewer that pass take 0.98 to 1.14 of the time
+// (96 x 24000 x 8 heads x 128 101 and 99 us, 48 x 24000 x 1 x 64 33 and 32), and a table much wider than its lengths
+// passes with any.
 constexpr int kClusterUnits = 16, kClusterBehind = 3;
+constexpr int64_t kOwnEnd = 2500, kOwnKeys = 1300;
 
 static AttnPlan attn_plan(const tgc_paged_attention_args &a, int sms) {
     AttnPlan q{};
@@ -961,7 +967,8 @@ static AttnPlan attn_plan(const tgc_paged_attention_args &a, int sms) {
     }
     const int64_t runs = q.items * units;
     q.grid = (int)(runs < 1 ? 1 : runs < room ? runs : room);
-    if (q.dp <= 128 && q.nt == 1 && a.heads_k % kAttnWarps == 0 && q.items >= q.dp) {
+    if (q.dp <= 128 && q.nt == 1 && a.heads_k % kAttnWarps == 0 && q.items >= q.dp &&
+        q.items * (most + kOwnEnd) >= room * kOwnKeys * group) {
         q.own = kAttnWarps;
         q.unit /= kAttnWarps;
     }
