@@ -161,7 +161,7 @@ def test_key_heads_by_fours_under_wide_tables(lens, Hk, group, D, page, dtype):
     """Tables wide enough that every warp takes a key head of its own, whatever the lengths are."""
     g = attention.gen(sum(lens) + D)
     items = len(lens) * Hk
-    wide = max(0, 2 * 304 * 1300 * group // items) // page + 1
+    wide = 2 * 304 * 900 * group // items // page + 1
     kp, vp, table, n, keys = attention.cache(lens, page, Hk, D, attention.DT[dtype], g, wide=wide)
     q = torch.randn(len(lens), Hk * group, D, generator=g, device="cuda").to(attention.DT[dtype])
     for window, cap in ((0, 0.0), (37, 5.0)):

@@ -936,14 +936,13 @@ struct AttnPlan {
 // 16 x 1000 (8 and 7), 12.0 and 18.3 for 32 x 500.  Runs: one for each of two CTAs an SM, no more than there can be units.
 // Own runs where what the four times longer rows and the meetings saved give is more than their four times as many parts
 // cost, which grow with the heads that share a key: where items * (most keys + kOwnEnd) is at least kOwnKeys a run and such
-// head.  1010 sizes (64, 80, 96, 128 elements, 1 to 8 heads a key, 16 to 2048 items of 200 to 24000 keys), own against
-// shared: 1.09 of the time within a quarter below the line, 0.98 within a third above it, 0.90 from four times it on:
-// of 128 elements, 384 items x 200 x 8 heads 21.9 us against 15.6, 256 x 1500 x 8 31.9 and 28.3 (below), 512 x 1500 x 1 43.4 and
-// 48.1 (above); of 64, 256 x 24000 x 8 138 and 149 (above).  And from as many items on as a head has elements: fewer that pass take 0.98 to 1.14 of the time
-// (96 x 24000 x 8 heads x 128 101 and 99 us, 48 x 24000 x 1 x 64 33 and 32), and a table much wider than its lengths
-// passes with any.
+// head.  1578 sizes (64 to 128 elements, 1 to 8 heads a key, 16 to 8192 items of up to 200 to 30000 keys, uneven), own against
+// shared: 1.06 of the time within a quarter below the line, 0.99 within a third above it, 1.09 under half of it, 0.89 from
+// four times it on; 384 items x 200 keys x 8 heads x 128 21.9 us and 15.6, 96 x 3000 x 8 x 64 20.7 and 16.3 (below), 512 x 1500 x 1 x 128
+// 43.4 and 48.1, 256 x 24000 x 8 x 64 138 and 149 (above).  Keys past kOwnMost do not count: a table that is much wider
+// than its lengths would pass with any.
 constexpr int kClusterUnits = 16, kClusterBehind = 3;
-constexpr int64_t kOwnEnd = 2500, kOwnKeys = 1300;
+constexpr int64_t kOwnEnd = 1500, kOwnMost = 16384, kOwnKeys = 900;
 
 static AttnPlan attn_plan(const tgc_paged_attention_args &a, int sms) {
     AttnPlan q{};
@@ -967,8 +966,8 @@ static AttnPlan attn_plan(const tgc_paged_attention_args &a, int sms) {
     }
     const int64_t runs = q.items * units;
     q.grid = (int)(runs < 1 ? 1 : runs < room ? runs : room);
-    if (q.dp <= 128 && q.nt == 1 && a.heads_k % kAttnWarps == 0 && q.items >= q.dp &&
-        q.items * (most + kOwnEnd) >= room * kOwnKeys * group) {
+    if (q.dp <= 128 && q.nt == 1 && a.heads_k % kAttnWarps == 0 &&
+        q.items * (std::min(most, kOwnMost) + kOwnEnd) >= room * kOwnKeys * group) {
         q.own = kAttnWarps;
         q.unit /= kAttnWarps;
     }
