@@ -236,8 +236,9 @@ def test_upkeep_without_pools():
 @pytest.mark.parametrize("back", [False, True])
 def test_angles_keep_their_bits(layout, back):
     """Fast and slow pairs at near and far positions against whole-number arithmetic.  The fraction of a turn is off by
-    2^-64 a position (2^-61.3 radians, with its product's 2^-106); the angle is rounded to fp32, 2^-24 of itself, and its
-    factor pi, sine and cosine by 2 units (2^-23 each): 2^-21 in all, of a small angle's sine relative to it."""
+    2^-64 a position (2^-61.3 radians, with its product's 2^-106); the angle is rounded to fp32 twice, 2^-23 of itself,
+    sine and cosine by 2 units (2^-23 each): 2^-23 |w cos w| + 2^-22 |sin w|, below 2^-21 up to w = pi and below
+    2^-21 w for a small one, and the same with sine and cosine the other way round."""
     freqs = [1.0, 0.7310585786300049, 0.11, 0.5, math.pi, 100.3, 12345.678, -0.9, 1e-3, 1e-7, 1e-9, 3e-12, -1e-10, 2.0 ** 40 + 0.5, 0.0]
     pos = [0, 1, 3, 4097, 999983, 16777217, 2 ** 31 - 1]
     R = 2 * len(freqs)

@@ -100,8 +100,8 @@ __device__ __forceinline__ uint64_t turn_fraction(double freq) {
 //
 // The angle: freq / 2 pi, taken modulo 1, is held as a 64-bit fraction of a turn (turn_fraction), and its product with
 // the position modulo 2^64 is the angle's: whole turns fall off the top.  The fraction is off by one 2^-64 at most, so
-// the angle by 2^-33 turns at the farthest position; it is rounded to fp32 relative to itself, so that a small
-// one keeps its bits, and sine and cosine are taken in fp32.  fp64 is needed once a pair and block.
+// the angle by 2^-33 turns at the farthest position; it is rounded to fp32 relative to itself (2^-23 of it), so that a
+// small one keeps its bits, and sine and cosine are taken in fp32.  fp64 is needed once a pair and block.
 //
 // Bound by HBM where there are many tokens, by the launch where there are few.
 constexpr int kRopeThreads = 256;
@@ -153,7 +153,12 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const RopeParams 
         const int t = p.half.of(i);
         const uint64_t angle = s_freq[i - t * half] * (uint64_t)(uint32_t)s_pos[t];
         float c, s;
-        sincospif((float)(int64_t)angle * 0x1p-63f, &s, &c);  // half turns
+        // its size in half turns: the halves one by one, as a conversion from 64 bits takes longer (8192 tokens of a head of 256
+        // fp32: 7.65 and 7.47 us)
+        const bool back = (int64_t)angle < 0;
+        const uint64_t size = back ? 0 - angle : angle;
+        const float half_turns = fmaf((float)(uint32_t)size, 0x1p-63f, (float)(uint32_t)(size >> 32) * 0x1p-31f);
+        sincospif(back ? -half_turns : half_turns, &s, &c);
         s_cos[i] = c * p.scale;
         s_sin[i] = s * p.scale * p.sign;
     }
