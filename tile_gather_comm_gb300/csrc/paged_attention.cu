@@ -2,8 +2,9 @@
 //
 //   x_j = scale q.k_j (capped by c tanh(x / c)),  out = sum_j softmax(x)_j v_j,  lse = log sum_j exp(x_j)
 //
-// Every key and value is read once and used for the G query heads that share it: 4 G flops for 4
-// bytes, so HBM is the bound and the design is about keeping loads in flight.
+// Every key and value is read once and used for the G query heads that share it (once for every 32 of them, 16 with
+// more than 128 elements, where G is larger): 4 G flops for 4 bytes, so HBM is the bound up to 8 heads and the design is
+// about keeping loads in flight.
 //
 // A CTA's 4 warps work for themselves: of each unit of keys a warp takes its quarter, or all of its own
 // head (a step), copies it with cp.async into its own ring of slots, and keeps its own reference, sum and
@@ -13,14 +14,16 @@
 //
 // Products: mma.sync m16n8k16 with keys (then elements of the values) as rows and the heads that share a key
 // as columns, padded to 8: scores^T = K Q^T, out^T = V^T P^T.  The scores come out with a key a lane group,
-// and movmatrix turns 8 x 8 of them into the second product's operand.  A quarter of an SM takes 32 clocks
-// for one of them: 768 for 16 keys of up to 8 heads x 128, whose bytes take HBM 1400 a quarter; with 16 heads the
-// products are the bound (64 x 1850 tokens, 2 x 16 heads x 128: 42 us, bytes 23).
+// and movmatrix turns 8 x 8 of them into the second product's operand.  A quarter of an SM takes 8 clocks for one of
+// them (21 where the next one needs its sums): 192 for 16 keys of up to 8 heads x 128, whose bytes take HBM 1400 a quarter.
+// With 16 and 32 heads neither products nor bytes are the bound, but the chain of scores, softmax and outputs in each of the
+// two warps that a quarter has: 64 x up to 4000 tokens, 2 x 16 heads x 128, 42 us (bytes 23): tensor pipe 19 % busy, HBM 49 %,
+// issue slots 36 %, and of 5.2 warp cycles an instruction 2.0 for fixed latencies, 1.0 for shared memory, 0.4 for loads; 1 x
+// 32 heads 42 us (bytes 11), 2 x 16 x 256 84 (45), where registers run out as well (192 and 124 bytes of spills read).
 // The same on tcgen05 -- 128 keys or elements as rows, heads as columns, scores and outputs in TMEM, warps of
 // their own for copies, products and softmax -- was built and measured: 66 us there, 98 against 83 with 256
-// elements a head, 220 against 126 for 170 sequences of 70 tokens.  A product of 128 rows takes it 130 clocks whatever its
-// 16 to 64 columns, also where neighbouring ones do not depend on each other: 2100 for 128 keys, and the way from
-// scores to probabilities to outputs does not hide behind it.
+// elements a head, 220 against 126 for 170 sequences of 70 tokens.  A product of 128 rows took 130 clocks there at 16 to 64
+// columns, more than the unit needs, so that form was not at its best; it is not kept.
 // The probabilities enter the second product as a high and a low 16-bit part: rounding them to
 // 16 bits once would add about as much error as rounding the output does.  Both parts lose 2^-17 of a probability at most in
 // bf16, 2^-23 in fp16; a third one would make the second product half as long again, for a 512th of the output's own rounding.
@@ -191,8 +194,8 @@ struct AttnShape {
 
 // How the work is dealt: see the top.
 enum AttnForm { kRuns, kOwnRuns, kClusters };
-// Shapes whose queries fit beside the rings, two CTAs an SM; with 16 heads a key (x 64) the products are the bound, and 43.6 and
-// 43.1 us the same (200 x 1000 tokens).
+// Shapes whose queries fit beside the rings, two CTAs an SM.  Those of 64 elements x 16 heads would: 200 x 1000 tokens of 4 x 16
+// heads take 40.3 us so and 40.4, 64 x 4000 38.5 both, 200 x 1000 of 8 x 9 61.2 and 66.7; no instances for it.
 template <int DP, int NT>
 constexpr bool kOwnFits = DP <= 128 && NT == 1;
 static_assert(AttnShape<128, 1>::kOwnSmem <= 112 * 1024 && AttnShape<64, 1>::kOwnSmem <= 112 * 1024, "two CTAs an SM");
