@@ -57,8 +57,8 @@ class Cache:
     def reserve(self, seqs, ok):
         tgc.tgc_kv_reserve(self.refs, self.table, self.lens, seqs, torch.ones_like(seqs), self.page, ok=ok)
 
-    def fork(self, src, dst):
-        tgc.tgc_kv_fork(self.pools, self.refs, self.table, self.lens, src, dst, self.page)
+    def fork(self, src, dst, ok=None):
+        tgc.tgc_kv_fork(self.pools, self.refs, self.table, self.lens, src, dst, self.page, ok=ok)
 
     def free(self, seqs):
         tgc.tgc_kv_free(self.refs, self.table, self.lens, seqs)
@@ -116,13 +116,18 @@ def main(argv=None):
     cache = Cache(model, S * (-(-most // a.page)), a.page, S, -(-most // a.page))
     prompt = torch.randint(0, len(model.embed), (40, S), generator=g, device=dev)
     parents = torch.arange(a.prompts, device=dev, dtype=torch.int32)
+    refused = torch.zeros((), device=dev, dtype=torch.int64)  # tokens and branches that found no room
+    ok = torch.empty_like(parents)
     for t in range(40):
-        logits = step(model, cache, prompt[t], parents)
+        logits = step(model, cache, prompt[t], parents, ok)
+        refused += (ok == 0).sum()
     children = torch.arange(a.prompts, S, device=dev, dtype=torch.int32)
-    cache.fork(children % a.prompts, children)
+    ok = torch.empty_like(children)
+    cache.fork(children % a.prompts, children, ok)
+    refused += (ok == 0).sum()
     live = torch.arange(S, device=dev, dtype=torch.int32)
     logits = logits[live % a.prompts]
-    ok, refused = torch.empty_like(live), torch.zeros((), device=dev, dtype=torch.int64)
+    ok = torch.empty_like(live)
     texts = []
     for t in range(a.steps):
         p = torch.softmax(logits.float(), -1)
@@ -137,7 +142,7 @@ def main(argv=None):
         logits = step(model, cache, tokens, live, ok)
         refused += (ok == 0).sum()
     if int(refused):
-        raise RuntimeError(f"the cache had no room for {int(refused)} tokens")
+        raise RuntimeError(f"the cache had no room for {int(refused)} tokens or branches")
     texts = torch.stack(texts, 1)
     for s in live.tolist():
         print(f"sequence {s:2d} ({int(cache.lens[s])} tokens): {texts[s].tolist()}")

@@ -87,6 +87,20 @@ def test_a_step_that_finds_no_room_keeps_every_token(held):
         assert same(tokens_of(cache, s, 8), before[s])
 
 
+def test_the_example_says_when_its_cache_is_too_small():
+    """Pages for the prompts and no branch's copy of a part-filled one: the run ends with an error, not with tokens of
+    sequences that were never made."""
+    m = example()
+
+    class Small(m.Cache):
+        def __init__(self, model, pages, page, seqs, max_pages):
+            super().__init__(model, 2 * -(-40 // page), page, seqs, max_pages)
+
+    m.Cache = Small
+    with pytest.raises(RuntimeError, match="no room"):
+        m.main(["--steps", "2", "--prompts", "2", "--branches", "1"])
+
+
 # ---------------------------------------------------------------- attention
 
 
