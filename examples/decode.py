@@ -68,7 +68,7 @@ class Cache:
 
 
 def step(model, cache, tokens, live, ok=None):
-    """One token of every sequence in ``live`` (int32, each once) through the model; tokens has one for every sequence of
+    """One token of every sequence in ``live`` (int32) through the model; tokens has one for every sequence of
     the cache.  Returns logits (sequences, vocabulary).  A sequence that is not in ``live``, or that the cache has
     no room for (``ok``, int32 beside ``live``, says which it had), keeps its tokens as they are; its row of the logits
     means nothing."""
@@ -77,9 +77,9 @@ def step(model, cache, tokens, live, ok=None):
     ok = torch.empty_like(live) if ok is None else ok
     cache.reserve(live, ok)
     # the new token's position where there is one, -1 elsewhere: nothing of those is appended
-    at = live.long()
+    at = live.long().clamp(0, S - 1)  # what is no sequence, or is named again, was refused
     pos = torch.full_like(cache.lens, -1)
-    pos.scatter_(0, at, torch.where(ok > 0, cache.lens[at] - 1, -1))
+    pos.scatter_reduce_(0, at, torch.where(ok > 0, cache.lens[at] - 1, -1), "amax")
     x = model.embed[tokens]
     for i, w in enumerate(model.layers):
         keys, values = cache.pools[2 * i:2 * i + 2]

@@ -87,6 +87,20 @@ def test_a_step_that_finds_no_room_keeps_every_token(held):
         assert same(tokens_of(cache, s, 8), before[s])
 
 
+def test_a_step_that_names_sequences_twice_and_none():
+    """The same as one that names each sequence once."""
+    m = example()
+    model = m.Model(seed=3)
+    caches = [m.Cache(model, 16, 4, 4, 5) for _ in range(2)]
+    for t in range(6):
+        tokens = torch.full((4,), 3 * t + 1, device="cuda")
+        want = m.step(model, caches[0], tokens, ints([0, 2, 3]))
+        ok = ints([9] * 7)
+        got = m.step(model, caches[1], tokens, ints([0, 3, 2, 0, -1, 4, 2]), ok)
+        assert ok.tolist() == [1, 1, 1, 0, 0, 0, 0] and caches[1].lens.tolist() == [t + 1, 0, t + 1, t + 1]
+        assert torch.equal(got[[0, 2, 3]], want[[0, 2, 3]])
+
+
 def test_the_example_says_when_its_cache_is_too_small():
     """Pages for the prompts and no branch's copy of a part-filled one: the run ends with an error, not with tokens of
     sequences that were never made."""
